@@ -369,6 +369,148 @@ int gemm_bf16_set_clock_sampling(int enable);
  */
 int gemm_bf16_clock_samples(uint64_t* out, int reset);
 
+/* ---------------------------------------------------------------------------
+ * 8-bit operands and the operators around the product.
+ *
+ * 8-bit values are e4m3 (4 exponent bits, 3 mantissa bits, largest value 448,
+ * NaN but no infinity), one byte each.  A scale (fp32) belongs to a block of
+ * 128 values along k, of one row or of 128 rows; the value a byte q stands
+ * for is q * scale.  Scales are stored with the k block first, so that the
+ * scales of consecutive rows at one k block are consecutive:
+ *
+ *     rows:    scale[kb * ld + r]          covers X[r][128 kb .. 128 kb + 127]
+ *     blocks:  scale[kb * ld + (r / 128)]  covers the same columns of 128 rows
+ *
+ * Quantising y: a block's scale is max|y| / 448, at least 2^-126, and each
+ * value becomes the nearest e4m3 value to y / scale (ties to even).  Blocks at
+ * the right and bottom edge hold fewer values.  A block that holds a NaN or
+ * an infinity gets a NaN or infinite scale, so every value it stands for is
+ * NaN or infinite; its bytes are unspecified.
+ *
+ * All entry points are asynchronous on `stream`, validate as gemm_bf16 does
+ * and return the same status codes.  Sizes and leading dimensions are in
+ * elements.  Row strides are arbitrary (a leading dimension at least the row
+ * length; anything goes for a single row), and bf16 pointers need 2-byte,
+ * fp32 pointers 4-byte alignment; 16-byte aligned rows are faster.  An output
+ * may not overlap an input or another output (GEMM_ERR_ALIAS) except where a
+ * function says so.  A type or block size that a function does not have is
+ * GEMM_ERR_INVALID_VALUE.  Arithmetic is fp32 (sums, statistics, scales), rounded
+ * once to each output's type.
+ * ------------------------------------------------------------------------- */
+
+/* Types of an output. */
+enum {
+    GEMM_TYPE_BF16 = 0,
+    GEMM_TYPE_FP8 = 1,   /* e4m3 bytes, with row scales */
+    GEMM_TYPE_FP32 = 2
+};
+
+/* The widest row gemm_rms_norm and gemm_rms_norm_bwd take (a row stays in one
+ * workgroup's registers). */
+enum { GEMM_NORM_MAX_WIDTH = 32768 };
+
+/*
+ * gemm_fp8_bt: C[M,N] = (A * SA) * (B * SB)^T for 8-bit A (M x K, row-major,
+ * lda >= K) and B stored N x K (ldb >= K):
+ *
+ *     C[i][j] = sum_kb SA[kb*ldsa + i] * SB[kb*ldsb + j / b_block_rows] *
+ *               sum_{k in block kb} A[i][k] * B[j][k]
+ *
+ * with k blocks of 128 (the last one may be shorter), both sums in fp32.
+ * b_block_rows is 128 (a weight's blocks, ldsb >= ceil(N / 128)) or 1 (row
+ * scales, ldsb >= N); ldsa >= M.  c_type is GEMM_TYPE_BF16 or GEMM_TYPE_FP32,
+ * ldc >= N.
+ *
+ * The same product serves a linear layer's forward pass (A activations, B the
+ * weight), its input gradient (A the output's gradient, B the transposed
+ * weight) and its weight gradient (both operands transposed and quantised
+ * along the tokens, b_block_rows 1, fp32 C): gemm_quantize_fp8 makes each
+ * operand.
+ *
+ * M, N, K >= 0, N and K at most 2^22, M below 2^31.  M == 0 or N == 0 is a
+ * no-op, K == 0 writes +0.  K and the leading dimensions of A and B multiples
+ * of 16 with 16-byte aligned A and B run directly; any other call copies the
+ * operands that need it, zero-padded, into temporary memory first.  Split k
+ * ranges (few output tiles, long K) put fp32 partial tiles there, summed in a
+ * fixed order.  Temporary memory is gemm_bf16's (kept blocks, see there).
+ * Results are deterministic for given sizes, strides and alignment.
+ */
+int gemm_fp8_bt(int64_t M, int64_t N, int64_t K,
+                const void* A, int64_t lda, const float* SA, int64_t ldsa,
+                const void* B, int64_t ldb, const float* SB, int64_t ldsb, int b_block_rows,
+                void* C, int64_t ldc, int c_type, void* stream);
+
+/*
+ * gemm_quantize_fp8: quantises bf16 X (M x K, ldx >= K) into Q and scales.
+ * block_rows 1: a scale for each row and k block; 128: for each 128 x 128
+ * block.  transposed != 0 quantises the transpose of X instead: Q is K x M
+ * (ldq >= M), its rows are X's columns and its k blocks run along M;
+ * otherwise Q is M x K (ldq >= K).  With R rows and L columns of Q the scales
+ * are ceil(L / 128) rows of R (block_rows 1) or ceil(R / 128) (128) values,
+ * lds apart.  M == 0 or K == 0 is a no-op.
+ */
+int gemm_quantize_fp8(int64_t M, int64_t K, const void* X, int64_t ldx,
+                      void* Q, int64_t ldq, float* scale, int64_t lds,
+                      int block_rows, int transposed, void* stream);
+
+/*
+ * gemm_rms_norm: for each of M rows of D values, with h = x + residual (h = x
+ * when residual is NULL):
+ *
+ *     rstd = 1 / sqrt(mean(h^2) + eps),   y = h * rstd * weight
+ *
+ * x, residual, weight (D values) are bf16.  H (M x D bf16) receives h; it is
+ * required with a residual and ignored without one, and it may be the very
+ * memory of x or of residual (same pointer and leading dimension).  y_type
+ * GEMM_TYPE_BF16: Y is bf16, and may be the very memory of x unless H is;
+ * scale is ignored.  GEMM_TYPE_FP8: Y is 8 bits
+ * with row scales (lds >= M).  The statistics and y use h before its rounding
+ * to bf16.  rstd (M fp32 values) is written unless NULL.
+ * M == 0 is a no-op.  D is 1 .. GEMM_NORM_MAX_WIDTH (GEMM_ERR_INVALID_VALUE
+ * below, GEMM_ERR_UNSUPPORTED_SHAPE above); eps must be >= 0 and finite.
+ */
+int gemm_rms_norm(int64_t M, int64_t D, const void* X, int64_t ldx,
+                  const void* residual, int64_t ldr, const void* weight, float eps,
+                  void* H, int64_t ldh, void* Y, int64_t ldy, int y_type,
+                  float* scale, int64_t lds, float* rstd, void* stream);
+
+/*
+ * gemm_rms_norm_bwd: the gradients of gemm_rms_norm.  dY is the gradient of
+ * y, dres (may be NULL) the gradient that reaches h directly (the residual
+ * stream), h and rstd what the forward pass read (x without a residual) and
+ * wrote.  With n = h * rstd:
+ *
+ *     dX = dres + rstd * (dY * weight - n * mean(dY * weight * n))
+ *     dweight[j] = sum over rows of dY[.][j] * n[.][j]
+ *
+ * dX (bf16) is the gradient of x and of residual alike; it may be the very
+ * memory of dY or dres.  dweight is fp32, D values, overwritten (M == 0
+ * writes zeros).  Rows are summed in a fixed order.  D as in gemm_rms_norm.
+ */
+int gemm_rms_norm_bwd(int64_t M, int64_t D, const void* dY, int64_t lddy,
+                      const void* H, int64_t ldh, const void* weight, const float* rstd,
+                      const void* dres, int64_t lddr, void* dX, int64_t lddx,
+                      float* dweight, void* stream);
+
+/*
+ * gemm_swiglu: y = g / (1 + exp(-g)) * u for bf16 GU (M x 2F, ldgu >= 2F; row
+ * i holds g in columns 0 .. F-1 and u in F .. 2F-1).  Y is M x F, bf16 or 8
+ * bits with row scales (lds >= M) by y_type.  M == 0 or F == 0 is a no-op.
+ */
+int gemm_swiglu(int64_t M, int64_t F, const void* GU, int64_t ldgu,
+                void* Y, int64_t ldy, int y_type, float* scale, int64_t lds, void* stream);
+
+/*
+ * gemm_swiglu_bwd: dGU (M x 2F bf16, the gradients of g and u side by side)
+ * from dY (M x F) and GU, with s = 1 / (1 + exp(-g)):
+ *
+ *     dg = dY * u * s * (1 + g * (1 - s)),   du = dY * g * s
+ *
+ * dGU may be the very memory of GU.
+ */
+int gemm_swiglu_bwd(int64_t M, int64_t F, const void* dY, int64_t lddy,
+                    const void* GU, int64_t ldgu, void* dGU, int64_t lddgu, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

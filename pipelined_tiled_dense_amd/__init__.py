@@ -8,10 +8,12 @@ from __future__ import annotations
 
 import importlib
 
-__all__ = ["binding", "inputs", "gemm", "GemmError", "SYNC_MODES"]
+_FROM_BINDING = ("gemm", "gemm_fp8", "quantize_fp8", "rms_norm", "rms_norm_backward", "swiglu", "swiglu_backward",
+                 "RmsNorm", "GemmError", "SYNC_MODES")
+__all__ = ["binding", "inputs", *_FROM_BINDING]
 
 
 def __getattr__(name):
-    if name in ("gemm", "GemmError", "SYNC_MODES"):
+    if name in _FROM_BINDING:
         return getattr(importlib.import_module(__name__ + ".binding"), name)
     raise AttributeError(name)

@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIBRARY = os.path.join(HERE, "libgemm_bf16.so")
@@ -26,6 +27,11 @@ GEMM_NOALLOC_SCRATCH_BYTES = 64 * 1024 * 1024
 
 SYNC_MODES = {"barrier": 0, "flags": 1, "wavespec": 2, "pingpong": 3}
 STAGES_WINDOWS = 5          # GEMM_STAGES_WINDOWS: the split-window ring (barrier sync)
+TYPE_BF16 = 0
+TYPE_FP8 = 1
+TYPE_FP32 = 2
+BLOCK = 128                 # values along k (and rows of a block) that share a scale
+NORM_MAX_WIDTH = 32768      # GEMM_NORM_MAX_WIDTH
 
 
 class GemmError(RuntimeError):
@@ -87,6 +93,15 @@ def library() -> ctypes.CDLL:
         lib.gemm_bf16_workspace_info.restype = i32
         lib.gemm_bf16_release_workspaces.argtypes = []
         lib.gemm_bf16_release_workspaces.restype = i32
+        lib.gemm_fp8_bt.argtypes = [i64, i64, i64, p, i64, p, i64, p, i64, p, i64, i32, p, i64, i32, p]
+        lib.gemm_quantize_fp8.argtypes = [i64, i64, p, i64, p, i64, p, i64, i32, i32, p]
+        lib.gemm_rms_norm.argtypes = [i64, i64, p, i64, p, i64, p, ctypes.c_float, p, i64, p, i64, i32, p, i64, p, p]
+        lib.gemm_rms_norm_bwd.argtypes = [i64, i64, p, i64, p, i64, p, p, p, i64, p, i64, p, p]
+        lib.gemm_swiglu.argtypes = [i64, i64, p, i64, p, i64, i32, p, i64, p]
+        lib.gemm_swiglu_bwd.argtypes = [i64, i64, p, i64, p, i64, p, i64, p]
+        for name in ("gemm_fp8_bt", "gemm_quantize_fp8", "gemm_rms_norm", "gemm_rms_norm_bwd", "gemm_swiglu",
+                     "gemm_swiglu_bwd"):
+            getattr(lib, name).restype = i32
         _lib = lib
     return _lib
 
@@ -176,6 +191,31 @@ def gemm_bf16_clock_samples(reset: bool = False) -> dict:
             "clock_ghz": shader / wall * hz / 1e9 if wall > 0 else None}
 
 
+def gemm_fp8_bt(M, N, K, A, lda, SA, ldsa, B, ldb, SB, ldsb, b_block_rows, C, ldc, c_type, stream) -> int:
+    return library().gemm_fp8_bt(M, N, K, A, lda, SA, ldsa, B, ldb, SB, ldsb, b_block_rows, C, ldc, c_type, stream)
+
+
+def gemm_quantize_fp8(M, K, X, ldx, Q, ldq, scale, lds, block_rows, transposed, stream) -> int:
+    return library().gemm_quantize_fp8(M, K, X, ldx, Q, ldq, scale, lds, block_rows, transposed, stream)
+
+
+def gemm_rms_norm(M, D, X, ldx, residual, ldr, weight, eps, H, ldh, Y, ldy, y_type, scale, lds, rstd, stream) -> int:
+    return library().gemm_rms_norm(M, D, X, ldx, residual, ldr, weight, eps, H, ldh, Y, ldy, y_type, scale, lds,
+                                   rstd, stream)
+
+
+def gemm_rms_norm_bwd(M, D, dY, lddy, H, ldh, weight, rstd, dres, lddr, dX, lddx, dweight, stream) -> int:
+    return library().gemm_rms_norm_bwd(M, D, dY, lddy, H, ldh, weight, rstd, dres, lddr, dX, lddx, dweight, stream)
+
+
+def gemm_swiglu(M, F, GU, ldgu, Y, ldy, y_type, scale, lds, stream) -> int:
+    return library().gemm_swiglu(M, F, GU, ldgu, Y, ldy, y_type, scale, lds, stream)
+
+
+def gemm_swiglu_bwd(M, F, dY, lddy, GU, ldgu, dGU, lddgu, stream) -> int:
+    return library().gemm_swiglu_bwd(M, F, dY, lddy, GU, ldgu, dGU, lddgu, stream)
+
+
 strerror = gemm_bf16_strerror
 
 
@@ -221,3 +261,209 @@ def gemm(A, B, *, b_transposed: bool = False, stages: int = 0, sync="barrier", o
     if rc != GEMM_OK:
         raise GemmError(rc, fn.__name__)
     return out
+
+
+# -- 8-bit operands and the operators around the product --------------------------
+# 8-bit tensors are torch.float8_e4m3fn.  Scales are float32 with the k block
+# first: shape (ceil(K / 128), rows) for row scales, (ceil(K / 128),
+# ceil(rows / 128)) for blocks.  Every function runs on the current stream
+# unless a torch stream is given; with one, results are allocated for that
+# stream and the arguments are marked as used on it.
+class RmsNorm(NamedTuple):
+    """What ``rms_norm`` returns; what was not asked for is None."""
+    y: object               # bfloat16, or float8_e4m3fn with ``scale``
+    scale: object = None    # float32 (ceil(D / 128), M)
+    h: object = None        # bfloat16, x + residual
+    rstd: object = None     # float32 (M,)
+
+
+def _matrix(name, x, dtype, shape=None):
+    """Checks a 2-D CUDA operand with unit inner stride; returns its leading dimension."""
+    if x.dtype != dtype or x.dim() != 2 or not x.is_cuda:
+        raise TypeError("%s must be a 2-D %s CUDA tensor" % (name, str(dtype).replace("torch.", "")))
+    if shape is not None and x.shape != shape:
+        raise ValueError("%s must have shape %s, not %s" % (name, tuple(shape), tuple(x.shape)))
+    rows, ld = x.shape[0], x.stride(0)
+    if x.shape[1] > 1 and x.stride(1) != 1 and rows > 0:
+        raise ValueError("%s needs unit stride along its second dimension" % name)
+    return max(ld, x.shape[1]) if rows <= 1 else ld
+
+
+def _vector(name, x, dtype, n):
+    if x.dtype != dtype or x.dim() != 1 or not x.is_cuda:
+        raise TypeError("%s must be a 1-D %s CUDA tensor" % (name, str(dtype).replace("torch.", "")))
+    if x.shape[0] != n or (n > 1 and x.stride(0) != 1):
+        raise ValueError("%s must hold %d contiguous values" % (name, n))
+
+
+class _On:
+    """The stream a call runs on: the current one, or the given one, for which
+    ``empty`` then allocates and on which ``uses`` marks the arguments."""
+
+    def __init__(self, stream, *tensors):
+        import torch
+
+        device = tensors[0].device
+        for x in tensors:
+            if x is not None and x.device != device:
+                raise ValueError("tensors on different devices: %s and %s" % (device, x.device))
+        if device.index != torch.cuda.current_device():
+            raise ValueError("tensors on %s, but the current device is cuda:%d" % (device, torch.cuda.current_device()))
+        self.torch, self.device, self.stream = torch, device, stream
+        if stream is None:
+            self.handle = torch.cuda.current_stream(device).cuda_stream
+        else:
+            self.handle = stream.cuda_stream
+            for x in tensors:
+                if x is not None:
+                    x.record_stream(stream)
+
+    def empty(self, shape, dtype):
+        if self.stream is None:
+            return self.torch.empty(shape, dtype=dtype, device=self.device)
+        with self.torch.cuda.stream(self.stream):
+            return self.torch.empty(shape, dtype=dtype, device=self.device)
+
+
+def _done(rc, name):
+    if rc != GEMM_OK:
+        raise GemmError(rc, name)
+
+
+def _blocks(n):
+    return (n + BLOCK - 1) // BLOCK
+
+
+def gemm_fp8(A, scale_a, B, scale_b, *, out_dtype=None, out=None, stream=None):
+    """C = (A * scale_a) @ (B * scale_b).T for 8-bit A (M, K) and B (N, K).
+
+    ``scale_a`` is (ceil(K / 128), M); ``scale_b`` is (ceil(K / 128), N) for a
+    B quantised row by row or (ceil(K / 128), ceil(N / 128)) for one quantised
+    in blocks.  Returns ``out`` (allocated if None) in ``out_dtype``, bfloat16
+    (the default) or float32."""
+    import torch
+
+    lda, ldb = _matrix("A", A, torch.float8_e4m3fn), _matrix("B", B, torch.float8_e4m3fn)
+    (M, K), N = A.shape, B.shape[0]
+    if B.shape[1] != K:
+        raise ValueError("inner dimensions differ: %d vs %d" % (K, B.shape[1]))
+    kb, rows = _blocks(K), 1
+    ldsa = _matrix("scale_a", scale_a, torch.float32, (kb, M))
+    if scale_b.dim() == 2 and scale_b.shape[1] != N:
+        rows = BLOCK
+    ldsb = _matrix("scale_b", scale_b, torch.float32, (kb, N if rows == 1 else _blocks(N)))
+    if out_dtype is None:
+        out_dtype = torch.bfloat16 if out is None else out.dtype
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("out_dtype must be bfloat16 or float32")
+    on = _On(stream, A, B, scale_a, scale_b, out)
+    if out is None:
+        out = on.empty((M, N), out_dtype)
+    ldc = _matrix("out", out, out_dtype, (M, N))
+    _done(library().gemm_fp8_bt(M, N, K, A.data_ptr(), lda, scale_a.data_ptr(), ldsa, B.data_ptr(), ldb,
+                                scale_b.data_ptr(), ldsb, rows, out.data_ptr(), ldc,
+                                TYPE_BF16 if out_dtype == torch.bfloat16 else TYPE_FP32, on.handle), "gemm_fp8_bt")
+    return out
+
+
+def quantize_fp8(x, *, block_rows=1, transposed=False, stream=None):
+    """(q, scale) of a bfloat16 matrix: e4m3 values with a scale for each row
+    and block of 128 columns (``block_rows`` 1) or each 128 x 128 block (128),
+    of x or, with ``transposed``, of its transpose."""
+    import torch
+
+    ldx = _matrix("x", x, torch.bfloat16)
+    M, K = x.shape
+    if block_rows not in (1, BLOCK):
+        raise ValueError("block_rows must be 1 or %d" % BLOCK)
+    R, L = (K, M) if transposed else (M, K)
+    on = _On(stream, x)
+    cols = R if block_rows == 1 else _blocks(R)
+    q, scale = on.empty((R, L), torch.float8_e4m3fn), on.empty((_blocks(L), cols), torch.float32)
+    _done(library().gemm_quantize_fp8(M, K, x.data_ptr(), ldx, q.data_ptr(), L, scale.data_ptr(), cols, block_rows,
+                                      int(bool(transposed)), on.handle), "gemm_quantize_fp8")
+    return q, scale
+
+
+def rms_norm(x, weight, *, residual=None, eps=1e-6, quantize=False, return_rstd=False, stream=None):
+    """Root-mean-square norm of h = x + residual (h = x without one) times
+    ``weight``, as an ``RmsNorm``: y in bfloat16 or, with ``quantize``, 8 bits
+    and its row scales; h where there is a residual; 1 / rms of each row with
+    ``return_rstd`` (the backward pass needs it)."""
+    import torch
+
+    bf16 = torch.bfloat16
+    ldx = _matrix("x", x, bf16)
+    M, D = x.shape
+    _vector("weight", weight, bf16, D)
+    ldr = _matrix("residual", residual, bf16, x.shape) if residual is not None else 0
+    on = _On(stream, x, weight, residual)
+    h = on.empty((M, D), bf16) if residual is not None else None
+    rstd = on.empty((M,), torch.float32) if return_rstd else None
+    if quantize:
+        y, scale = on.empty((M, D), torch.float8_e4m3fn), on.empty((_blocks(D), M), torch.float32)
+    else:
+        y, scale = on.empty((M, D), bf16), None
+    _done(library().gemm_rms_norm(M, D, x.data_ptr(), ldx, residual.data_ptr() if residual is not None else None, ldr,
+                                  weight.data_ptr(), float(eps), h.data_ptr() if h is not None else None, D,
+                                  y.data_ptr(), D, TYPE_FP8 if quantize else TYPE_BF16,
+                                  scale.data_ptr() if quantize else None, M,
+                                  rstd.data_ptr() if return_rstd else None, on.handle), "gemm_rms_norm")
+    return RmsNorm(y, scale, h, rstd)
+
+
+def rms_norm_backward(dy, h, weight, rstd, *, dresidual=None, stream=None):
+    """(dx, dweight) of ``rms_norm`` for the gradient ``dy`` of y and, where h
+    is used further on, the gradient ``dresidual`` that reaches it there.  h is
+    the forward pass's h (its x without a residual) and rstd its result; dx
+    (bfloat16) is the gradient of x and residual alike, dweight is float32."""
+    import torch
+
+    bf16 = torch.bfloat16
+    lddy = _matrix("dy", dy, bf16)
+    M, D = dy.shape
+    ldh = _matrix("h", h, bf16, dy.shape)
+    _vector("weight", weight, bf16, D)
+    _vector("rstd", rstd, torch.float32, M)
+    lddr = _matrix("dresidual", dresidual, bf16, dy.shape) if dresidual is not None else 0
+    on = _On(stream, dy, h, weight, rstd, dresidual)
+    dx, dweight = on.empty((M, D), bf16), on.empty((D,), torch.float32)
+    _done(library().gemm_rms_norm_bwd(M, D, dy.data_ptr(), lddy, h.data_ptr(), ldh, weight.data_ptr(), rstd.data_ptr(),
+                                      dresidual.data_ptr() if dresidual is not None else None, lddr, dx.data_ptr(), D,
+                                      dweight.data_ptr(), on.handle), "gemm_rms_norm_bwd")
+    return dx, dweight
+
+
+def swiglu(gu, *, quantize=False, stream=None):
+    """silu(g) * u for gu = [g, u] side by side (M, 2F): y (M, F) in bfloat16
+    or, with ``quantize``, the pair of 8-bit y and its row scales."""
+    import torch
+
+    ldgu = _matrix("gu", gu, torch.bfloat16)
+    M, F = gu.shape[0], gu.shape[1] // 2
+    if gu.shape[1] != 2 * F:
+        raise ValueError("gu must have an even number of columns")
+    on = _On(stream, gu)
+    if quantize:
+        y, scale = on.empty((M, F), torch.float8_e4m3fn), on.empty((_blocks(F), M), torch.float32)
+    else:
+        y, scale = on.empty((M, F), torch.bfloat16), None
+    _done(library().gemm_swiglu(M, F, gu.data_ptr(), ldgu, y.data_ptr(), F, TYPE_FP8 if quantize else TYPE_BF16,
+                                scale.data_ptr() if quantize else None, M, on.handle), "gemm_swiglu")
+    return (y, scale) if quantize else y
+
+
+def swiglu_backward(dy, gu, *, stream=None):
+    """The gradient of gu = [g, u] (bfloat16, (M, 2F)) for the gradient dy (M, F) of ``swiglu``."""
+    import torch
+
+    ldgu = _matrix("gu", gu, torch.bfloat16)
+    M, F = gu.shape[0], gu.shape[1] // 2
+    if gu.shape[1] != 2 * F:
+        raise ValueError("gu must have an even number of columns")
+    lddy = _matrix("dy", dy, torch.bfloat16, (M, F))
+    on = _On(stream, dy, gu)
+    dgu = on.empty((M, 2 * F), torch.bfloat16)
+    _done(library().gemm_swiglu_bwd(M, F, dy.data_ptr(), lddy, gu.data_ptr(), ldgu, dgu.data_ptr(), 2 * F, on.handle),
+          "gemm_swiglu_bwd")
+    return dgu

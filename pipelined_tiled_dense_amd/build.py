@@ -20,7 +20,7 @@ HIP_FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++20", "-shared", "-fPIC",
              "-I", INCLUDE]
 
 LIBRARIES = {
-    "libgemm_bf16.so": "csrc/gemm_bf16.hip",
+    "libgemm_bf16.so": "csrc/library.hip",
     "libgemm_probes.so": "csrc/probes.hip",
 }
 

@@ -1,0 +1,639 @@
+// The product of 8-bit operands with a scale for each block of 128 along k (part
+// of library.hip).
+//
+//   C[i][j] = sum_kb sa[kb][i] * sb[kb][j or j / 128] * sum_{k in kb} A[i][k] * B[j][k]
+//
+// A block's partial sums start from zero and enter the running sums by one fused
+// multiply-add each, times the product of the two scales.  The MFMA's rows are
+// B's (n) and its columns A's (m): a lane then holds 4 consecutive columns of one
+// row of C, so a block's scale product is one value per lane and fragment,
+// shared by every fragment of that row against the same 128 columns.
+//
+// Two ways to contract a block of 128:
+//   fast    one v_mfma_f32_16x16x128_f8f6f4, twice the rate of bf16.  It adds
+//           each run of 8 products on a grid set by the largest of them: a share
+//           of about 2^-13 is lost (measured: 65536 + 1 = 65536 within a run,
+//           and an error of 1.5e-5 of the result's norm on random operands).
+//           That is a hundredth of bf16's rounding.
+//   exact   the bytes converted to bf16, which holds every e4m3 value, and four
+//           v_mfma_f32_16x16x32_bf16, whose sums are fp32's (1e-8 on the same
+//           operands).  Half the matrix rate, and 16 conversions a fragment.
+// An fp32 C is computed exactly.  So is whatever does not wait for the matrix
+// cores: few rows (bound by B's bytes) and short sums (bound by C's).
+//
+// A tile row of 128 bytes is what the bf16 product calls a row of 64 elements,
+// so the ring, its swizzle and its loader are those of the bf16 product with
+// sizes and leading dimensions counted in 2-byte units.
+#pragma once
+
+namespace {
+
+typedef __attribute__((ext_vector_type(8))) int i32x8_t;
+typedef LDS_AS float lds_f32;
+
+// What the product needs beside the loader's Params (sizes there in 2-byte
+// units along k).
+struct Fp8Params {
+    const float* sa;
+    const float* sb;
+    char* c;
+    int64_t ldsa, ldsb, ldc;
+    int64_t K;               // bytes
+    int64_t sb_cols;         // scales per k block of B
+    int32_t kblocks;         // ceil(K / 128)
+    int32_t sb_shift;        // log2 of B's rows per scale: 7 or 0
+    int32_t c_fp32;
+};
+
+// One block of 128 of 16 rows of an operand: lane (r16, g) holds 32 bytes of row
+// r16, in an order along k that is the same for both operands.
+template <bool EXACT>
+struct Fp8Frag {
+    i32x8_t v;
+    __device__ __forceinline__ Fp8Frag() {}
+    __device__ __forceinline__ Fp8Frag(u32x4_t lo, u32x4_t hi)
+        : v(__builtin_bit_cast(i32x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7)))
+    {
+    }
+};
+
+template <>
+struct Fp8Frag<true> {
+    bf16x8_t v[4];
+    __device__ __forceinline__ Fp8Frag() {}
+    __device__ __forceinline__ Fp8Frag(u32x4_t lo, u32x4_t hi)
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t w0 = i < 2 ? lo[2 * i] : hi[2 * i - 4], w1 = i < 2 ? lo[2 * i + 1] : hi[2 * i - 3];
+            const bf16x2_t a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, 1.0f, false);
+            const bf16x2_t b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, 1.0f, true);
+            const bf16x2_t c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, 1.0f, false);
+            const bf16x2_t d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, 1.0f, true);
+            v[i] = bf16x8_t{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+        }
+    }
+};
+
+__device__ __forceinline__ f32x4_t block_sums(const Fp8Frag<false>& b, const Fp8Frag<false>& a)
+{
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b.v, a.v, f32x4_t{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0, 0, 0, 0);
+}
+
+__device__ __forceinline__ f32x4_t block_sums(const Fp8Frag<true>& b, const Fp8Frag<true>& a)
+{
+    f32x4_t d = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b.v[i], a.v[i], d, 0, 0, 0);
+    return d;
+}
+
+// 4 consecutive values of a row of C at column n (any alignment).
+__device__ __forceinline__ void store_c4(const Fp8Params& q, int64_t m, int64_t n, int64_t N, f32x4_t v)
+{
+    const int64_t at = m * q.ldc + n;
+    if (q.c_fp32) {
+        float* c = (float*)q.c + at;
+        if (n + 4 <= N) {
+            __builtin_memcpy(c, &v, 16);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 3; ++e)
+                if (n + e < N)
+                    c[e] = v[e];
+        }
+    } else {
+        uint16_t* c = (uint16_t*)q.c + at;
+        const u32x2_t w = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+        if (n + 4 <= N) {
+            __builtin_memcpy(c, &w, 8);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 3; ++e)
+                if (n + e < N)
+                    c[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Large products: 128-byte k-steps through the two-stage LDS ring.
+// ---------------------------------------------------------------------------
+template <int BM, int BN, int WM, int WN>
+using Fp8Cfg = Cfg<BM, BN, 64, 2, WM, WN, SYNC_BARRIER, true, 0, false, 16>;
+
+// The column of the wave's tile that MFMA row i of fragment j holds: a lane's 4
+// rows of each fragment follow one another, so that the lane ends up with 4 * FN
+// consecutive columns of C.
+template <class C>
+__device__ __forceinline__ int fp8_col(int j, int i)
+{
+    return (i >> 2) * (4 * C::FN) + j * 4 + (i & 3);
+}
+
+// The scales of one k-step: BM of A's rows, then BN of B's columns, fetched into
+// LDS by one 4-byte-per-lane load of each wave.  Rows and columns past the
+// matrix, and k blocks past K, read as zeros.
+template <class C>
+struct ScaleLoader {
+    static constexpr int BYTES = (C::BM + C::BN) * 4;
+    static constexpr int AW = C::BM / 64;   // waves that fetch A's scales
+    static_assert((C::BM + C::BN) / 64 == C::NCW, "one load per wave");
+
+    const float* base;   // at the position's k block
+    int64_t step;
+    uint32_t nrec, voff;
+    int32_t kb, kt, ti;
+
+    __device__ __forceinline__ void enter(const Params& p, const Fp8Params& q, int32_t n_tiles, int w, int lane)
+    {
+        int32_t tm, tn, sp, u;
+        tile_coords(p, (int32_t)blockIdx.x + min(ti, n_tiles - 1) * (int32_t)gridDim.x, (int32_t)gridDim.x, tm, tn, sp,
+                    u);
+        kb = sp * p.k_steps;
+        kt = 0;
+        const int64_t m0 = (int64_t)tm * C::BM, n0 = (int64_t)tn * C::BN;
+        const bool a = w < AW;
+        step = a ? q.ldsa : q.ldsb;
+        base = (a ? q.sa + m0 : q.sb + (n0 >> q.sb_shift)) + kb * step;
+        const int64_t rem = a ? p.M - m0 : q.sb_cols - (n0 >> q.sb_shift);
+        nrec = ti < n_tiles ? (uint32_t)min(rem, (int64_t)1024) * 4u : 0u;
+        const int at = (a ? w : w - AW) * 64 + lane;
+        voff = (uint32_t)(a ? at : at >> q.sb_shift) * 4u;
+    }
+
+    __device__ __forceinline__ void issue_next(const Params& p, const Fp8Params& q, int32_t n_tiles, lds_char* dst,
+                                               int w, int lane)
+    {
+        const __amdgpu_buffer_rsrc_t r = rsrc_n(base, kb < q.kblocks ? nrec : 0u);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (LDS_AS void*)(dst + w * 256), 4, voff, 0, 0, 0);
+        if (++kt == p.k_steps) {
+            ++ti;
+            enter(p, q, n_tiles, w, lane);
+        } else {
+            ++kb;
+            base += step;
+        }
+    }
+};
+
+template <class C, bool ROWB, bool EXACT>
+__global__ void __launch_bounds__(C::THREADS) k_gemm_fp8(Params p, Fp8Params q)
+{
+    using SL = ScaleLoader<C>;
+    __shared__ __attribute__((aligned(1024))) char smem_raw[C::RING_BYTES + 2 * SL::BYTES];
+    lds_char* smem = (lds_char*)smem_raw;
+    const int lane = threadIdx.x & 63, r16 = lane & 15, g = lane >> 4;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = w / C::WN, wn = w % C::WN;
+
+    const int32_t G = gridDim.x, b = blockIdx.x;
+    const int32_t n_tiles = (b < p.tiles) ? (p.tiles - 1 - b) / G + 1 : 0;
+    if (n_tiles == 0)
+        return;
+    Loader<C, false, true> ld;
+    ld.init(p, n_tiles, w, lane);
+    // LDS row L of B's tile holds the column fp8_col gives (the loader's rows
+    // are in order).
+#pragma unroll
+    for (int t = 0; t < C::B_LOADS; ++t) {
+        const int row = ld.krow(ld.slot(t, w, lane));
+        const int col = row / C::TN * C::TN + fp8_col<C>(row % C::TN / 16, row & 15);
+        ld.voffB[t] += (uint32_t)(col - row) * ((uint32_t)p.ldb * 2u);
+    }
+    SL sl;
+    sl.ti = 0;
+    sl.enter(p, q, n_tiles, w, lane);
+    auto issue = [&](int s) {
+        sl.issue_next(p, q, n_tiles, smem + C::RING_BYTES + s * SL::BYTES, w, lane);
+        ld.issue_next(p, smem + s * C::STAGE_BYTES, w, lane);
+    };
+    issue(0);
+
+    // Lane (r16, g) reads chunks g and g + 4 of row r16 of each fragment (both
+    // operands in the same order, so the order along k does not matter).
+    const int swz = swz_k<64>(r16);
+    const uint32_t lo = (uint32_t)r16 * 128u + (uint32_t)((g ^ swz) * 16), hi = lo ^ 64u;
+
+    int s = 0;
+    for (int32_t it = 0; it < n_tiles; ++it) {
+        int32_t tm, tn, sp, u;
+        tile_coords(p, b + it * G, G, tm, tn, sp, u);
+        f32x4_t acc[C::FM][C::FN];
+#pragma unroll
+        for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+            for (int j = 0; j < C::FN; ++j)
+                acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int32_t kt = 0; kt < p.k_steps; ++kt) {
+            // This wave's loads of the step have landed and its fragment reads of
+            // the previous step have completed; the barrier makes both so for
+            // every wave, and the other stage takes the next step.
+            wait_vmcnt<0>();
+            wait_lgkm0();
+            block_barrier();
+            issue(s ^ 1);
+            const lds_char* at = smem + s * C::STAGE_BYTES + wm * C::TM * 128;
+            const lds_char* bt = smem + s * C::STAGE_BYTES + C::A_BYTES + wn * C::TN * 128;
+            const lds_f32* sa = (const lds_f32*)(smem + C::RING_BYTES + s * SL::BYTES) + wm * C::TM + r16;
+            const lds_f32* sb = (const lds_f32*)(smem + C::RING_BYTES + s * SL::BYTES) + C::BM + wn * C::TN;
+            Fp8Frag<EXACT> bf[C::FN];
+            f32x4_t sbv[C::FN];
+#pragma unroll
+            for (int j = 0; j < C::FN; ++j) {
+                bf[j] = Fp8Frag<EXACT>(*(const LDS_AS u32x4_t*)(bt + j * 2048 + lo),
+                                       *(const LDS_AS u32x4_t*)(bt + j * 2048 + hi));
+                if constexpr (ROWB)
+                    sbv[j] = *(const LDS_AS f32x4_t*)(sb + g * (4 * C::FN) + j * 4);
+            }
+            const float sb1 = ROWB ? 1.0f : sb[0];
+#pragma unroll
+            for (int i = 0; i < C::FM; ++i) {
+                const Fp8Frag<EXACT> af(*(const LDS_AS u32x4_t*)(at + i * 2048 + lo),
+                                        *(const LDS_AS u32x4_t*)(at + i * 2048 + hi));
+                const float sc = sa[i * 16] * sb1;
+#pragma unroll
+                for (int j = 0; j < C::FN; ++j) {
+                    const f32x4_t d = block_sums(bf[j], af);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        acc[i][j][e] = __builtin_fmaf(d[e], ROWB ? sc * sbv[j][e] : sc, acc[i][j][e]);
+                }
+            }
+            s ^= 1;
+        }
+        if (p.splits > 1) {
+            float* part = p.partial + (int64_t)(sp * p.span + u) * (C::BM * C::BN);
+#pragma unroll
+            for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+                for (int j = 0; j < C::FN; ++j)
+                    *(f32x4_t*)(part + (((w * C::FM + i) * C::FN + j) * 64 + lane) * 4) = acc[i][j];
+        } else {
+#pragma unroll
+            for (int i = 0; i < C::FM; ++i) {
+                const int64_t m = (int64_t)tm * C::BM + wm * C::TM + i * 16 + r16;
+                if (m < p.M) {
+#pragma unroll
+                    for (int j = 0; j < C::FN; ++j)
+                        store_c4(q, m, (int64_t)tn * C::BN + wn * C::TN + g * (4 * C::FN) + j * 4, p.N, acc[i][j]);
+                }
+            }
+        }
+    }
+    wait_vmcnt<0>();   // the last, empty position's loads still write LDS
+}
+
+// Sums the k chunks' partial tiles in chunk order and stores C.  A thread takes
+// 4 consecutive columns, in the order the partial tiles are stored in.
+template <class C>
+__global__ void __launch_bounds__(256) k_reduce_fp8(Params p, Fp8Params q)
+{
+    constexpr int QUADS = C::BM * C::BN / 4;
+    const int64_t total = (int64_t)p.span * QUADS;
+    for (int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x; id < total; id += (int64_t)gridDim.x * 256) {
+        const int32_t u = (int32_t)(id / QUADS);
+        const int at = (int)(id % QUADS);
+        f32x4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int32_t sp = 0; sp < p.splits; ++sp)
+            v += *(const f32x4_t*)(p.partial + (int64_t)(sp * p.span + u) * (C::BM * C::BN) + at * 4);
+        const int lane = at & 63, j = at / 64 % C::FN, i = at / (64 * C::FN) % C::FM, w = at / (64 * C::FN * C::FM);
+        int32_t tm, tn;
+        raster_tile(p, u, tm, tn);
+        const int64_t m = (int64_t)tm * C::BM + w / C::WN * C::TM + i * 16 + (lane & 15);
+        const int64_t n = (int64_t)tn * C::BN + w % C::WN * C::TN + (lane >> 4) * (4 * C::FN) + j * 4;
+        if (m < p.M)
+            store_c4(q, m, n, p.N, v);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Few rows: the product is bound by B's bytes.  A workgroup of 8 waves takes MF
+// x NF fragments of C; its waves share out the k blocks (wave w takes blocks w,
+// w + 8, ...), stream their fragments from global memory straight into
+// registers, DEPTH blocks in flight at a time, and add their sums through LDS in
+// wave order.  So every compute unit has loads in flight over the whole of k
+// even where N gives few workgroups, with no second launch.
+// ---------------------------------------------------------------------------
+struct SkinnyParams {
+    const char* a;
+    const char* b;
+    int64_t M, N, lda, ldb;
+};
+
+constexpr int kSkinnyWaves = 8;
+
+template <int MF, int NF, int DEPTH, bool ROWB>
+__global__ void __launch_bounds__(kSkinnyWaves * 64) k_gemm_fp8_skinny(SkinnyParams p, Fp8Params q)
+{
+    __shared__ __attribute__((aligned(16))) f32x4_t sums[kSkinnyWaves][MF * NF][64];
+    const int lane = threadIdx.x & 63, r16 = lane & 15, g = lane >> 4;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t tiles_m = (p.M + MF * 16 - 1) / (MF * 16);
+    const int64_t m0 = (int64_t)blockIdx.x % tiles_m * (MF * 16), n0 = (int64_t)blockIdx.x / tiles_m * (NF * 16);
+
+    // Rows past the end read as zeros: their offset is past the resource.
+    const int64_t a_rows = min(p.M - m0, (int64_t)MF * 16), b_rows = min(p.N - n0, (int64_t)NF * 16);
+    const __amdgpu_buffer_rsrc_t ra = make_rsrc(p.a + m0 * p.lda, (a_rows - 1) * p.lda + q.K);
+    const __amdgpu_buffer_rsrc_t rb = make_rsrc(p.b + n0 * p.ldb, (b_rows - 1) * p.ldb + q.K);
+    uint32_t va[MF], vb[NF];
+    int64_t ia[MF];
+#pragma unroll
+    for (int i = 0; i < MF; ++i) {
+        va[i] = i * 16 + r16 < a_rows ? (uint32_t)(i * 16 + r16) * (uint32_t)p.lda : kOOB;
+        ia[i] = m0 + min((int64_t)i * 16 + r16, a_rows - 1);
+    }
+#pragma unroll
+    for (int j = 0; j < NF; ++j)
+        vb[j] = j * 16 + r16 < b_rows ? (uint32_t)(j * 16 + r16) * (uint32_t)p.ldb : kOOB;
+
+    f32x4_t acc[MF][NF];
+#pragma unroll
+    for (int i = 0; i < MF; ++i)
+#pragma unroll
+        for (int j = 0; j < NF; ++j)
+            acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+
+    for (int32_t kb0 = w; kb0 < q.kblocks; kb0 += kSkinnyWaves * DEPTH) {
+        u32x4_t av[DEPTH][MF][2], bv[DEPTH][NF][2];
+        float sa[DEPTH][MF], sb[DEPTH][ROWB ? NF * 4 : 1];
+#pragma unroll
+        for (int d = 0; d < DEPTH; ++d) {
+            const int32_t kb = kb0 + d * kSkinnyWaves;
+            const int32_t kc = min(kb, q.kblocks - 1);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int64_t k = (int64_t)kb * kBlock + (h * 4 + g) * 16;
+                const bool ok = k < q.K;
+#pragma unroll
+                for (int j = 0; j < NF; ++j)
+                    bv[d][j][h] = __builtin_bit_cast(
+                        u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rb, ok ? vb[j] + (uint32_t)k : kOOB, 0, 0));
+#pragma unroll
+                for (int i = 0; i < MF; ++i)
+                    av[d][i][h] = __builtin_bit_cast(
+                        u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(ra, ok ? va[i] + (uint32_t)k : kOOB, 0, 0));
+            }
+#pragma unroll
+            for (int i = 0; i < MF; ++i)
+                sa[d][i] = kb < q.kblocks ? q.sa[kc * q.ldsa + ia[i]] : 0.0f;
+            if constexpr (ROWB) {
+#pragma unroll
+                for (int j = 0; j < NF; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        sb[d][j * 4 + e] = q.sb[kc * q.ldsb + min(n0 + j * 16 + g * 4 + e, p.N - 1)];
+            } else {
+                sb[d][0] = q.sb[kc * q.ldsb + (n0 >> 7)];
+            }
+        }
+#pragma unroll
+        for (int d = 0; d < DEPTH; ++d) {
+            Fp8Frag<true> bf[NF];
+#pragma unroll
+            for (int j = 0; j < NF; ++j)
+                bf[j] = Fp8Frag<true>(bv[d][j][0], bv[d][j][1]);
+#pragma unroll
+            for (int i = 0; i < MF; ++i) {
+                const Fp8Frag<true> af(av[d][i][0], av[d][i][1]);
+#pragma unroll
+                for (int j = 0; j < NF; ++j) {
+                    const f32x4_t v = block_sums(bf[j], af);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        acc[i][j][e] =
+                            __builtin_fmaf(v[e], sa[d][i] * sb[d][ROWB ? j * 4 + e : 0], acc[i][j][e]);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < MF; ++i)
+#pragma unroll
+        for (int j = 0; j < NF; ++j)
+            sums[w][i * NF + j][lane] = acc[i][j];
+    __syncthreads();
+    for (int f = w; f < MF * NF; f += kSkinnyWaves) {
+        f32x4_t v = sums[0][f][lane];
+#pragma unroll
+        for (int x = 1; x < kSkinnyWaves; ++x)
+            v += sums[x][f][lane];
+        const int64_t m = m0 + f / NF * 16 + r16;
+        if (m < p.M)
+            store_c4(q, m, n0 + f % NF * 16 + g * 4, p.N, v);
+    }
+}
+
+// A byte matrix copied to rows of `dst_cols` bytes (a multiple of 16), zeros
+// past src_cols; any source stride and alignment.
+__global__ void __launch_bounds__(256) k_pad_copy8(const uint8_t* src, int64_t rows, int64_t src_cols, int64_t ld_src,
+                                                   uint8_t* dst, int64_t dst_cols)
+{
+    const int64_t per_row = dst_cols / 16, total = rows * per_row;
+    for (int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x; id < total; id += (int64_t)gridDim.x * 256) {
+        const int64_t r = id / per_row, c = (id - r * per_row) * 16;
+        const uint8_t* s = src + r * ld_src + c;
+        u32x4_t v = {0u, 0u, 0u, 0u};
+        if (c + 16 <= src_cols) {
+            __builtin_memcpy(&v, s, 16);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 15; ++e)
+                if (c + e < src_cols)
+                    v[e >> 2] |= (uint32_t)s[e] << (8 * (e & 3));
+        }
+        *(u32x4_t*)(dst + r * dst_cols + c) = v;
+    }
+}
+
+__global__ void __launch_bounds__(256) k_zero_c(Fp8Params q, int64_t M, int64_t N)
+{
+    const int64_t quads = (N + 3) / 4, total = M * quads;
+    for (int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x; id < total; id += (int64_t)gridDim.x * 256)
+        store_c4(q, id / quads, id % quads * 4, N, f32x4_t{0.0f, 0.0f, 0.0f, 0.0f});
+}
+
+// ---------------------------------------------------------------------------
+// Host side.
+// ---------------------------------------------------------------------------
+unsigned flat_grid(int64_t threads)
+{
+    const int64_t n = (threads + 255) / 256;
+    return (unsigned)(n < 65536 ? n : 65536);
+}
+
+template <int MF, int NF, int DEPTH>
+int launch_skinny(const SkinnyParams& p, const Fp8Params& q, hipStream_t s)
+{
+    const int64_t n = (p.M + MF * 16 - 1) / (MF * 16) * ((p.N + NF * 16 - 1) / (NF * 16));
+    const dim3 g((unsigned)n), b(kSkinnyWaves * 64);
+    if (q.sb_shift == 0)
+        hipLaunchKernelGGL(HIP_KERNEL_NAME(k_gemm_fp8_skinny<MF, NF, DEPTH, true>), g, b, 0, s, p, q);
+    else
+        hipLaunchKernelGGL(HIP_KERNEL_NAME(k_gemm_fp8_skinny<MF, NF, DEPTH, false>), g, b, 0, s, p, q);
+    return launched();
+}
+
+// Sums of up to this many blocks are computed exactly (see the top).
+constexpr int kShortBlocks = 2;
+
+template <class C>
+int launch_tiles(Params p, const Fp8Params& q, int cus, int per_cu, TempMem& tm, hipStream_t s)
+{
+    p.tiles_m = (int32_t)((p.M + C::BM - 1) / C::BM);
+    p.tiles_n = (int32_t)((p.N + C::BN - 1) / C::BN);
+    const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n, slots = (int64_t)cus * per_cu;
+    if (tiles * kMaxSplits > INT32_MAX)
+        return GEMM_ERR_UNSUPPORTED_SHAPE;
+    // Few tiles: split k until the card is full, as long as a chunk keeps 4
+    // k-steps.
+    int64_t splits = 1;
+    if (tiles * 2 <= slots) {
+        splits = slots / tiles;
+        if (splits > kMaxSplits)
+            splits = kMaxSplits;
+        if (splits > q.kblocks / 4)
+            splits = q.kblocks / 4 < 1 ? 1 : q.kblocks / 4;
+    }
+    p.k_steps = (int32_t)((q.kblocks + splits - 1) / splits);
+    p.splits = (int32_t)((q.kblocks + p.k_steps - 1) / p.k_steps);   // no empty chunk
+    p.ksplit = (int64_t)p.k_steps * (kBlock / 2);
+    p.tiles_mn = p.span = (int32_t)tiles;
+    p.tile_base = 0;
+    p.tiles = p.span * p.splits;
+    p.group_m = 4;
+    p.partial = nullptr;
+    void* ws = nullptr;
+    hipEvent_t done = nullptr;
+    if (p.splits > 1) {
+        const int rc = temp_take(tm, (int64_t)p.tiles * C::BM * C::BN * 4, s, &ws, &done);
+        if (rc != GEMM_OK)
+            return rc;
+        p.partial = (float*)ws;
+    }
+    const dim3 grid((unsigned)(p.tiles < slots ? p.tiles : slots)), block(C::THREADS);
+    const bool rowb = q.sb_shift == 0, exact = q.c_fp32 || q.kblocks <= kShortBlocks;
+    if (rowb && exact)
+        hipLaunchKernelGGL(HIP_KERNEL_NAME(k_gemm_fp8<C, true, true>), grid, block, 0, s, p, q);
+    else if (rowb)
+        hipLaunchKernelGGL(HIP_KERNEL_NAME(k_gemm_fp8<C, true, false>), grid, block, 0, s, p, q);
+    else if (exact)
+        hipLaunchKernelGGL(HIP_KERNEL_NAME(k_gemm_fp8<C, false, true>), grid, block, 0, s, p, q);
+    else
+        hipLaunchKernelGGL(HIP_KERNEL_NAME(k_gemm_fp8<C, false, false>), grid, block, 0, s, p, q);
+    int rc = launched();
+    if (p.splits > 1) {
+        if (rc == GEMM_OK) {
+            hipExtLaunchKernelGGL(k_reduce_fp8<C>, dim3(flat_grid(tiles * (C::BM * C::BN / 4))), dim3(256), 0, s,
+                                  nullptr, done, 0, p, q);
+            rc = launched();
+        }
+        const int frc = temp_give(tm, ws, s, rc == GEMM_OK && done != nullptr);
+        rc = rc != GEMM_OK ? rc : frc;
+    }
+    return rc;
+}
+
+// The product on operands whose rows start on 16-byte boundaries, K a multiple
+// of 16.
+int gemm_fp8_direct(int64_t M, int64_t N, const char* A, int64_t lda, const char* B, int64_t ldb, const Fp8Params& q,
+                    int cus, TempMem& tm, hipStream_t s)
+{
+    if (M <= 64) {
+        const SkinnyParams p{A, B, M, N, lda, ldb};
+        if (M <= 16)
+            return launch_skinny<1, 1, 8>(p, q, s);
+        if (M <= 32)
+            return launch_skinny<2, 2, 4>(p, q, s);
+        return launch_skinny<4, 2, 2>(p, q, s);
+    }
+    Params p;
+    memset(&p, 0, sizeof p);
+    p.A = A;
+    p.B = B;
+    p.M = M;
+    p.N = N;
+    p.K = q.K / 2;
+    p.lda = lda / 2;
+    p.ldb = ldb / 2;
+    if ((M + 255) / 256 * ((N + 255) / 256) >= cus)
+        return launch_tiles<Fp8Cfg<256, 256, 2, 4>>(p, q, cus, 1, tm, s);
+    return launch_tiles<Fp8Cfg<128, 128, 2, 2>>(p, q, cus, 2, tm, s);
+}
+
+}  // namespace
+
+extern "C" int gemm_fp8_bt(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const float* SA, int64_t ldsa,
+                           const void* B, int64_t ldb, const float* SB, int64_t ldsb, int b_block_rows, void* C,
+                           int64_t ldc, int c_type, void* stream)
+{
+    if (M < 0 || N < 0 || K < 0 || (b_block_rows != 1 && b_block_rows != kBlock) ||
+        (c_type != GEMM_TYPE_BF16 && c_type != GEMM_TYPE_FP32))
+        return GEMM_ERR_INVALID_VALUE;
+    if (M > kMaxRows || N > kMaxLd || K > kMaxLd)
+        return GEMM_ERR_UNSUPPORTED_SHAPE;
+    if (M == 0 || N == 0)
+        return GEMM_OK;
+    const int64_t kblocks = (K + kBlock - 1) / kBlock, sb_cols = b_block_rows == 1 ? N : (N + kBlock - 1) / kBlock;
+    const Operand c{C, M, N, ldc, c_type == GEMM_TYPE_FP32 ? 4 : 2};
+    const Operand in[] = {{A, M, K, lda, 1}, {B, N, K, ldb, 1}, {SA, kblocks, M, ldsa, 4}, {SB, kblocks, sb_cols, ldsb, 4}};
+    int rc = check_operand(c);
+    if (rc == GEMM_OK && K > 0)
+        rc = check_operands(in, 4);
+    if (rc != GEMM_OK)
+        return rc;
+    if (K > 0)
+        for (const Operand& o : in)
+            if (meet(c, o))
+                return GEMM_ERR_ALIAS;
+    int cus = 0;
+    TempMem tm;
+    rc = device_info(&cus, &tm.pool, nullptr, &tm.info);
+    if (rc != GEMM_OK)
+        return rc;
+    hipStream_t s = (hipStream_t)stream;
+    Fp8Params q{SA, SB, (char*)C, ldsa, ldsb, ldc, K, sb_cols, (int32_t)kblocks, b_block_rows == 1 ? 0 : 7,
+                c_type == GEMM_TYPE_FP32};
+    if (K == 0) {
+        hipLaunchKernelGGL(k_zero_c, dim3(flat_grid(M * ((N + 3) / 4))), dim3(256), 0, s, q, M, N);
+        return launched();
+    }
+    // A single row has no stride: give it one that suits.
+    const int64_t K16 = (K + 15) & ~(int64_t)15;
+    if (M == 1)
+        lda = K16;
+    if (N == 1)
+        ldb = K16;
+    auto fits = [&](const void* ptr, int64_t ld) {
+        return K % 16 == 0 && ld % 16 == 0 && ld <= 2 * kMaxLd && ((uintptr_t)ptr & 15) == 0;
+    };
+    const int64_t a_pad = fits(A, lda) ? 0 : align256(M * K16), b_pad = fits(B, ldb) ? 0 : align256(N * K16);
+    void* ws = nullptr;
+    if (a_pad + b_pad > 0) {
+        rc = temp_take(tm, a_pad + b_pad, s, &ws);
+        if (rc != GEMM_OK)
+            return rc;
+        auto copy = [&](const void* src, int64_t rows, int64_t ld, char* dst) {
+            hipLaunchKernelGGL(k_pad_copy8, dim3(flat_grid(rows * (K16 / 16))), dim3(256), 0, s, (const uint8_t*)src,
+                               rows, K, ld, (uint8_t*)dst, K16);
+            return launched();
+        };
+        if (a_pad) {
+            rc = copy(A, M, lda, (char*)ws);
+            A = ws;
+            lda = K16;
+        }
+        if (b_pad && rc == GEMM_OK) {
+            rc = copy(B, N, ldb, (char*)ws + a_pad);
+            B = (char*)ws + a_pad;
+            ldb = K16;
+        }
+        // The copies' zeros extend K to the 16-byte grid.
+        q.K = K16;
+    }
+    if (rc == GEMM_OK)
+        rc = gemm_fp8_direct(M, N, (const char*)A, lda, (const char*)B, ldb, q, cus, tm, s);
+    const int frc = temp_give(tm, ws, s);
+    return rc != GEMM_OK ? rc : frc;
+}

@@ -1,0 +1,173 @@
+// The gated unit y = silu(g) * u and its gradient (part of library.hip).
+//
+// Bound by memory: every value is read once and written once, 8 at a time.  A
+// unit of work is 128 columns of a row, 16 lanes of one chunk, so that an 8-bit
+// output's scale is a maximum over one DPP row.
+#pragma once
+
+namespace {
+
+// s = 1 / (1 + exp(-x)) and c = 1 - s, from t = exp(-|x|) <= 1:
+//
+//   s = (x < 0 ? t : 1) / (1 + t),   c = (x < 0 ? 1 : t) / (1 + t)
+//
+// so nothing overflows and neither of the two cancels.  t = 2^(-|x| log2 e): the
+// product with log2 e is split into its rounded value and the rest, which
+// enters to first order (a single rounded product would be off by |x| ulp).
+// v_exp_f32 returns zero where the result is subnormal, so it computes the
+// square root of t; the product of two roots keeps the subnormal values.  |x|
+// is bounded where t is zero anyway, which leaves no infinity minus infinity;
+// a NaN passes the comparison.
+struct Sigmoid {
+    float s, c;
+};
+
+__device__ __forceinline__ Sigmoid sigmoid(float x)
+{
+    constexpr float kLog2e = 0x1.715476p+0f;      // log2 e rounded to fp32
+    constexpr float kLog2eRest = 0x1.4ae0cp-26f;  // log2 e - kLog2e
+    constexpr float kLn2 = 0x1.62e430p-1f;
+    const float ax = __builtin_fabsf(x), nx = ax > 150.0f ? -150.0f : -ax;
+    const float p = nx * kLog2e;
+    const float rest = __builtin_fmaf(nx, kLog2e, -p) + nx * kLog2eRest;
+    const float root = __builtin_amdgcn_exp2f(0.5f * p);
+    const float t = root * __builtin_fmaf(root, rest * kLn2, root);
+    // 1 <= 1 + t <= 2: the hardware reciprocal and one Newton step.
+    const float d = 1.0f + t, r0 = __builtin_amdgcn_rcpf(d);
+    const float r = __builtin_fmaf(__builtin_fmaf(-d, r0, 1.0f), r0, r0);
+    const float tr = t * r;
+    return x < 0.0f ? Sigmoid{tr, r} : Sigmoid{r, tr};
+}
+
+struct SwigluParams {
+    const uint16_t* dy;   // gradient only
+    const uint16_t* gu;
+    void* y;              // bf16 or e4m3; the gradient of gu
+    float* scale;
+    int64_t M, F, lddy, ldgu, ldy, lds;
+    int64_t units;        // M * ceil(F / 128)
+    int32_t per_row;      // ceil(F / 128)
+};
+
+template <bool FP8>
+__global__ void __launch_bounds__(256) k_swiglu(SwigluParams p)
+{
+    constexpr int UNITS = 256 / kLanes;   // per workgroup
+    for (int64_t u0 = (int64_t)blockIdx.x * UNITS; u0 < p.units; u0 += (int64_t)gridDim.x * UNITS) {
+        const int64_t unit = u0 + threadIdx.x / kLanes;
+        if (unit >= p.units)
+            continue;   // whole 16-lane groups drop out: the maximum stays inside a group
+        int64_t row, c;
+        unit_place(unit, p.per_row, row, c);
+        const int n = left(p.F, c);
+        const uint16_t* src = p.gu + row * p.ldgu + c;
+        const u32x4_t gv = load_chunk(src, n), uv = load_chunk(src + p.F, n);
+        float y[kChunk];
+#pragma unroll
+        for (int e = 0; e < kChunk; ++e) {
+            const float g = chunk_at(gv, e);
+            y[e] = g * sigmoid(g).s * chunk_at(uv, e);
+        }
+        if constexpr (FP8) {
+            const BlockScale b = block_scale(block_top(y));
+            store_chunk8((uint8_t*)p.y + row * p.ldy + c, n, chunk_fp8(y, b));
+            if ((threadIdx.x & (kLanes - 1)) == 0)
+                p.scale[c / kBlock * p.lds + row] = b.scale;
+        } else {
+            store_chunk((uint16_t*)p.y + row * p.ldy + c, n, chunk_bf16(y));
+        }
+    }
+}
+
+__global__ void __launch_bounds__(256) k_swiglu_bwd(SwigluParams p)
+{
+    constexpr int UNITS = 256 / kLanes;
+    for (int64_t u0 = (int64_t)blockIdx.x * UNITS; u0 < p.units; u0 += (int64_t)gridDim.x * UNITS) {
+        const int64_t unit = u0 + threadIdx.x / kLanes;
+        if (unit >= p.units)
+            continue;
+        int64_t row, c;
+        unit_place(unit, p.per_row, row, c);
+        const int n = left(p.F, c);
+        const uint16_t* src = p.gu + row * p.ldgu + c;
+        const u32x4_t gv = load_chunk(src, n), uv = load_chunk(src + p.F, n);
+        const u32x4_t dv = load_chunk(p.dy + row * p.lddy + c, n);
+        float dg[kChunk], du[kChunk];
+#pragma unroll
+        for (int e = 0; e < kChunk; ++e) {
+            const float g = chunk_at(gv, e), d = chunk_at(dv, e);
+            const Sigmoid s = sigmoid(g);
+            du[e] = d * (g * s.s);
+            dg[e] = d * chunk_at(uv, e) * (s.s * __builtin_fmaf(g, s.c, 1.0f));
+        }
+        uint16_t* dst = (uint16_t*)p.y + row * p.ldy + c;
+        store_chunk(dst, n, chunk_bf16(dg));
+        store_chunk(dst + p.F, n, chunk_bf16(du));
+    }
+}
+
+int swiglu_shape(int64_t M, int64_t F)
+{
+    if (M < 0 || F < 0)
+        return GEMM_ERR_INVALID_VALUE;
+    return M > kMaxRows || F > kMaxRows / 2 ? GEMM_ERR_UNSUPPORTED_SHAPE : GEMM_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int gemm_swiglu(int64_t M, int64_t F, const void* GU, int64_t ldgu, void* Y, int64_t ldy, int y_type, float* scale,
+                int64_t lds, void* stream)
+{
+    if (int rc = swiglu_shape(M, F))
+        return rc;
+    const bool fp8 = y_type == GEMM_TYPE_FP8;
+    if (!fp8 && y_type != GEMM_TYPE_BF16)
+        return GEMM_ERR_INVALID_VALUE;
+    if (M == 0 || F == 0)
+        return GEMM_OK;
+    const int64_t per_row = (F + kBlock - 1) / kBlock;
+    const Operand gu{GU, M, 2 * F, ldgu, 2}, y{Y, M, F, ldy, fp8 ? 1 : 2}, s{fp8 ? scale : nullptr, per_row, M, lds, 4};
+    const Operand all[] = {gu, y, s};
+    if (const int rc = check_operands(all, fp8 ? 3 : 2))
+        return rc;
+    if (meet(y, gu) || meet(s, gu) || meet(s, y))
+        return GEMM_ERR_ALIAS;
+    int cus = 0;
+    if (const int rc = device_info(&cus))
+        return rc;
+    const SwigluParams p{nullptr, (const uint16_t*)GU, Y, scale, M, F, 0, ldgu, ldy, lds, M * per_row, (int32_t)per_row};
+    const dim3 grid(unit_grid(p.units));
+    if (fp8)
+        hipLaunchKernelGGL(k_swiglu<true>, grid, dim3(256), 0, (hipStream_t)stream, p);
+    else
+        hipLaunchKernelGGL(k_swiglu<false>, grid, dim3(256), 0, (hipStream_t)stream, p);
+    return launched();
+}
+
+int gemm_swiglu_bwd(int64_t M, int64_t F, const void* dY, int64_t lddy, const void* GU, int64_t ldgu, void* dGU,
+                    int64_t lddgu, void* stream)
+{
+    if (int rc = swiglu_shape(M, F))
+        return rc;
+    if (M == 0 || F == 0)
+        return GEMM_OK;
+    const Operand dy{dY, M, F, lddy, 2}, gu{GU, M, 2 * F, ldgu, 2}, dgu{dGU, M, 2 * F, lddgu, 2};
+    const Operand all[] = {dy, gu, dgu};
+    if (const int rc = check_operands(all, 3))
+        return rc;
+    // A lane reads its g and u before it writes their gradients in the same places.
+    if (meet(dgu, dy) || (meet(dgu, gu) && !same_memory(dgu, gu)))
+        return GEMM_ERR_ALIAS;
+    int cus = 0;
+    if (const int rc = device_info(&cus))
+        return rc;
+    const int64_t per_row = (F + kBlock - 1) / kBlock;
+    const SwigluParams p{(const uint16_t*)dY, (const uint16_t*)GU, dGU, nullptr, M, F, lddy, ldgu, lddgu, 0,
+                         M * per_row, (int32_t)per_row};
+    hipLaunchKernelGGL(k_swiglu_bwd, dim3(unit_grid(p.units)), dim3(256), 0, (hipStream_t)stream, p);
+    return launched();
+}
+
+}  // extern "C"
