@@ -21,9 +21,9 @@
 // An fp32 C is computed exactly.  So is whatever does not wait for the matrix
 // cores: few rows (bound by B's bytes) and short sums (bound by C's).
 //
-// A tile row of 128 bytes is what the bf16 product calls a row of 64 elements,
-// so the ring, its swizzle and its loader are those of the bf16 product with
-// sizes and leading dimensions counted in 2-byte units.
+// A tile row of 128 bytes is what the bf16 product calls a row of 64 elements:
+// the tile configurations, the LDS ring with its swizzle and the raster are the
+// bf16 product's, with K, lda and ldb in Params counted in 2-byte units.
 #pragma once
 
 namespace {
@@ -132,57 +132,147 @@ __device__ __forceinline__ int fp8_col(int j, int i)
     return (i >> 2) * (4 * C::FN) + j * 4 + (i & 3);
 }
 
-// The scales of one k-step: BM of A's rows, then BN of B's columns, fetched into
-// LDS by one 4-byte-per-lane load of each wave.  Rows and columns past the
-// matrix, and k blocks past K, read as zeros.
+// The load stream of one workgroup: positions (output tile, k-step), each an A
+// tile, a B tile and, in LDS beside them, the scales of BM rows and BN columns.
+//
+// As in the bf16 loader, slot s of a 1 KiB load holds tile row s / 8 and the
+// 16-byte chunk that the swizzle puts there, and a resource ends at the
+// operand's last byte, so rows past the matrix read as zeros; chunks past K are
+// masked per lane.  The row of a B slot is fp8_col's, which makes the lanes'
+// columns of C consecutive.  A scale load is 4 bytes per lane, one load a wave.
+//
+// The cursor is free of branches: it steps through a tile's k range with the
+// loads' scalar offset, and at a given k-step takes over the next tile's
+// origin, which is worked out once per tile.  A resource's byte count is capped
+// below 2^31, which no access of a tile reaches (255 rows of at most 2^23
+// bytes, and K).
 template <class C>
-struct ScaleLoader {
-    static constexpr int BYTES = (C::BM + C::BN) * 4;
+struct Fp8Loader {
+    static constexpr int SCALE_BYTES = (C::BM + C::BN) * 4;
     static constexpr int AW = C::BM / 64;   // waves that fetch A's scales
-    static_assert((C::BM + C::BN) / 64 == C::NCW, "one load per wave");
+    static_assert((C::BM + C::BN) / 64 == C::NCW && C::BK == 64, "one scale load per wave, 128-byte tile rows");
 
-    const float* base;   // at the position's k block
-    int64_t step;
-    uint32_t nrec, voff;
-    int32_t kb, kt, ti;
+    uint32_t voffA[C::A_LOADS], voffB[C::B_LOADS], voffS;
+    int32_t kofs[C::LOADS];                 // of each load's chunk within the k-step, bytes
+    struct Position {
+        const char* a;
+        const char* b;
+        const char* s;                      // this wave's scales at the position's k block
+        uint32_t na, nb, ns;                // bytes left to the end of each operand
+        int32_t k, kleft;                   // bytes: offset within the chunk's k range, left of K
+    };
+    Position cur, nxt;
+    int64_t sstep;                          // bytes per k block of this wave's scales
 
-    __device__ __forceinline__ void enter(const Params& p, const Fp8Params& q, int32_t n_tiles, int w, int lane)
+    __device__ __forceinline__ void init(const Params& p, const Fp8Params& q, int w, int lane)
+    {
+        const uint32_t lda = (uint32_t)p.lda * 2u, ldb = (uint32_t)p.ldb * 2u;
+#pragma unroll
+        for (int t = 0; t < C::LOADS; ++t) {
+            const int s = ((t < C::A_LOADS ? t : t - C::A_LOADS) * C::NLW + w) * 64 + lane;
+            const int row = s / 8;
+            kofs[t] = ((s % 8) ^ swz_k<64>(row)) * 16;
+            if (t < C::A_LOADS)
+                voffA[t] = (uint32_t)row * lda + (uint32_t)kofs[t];
+            else
+                voffB[t - C::A_LOADS] =
+                    (uint32_t)(row / C::TN * C::TN + fp8_col<C>(row % C::TN / 16, row & 15)) * ldb + (uint32_t)kofs[t];
+        }
+        const bool a = w < AW;
+        // A's scales in the order a lane reads them: word FM * r + i of a wave's
+        // rows holds row 16 * i + r.
+        const int at = (a ? w : w - AW) * 64 + lane, in = at % C::TM;
+        voffS = (uint32_t)(a ? at - in + in % C::FM * 16 + in / C::FM : at >> q.sb_shift) * 4u;
+        sstep = (a ? q.ldsa : q.ldsb) * 4;
+    }
+
+    // The first position of the workgroup's work item `ti`; an empty one past
+    // the last item.
+    __device__ __forceinline__ Position first(const Params& p, const Fp8Params& q, int32_t ti, int32_t n_tiles, int w) const
     {
         int32_t tm, tn, sp, u;
         tile_coords(p, (int32_t)blockIdx.x + min(ti, n_tiles - 1) * (int32_t)gridDim.x, (int32_t)gridDim.x, tm, tn, sp,
                     u);
-        kb = sp * p.k_steps;
-        kt = 0;
-        const int64_t m0 = (int64_t)tm * C::BM, n0 = (int64_t)tn * C::BN;
-        const bool a = w < AW;
-        step = a ? q.ldsa : q.ldsb;
-        base = (a ? q.sa + m0 : q.sb + (n0 >> q.sb_shift)) + kb * step;
-        const int64_t rem = a ? p.M - m0 : q.sb_cols - (n0 >> q.sb_shift);
-        nrec = ti < n_tiles ? (uint32_t)min(rem, (int64_t)1024) * 4u : 0u;
-        const int at = (a ? w : w - AW) * 64 + lane;
-        voff = (uint32_t)(a ? at : at >> q.sb_shift) * 4u;
+        const int64_t m0 = (int64_t)tm * C::BM, n0 = (int64_t)tn * C::BN, k0 = (int64_t)sp * p.k_steps * kBlock;
+        const bool live = ti < n_tiles, a = w < AW;
+        Position r;
+        r.a = p.A + m0 * p.lda * 2 + k0;
+        r.b = p.B + n0 * p.ldb * 2 + k0;
+        r.na = live ? records((uint64_t)(((p.M - 1 - m0) * p.lda * 2) + q.K - k0)) : 0u;
+        r.nb = live ? records((uint64_t)(((p.N - 1 - n0) * p.ldb * 2) + q.K - k0)) : 0u;
+        r.k = 0;
+        r.kleft = (int32_t)(q.K - k0);
+        const int64_t n0s = n0 >> q.sb_shift, left = a ? p.M - m0 : q.sb_cols - n0s;
+        r.s = (a ? (const char*)(q.sa + m0) : (const char*)(q.sb + n0s)) + (int64_t)sp * p.k_steps * sstep;
+        r.ns = live ? (uint32_t)min(left, (int64_t)C::BM + C::BN) * 4u : 0u;
+        return r;
     }
 
-    __device__ __forceinline__ void issue_next(const Params& p, const Fp8Params& q, int32_t n_tiles, lds_char* dst,
-                                               int w, int lane)
+    // The next position; `enter` (uniform) takes the next tile's first one.
+    // Member by member, which compiles to selects: a branch here would cut the
+    // k-step's schedule in two, and the compiler moves sums across the cut.
+    __device__ __forceinline__ void step(bool enter)
     {
-        const __amdgpu_buffer_rsrc_t r = rsrc_n(base, kb < q.kblocks ? nrec : 0u);
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (LDS_AS void*)(dst + w * 256), 4, voff, 0, 0, 0);
-        if (++kt == p.k_steps) {
-            ++ti;
-            enter(p, q, n_tiles, w, lane);
-        } else {
-            ++kb;
-            base += step;
-        }
+        cur.a = enter ? nxt.a : cur.a;
+        cur.b = enter ? nxt.b : cur.b;
+        cur.s = enter ? nxt.s : cur.s + sstep;
+        cur.na = enter ? nxt.na : cur.na;
+        cur.nb = enter ? nxt.nb : cur.nb;
+        cur.ns = enter ? nxt.ns : cur.ns;
+        cur.k = enter ? nxt.k : cur.k + kBlock;
+        cur.kleft = enter ? nxt.kleft : cur.kleft - kBlock;
+    }
+
+    __device__ __forceinline__ void fire(const Position& r, int t, lds_char* stage, int w) const
+    {
+        const bool ok = kofs[t] < r.kleft;
+        if (t < C::A_LOADS)
+            lds_dma16(rsrc_n(r.a, r.na), stage + (t * C::NLW + w) * 1024, ok ? voffA[t] : kOOB, (uint32_t)r.k);
+        else
+            lds_dma16(rsrc_n(r.b, r.nb), stage + C::A_BYTES + ((t - C::A_LOADS) * C::NLW + w) * 1024,
+                      ok ? voffB[t - C::A_LOADS] : kOOB, (uint32_t)r.k);
+    }
+
+    // k blocks past K have no scales: they read as zeros.
+    __device__ __forceinline__ void fire_scales(const Position& r, lds_char* scales, int w) const
+    {
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc_n(r.s, r.kleft > 0 ? r.ns : 0u), (LDS_AS void*)(scales + w * 256),
+                                                 4, voffS, 0, 0, 0);
     }
 };
+
+// Columns of C that lane group g of a wave holds of one row: 4 * FN consecutive
+// ones from n on.
+template <class C>
+__device__ __forceinline__ void store_row(const Fp8Params& q, int64_t m, int64_t n, int64_t N, const f32x4_t (&v)[C::FN])
+{
+    if (n + 4 * C::FN <= N) {
+        if (q.c_fp32) {
+            float* c = (float*)q.c + m * q.ldc + n;
+#pragma unroll
+            for (int j = 0; j < C::FN; ++j)
+                __builtin_memcpy(c + j * 4, &v[j], 16);
+        } else {
+            uint16_t* c = (uint16_t*)q.c + m * q.ldc + n;
+#pragma unroll
+            for (int j = 0; j < C::FN; j += 2) {
+                const u32x4_t x = {pack_bf16x2(v[j][0], v[j][1]), pack_bf16x2(v[j][2], v[j][3]),
+                                   pack_bf16x2(v[j + 1][0], v[j + 1][1]), pack_bf16x2(v[j + 1][2], v[j + 1][3])};
+                __builtin_memcpy(c + j * 4, &x, 16);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j)
+            store_c4(q, m, n + j * 4, N, v[j]);
+    }
+}
 
 template <class C, bool ROWB, bool EXACT>
 __global__ void __launch_bounds__(C::THREADS) k_gemm_fp8(Params p, Fp8Params q)
 {
-    using SL = ScaleLoader<C>;
-    __shared__ __attribute__((aligned(1024))) char smem_raw[C::RING_BYTES + 2 * SL::BYTES];
+    using LD = Fp8Loader<C>;
+    __shared__ __attribute__((aligned(1024))) char smem_raw[C::RING_BYTES + 2 * LD::SCALE_BYTES];
     lds_char* smem = (lds_char*)smem_raw;
     const int lane = threadIdx.x & 63, r16 = lane & 15, g = lane >> 4;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -192,76 +282,156 @@ __global__ void __launch_bounds__(C::THREADS) k_gemm_fp8(Params p, Fp8Params q)
     const int32_t n_tiles = (b < p.tiles) ? (p.tiles - 1 - b) / G + 1 : 0;
     if (n_tiles == 0)
         return;
-    Loader<C, false, true> ld;
-    ld.init(p, n_tiles, w, lane);
-    // LDS row L of B's tile holds the column fp8_col gives (the loader's rows
-    // are in order).
-#pragma unroll
-    for (int t = 0; t < C::B_LOADS; ++t) {
-        const int row = ld.krow(ld.slot(t, w, lane));
-        const int col = row / C::TN * C::TN + fp8_col<C>(row % C::TN / 16, row & 15);
-        ld.voffB[t] += (uint32_t)(col - row) * ((uint32_t)p.ldb * 2u);
-    }
-    SL sl;
-    sl.ti = 0;
-    sl.enter(p, q, n_tiles, w, lane);
-    auto issue = [&](int s) {
-        sl.issue_next(p, q, n_tiles, smem + C::RING_BYTES + s * SL::BYTES, w, lane);
-        ld.issue_next(p, smem + s * C::STAGE_BYTES, w, lane);
-    };
-    issue(0);
+    LD ld;
+    ld.init(p, q, w, lane);
+    ld.cur = ld.first(p, q, 0, n_tiles, w);
+    auto stage_at = [&](int st) { return smem + st * C::STAGE_BYTES; };
+    auto scales_at = [&](int st) { return smem + C::RING_BYTES + st * LD::SCALE_BYTES; };
 
     // Lane (r16, g) reads chunks g and g + 4 of row r16 of each fragment (both
     // operands in the same order, so the order along k does not matter).
     const int swz = swz_k<64>(r16);
     const uint32_t lo = (uint32_t)r16 * 128u + (uint32_t)((g ^ swz) * 16), hi = lo ^ 64u;
+    struct Raw {
+        u32x4_t lo, hi;
+    };
+    Raw ar[2], br[C::FN];
+    f32x4_t sar[C::FM / 4], sbr[ROWB ? C::FN : 1];
+    float sb1 = 0.0f;
+    auto read_a = [&](int st, int i) {
+        const lds_char* t = stage_at(st) + wm * C::TM * 128 + i * 2048;
+        ar[i & 1] = Raw{*(const LDS_AS u32x4_t*)(t + lo), *(const LDS_AS u32x4_t*)(t + hi)};
+    };
+    auto read_b = [&](int st, int j) {
+        const lds_char* t = stage_at(st) + C::A_BYTES + wn * C::TN * 128 + j * 2048;
+        br[j] = Raw{*(const LDS_AS u32x4_t*)(t + lo), *(const LDS_AS u32x4_t*)(t + hi)};
+    };
+    auto read_scales = [&](int st) {
+        const lds_char* t = scales_at(st) + (wm * C::TM + r16 * C::FM) * 4;
+#pragma unroll
+        for (int i = 0; i < C::FM / 4; ++i)
+            sar[i] = *(const LDS_AS f32x4_t*)(t + i * 16);
+        const lds_char* u = scales_at(st) + (C::BM + wn * C::TN) * 4;
+        if constexpr (ROWB) {
+#pragma unroll
+            for (int j = 0; j < C::FN; ++j)
+                sbr[j] = *(const LDS_AS f32x4_t*)(u + (g * (4 * C::FN) + j * 4) * 4);
+        } else {
+            sb1 = *(const lds_f32*)u;
+        }
+    };
 
+    // Position 0 whole; then what a k-step leaves behind: the cursor on position
+    // 1, with its scales under way, and the first fragments and the scales of
+    // position 0 in registers.
+    ld.fire_scales(ld.cur, scales_at(0), w);
+#pragma unroll
+    for (int t = 0; t < C::LOADS; ++t)
+        ld.fire(ld.cur, t, stage_at(0), w);
+    ld.step(false);
+    wait_vmcnt<0>();
+    block_barrier();
+    ld.fire_scales(ld.cur, scales_at(1), w);
+#pragma unroll
+    for (int j = 0; j < C::FN; ++j)
+        read_b(0, j);
+    read_a(0, 0);
+    read_scales(0);
+
+    // MFMA n of a k-step is fragment pair (n / FN, n % FN).  Its partial sums are
+    // added to the running sums LAG MFMAs later, when they are sure to be there;
+    // the last LAG of a k-step are added in the next one (with `held`, the scale
+    // they belong to).
+    constexpr int NM = C::FM * C::FN, LAG = 2, RING = 4;
+    static_assert(NM % RING == 0 && LAG < RING && LAG <= C::FN && C::LOADS <= NM - C::FN, "k-step schedule");
+    f32x4_t part[RING];
     int s = 0;
     for (int32_t it = 0; it < n_tiles; ++it) {
         int32_t tm, tn, sp, u;
         tile_coords(p, b + it * G, G, tm, tn, sp, u);
+        ld.nxt = ld.first(p, q, it + 1, n_tiles, w);
         f32x4_t acc[C::FM][C::FN];
 #pragma unroll
         for (int i = 0; i < C::FM; ++i)
 #pragma unroll
             for (int j = 0; j < C::FN; ++j)
                 acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < RING; ++i)
+            part[i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+        float held = 0.0f;
+        auto add = [&](int n, float sa, const f32x4_t& sb) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                acc[n / C::FN][n % C::FN][e] =
+                    __builtin_fmaf(part[n % RING][e], ROWB ? sa * sb[e] : sa, acc[n / C::FN][n % C::FN][e]);
+        };
         for (int32_t kt = 0; kt < p.k_steps; ++kt) {
-            // This wave's loads of the step have landed and its fragment reads of
-            // the previous step have completed; the barrier makes both so for
-            // every wave, and the other stage takes the next step.
-            wait_vmcnt<0>();
-            wait_lgkm0();
-            block_barrier();
-            issue(s ^ 1);
-            const lds_char* at = smem + s * C::STAGE_BYTES + wm * C::TM * 128;
-            const lds_char* bt = smem + s * C::STAGE_BYTES + C::A_BYTES + wn * C::TN * 128;
-            const lds_f32* sa = (const lds_f32*)(smem + C::RING_BYTES + s * SL::BYTES) + wm * C::TM + r16;
-            const lds_f32* sb = (const lds_f32*)(smem + C::RING_BYTES + s * SL::BYTES) + C::BM + wn * C::TN;
             Fp8Frag<EXACT> bf[C::FN];
-            f32x4_t sbv[C::FN];
 #pragma unroll
-            for (int j = 0; j < C::FN; ++j) {
-                bf[j] = Fp8Frag<EXACT>(*(const LDS_AS u32x4_t*)(bt + j * 2048 + lo),
-                                       *(const LDS_AS u32x4_t*)(bt + j * 2048 + hi));
-                if constexpr (ROWB)
-                    sbv[j] = *(const LDS_AS f32x4_t*)(sb + g * (4 * C::FN) + j * 4);
+            for (int j = 0; j < C::FN; ++j)
+                bf[j] = Fp8Frag<EXACT>(br[j].lo, br[j].hi);
+            float sc[C::FM];
+            f32x4_t sbv[ROWB ? C::FN : 1];
+#pragma unroll
+            for (int i = 0; i < C::FM; ++i)
+                sc[i] = ROWB ? sar[i / 4][i % 4] : sar[i / 4][i % 4] * sb1;
+            if constexpr (ROWB) {
+#pragma unroll
+                for (int j = 0; j < C::FN; ++j)
+                    sbv[j] = sbr[j];
             }
-            const float sb1 = ROWB ? 1.0f : sb[0];
+            Fp8Frag<EXACT> af;
+            // One slot of the schedule: an MFMA, what is loaded beside it, and
+            // the sums of an earlier MFMA.
+            auto slot = [&]<int n>() {
+                constexpr int i = n / C::FN, j = n % C::FN;
+                if constexpr (j == 0)
+                    af = Fp8Frag<EXACT>(ar[i & 1].lo, ar[i & 1].hi);
+                part[n % RING] = block_sums(bf[j], af);
+                __builtin_amdgcn_sched_barrier(0);
+                if constexpr (j == 0 && i + 1 < C::FM)
+                    read_a(s, i + 1);
+                if constexpr (n < C::LOADS)
+                    ld.fire(ld.cur, n, stage_at(s ^ 1), w);
+                if constexpr (i + 1 == C::FM)
+                    read_b(s ^ 1, j);
+                if constexpr (n + 1 == NM)
+                    read_a(s ^ 1, 0);
+                if constexpr (n >= LAG)
+                    add(n - LAG, sc[(n - LAG) / C::FN], sbv[ROWB ? (n - LAG) % C::FN : 0]);
+                else if constexpr (!ROWB)
+                    add(NM - LAG + n, held, sbv[0]);
+                __builtin_amdgcn_sched_barrier(0);
+            };
+            [&]<int... NS>(std::integer_sequence<int, NS...>) {
+                (slot.template operator()<NS>(), ...);
+            }(std::make_integer_sequence<int, NM - C::FN>{});
+            ld.step(kt == p.k_steps - 2);
+            // Every fragment of this stage is in registers and the next
+            // position's loads have landed, here and, after the barrier, in
+            // every wave: this stage takes the position after next.
+            wait_lgkm0();
+            wait_vmcnt<0>();
+            block_barrier();
+            ld.fire_scales(ld.cur, scales_at(s), w);
+            read_scales(s ^ 1);
+            [&]<int... NS>(std::integer_sequence<int, NS...>) {
+                (slot.template operator()<NM - C::FN + NS>(), ...);
+            }(std::make_integer_sequence<int, C::FN>{});
+            if constexpr (ROWB) {
 #pragma unroll
-            for (int i = 0; i < C::FM; ++i) {
-                const Fp8Frag<EXACT> af(*(const LDS_AS u32x4_t*)(at + i * 2048 + lo),
-                                        *(const LDS_AS u32x4_t*)(at + i * 2048 + hi));
-                const float sc = sa[i * 16] * sb1;
-#pragma unroll
-                for (int j = 0; j < C::FN; ++j) {
-                    const f32x4_t d = block_sums(bf[j], af);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        acc[i][j][e] = __builtin_fmaf(d[e], ROWB ? sc * sbv[j][e] : sc, acc[i][j][e]);
-                }
+                for (int n = NM - LAG; n < NM; ++n)
+                    add(n, sc[C::FM - 1], sbv[n % C::FN]);
+            } else {
+                held = sc[C::FM - 1];
             }
             s ^= 1;
+        }
+        if constexpr (!ROWB) {
+#pragma unroll
+            for (int n = NM - LAG; n < NM; ++n)
+                add(n, held, f32x4_t{});
         }
         if (p.splits > 1) {
             float* part = p.partial + (int64_t)(sp * p.span + u) * (C::BM * C::BN);
@@ -274,11 +444,8 @@ __global__ void __launch_bounds__(C::THREADS) k_gemm_fp8(Params p, Fp8Params q)
 #pragma unroll
             for (int i = 0; i < C::FM; ++i) {
                 const int64_t m = (int64_t)tm * C::BM + wm * C::TM + i * 16 + r16;
-                if (m < p.M) {
-#pragma unroll
-                    for (int j = 0; j < C::FN; ++j)
-                        store_c4(q, m, (int64_t)tn * C::BN + wn * C::TN + g * (4 * C::FN) + j * 4, p.N, acc[i][j]);
-                }
+                if (m < p.M)
+                    store_row<C>(q, m, (int64_t)tn * C::BN + wn * C::TN + g * (4 * C::FN), p.N, acc[i]);
             }
         }
     }
@@ -478,7 +645,7 @@ int launch_skinny(const SkinnyParams& p, const Fp8Params& q, hipStream_t s)
 // Sums of up to this many blocks are computed exactly (see the top).
 constexpr int kShortBlocks = 2;
 
-template <class C>
+template <class C, bool EXACT>
 int launch_tiles(Params p, const Fp8Params& q, int cus, int per_cu, TempMem& tm, hipStream_t s)
 {
     p.tiles_m = (int32_t)((p.M + C::BM - 1) / C::BM);
@@ -498,6 +665,10 @@ int launch_tiles(Params p, const Fp8Params& q, int cus, int per_cu, TempMem& tm,
     }
     p.k_steps = (int32_t)((q.kblocks + splits - 1) / splits);
     p.splits = (int32_t)((q.kblocks + p.k_steps - 1) / p.k_steps);   // no empty chunk
+    // The load cursor runs two positions ahead and crosses at most one tile
+    // border: a single k-step is followed by one that reads zeros.
+    if (p.k_steps < 2)
+        p.k_steps = 2;
     p.ksplit = (int64_t)p.k_steps * (kBlock / 2);
     p.tiles_mn = p.span = (int32_t)tiles;
     p.tile_base = 0;
@@ -513,15 +684,11 @@ int launch_tiles(Params p, const Fp8Params& q, int cus, int per_cu, TempMem& tm,
         p.partial = (float*)ws;
     }
     const dim3 grid((unsigned)(p.tiles < slots ? p.tiles : slots)), block(C::THREADS);
-    const bool rowb = q.sb_shift == 0, exact = q.c_fp32 || q.kblocks <= kShortBlocks;
-    if (rowb && exact)
-        hipLaunchKernelGGL(HIP_KERNEL_NAME(k_gemm_fp8<C, true, true>), grid, block, 0, s, p, q);
-    else if (rowb)
-        hipLaunchKernelGGL(HIP_KERNEL_NAME(k_gemm_fp8<C, true, false>), grid, block, 0, s, p, q);
-    else if (exact)
-        hipLaunchKernelGGL(HIP_KERNEL_NAME(k_gemm_fp8<C, false, true>), grid, block, 0, s, p, q);
+    const bool rowb = q.sb_shift == 0;
+    if (rowb)
+        hipLaunchKernelGGL(HIP_KERNEL_NAME(k_gemm_fp8<C, true, EXACT>), grid, block, 0, s, p, q);
     else
-        hipLaunchKernelGGL(HIP_KERNEL_NAME(k_gemm_fp8<C, false, false>), grid, block, 0, s, p, q);
+        hipLaunchKernelGGL(HIP_KERNEL_NAME(k_gemm_fp8<C, false, EXACT>), grid, block, 0, s, p, q);
     int rc = launched();
     if (p.splits > 1) {
         if (rc == GEMM_OK) {
@@ -557,9 +724,13 @@ int gemm_fp8_direct(int64_t M, int64_t N, const char* A, int64_t lda, const char
     p.K = q.K / 2;
     p.lda = lda / 2;
     p.ldb = ldb / 2;
+    // The exact way takes 128 x 128 tiles at any size: its fragments are twice
+    // as large, and beside 128 running sums they do not fit a wave's registers.
+    if (q.c_fp32 || q.kblocks <= kShortBlocks)
+        return launch_tiles<Fp8Cfg<128, 128, 2, 2>, true>(p, q, cus, 2, tm, s);
     if ((M + 255) / 256 * ((N + 255) / 256) >= cus)
-        return launch_tiles<Fp8Cfg<256, 256, 2, 4>>(p, q, cus, 1, tm, s);
-    return launch_tiles<Fp8Cfg<128, 128, 2, 2>>(p, q, cus, 2, tm, s);
+        return launch_tiles<Fp8Cfg<256, 256, 2, 4>, false>(p, q, cus, 1, tm, s);
+    return launch_tiles<Fp8Cfg<128, 128, 2, 2>, false>(p, q, cus, 2, tm, s);
 }
 
 }  // namespace
