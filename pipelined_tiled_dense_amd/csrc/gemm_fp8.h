@@ -145,15 +145,27 @@ __device__ __forceinline__ int fp8_col(int j, int i)
 // loads' scalar offset, and at a given k-step takes over the next tile's
 // origin, which is worked out once per tile.  A resource's byte count is capped
 // below 2^31, which no access of a tile reaches (255 rows of at most 2^23
-// bytes, and K).
+// bytes, and K); a masked lane's offset is past it whatever is added.
 template <class C>
 struct Fp8Loader {
     static constexpr int SCALE_BYTES = (C::BM + C::BN) * 4;
     static constexpr int AW = C::BM / 64;   // waves that fetch A's scales
     static_assert((C::BM + C::BN) / 64 == C::NCW && C::BK == 64, "one scale load per wave, 128-byte tile rows");
 
-    uint32_t voffA[C::A_LOADS], voffB[C::B_LOADS], voffS;
-    int32_t kofs[C::LOADS];                 // of each load's chunk within the k-step, bytes
+    // A lane's place in the first load of each operand.  Its place in load t is
+    // RSTEP tile rows further per load at the same chunk (RSTEP rows are whole
+    // periods of the swizzle), a scalar distance for A and, fp8_col being
+    // additive in them, for B.
+    static constexpr int RSTEP = C::NLW * 8;
+    static_assert(RSTEP % 16 == 0 && (RSTEP % C::TN == 0 || C::TN % RSTEP == 0), "loads of a lane");
+    uint32_t voffA, voffB, voffS;
+    uint32_t ldaB, ldbB;                    // row strides in bytes
+    int32_t kofs;                           // of the lane's chunk within the k-step, bytes
+    static constexpr int rows_a(int t) { return t * RSTEP; }
+    static constexpr int cols_b(int t)
+    {
+        return RSTEP % C::TN == 0 ? t * RSTEP : t * RSTEP / C::TN * C::TN + t * RSTEP % C::TN / 16 * 4;
+    }
     struct Position {
         const char* a;
         const char* b;
@@ -166,18 +178,12 @@ struct Fp8Loader {
 
     __device__ __forceinline__ void init(const Params& p, const Fp8Params& q, int w, int lane)
     {
-        const uint32_t lda = (uint32_t)p.lda * 2u, ldb = (uint32_t)p.ldb * 2u;
-#pragma unroll
-        for (int t = 0; t < C::LOADS; ++t) {
-            const int s = ((t < C::A_LOADS ? t : t - C::A_LOADS) * C::NLW + w) * 64 + lane;
-            const int row = s / 8;
-            kofs[t] = ((s % 8) ^ swz_k<64>(row)) * 16;
-            if (t < C::A_LOADS)
-                voffA[t] = (uint32_t)row * lda + (uint32_t)kofs[t];
-            else
-                voffB[t - C::A_LOADS] =
-                    (uint32_t)(row / C::TN * C::TN + fp8_col<C>(row % C::TN / 16, row & 15)) * ldb + (uint32_t)kofs[t];
-        }
+        ldaB = (uint32_t)p.lda * 2u;
+        ldbB = (uint32_t)p.ldb * 2u;
+        const int row = w * 8 + lane / 8;
+        kofs = ((lane % 8) ^ swz_k<64>(row)) * 16;
+        voffA = (uint32_t)row * ldaB + (uint32_t)kofs;
+        voffB = (uint32_t)(row / C::TN * C::TN + fp8_col<C>(row % C::TN / 16, row & 15)) * ldbB + (uint32_t)kofs;
         const bool a = w < AW;
         // A's scales in the order a lane reads them: word FM * r + i of a wave's
         // rows holds row 16 * i + r.
@@ -225,12 +231,14 @@ struct Fp8Loader {
 
     __device__ __forceinline__ void fire(const Position& r, int t, lds_char* stage, int w) const
     {
-        const bool ok = kofs[t] < r.kleft;
+        const bool ok = kofs < r.kleft;
+        const int tb = t - C::A_LOADS;
         if (t < C::A_LOADS)
-            lds_dma16(rsrc_n(r.a, r.na), stage + (t * C::NLW + w) * 1024, ok ? voffA[t] : kOOB, (uint32_t)r.k);
+            lds_dma16(rsrc_n(r.a, r.na), stage + (t * C::NLW + w) * 1024, ok ? voffA : kOOB,
+                      (uint32_t)r.k + (uint32_t)rows_a(t) * ldaB);
         else
-            lds_dma16(rsrc_n(r.b, r.nb), stage + C::A_BYTES + ((t - C::A_LOADS) * C::NLW + w) * 1024,
-                      ok ? voffB[t - C::A_LOADS] : kOOB, (uint32_t)r.k);
+            lds_dma16(rsrc_n(r.b, r.nb), stage + C::A_BYTES + (tb * C::NLW + w) * 1024, ok ? voffB : kOOB,
+                      (uint32_t)r.k + (uint32_t)cols_b(tb) * ldbB);
     }
 
     // k blocks past K have no scales: they read as zeros.
@@ -282,6 +290,7 @@ __global__ void __launch_bounds__(C::THREADS) k_gemm_fp8(Params p, Fp8Params q)
     const int32_t n_tiles = (b < p.tiles) ? (p.tiles - 1 - b) / G + 1 : 0;
     if (n_tiles == 0)
         return;
+    clock_begin(p);
     LD ld;
     ld.init(p, q, w, lane);
     ld.cur = ld.first(p, q, 0, n_tiles, w);
@@ -450,6 +459,7 @@ __global__ void __launch_bounds__(C::THREADS) k_gemm_fp8(Params p, Fp8Params q)
         }
     }
     wait_vmcnt<0>();   // the last, empty position's loads still write LDS
+    clock_end(p);
 }
 
 // Sums the k chunks' partial tiles in chunk order and stores C.  A thread takes
@@ -724,6 +734,7 @@ int gemm_fp8_direct(int64_t M, int64_t N, const char* A, int64_t lda, const char
     p.K = q.K / 2;
     p.lda = lda / 2;
     p.ldb = ldb / 2;
+    p.clock_on = g_clock_on.load(std::memory_order_relaxed) ? 1u : 0u;
     // The exact way takes 128 x 128 tiles at any size: its fragments are twice
     // as large, and beside 128 running sums they do not fit a wave's registers.
     if (q.c_fp32 || q.kblocks <= kShortBlocks)
