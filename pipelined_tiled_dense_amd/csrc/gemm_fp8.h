@@ -63,14 +63,20 @@ struct Fp8Frag<true> {
     __device__ __forceinline__ Fp8Frag() {}
     __device__ __forceinline__ Fp8Frag(u32x4_t lo, u32x4_t hi)
     {
+        convert<0>(lo);
+        convert<1>(hi);
+    }
+    // Half HALF of the fragment from its 16 bytes.
+    template <int HALF>
+    __device__ __forceinline__ void convert(u32x4_t x)
+    {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t w0 = i < 2 ? lo[2 * i] : hi[2 * i - 4], w1 = i < 2 ? lo[2 * i + 1] : hi[2 * i - 3];
-            const bf16x2_t a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, 1.0f, false);
-            const bf16x2_t b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, 1.0f, true);
-            const bf16x2_t c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, 1.0f, false);
-            const bf16x2_t d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, 1.0f, true);
-            v[i] = bf16x8_t{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+        for (int i = 0; i < 2; ++i) {
+            const bf16x2_t a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[2 * i], 1.0f, false);
+            const bf16x2_t b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[2 * i], 1.0f, true);
+            const bf16x2_t c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[2 * i + 1], 1.0f, false);
+            const bf16x2_t d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[2 * i + 1], 1.0f, true);
+            v[2 * HALF + i] = bf16x8_t{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
         }
     }
 };
@@ -277,7 +283,7 @@ __device__ __forceinline__ void store_row(const Fp8Params& q, int64_t m, int64_t
 }
 
 template <class C, bool ROWB, bool EXACT>
-__global__ void __launch_bounds__(C::THREADS) k_gemm_fp8(Params p, Fp8Params q)
+__global__ void __launch_bounds__(C::THREADS, 2) k_gemm_fp8(Params p, Fp8Params q)
 {
     using LD = Fp8Loader<C>;
     __shared__ __attribute__((aligned(1024))) char smem_raw[C::RING_BYTES + 2 * LD::SCALE_BYTES];
@@ -304,12 +310,12 @@ __global__ void __launch_bounds__(C::THREADS) k_gemm_fp8(Params p, Fp8Params q)
     struct Raw {
         u32x4_t lo, hi;
     };
-    Raw ar[2], br[C::FN];
+    Raw ar[4], br[C::FN];
     f32x4_t sar[C::FM / 4], sbr[ROWB ? C::FN : 1];
     float sb1 = 0.0f;
     auto read_a = [&](int st, int i) {
         const lds_char* t = stage_at(st) + wm * C::TM * 128 + i * 2048;
-        ar[i & 1] = Raw{*(const LDS_AS u32x4_t*)(t + lo), *(const LDS_AS u32x4_t*)(t + hi)};
+        ar[i & 3] = Raw{*(const LDS_AS u32x4_t*)(t + lo), *(const LDS_AS u32x4_t*)(t + hi)};
     };
     auto read_b = [&](int st, int j) {
         const lds_char* t = stage_at(st) + C::A_BYTES + wn * C::TN * 128 + j * 2048;
@@ -330,9 +336,8 @@ __global__ void __launch_bounds__(C::THREADS) k_gemm_fp8(Params p, Fp8Params q)
         }
     };
 
-    // Position 0 whole; then what a k-step leaves behind: the cursor on position
-    // 1, with its scales under way, and the first fragments and the scales of
-    // position 0 in registers.
+    // Position 0 whole; then what a k-step leaves behind: position 1 under way and
+    // the first fragments of position 0 in registers.
     ld.fire_scales(ld.cur, scales_at(0), w);
 #pragma unroll
     for (int t = 0; t < C::LOADS; ++t)
@@ -341,19 +346,43 @@ __global__ void __launch_bounds__(C::THREADS) k_gemm_fp8(Params p, Fp8Params q)
     wait_vmcnt<0>();
     block_barrier();
     ld.fire_scales(ld.cur, scales_at(1), w);
+    read_a(0, 0);
+    read_a(0, 1);
 #pragma unroll
     for (int j = 0; j < C::FN; ++j)
         read_b(0, j);
-    read_a(0, 0);
-    read_scales(0);
 
-    // MFMA n of a k-step is fragment pair (n / FN, n % FN).  Its partial sums are
-    // added to the running sums LAG MFMAs later, when they are sure to be there;
-    // the last LAG of a k-step are added in the next one (with `held`, the scale
-    // they belong to).
-    constexpr int NM = C::FM * C::FN, LAG = 2, RING = 4;
-    static_assert(NM % RING == 0 && LAG < RING && LAG <= C::FN && C::LOADS <= NM - C::FN, "k-step schedule");
+    // The MFMAs of a k-step go by pairs of fragment rows, column by column.  So in
+    // the last pair a fragment of B has its last use two MFMAs before the next
+    // one's, and its successor, the next k-step's, is read in between; it is
+    // needed only after as many MFMAs, 2 * FN, whose time covers the read.  A's
+    // fragments are read a pair ahead.  The barrier stands before the last pair:
+    // by then the wave has read every fragment of the stage, so the stage can be
+    // refilled and the next one be read.  The refill's loads go out one every
+    // GAP MFMAs, into the next k-step.
+    //
+    // The partial sums of MFMA n are added to the running sums after MFMA n +
+    // LAG, when they are sure to be there; the last LAG of a k-step in the next
+    // one, with the scales they belong to (`held`).
+    constexpr int NM = C::FM * C::FN, PAIR = 2 * C::FN, TAIL = NM - PAIR, LAG = 3, RING = 4, GAP = 2;
+    constexpr auto row_of = [](int n) { return n / PAIR * 2 + n % 2; };
+    constexpr auto col_of = [](int n) { return n % PAIR / 2; };
+    // The load that goes out at MFMA n, counted from the barrier on; none: -1.
+    constexpr auto load_at = [](int n) {
+        const int t = n >= TAIL ? n - TAIL : n + PAIR;
+        return t % GAP == 0 && t / GAP < C::LOADS ? t / GAP : -1;
+    };
+    static_assert(NM % RING == 0 && LAG < RING && LAG <= PAIR && C::LOADS * GAP <= NM && C::FM % 4 == 0,
+                  "k-step schedule");
+    [&]<int... NS>(std::integer_sequence<int, NS...>) {
+        ((load_at(TAIL + NS) >= 0 ? ld.fire(ld.cur, load_at(TAIL + NS), stage_at(1), w) : (void)0), ...);
+    }(std::make_integer_sequence<int, PAIR>{});
     f32x4_t part[RING];
+    Fp8Frag<EXACT> bf[C::FN], af[2];
+    if constexpr (EXACT) {
+        bf[0] = Fp8Frag<EXACT>(br[0].lo, br[0].hi);
+        af[0] = Fp8Frag<EXACT>(ar[0].lo, ar[0].hi);
+    }
     int s = 0;
     for (int32_t it = 0; it < n_tiles; ++it) {
         int32_t tm, tn, sp, u;
@@ -368,54 +397,81 @@ __global__ void __launch_bounds__(C::THREADS) k_gemm_fp8(Params p, Fp8Params q)
 #pragma unroll
         for (int i = 0; i < RING; ++i)
             part[i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-        float held = 0.0f;
+        float held[2] = {0.0f, 0.0f};
         auto add = [&](int n, float sa, const f32x4_t& sb) {
+            f32x4_t& sum = acc[row_of(n)][col_of(n)];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                acc[n / C::FN][n % C::FN][e] =
-                    __builtin_fmaf(part[n % RING][e], ROWB ? sa * sb[e] : sa, acc[n / C::FN][n % C::FN][e]);
+                sum[e] = __builtin_fmaf(part[n % RING][e], ROWB ? sa * sb[e] : sa, sum[e]);
         };
+        // Nothing of the scalar loads before may be pending in the loop: scalar
+        // and LDS loads share a counter but not an order, and the loop's waits
+        // would then be for everything instead of for the fragments they need.
+        wait_lgkm0();
         for (int32_t kt = 0; kt < p.k_steps; ++kt) {
-            Fp8Frag<EXACT> bf[C::FN];
-#pragma unroll
-            for (int j = 0; j < C::FN; ++j)
-                bf[j] = Fp8Frag<EXACT>(br[j].lo, br[j].hi);
-            float sc[C::FM];
-            f32x4_t sbv[ROWB ? C::FN : 1];
-#pragma unroll
-            for (int i = 0; i < C::FM; ++i)
-                sc[i] = ROWB ? sar[i / 4][i % 4] : sar[i / 4][i % 4] * sb1;
-            if constexpr (ROWB) {
+            if constexpr (!EXACT) {
 #pragma unroll
                 for (int j = 0; j < C::FN; ++j)
-                    sbv[j] = sbr[j];
+                    bf[j] = Fp8Frag<EXACT>(br[j].lo, br[j].hi);
             }
-            Fp8Frag<EXACT> af;
+            float sc[C::FM];
             // One slot of the schedule: an MFMA, what is loaded beside it, and
             // the sums of an earlier MFMA.
             auto slot = [&]<int n>() {
-                constexpr int i = n / C::FN, j = n % C::FN;
+                constexpr int i = row_of(n), j = col_of(n), f = load_at(n);
+                if constexpr (!EXACT && j == 0)
+                    af[i & 1] = Fp8Frag<EXACT>(ar[i & 3].lo, ar[i & 3].hi);
+                part[n % RING] = block_sums(bf[j], af[i & 1]);
+                if constexpr (!EXACT) {
+                    __builtin_amdgcn_sched_barrier(0);
+                } else {
+                    // Fragments are converted a few MFMAs before their use, when
+                    // their predecessors have had theirs: B's next column in the
+                    // first pair, A's rows about the turn of each pair.
+                    if constexpr (n < PAIR && j + 1 < C::FN) {
+                        if constexpr (n % 2 == 0)
+                            bf[j + 1].template convert<0>(br[j + 1].lo);
+                        else
+                            bf[j + 1].template convert<1>(br[j + 1].hi);
+                    }
+                    if constexpr (n == NM - 2)
+                        bf[0] = Fp8Frag<EXACT>(br[0].lo, br[0].hi);
+                    if constexpr (n % PAIR == PAIR - 1)
+                        af[0] = Fp8Frag<EXACT>(ar[(i + 1) & 3].lo, ar[(i + 1) & 3].hi);
+                    if constexpr (n % PAIR == 0)
+                        af[1] = Fp8Frag<EXACT>(ar[(i + 1) & 3].lo, ar[(i + 1) & 3].hi);
+                }
                 if constexpr (j == 0)
-                    af = Fp8Frag<EXACT>(ar[i & 1].lo, ar[i & 1].hi);
-                part[n % RING] = block_sums(bf[j], af);
-                __builtin_amdgcn_sched_barrier(0);
-                if constexpr (j == 0 && i + 1 < C::FM)
-                    read_a(s, i + 1);
-                if constexpr (n < C::LOADS)
-                    ld.fire(ld.cur, n, stage_at(s ^ 1), w);
-                if constexpr (i + 1 == C::FM)
+                    read_a(n < TAIL ? s : s ^ 1, (i + 2) % C::FM);
+                if constexpr (n >= TAIL && n % 2 == 1)
                     read_b(s ^ 1, j);
-                if constexpr (n + 1 == NM)
-                    read_a(s ^ 1, 0);
+                if constexpr (f >= 0)
+                    ld.fire(ld.cur, f, stage_at(n < TAIL ? s ^ 1 : s), w);
+                // The step's scales: read at its start, needed LAG MFMAs on.
+                if constexpr (n == 0)
+                    read_scales(s);
+                if constexpr (n == LAG) {
+#pragma unroll
+                    for (int x = 0; x < C::FM; ++x)
+                        sc[x] = ROWB ? sar[x / 4][x % 4] : sar[x / 4][x % 4] * sb1;
+                }
                 if constexpr (n >= LAG)
-                    add(n - LAG, sc[(n - LAG) / C::FN], sbv[ROWB ? (n - LAG) % C::FN : 0]);
+                    add(n - LAG, sc[row_of(n - LAG)], sbr[ROWB ? col_of(n - LAG) : 0]);
                 else if constexpr (!ROWB)
-                    add(NM - LAG + n, held, sbv[0]);
+                    add(NM - LAG + n, held[row_of(NM - LAG + n) & 1], f32x4_t{});
+                if constexpr (EXACT) {
+                    // Four dependent MFMAs with the vector work between them.
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                        __builtin_amdgcn_sched_group_barrier(0x002, 6, 0);
+                    }
+                }
                 __builtin_amdgcn_sched_barrier(0);
             };
             [&]<int... NS>(std::integer_sequence<int, NS...>) {
                 (slot.template operator()<NS>(), ...);
-            }(std::make_integer_sequence<int, NM - C::FN>{});
+            }(std::make_integer_sequence<int, TAIL>{});
             ld.step(kt == p.k_steps - 2);
             // Every fragment of this stage is in registers and the next
             // position's loads have landed, here and, after the barrier, in
@@ -424,23 +480,23 @@ __global__ void __launch_bounds__(C::THREADS) k_gemm_fp8(Params p, Fp8Params q)
             wait_vmcnt<0>();
             block_barrier();
             ld.fire_scales(ld.cur, scales_at(s), w);
-            read_scales(s ^ 1);
             [&]<int... NS>(std::integer_sequence<int, NS...>) {
-                (slot.template operator()<NM - C::FN + NS>(), ...);
-            }(std::make_integer_sequence<int, C::FN>{});
+                (slot.template operator()<TAIL + NS>(), ...);
+            }(std::make_integer_sequence<int, PAIR>{});
             if constexpr (ROWB) {
 #pragma unroll
                 for (int n = NM - LAG; n < NM; ++n)
-                    add(n, sc[C::FM - 1], sbv[n % C::FN]);
+                    add(n, sc[row_of(n)], sbr[col_of(n)]);
             } else {
-                held = sc[C::FM - 1];
+                held[0] = sc[C::FM - 2];
+                held[1] = sc[C::FM - 1];
             }
             s ^= 1;
         }
         if constexpr (!ROWB) {
 #pragma unroll
             for (int n = NM - LAG; n < NM; ++n)
-                add(n, held, f32x4_t{});
+                add(n, held[row_of(n) & 1], f32x4_t{});
         }
         if (p.splits > 1) {
             float* part = p.partial + (int64_t)(sp * p.span + u) * (C::BM * C::BN);
