@@ -269,6 +269,9 @@ def gemm(A, B, *, b_transposed: bool = False, stages: int = 0, sync="barrier", o
 # ceil(rows / 128)) for blocks.  Every function runs on the current stream
 # unless a torch stream is given; with one, results are allocated for that
 # stream and the arguments are marked as used on it.
+#
+# For a few rows these calls take the host longer than the GPU, so the helpers
+# below touch each tensor as little as they can.
 class RmsNorm(NamedTuple):
     """What ``rms_norm`` returns; what was not asked for is None."""
     y: object               # bfloat16, or float8_e4m3fn with ``scale``
@@ -277,52 +280,51 @@ class RmsNorm(NamedTuple):
     rstd: object = None     # float32 (M,)
 
 
-def _matrix(name, x, dtype, shape=None):
+def _matrix(name, x, dtype):
     """Checks a 2-D CUDA operand with unit inner stride; returns its leading dimension."""
-    if x.dtype != dtype or x.dim() != 2 or not x.is_cuda:
+    if x.dtype is not dtype or x.ndim != 2 or not x.is_cuda:
         raise TypeError("%s must be a 2-D %s CUDA tensor" % (name, str(dtype).replace("torch.", "")))
-    if shape is not None and x.shape != shape:
-        raise ValueError("%s must have shape %s, not %s" % (name, tuple(shape), tuple(x.shape)))
-    rows, ld = x.shape[0], x.stride(0)
-    if x.shape[1] > 1 and x.stride(1) != 1 and rows > 0:
+    rows, cols = x.shape
+    ld, inner = x.stride()
+    if inner != 1 and cols > 1 and rows > 0:
         raise ValueError("%s needs unit stride along its second dimension" % name)
-    return max(ld, x.shape[1]) if rows <= 1 else ld
+    return ld if rows > 1 else max(ld, cols)
+
+
+def _shaped(name, x, rows, cols):
+    if x.shape != (rows, cols):
+        raise ValueError("%s must have shape %s, not %s" % (name, (rows, cols), tuple(x.shape)))
 
 
 def _vector(name, x, dtype, n):
-    if x.dtype != dtype or x.dim() != 1 or not x.is_cuda:
+    if x.dtype is not dtype or x.ndim != 1 or not x.is_cuda:
         raise TypeError("%s must be a 1-D %s CUDA tensor" % (name, str(dtype).replace("torch.", "")))
     if x.shape[0] != n or (n > 1 and x.stride(0) != 1):
         raise ValueError("%s must hold %d contiguous values" % (name, n))
 
 
-class _On:
-    """The stream a call runs on: the current one, or the given one, for which
-    ``empty`` then allocates and on which ``uses`` marks the arguments."""
+def _current(torch, x, *others):
+    """The raw handle of the current stream of the device that all tensors are
+    on, which has to be the current one."""
+    d = x.get_device()
+    for t in others:
+        if t is not None and t.get_device() != d:
+            raise ValueError("tensors on different devices: cuda:%d and %s" % (d, t.device))
+    if d != torch.cuda.current_device():
+        raise ValueError("tensors on cuda:%d, but the current device is cuda:%d" % (d, torch.cuda.current_device()))
+    return torch._C._cuda_getCurrentRawStream(d)
 
-    def __init__(self, stream, *tensors):
-        import torch
 
-        device = tensors[0].device
-        for x in tensors:
-            if x is not None and x.device != device:
-                raise ValueError("tensors on different devices: %s and %s" % (device, x.device))
-        if device.index != torch.cuda.current_device():
-            raise ValueError("tensors on %s, but the current device is cuda:%d" % (device, torch.cuda.current_device()))
-        self.torch, self.device, self.stream = torch, device, stream
-        if stream is None:
-            self.handle = torch.cuda.current_stream(device).cuda_stream
-        else:
-            self.handle = stream.cuda_stream
-            for x in tensors:
-                if x is not None:
-                    x.record_stream(stream)
+def _on_stream(stream, tensors, call):
+    """``call`` with ``stream`` as the current stream, for which it then
+    allocates; the tensors it reads are marked as used there."""
+    import torch
 
-    def empty(self, shape, dtype):
-        if self.stream is None:
-            return self.torch.empty(shape, dtype=dtype, device=self.device)
-        with self.torch.cuda.stream(self.stream):
-            return self.torch.empty(shape, dtype=dtype, device=self.device)
+    for t in tensors:
+        if t is not None and t.is_cuda:
+            t.record_stream(stream)
+    with torch.cuda.stream(stream):
+        return call()
 
 
 def _done(rc, name):
@@ -343,26 +345,32 @@ def gemm_fp8(A, scale_a, B, scale_b, *, out_dtype=None, out=None, stream=None):
     (the default) or float32."""
     import torch
 
-    lda, ldb = _matrix("A", A, torch.float8_e4m3fn), _matrix("B", B, torch.float8_e4m3fn)
-    (M, K), N = A.shape, B.shape[0]
-    if B.shape[1] != K:
-        raise ValueError("inner dimensions differ: %d vs %d" % (K, B.shape[1]))
-    kb, rows = _blocks(K), 1
-    ldsa = _matrix("scale_a", scale_a, torch.float32, (kb, M))
-    if scale_b.dim() == 2 and scale_b.shape[1] != N:
-        rows = BLOCK
-    ldsb = _matrix("scale_b", scale_b, torch.float32, (kb, N if rows == 1 else _blocks(N)))
+    if stream is not None:
+        return _on_stream(stream, (A, scale_a, B, scale_b, out),
+                          lambda: gemm_fp8(A, scale_a, B, scale_b, out_dtype=out_dtype, out=out))
+    f8, f32, bf16 = torch.float8_e4m3fn, torch.float32, torch.bfloat16
+    lda, ldb = _matrix("A", A, f8), _matrix("B", B, f8)
+    (M, K), (N, KB) = A.shape, B.shape
+    if KB != K:
+        raise ValueError("inner dimensions differ: %d vs %d" % (K, KB))
+    ldsa, ldsb = _matrix("scale_a", scale_a, f32), _matrix("scale_b", scale_b, f32)
+    kb = _blocks(K)
+    _shaped("scale_a", scale_a, kb, M)
+    rows = 1 if scale_b.shape[1] == N else BLOCK
+    _shaped("scale_b", scale_b, kb, N if rows == 1 else _blocks(N))
     if out_dtype is None:
-        out_dtype = torch.bfloat16 if out is None else out.dtype
-    if out_dtype not in (torch.bfloat16, torch.float32):
+        out_dtype = bf16 if out is None else out.dtype
+    if out_dtype is not bf16 and out_dtype is not f32:
         raise TypeError("out_dtype must be bfloat16 or float32")
-    on = _On(stream, A, B, scale_a, scale_b, out)
+    s = _current(torch, A, B, scale_a, scale_b, out)
     if out is None:
-        out = on.empty((M, N), out_dtype)
-    ldc = _matrix("out", out, out_dtype, (M, N))
+        out, ldc = torch.empty(M, N, dtype=out_dtype, device=A.device), N
+    else:
+        ldc = _matrix("out", out, out_dtype)
+        _shaped("out", out, M, N)
     _done(library().gemm_fp8_bt(M, N, K, A.data_ptr(), lda, scale_a.data_ptr(), ldsa, B.data_ptr(), ldb,
                                 scale_b.data_ptr(), ldsb, rows, out.data_ptr(), ldc,
-                                TYPE_BF16 if out_dtype == torch.bfloat16 else TYPE_FP32, on.handle), "gemm_fp8_bt")
+                                TYPE_BF16 if out_dtype is bf16 else TYPE_FP32, s), "gemm_fp8_bt")
     return out
 
 
@@ -372,16 +380,18 @@ def quantize_fp8(x, *, block_rows=1, transposed=False, stream=None):
     of x or, with ``transposed``, of its transpose."""
     import torch
 
+    if stream is not None:
+        return _on_stream(stream, (x,), lambda: quantize_fp8(x, block_rows=block_rows, transposed=transposed))
     ldx = _matrix("x", x, torch.bfloat16)
     M, K = x.shape
     if block_rows not in (1, BLOCK):
         raise ValueError("block_rows must be 1 or %d" % BLOCK)
     R, L = (K, M) if transposed else (M, K)
-    on = _On(stream, x)
-    cols = R if block_rows == 1 else _blocks(R)
-    q, scale = on.empty((R, L), torch.float8_e4m3fn), on.empty((_blocks(L), cols), torch.float32)
+    cols, dev, s = R if block_rows == 1 else _blocks(R), x.device, _current(torch, x)
+    q = torch.empty(R, L, dtype=torch.float8_e4m3fn, device=dev)
+    scale = torch.empty(_blocks(L), cols, dtype=torch.float32, device=dev)
     _done(library().gemm_quantize_fp8(M, K, x.data_ptr(), ldx, q.data_ptr(), L, scale.data_ptr(), cols, block_rows,
-                                      int(bool(transposed)), on.handle), "gemm_quantize_fp8")
+                                      1 if transposed else 0, s), "gemm_quantize_fp8")
     return q, scale
 
 
@@ -392,23 +402,32 @@ def rms_norm(x, weight, *, residual=None, eps=1e-6, quantize=False, return_rstd=
     ``return_rstd`` (the backward pass needs it)."""
     import torch
 
-    bf16 = torch.bfloat16
+    if stream is not None:
+        return _on_stream(stream, (x, weight, residual),
+                          lambda: rms_norm(x, weight, residual=residual, eps=eps, quantize=quantize,
+                                           return_rstd=return_rstd))
+    bf16, f32 = torch.bfloat16, torch.float32
     ldx = _matrix("x", x, bf16)
     M, D = x.shape
     _vector("weight", weight, bf16, D)
-    ldr = _matrix("residual", residual, bf16, x.shape) if residual is not None else 0
-    on = _On(stream, x, weight, residual)
-    h = on.empty((M, D), bf16) if residual is not None else None
-    rstd = on.empty((M,), torch.float32) if return_rstd else None
+    h, rstd, scale, ldr, dev = None, None, None, 0, x.device
+    if residual is not None:
+        ldr = _matrix("residual", residual, bf16)
+        _shaped("residual", residual, M, D)
+    s = _current(torch, x, weight, residual)
+    if residual is not None:
+        h = torch.empty(M, D, dtype=bf16, device=dev)
+    if return_rstd:
+        rstd = torch.empty(M, dtype=f32, device=dev)
     if quantize:
-        y, scale = on.empty((M, D), torch.float8_e4m3fn), on.empty((_blocks(D), M), torch.float32)
+        y = torch.empty(M, D, dtype=torch.float8_e4m3fn, device=dev)
+        scale = torch.empty(_blocks(D), M, dtype=f32, device=dev)
     else:
-        y, scale = on.empty((M, D), bf16), None
-    _done(library().gemm_rms_norm(M, D, x.data_ptr(), ldx, residual.data_ptr() if residual is not None else None, ldr,
-                                  weight.data_ptr(), float(eps), h.data_ptr() if h is not None else None, D,
-                                  y.data_ptr(), D, TYPE_FP8 if quantize else TYPE_BF16,
-                                  scale.data_ptr() if quantize else None, M,
-                                  rstd.data_ptr() if return_rstd else None, on.handle), "gemm_rms_norm")
+        y = torch.empty(M, D, dtype=bf16, device=dev)
+    _done(library().gemm_rms_norm(M, D, x.data_ptr(), ldx, None if residual is None else residual.data_ptr(), ldr,
+                                  weight.data_ptr(), eps, None if h is None else h.data_ptr(), D, y.data_ptr(), D,
+                                  TYPE_FP8 if quantize else TYPE_BF16, None if scale is None else scale.data_ptr(), M,
+                                  None if rstd is None else rstd.data_ptr(), s), "gemm_rms_norm")
     return RmsNorm(y, scale, h, rstd)
 
 
@@ -419,19 +438,32 @@ def rms_norm_backward(dy, h, weight, rstd, *, dresidual=None, stream=None):
     (bfloat16) is the gradient of x and residual alike, dweight is float32."""
     import torch
 
+    if stream is not None:
+        return _on_stream(stream, (dy, h, weight, rstd, dresidual),
+                          lambda: rms_norm_backward(dy, h, weight, rstd, dresidual=dresidual))
     bf16 = torch.bfloat16
-    lddy = _matrix("dy", dy, bf16)
+    lddy, ldh = _matrix("dy", dy, bf16), _matrix("h", h, bf16)
     M, D = dy.shape
-    ldh = _matrix("h", h, bf16, dy.shape)
+    _shaped("h", h, M, D)
     _vector("weight", weight, bf16, D)
     _vector("rstd", rstd, torch.float32, M)
-    lddr = _matrix("dresidual", dresidual, bf16, dy.shape) if dresidual is not None else 0
-    on = _On(stream, dy, h, weight, rstd, dresidual)
-    dx, dweight = on.empty((M, D), bf16), on.empty((D,), torch.float32)
+    lddr, dev = 0, dy.device
+    if dresidual is not None:
+        lddr = _matrix("dresidual", dresidual, bf16)
+        _shaped("dresidual", dresidual, M, D)
+    s = _current(torch, dy, h, weight, rstd, dresidual)
+    dx, dweight = torch.empty(M, D, dtype=bf16, device=dev), torch.empty(D, dtype=torch.float32, device=dev)
     _done(library().gemm_rms_norm_bwd(M, D, dy.data_ptr(), lddy, h.data_ptr(), ldh, weight.data_ptr(), rstd.data_ptr(),
-                                      dresidual.data_ptr() if dresidual is not None else None, lddr, dx.data_ptr(), D,
-                                      dweight.data_ptr(), on.handle), "gemm_rms_norm_bwd")
+                                      None if dresidual is None else dresidual.data_ptr(), lddr, dx.data_ptr(), D,
+                                      dweight.data_ptr(), s), "gemm_rms_norm_bwd")
     return dx, dweight
+
+
+def _gated(gu):
+    M, F2 = gu.shape
+    if F2 % 2:
+        raise ValueError("gu must have an even number of columns")
+    return M, F2 // 2
 
 
 def swiglu(gu, *, quantize=False, stream=None):
@@ -439,31 +471,33 @@ def swiglu(gu, *, quantize=False, stream=None):
     or, with ``quantize``, the pair of 8-bit y and its row scales."""
     import torch
 
-    ldgu = _matrix("gu", gu, torch.bfloat16)
-    M, F = gu.shape[0], gu.shape[1] // 2
-    if gu.shape[1] != 2 * F:
-        raise ValueError("gu must have an even number of columns")
-    on = _On(stream, gu)
-    if quantize:
-        y, scale = on.empty((M, F), torch.float8_e4m3fn), on.empty((_blocks(F), M), torch.float32)
-    else:
-        y, scale = on.empty((M, F), torch.bfloat16), None
-    _done(library().gemm_swiglu(M, F, gu.data_ptr(), ldgu, y.data_ptr(), F, TYPE_FP8 if quantize else TYPE_BF16,
-                                scale.data_ptr() if quantize else None, M, on.handle), "gemm_swiglu")
-    return (y, scale) if quantize else y
+    if stream is not None:
+        return _on_stream(stream, (gu,), lambda: swiglu(gu, quantize=quantize))
+    ldgu, dev = _matrix("gu", gu, torch.bfloat16), gu.device
+    M, F = _gated(gu)
+    s = _current(torch, gu)
+    if not quantize:
+        y = torch.empty(M, F, dtype=torch.bfloat16, device=dev)
+        _done(library().gemm_swiglu(M, F, gu.data_ptr(), ldgu, y.data_ptr(), F, TYPE_BF16, None, 0, s), "gemm_swiglu")
+        return y
+    q = torch.empty(M, F, dtype=torch.float8_e4m3fn, device=dev)
+    scale = torch.empty(_blocks(F), M, dtype=torch.float32, device=dev)
+    _done(library().gemm_swiglu(M, F, gu.data_ptr(), ldgu, q.data_ptr(), F, TYPE_FP8, scale.data_ptr(), M, s),
+          "gemm_swiglu")
+    return q, scale
 
 
 def swiglu_backward(dy, gu, *, stream=None):
     """The gradient of gu = [g, u] (bfloat16, (M, 2F)) for the gradient dy (M, F) of ``swiglu``."""
     import torch
 
-    ldgu = _matrix("gu", gu, torch.bfloat16)
-    M, F = gu.shape[0], gu.shape[1] // 2
-    if gu.shape[1] != 2 * F:
-        raise ValueError("gu must have an even number of columns")
-    lddy = _matrix("dy", dy, torch.bfloat16, (M, F))
-    on = _On(stream, dy, gu)
-    dgu = on.empty((M, 2 * F), torch.bfloat16)
-    _done(library().gemm_swiglu_bwd(M, F, dy.data_ptr(), lddy, gu.data_ptr(), ldgu, dgu.data_ptr(), 2 * F, on.handle),
+    if stream is not None:
+        return _on_stream(stream, (dy, gu), lambda: swiglu_backward(dy, gu))
+    ldgu, lddy = _matrix("gu", gu, torch.bfloat16), _matrix("dy", dy, torch.bfloat16)
+    M, F = _gated(gu)
+    _shaped("dy", dy, M, F)
+    s = _current(torch, dy, gu)
+    dgu = torch.empty(M, 2 * F, dtype=torch.bfloat16, device=gu.device)
+    _done(library().gemm_swiglu_bwd(M, F, dy.data_ptr(), lddy, gu.data_ptr(), ldgu, dgu.data_ptr(), 2 * F, s),
           "gemm_swiglu_bwd")
     return dgu
