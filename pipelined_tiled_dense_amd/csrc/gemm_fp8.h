@@ -542,44 +542,80 @@ __global__ void __launch_bounds__(256) k_reduce_fp8(Params p, Fp8Params q)
 }
 
 // ---------------------------------------------------------------------------
-// Few rows: the product is bound by B's bytes.  A workgroup of 8 waves takes MF
-// x NF fragments of C; its waves share out the k blocks (wave w takes blocks w,
-// w + 8, ...), stream their fragments from global memory straight into
-// registers, DEPTH blocks in flight at a time, and add their sums through LDS in
-// wave order.  So every compute unit has loads in flight over the whole of k
-// even where N gives few workgroups, with no second launch.
+// Few rows, or little work: the product is bound by B's bytes and by latency.  A
+// workgroup of 8 waves takes MF x NF fragments of C; its waves share out the k
+// blocks (wave w takes blocks w, w + 8, ...), stream their fragments from global
+// memory straight into registers, DEPTH blocks in use and DEPTH more in flight,
+// and add their sums through LDS in wave order.  So every compute unit has loads
+// in flight over the whole of k even where C gives few workgroups, with no
+// second launch.
 // ---------------------------------------------------------------------------
 struct SkinnyParams {
     const char* a;
     const char* b;
     int64_t M, N, lda, ldb;
+    int32_t tiles_m, tiles_n;
 };
 
 constexpr int kSkinnyWaves = 8;
 
-template <int MF, int NF, int DEPTH, bool ROWB>
+template <int MF, int NF, int DEPTH, bool ROWB, bool EXACT>
 __global__ void __launch_bounds__(kSkinnyWaves * 64) k_gemm_fp8_skinny(SkinnyParams p, Fp8Params q)
 {
     __shared__ __attribute__((aligned(16))) f32x4_t sums[kSkinnyWaves][MF * NF][64];
     const int lane = threadIdx.x & 63, r16 = lane & 15, g = lane >> 4;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t tiles_m = (p.M + MF * 16 - 1) / (MF * 16);
-    const int64_t m0 = (int64_t)blockIdx.x % tiles_m * (MF * 16), n0 = (int64_t)blockIdx.x / tiles_m * (NF * 16);
+    // The row tiles of one column tile go to one XCD (workgroups are dealt to the
+    // 8 XCDs in turn), which then reads B once.
+    const int32_t x = blockIdx.x & 7, y = blockIdx.x >> 3;
+    const int32_t tm = y % p.tiles_m, tn = y / p.tiles_m * 8 + x;
+    if (tn >= p.tiles_n)
+        return;
+    const int64_t m0 = (int64_t)tm * (MF * 16), n0 = (int64_t)tn * (NF * 16);
 
     // Rows past the end read as zeros: their offset is past the resource.
     const int64_t a_rows = min(p.M - m0, (int64_t)MF * 16), b_rows = min(p.N - n0, (int64_t)NF * 16);
     const __amdgpu_buffer_rsrc_t ra = make_rsrc(p.a + m0 * p.lda, (a_rows - 1) * p.lda + q.K);
     const __amdgpu_buffer_rsrc_t rb = make_rsrc(p.b + n0 * p.ldb, (b_rows - 1) * p.ldb + q.K);
     uint32_t va[MF], vb[NF];
-    int64_t ia[MF];
 #pragma unroll
-    for (int i = 0; i < MF; ++i) {
-        va[i] = i * 16 + r16 < a_rows ? (uint32_t)(i * 16 + r16) * (uint32_t)p.lda : kOOB;
-        ia[i] = m0 + min((int64_t)i * 16 + r16, a_rows - 1);
-    }
+    for (int i = 0; i < MF; ++i)
+        va[i] = i * 16 + r16 < a_rows ? (uint32_t)(i * 16 + r16) * (uint32_t)p.lda + g * 16 : kOOB;
 #pragma unroll
     for (int j = 0; j < NF; ++j)
-        vb[j] = j * 16 + r16 < b_rows ? (uint32_t)(j * 16 + r16) * (uint32_t)p.ldb : kOOB;
+        vb[j] = j * 16 + r16 < b_rows ? (uint32_t)(j * 16 + r16) * (uint32_t)p.ldb + g * 16 : kOOB;
+
+    struct Block {
+        u32x4_t a[MF][2], b[NF][2];
+        float sa[MF], sb[ROWB ? NF * 4 : 1];
+    };
+    auto load = [&](Block& v, int32_t kb) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const bool ok = kb * kBlock + (h * 4 + g) * 16 < (int32_t)q.K;
+            const uint32_t k = (uint32_t)kb * kBlock + h * 64;
+#pragma unroll
+            for (int j = 0; j < NF; ++j)
+                v.b[j][h] = __builtin_bit_cast(
+                    u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rb, ok ? vb[j] : kOOB, (int)k, 0));
+#pragma unroll
+            for (int i = 0; i < MF; ++i)
+                v.a[i][h] = __builtin_bit_cast(
+                    u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(ra, ok ? va[i] : kOOB, (int)k, 0));
+        }
+        // The scales, each checked against the end of its array.
+        const bool in = kb < q.kblocks;
+        const __amdgpu_buffer_rsrc_t rsa = make_rsrc(q.sa + (in ? kb * q.ldsa : 0) + m0, in ? a_rows * 4 : 0);
+#pragma unroll
+        for (int i = 0; i < MF; ++i)
+            v.sa[i] = as_float(__builtin_amdgcn_raw_buffer_load_b32(rsa, r16 * 4, i * 64, 0));
+        const __amdgpu_buffer_rsrc_t rsb =
+            make_rsrc(q.sb + (in ? kb * q.ldsb : 0) + (n0 >> q.sb_shift), in ? (ROWB ? b_rows * 4 : 4) : 0);
+#pragma unroll
+        for (int e = 0; e < (ROWB ? NF * 4 : 1); ++e)
+            v.sb[e] = as_float(
+                __builtin_amdgcn_raw_buffer_load_b32(rsb, ROWB ? g * 16 + e % 4 * 4 : 0, ROWB ? e / 4 * 64 : 0, 0));
+    };
 
     f32x4_t acc[MF][NF];
 #pragma unroll
@@ -587,60 +623,56 @@ __global__ void __launch_bounds__(kSkinnyWaves * 64) k_gemm_fp8_skinny(SkinnyPar
 #pragma unroll
         for (int j = 0; j < NF; ++j)
             acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    auto compute = [&](const Block& v) {
+        Fp8Frag<EXACT> bf[NF];
+#pragma unroll
+        for (int j = 0; j < NF; ++j)
+            bf[j] = Fp8Frag<EXACT>(v.b[j][0], v.b[j][1]);
+#pragma unroll
+        for (int i = 0; i < MF; ++i) {
+            const Fp8Frag<EXACT> af(v.a[i][0], v.a[i][1]);
+#pragma unroll
+            for (int j = 0; j < NF; ++j) {
+                const f32x4_t d = block_sums(bf[j], af);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    acc[i][j][e] = __builtin_fmaf(d[e], v.sa[i] * v.sb[ROWB ? j * 4 + e : 0], acc[i][j][e]);
+            }
+        }
+    };
 
-    for (int32_t kb0 = w; kb0 < q.kblocks; kb0 += kSkinnyWaves * DEPTH) {
-        u32x4_t av[DEPTH][MF][2], bv[DEPTH][NF][2];
-        float sa[DEPTH][MF], sb[DEPTH][ROWB ? NF * 4 : 1];
+    // A block past the end loads nothing and is not computed (its bytes read as
+    // zeros, but a scale may be infinite).
+    Block cur[DEPTH], nxt[DEPTH];
+    constexpr int STEP = kSkinnyWaves * DEPTH;
+    auto load_all = [&](Block (&v)[DEPTH], int32_t kb0) {
+        if (kb0 < q.kblocks) {
 #pragma unroll
-        for (int d = 0; d < DEPTH; ++d) {
-            const int32_t kb = kb0 + d * kSkinnyWaves;
-            const int32_t kc = min(kb, q.kblocks - 1);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int64_t k = (int64_t)kb * kBlock + (h * 4 + g) * 16;
-                const bool ok = k < q.K;
-#pragma unroll
-                for (int j = 0; j < NF; ++j)
-                    bv[d][j][h] = __builtin_bit_cast(
-                        u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rb, ok ? vb[j] + (uint32_t)k : kOOB, 0, 0));
-#pragma unroll
-                for (int i = 0; i < MF; ++i)
-                    av[d][i][h] = __builtin_bit_cast(
-                        u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(ra, ok ? va[i] + (uint32_t)k : kOOB, 0, 0));
-            }
-#pragma unroll
-            for (int i = 0; i < MF; ++i)
-                sa[d][i] = kb < q.kblocks ? q.sa[kc * q.ldsa + ia[i]] : 0.0f;
-            if constexpr (ROWB) {
-#pragma unroll
-                for (int j = 0; j < NF; ++j)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        sb[d][j * 4 + e] = q.sb[kc * q.ldsb + min(n0 + j * 16 + g * 4 + e, p.N - 1)];
-            } else {
-                sb[d][0] = q.sb[kc * q.ldsb + (n0 >> 7)];
-            }
+            for (int d = 0; d < DEPTH; ++d)
+                load(v[d], kb0 + d * kSkinnyWaves);
         }
+    };
+    auto compute_all = [&](const Block (&v)[DEPTH], int32_t kb0) {
 #pragma unroll
-        for (int d = 0; d < DEPTH; ++d) {
-            Fp8Frag<true> bf[NF];
-#pragma unroll
-            for (int j = 0; j < NF; ++j)
-                bf[j] = Fp8Frag<true>(bv[d][j][0], bv[d][j][1]);
-#pragma unroll
-            for (int i = 0; i < MF; ++i) {
-                const Fp8Frag<true> af(av[d][i][0], av[d][i][1]);
-#pragma unroll
-                for (int j = 0; j < NF; ++j) {
-                    const f32x4_t v = block_sums(bf[j], af);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        acc[i][j][e] =
-                            __builtin_fmaf(v[e], sa[d][i] * sb[d][ROWB ? j * 4 + e : 0], acc[i][j][e]);
-                }
-            }
-        }
+        for (int d = 0; d < DEPTH; ++d)
+            if (kb0 + d * kSkinnyWaves < q.kblocks)
+                compute(v[d]);
+    };
+    // Workgroups start at different places along k: with a power-of-two row
+    // stride, all of them reading the same columns at once fall on the same few
+    // memory channels (8192 x 8192 weight, one token: 18.4 us, and 12.8 so).
+    const int32_t rounds = (q.kblocks + STEP - 1) / STEP, rot = (int32_t)(blockIdx.x % (unsigned)rounds);
+    auto at = [&](int32_t t) {
+        return t < rounds ? w + (t + rot < rounds ? t + rot : t + rot - rounds) * STEP : q.kblocks;
+    };
+    load_all(cur, at(0));
+    for (int32_t t = 0; t < rounds; t += 2) {
+        load_all(nxt, at(t + 1));
+        compute_all(cur, at(t));
+        load_all(cur, at(t + 2));
+        compute_all(nxt, at(t + 1));
     }
+
 #pragma unroll
     for (int i = 0; i < MF; ++i)
 #pragma unroll
@@ -650,8 +682,8 @@ __global__ void __launch_bounds__(kSkinnyWaves * 64) k_gemm_fp8_skinny(SkinnyPar
     for (int f = w; f < MF * NF; f += kSkinnyWaves) {
         f32x4_t v = sums[0][f][lane];
 #pragma unroll
-        for (int x = 1; x < kSkinnyWaves; ++x)
-            v += sums[x][f][lane];
+        for (int z = 1; z < kSkinnyWaves; ++z)
+            v += sums[z][f][lane];
         const int64_t m = m0 + f / NF * 16 + r16;
         if (m < p.M)
             store_c4(q, m, n0 + f % NF * 16 + g * 4, p.N, v);
@@ -697,38 +729,82 @@ unsigned flat_grid(int64_t threads)
 }
 
 template <int MF, int NF, int DEPTH>
-int launch_skinny(const SkinnyParams& p, const Fp8Params& q, hipStream_t s)
+int launch_skinny(SkinnyParams p, const Fp8Params& q, bool exact, hipStream_t s)
 {
-    const int64_t n = (p.M + MF * 16 - 1) / (MF * 16) * ((p.N + NF * 16 - 1) / (NF * 16));
-    const dim3 g((unsigned)n), b(kSkinnyWaves * 64);
-    if (q.sb_shift == 0)
-        hipLaunchKernelGGL(HIP_KERNEL_NAME(k_gemm_fp8_skinny<MF, NF, DEPTH, true>), g, b, 0, s, p, q);
+    p.tiles_m = (int32_t)((p.M + MF * 16 - 1) / (MF * 16));
+    p.tiles_n = (int32_t)((p.N + NF * 16 - 1) / (NF * 16));
+    const dim3 g((unsigned)((p.tiles_n + 7) / 8 * 8 * p.tiles_m)), b(kSkinnyWaves * 64);
+    const bool rowb = q.sb_shift == 0;
+    if (rowb && exact)
+        hipLaunchKernelGGL(HIP_KERNEL_NAME(k_gemm_fp8_skinny<MF, NF, DEPTH, true, true>), g, b, 0, s, p, q);
+    else if (rowb)
+        hipLaunchKernelGGL(HIP_KERNEL_NAME(k_gemm_fp8_skinny<MF, NF, DEPTH, true, false>), g, b, 0, s, p, q);
+    else if (exact)
+        hipLaunchKernelGGL(HIP_KERNEL_NAME(k_gemm_fp8_skinny<MF, NF, DEPTH, false, true>), g, b, 0, s, p, q);
     else
-        hipLaunchKernelGGL(HIP_KERNEL_NAME(k_gemm_fp8_skinny<MF, NF, DEPTH, false>), g, b, 0, s, p, q);
+        hipLaunchKernelGGL(HIP_KERNEL_NAME(k_gemm_fp8_skinny<MF, NF, DEPTH, false, false>), g, b, 0, s, p, q);
     return launched();
 }
 
 // Sums of up to this many blocks are computed exactly (see the top).
 constexpr int kShortBlocks = 2;
 
+// Estimated times, in ns, by which a call chooses its kernel and its splits;
+// what they were read off is measured on an MI355X and noted at each.  Only their
+// order matters, and the launch itself is common to all.
+struct TileTimes {
+    int64_t alone, shared;   // a k-step of a workgroup, of each of two on a compute unit
+};
+constexpr TileTimes kFast256{1550, 1550 * 2};   // 8192^3: 256 k-steps per compute unit in 0.42 ms
+// 1024 x 1024 x 32768 unsplit 182 us for 256 k-steps; 8 splits of 32, two
+// workgroups on every compute unit, 54 us with the reduction.
+constexpr TileTimes kFast128{700, 1000};
+constexpr TileTimes kExact128{1300, 2200};      // the same shape, 80 us with 8 splits
+// A split: the reduction's launch, and a partial tile's way to memory and back
+// (128 x 4096 x 4096: 20.2 us with 4 splits, 22.2 with 8, 27.9 with none).
+constexpr int64_t kSplitLaunch = 6500, kSplitTile = 38;
+// Few-rows kernel: bytes a compute unit's workgroup reads per ns, all of them
+// reading (12.8 us for one token and 8192 x 8192, 28 us for 64 rows).
+constexpr int64_t kSkinnyBytes = 33;
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+int64_t tiles_time(const TileTimes& t, int64_t tile, int per_cu, int64_t M, int64_t N, int64_t kblocks, int64_t splits,
+                   int cus)
+{
+    const int64_t items = ceil_div(M, tile) * ceil_div(N, tile) * splits, steps = ceil_div(kblocks, splits);
+    const int64_t run = items <= cus ? steps * t.alone
+                        : per_cu == 1 ? ceil_div(items, cus) * steps * t.alone
+                                      : ceil_div(items, 2 * (int64_t)cus) * steps * t.shared;
+    return run + (splits > 1 ? kSplitLaunch + kSplitTile * items : 0);
+}
+
+// The number of k chunks that is estimated fastest, among those that leave a
+// chunk 4 k-steps and fit the card at once.
+int64_t choose_fp8_splits(const TileTimes& t, int64_t M, int64_t N, int64_t kblocks, int cus, int64_t* time)
+{
+    int64_t best = 1;
+    *time = tiles_time(t, 128, 2, M, N, kblocks, 1, cus);
+    for (int64_t s = 2; s <= kMaxSplits && s * 4 <= kblocks; ++s) {
+        if (ceil_div(M, 128) * ceil_div(N, 128) * s > 2 * (int64_t)cus)
+            break;
+        const int64_t v = tiles_time(t, 128, 2, M, N, kblocks, s, cus);
+        if (v < *time) {
+            *time = v;
+            best = s;
+        }
+    }
+    return best;
+}
+
 template <class C, bool EXACT>
-int launch_tiles(Params p, const Fp8Params& q, int cus, int per_cu, TempMem& tm, hipStream_t s)
+int launch_tiles(Params p, const Fp8Params& q, int64_t splits, int cus, int per_cu, TempMem& tm, hipStream_t s)
 {
     p.tiles_m = (int32_t)((p.M + C::BM - 1) / C::BM);
     p.tiles_n = (int32_t)((p.N + C::BN - 1) / C::BN);
     const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n, slots = (int64_t)cus * per_cu;
     if (tiles * kMaxSplits > INT32_MAX)
         return GEMM_ERR_UNSUPPORTED_SHAPE;
-    // Few tiles: split k until the card is full, as long as a chunk keeps 4
-    // k-steps.
-    int64_t splits = 1;
-    if (tiles * 2 <= slots) {
-        splits = slots / tiles;
-        if (splits > kMaxSplits)
-            splits = kMaxSplits;
-        if (splits > q.kblocks / 4)
-            splits = q.kblocks / 4 < 1 ? 1 : q.kblocks / 4;
-    }
     p.k_steps = (int32_t)((q.kblocks + splits - 1) / splits);
     p.splits = (int32_t)((q.kblocks + p.k_steps - 1) / p.k_steps);   // no empty chunk
     // The load cursor runs two positions ahead and crosses at most one tile
@@ -773,13 +849,37 @@ int launch_tiles(Params p, const Fp8Params& q, int cus, int per_cu, TempMem& tm,
 int gemm_fp8_direct(int64_t M, int64_t N, const char* A, int64_t lda, const char* B, int64_t ldb, const Fp8Params& q,
                     int cus, TempMem& tm, hipStream_t s)
 {
-    if (M <= 64) {
-        const SkinnyParams p{A, B, M, N, lda, ldb};
-        if (M <= 16)
-            return launch_skinny<1, 1, 8>(p, q, s);
-        if (M <= 32)
-            return launch_skinny<2, 2, 4>(p, q, s);
-        return launch_skinny<4, 2, 2>(p, q, s);
+    const bool exact = q.c_fp32 || q.kblocks <= kShortBlocks;
+    const TileTimes& t128 = exact ? kExact128 : kFast128;
+    int64_t time128 = 0;
+    const int64_t splits = choose_fp8_splits(t128, M, N, q.kblocks, cus, &time128);
+
+    // The few-rows kernel's shapes: rows in fragments of 16, and as many columns
+    // as keep the most compute units busy for the fewest bytes.
+    constexpr struct {
+        int mf, nf;
+    } kShapes[] = {{1, 1}, {1, 2}, {2, 2}, {4, 2}};
+    int shape = -1;
+    int64_t skinny = 0;
+    for (int i = 0; i < 4; ++i) {
+        const int64_t rows = kShapes[i].mf * 16, cols = kShapes[i].nf * 16;
+        const int64_t groups = ceil_div(M, rows) * ceil_div(N, cols);
+        if (groups >= (int64_t)1 << 22)
+            continue;   // far from few rows, and past what a launch takes
+        const int64_t v = ceil_div(groups, cus) * ((M < rows ? M : rows) + cols) * q.kblocks * kBlock / kSkinnyBytes;
+        if (shape < 0 || v < skinny) {
+            shape = i;
+            skinny = v;
+        }
+    }
+    if (shape >= 0 && skinny < time128) {
+        const SkinnyParams p{A, B, M, N, lda, ldb, 0, 0};
+        switch (shape) {
+        case 0: return launch_skinny<1, 1, 2>(p, q, exact, s);
+        case 1: return launch_skinny<1, 2, 2>(p, q, exact, s);
+        case 2: return launch_skinny<2, 2, 2>(p, q, exact, s);
+        default: return launch_skinny<4, 2, 1>(p, q, exact, s);
+        }
     }
     Params p;
     memset(&p, 0, sizeof p);
@@ -793,11 +893,11 @@ int gemm_fp8_direct(int64_t M, int64_t N, const char* A, int64_t lda, const char
     p.clock_on = g_clock_on.load(std::memory_order_relaxed) ? 1u : 0u;
     // The exact way takes 128 x 128 tiles at any size: its fragments are twice
     // as large, and beside 128 running sums they do not fit a wave's registers.
-    if (q.c_fp32 || q.kblocks <= kShortBlocks)
-        return launch_tiles<Fp8Cfg<128, 128, 2, 2>, true>(p, q, cus, 2, tm, s);
-    if ((M + 255) / 256 * ((N + 255) / 256) >= cus)
-        return launch_tiles<Fp8Cfg<256, 256, 2, 4>, false>(p, q, cus, 1, tm, s);
-    return launch_tiles<Fp8Cfg<128, 128, 2, 2>, false>(p, q, cus, 2, tm, s);
+    if (exact)
+        return launch_tiles<Fp8Cfg<128, 128, 2, 2>, true>(p, q, splits, cus, 2, tm, s);
+    if (tiles_time(kFast256, 256, 1, M, N, q.kblocks, 1, cus) < time128)
+        return launch_tiles<Fp8Cfg<256, 256, 2, 4>, false>(p, q, 1, cus, 1, tm, s);
+    return launch_tiles<Fp8Cfg<128, 128, 2, 2>, false>(p, q, splits, cus, 2, tm, s);
 }
 
 }  // namespace
