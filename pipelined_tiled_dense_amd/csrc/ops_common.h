@@ -152,7 +152,7 @@ __device__ __forceinline__ float quotient(float y, const BlockScale& b)
 {
     const float q = y * b.inv;
     const float r = __builtin_fmaf(__builtin_fmaf(-q, b.scale, y), b.inv, q);
-    return __builtin_fminf(__builtin_fmaxf(r, -kFp8Max), kFp8Max);
+    return __builtin_amdgcn_fmed3f(r, -kFp8Max, kFp8Max);
 }
 
 // Four values to e4m3 bytes (v_cvt_pk_fp8_f32 rounds to nearest even; the
