@@ -133,13 +133,19 @@ struct BlockScale {
 };
 
 // The scale of a block whose largest magnitude is `top`.  The lower bound
-// keeps 1 / scale finite, for a block of zeros too; NaN passes through.
+// keeps 1 / scale finite, for a block of zeros too; NaN passes through.  The
+// division by 448 is a product and one residual step, which rounds correctly
+// in three instructions instead of a dozen; the reciprocal may be an ulp off
+// (quotient corrects for it).
 __device__ __forceinline__ BlockScale block_scale(uint32_t top)
 {
-    const float s = as_float(top) / kFp8Max;
+    constexpr float kInv = 1.0f / kFp8Max;
+    const float t = as_float(top), s0 = t * kInv;
+    const float s = __builtin_fmaf(__builtin_fmaf(-s0, kFp8Max, t), kInv, s0);
     BlockScale b;
     b.scale = s < kMinScale ? kMinScale : s;
-    b.inv = 1.0f / b.scale;
+    const float r = __builtin_amdgcn_rcpf(b.scale);
+    b.inv = __builtin_fmaf(__builtin_fmaf(-b.scale, r, 1.0f), r, r);
     return b;
 }
 
@@ -184,27 +190,20 @@ __device__ __forceinline__ uint32_t block_top(const float (&y)[kChunk])
     return row16_max(m);
 }
 
-// ---------------------------------------------------------------------------
-// Work items to workgroups.
-// ---------------------------------------------------------------------------
-// The hardware deals workgroups to the 8 XCDs in turn; give each XCD a
-// contiguous run of items, so that the scales of neighbouring rows, which
-// share cache lines, are written through one L2.
-__device__ __forceinline__ int64_t xcd_item(int64_t b, int64_t n)
-{
-    const int64_t per = n >> 3;
-    return b < 8 * per ? (b & 7) * per + (b >> 3) : b;
-}
-
 // A unit is one block of 128 columns of a row, 16 lanes of one chunk each, so
-// that a block's maximum stays inside the unit.  The row and first column of lane t's chunk of unit `unit`.
-__device__ __forceinline__ void unit_place(int64_t unit, int32_t per_row, int64_t& row, int64_t& c)
+// that a block's maximum stays inside the unit; a workgroup of 256 takes 16
+// units in a row from u0 on.  The row and first column of a lane's chunk.  Only
+// the workgroup's first unit is divided in full; the others lie in the same row
+// or the next, or, with short rows, a few rows on.
+constexpr int kUnits = 256 / kLanes;
+
+__device__ __forceinline__ void unit_place(int64_t u0, int32_t per_row, int64_t& row, int64_t& c)
 {
-    if (unit >> 32 == 0)
-        row = (int64_t)((uint32_t)unit / (uint32_t)per_row);
-    else
-        row = unit / per_row;
-    c = (unit - row * per_row) * kBlock + (threadIdx.x & (kLanes - 1)) * kChunk;
+    const int64_t row0 = (u0 >> 32) == 0 ? (int64_t)((uint32_t)u0 / (uint32_t)per_row) : u0 / per_row;
+    const uint32_t at = (uint32_t)(u0 - row0 * per_row) + threadIdx.x / kLanes;
+    const uint32_t more = per_row >= kUnits ? (at >= (uint32_t)per_row ? 1u : 0u) : at / (uint32_t)per_row;
+    row = row0 + more;
+    c = (int64_t)(at - more * (uint32_t)per_row) * kBlock + (threadIdx.x & (kLanes - 1)) * kChunk;
 }
 
 __device__ __forceinline__ int left(int64_t n, int64_t c)
@@ -219,7 +218,7 @@ __device__ __forceinline__ int left(int64_t n, int64_t c)
 // hold, whole strides beyond.
 unsigned unit_grid(int64_t units)
 {
-    const int64_t n = (units + 15) / 16;
+    const int64_t n = (units + kUnits - 1) / kUnits;
     return (unsigned)(n < (1 << 22) ? n : (1 << 22));
 }
 

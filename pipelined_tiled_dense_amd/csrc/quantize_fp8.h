@@ -20,13 +20,11 @@ struct QuantParams {
 
 __global__ void __launch_bounds__(256) k_quantize_rows(QuantParams p)
 {
-    constexpr int UNITS = 256 / kLanes;
-    for (int64_t u0 = (int64_t)blockIdx.x * UNITS; u0 < p.units; u0 += (int64_t)gridDim.x * UNITS) {
-        const int64_t unit = u0 + threadIdx.x / kLanes;
-        if (unit >= p.units)
+    for (int64_t u0 = (int64_t)blockIdx.x * kUnits; u0 < p.units; u0 += (int64_t)gridDim.x * kUnits) {
+        if (u0 + threadIdx.x / kLanes >= p.units)
             continue;   // whole 16-lane groups drop out
         int64_t row, c;
-        unit_place(unit, p.per_row, row, c);
+        unit_place(u0, p.per_row, row, c);
         const int n = left(p.K, c);
         const u32x4_t v = load_chunk(p.x + row * p.ldx + c, n);
         float y[kChunk];
@@ -52,7 +50,7 @@ __global__ void __launch_bounds__(256) k_quantize_rows(QuantParams p)
 constexpr int kTileLd = kBlock + 8;
 
 template <bool BLOCKS, bool TRANSPOSED>
-__global__ void __launch_bounds__(256) k_quantize_tile(QuantParams p)
+__global__ void __launch_bounds__(256, 4) k_quantize_tile(QuantParams p)
 {
     static_assert(BLOCKS || TRANSPOSED, "row scales of X itself are k_quantize_rows'");
     __shared__ uint32_t tops[4][kBlock];

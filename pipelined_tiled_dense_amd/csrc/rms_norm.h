@@ -53,8 +53,7 @@ __global__ void __launch_bounds__(1024) k_rms_norm(NormParams p, int nw)
     const int64_t groups = (p.M + rows_per_wg - 1) / rows_per_wg;
     int parity = 0;
     for (int64_t g = blockIdx.x; g < groups; g += gridDim.x) {
-        // (A grid smaller than the item count runs the items in order.)
-        const int64_t row = (gridDim.x == groups ? xcd_item(g, groups) : g) * rows_per_wg + sub;
+        const int64_t row = g * rows_per_wg + sub;
         if (row >= p.M)
             continue;   // single-wave rows only: no barrier is skipped
         const uint16_t* x = p.x + row * p.ldx;
@@ -110,8 +109,9 @@ __global__ void __launch_bounds__(1024) k_rms_norm(NormParams p, int nw)
 //
 //   dx = dres + rstd * (t - n * mean(t * n)),    dweight += dy * n
 //
-// One pass: a workgroup takes a contiguous run of rows, keeps each row in
-// registers across the mean, and sums its rows' share of dweight in registers;
+// One pass: a workgroup takes every gridDim-th row (so that neighbouring rows
+// are in flight together), keeps each row in registers across the mean, and sums
+// its rows' share of dweight in registers;
 // the workgroups' shares go to temporary memory and a second, small launch adds
 // them in workgroup order, so the sum does not depend on timing.
 // ---------------------------------------------------------------------------
@@ -133,7 +133,6 @@ __global__ void __launch_bounds__(1024) k_rms_norm_bwd(NormBwdParams p, int nw)
 {
     __shared__ float red[2][16];
     const int lanes = nw * 64, t = threadIdx.x;
-    const int64_t r0 = p.M * blockIdx.x / gridDim.x, r1 = p.M * (blockIdx.x + 1) / gridDim.x;
     u32x4_t wv[NCH];
     float dw[NCH][kChunk];
 #pragma unroll
@@ -158,7 +157,7 @@ __global__ void __launch_bounds__(1024) k_rms_norm_bwd(NormBwdParams p, int nw)
         rs = p.rstd[row];
     };
     int parity = 0;
-    for (int64_t row = r0; row < r1; ++row) {
+    for (int64_t row = blockIdx.x; row < p.M; row += gridDim.x) {
         load_row(row);
         float dot = 0.0f;
 #pragma unroll
@@ -294,7 +293,7 @@ int gemm_rms_norm(int64_t M, int64_t D, const void* X, int64_t ldx, const void* 
         return rc;
     NormParams p{(const uint16_t*)X, (const uint16_t*)residual, (const uint16_t*)weight, (uint16_t*)H, Y, scale, rstd,
                  M, ldx, ldr, ldh, ldy, lds, (int32_t)D, eps, 1.0f / (float)D};
-    const RowShape rs = row_shape(D, M < 2 * cus ? 1 : 4);
+    const RowShape rs = row_shape(D, M < 2 * cus ? 1 : 2);
     const int threads = rs.nw == 1 ? 256 : rs.nw * 64;
     const int64_t groups = rs.nw == 1 ? (M + 3) / 4 : M;
     const dim3 grid((unsigned)(groups < (1 << 20) ? groups : (1 << 20)));
@@ -348,10 +347,11 @@ int gemm_rms_norm_bwd(int64_t M, int64_t D, const void* dY, int64_t lddy, const 
     if (rc != GEMM_OK)
         return rc;
     hipStream_t st = (hipStream_t)stream;
-    const RowShape rs = row_shape(D, 4);
-    // Each workgroup writes D partial sums, so there are no more of them than
-    // fill the card, and none with fewer than 4 rows.
-    int64_t grid = (int64_t)cus * 2;
+    const RowShape rs = row_shape(D, 1);
+    // Each workgroup writes D partial sums, so there are only as many as give a
+    // compute unit 8 waves (8191 x 4096, 8 waves a row: one workgroup each 60.3
+    // us, two 60.8, three 62.9), and none with fewer than 4 rows.
+    int64_t grid = (int64_t)cus * ((8 + rs.nw - 1) / rs.nw);
     if (grid > (M + 3) / 4)
         grid = (M + 3) / 4;
     void* ws = nullptr;

@@ -69,13 +69,11 @@ struct SwigluParams {
 template <bool FP8>
 __global__ void __launch_bounds__(256) k_swiglu(SwigluParams p)
 {
-    constexpr int UNITS = 256 / kLanes;   // per workgroup
-    for (int64_t u0 = (int64_t)blockIdx.x * UNITS; u0 < p.units; u0 += (int64_t)gridDim.x * UNITS) {
-        const int64_t unit = u0 + threadIdx.x / kLanes;
-        if (unit >= p.units)
+    for (int64_t u0 = (int64_t)blockIdx.x * kUnits; u0 < p.units; u0 += (int64_t)gridDim.x * kUnits) {
+        if (u0 + threadIdx.x / kLanes >= p.units)
             continue;   // whole 16-lane groups drop out: the maximum stays inside a group
         int64_t row, c;
-        unit_place(unit, p.per_row, row, c);
+        unit_place(u0, p.per_row, row, c);
         const int n = left(p.F, c);
         const uint16_t* src = p.gu + row * p.ldgu + c;
         const u32x4_t gv = load_chunk(src, n), uv = load_chunk(src + p.F, n);
@@ -98,13 +96,11 @@ __global__ void __launch_bounds__(256) k_swiglu(SwigluParams p)
 
 __global__ void __launch_bounds__(256) k_swiglu_bwd(SwigluParams p)
 {
-    constexpr int UNITS = 256 / kLanes;
-    for (int64_t u0 = (int64_t)blockIdx.x * UNITS; u0 < p.units; u0 += (int64_t)gridDim.x * UNITS) {
-        const int64_t unit = u0 + threadIdx.x / kLanes;
-        if (unit >= p.units)
+    for (int64_t u0 = (int64_t)blockIdx.x * kUnits; u0 < p.units; u0 += (int64_t)gridDim.x * kUnits) {
+        if (u0 + threadIdx.x / kLanes >= p.units)
             continue;
         int64_t row, c;
-        unit_place(unit, p.per_row, row, c);
+        unit_place(u0, p.per_row, row, c);
         const int n = left(p.F, c);
         const uint16_t* src = p.gu + row * p.ldgu + c;
         const u32x4_t gv = load_chunk(src, n), uv = load_chunk(src + p.F, n);
