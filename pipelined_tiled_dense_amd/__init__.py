@@ -10,10 +10,12 @@ import importlib
 
 _FROM_BINDING = ("gemm", "gemm_fp8", "quantize_fp8", "rms_norm", "rms_norm_backward", "swiglu", "swiglu_backward",
                  "RmsNorm", "GemmError", "SYNC_MODES")
-__all__ = ["binding", "inputs", *_FROM_BINDING]
+__all__ = ["binding", "inputs", "mlp", *_FROM_BINDING, "FeedForward"]
 
 
 def __getattr__(name):
     if name in _FROM_BINDING:
         return getattr(importlib.import_module(__name__ + ".binding"), name)
+    if name == "FeedForward":
+        return importlib.import_module(__name__ + ".mlp").FeedForward
     raise AttributeError(name)
