@@ -95,6 +95,19 @@ __device__ __forceinline__ f32x4_t block_sums(const Fp8Frag<true>& b, const Fp8F
     return d;
 }
 
+// Two blocks against one: the two chains of dependent MFMAs take turns, so that
+// neither waits for its own last result.
+__device__ __forceinline__ void block_sums2(f32x4_t& d0, f32x4_t& d1, const Fp8Frag<true>& b0, const Fp8Frag<true>& b1,
+                                            const Fp8Frag<true>& a)
+{
+    d0 = d1 = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        d0 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b0.v[i], a.v[i], d0, 0, 0, 0);
+        d1 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b1.v[i], a.v[i], d1, 0, 0, 0);
+    }
+}
+
 // 4 consecutive values of a row of C at column n (any alignment).
 __device__ __forceinline__ void store_c4(const Fp8Params& q, int64_t m, int64_t n, int64_t N, f32x4_t v)
 {
@@ -352,21 +365,28 @@ __global__ void __launch_bounds__(C::THREADS, 2) k_gemm_fp8(Params p, Fp8Params 
     for (int j = 0; j < C::FN; ++j)
         read_b(0, j);
 
-    // The MFMAs of a k-step go by pairs of fragment rows, column by column.  So in
-    // the last pair a fragment of B has its last use two MFMAs before the next
-    // one's, and its successor, the next k-step's, is read in between; it is
-    // needed only after as many MFMAs, 2 * FN, whose time covers the read.  A's
-    // fragments are read a pair ahead.  The barrier stands before the last pair:
-    // by then the wave has read every fragment of the stage, so the stage can be
+    // The k-step's schedule, NM slots of one block product each.  Both ways:
+    // the barrier stands before the last two fragment rows' slots (TAIL); by
+    // then the wave has read every fragment of the stage, so the stage can be
     // refilled and the next one be read.  The refill's loads go out one every
-    // GAP MFMAs, into the next k-step.
+    // GAP slots, into the next k-step.  A's fragments are read two rows ahead.
+    // The partial sums of slot n are added to the running sums LAG slots later,
+    // when they are sure to be there; the last LAG of a k-step in the next one,
+    // with the scales they belong to (`held`).
     //
-    // The partial sums of MFMA n are added to the running sums after MFMA n +
-    // LAG, when they are sure to be there; the last LAG of a k-step in the next
-    // one, with the scales they belong to (`held`).
-    constexpr int NM = C::FM * C::FN, PAIR = 2 * C::FN, TAIL = NM - PAIR, LAG = 3, RING = 4, GAP = 2;
-    constexpr auto row_of = [](int n) { return n / PAIR * 2 + n % 2; };
-    constexpr auto col_of = [](int n) { return n % PAIR / 2; };
+    // Fast: pairs of fragment rows, column by column.  So in the last pair a
+    // fragment of B has its last use two MFMAs before the next one's, and its
+    // successor, the next k-step's, is read in between; it is needed only after
+    // as many MFMAs, 2 * FN, whose time covers the read.
+    //
+    // Exact: row by row, two columns at a time (block_sums2).  A fragment is
+    // converted when its predecessor has had its last use and before its own
+    // first: A's next row during a row, B's first two columns at the end of a
+    // k-step and its last two at the start of the next.
+    constexpr int NM = C::FM * C::FN, PAIR = 2 * C::FN, TAIL = NM - PAIR, LAG = EXACT ? 2 : 3, RING = 4, GAP = 2;
+    constexpr auto row_of = [](int n) { return EXACT ? n / C::FN : n / PAIR * 2 + n % 2; };
+    constexpr auto col_of = [](int n) { return EXACT ? n % C::FN : n % PAIR / 2; };
+    static_assert(C::FN == 4, "B's fragments are converted in halves of a row");
     // The load that goes out at MFMA n, counted from the barrier on; none: -1.
     constexpr auto load_at = [](int n) {
         const int t = n >= TAIL ? n - TAIL : n + PAIR;
@@ -381,6 +401,7 @@ __global__ void __launch_bounds__(C::THREADS, 2) k_gemm_fp8(Params p, Fp8Params 
     Fp8Frag<EXACT> bf[C::FN], af[2];
     if constexpr (EXACT) {
         bf[0] = Fp8Frag<EXACT>(br[0].lo, br[0].hi);
+        bf[1] = Fp8Frag<EXACT>(br[1].lo, br[1].hi);
         af[0] = Fp8Frag<EXACT>(ar[0].lo, ar[0].hi);
     }
     int s = 0;
@@ -415,36 +436,32 @@ __global__ void __launch_bounds__(C::THREADS, 2) k_gemm_fp8(Params p, Fp8Params 
                     bf[j] = Fp8Frag<EXACT>(br[j].lo, br[j].hi);
             }
             float sc[C::FM];
-            // One slot of the schedule: an MFMA, what is loaded beside it, and
-            // the sums of an earlier MFMA.
+            // One slot of the schedule: a block product (two of them in every
+            // other slot of the exact way), what is loaded beside it, and the sums
+            // of an earlier one.
             auto slot = [&]<int n>() {
                 constexpr int i = row_of(n), j = col_of(n), f = load_at(n);
-                if constexpr (!EXACT && j == 0)
-                    af[i & 1] = Fp8Frag<EXACT>(ar[i & 3].lo, ar[i & 3].hi);
-                part[n % RING] = block_sums(bf[j], af[i & 1]);
-                if constexpr (!EXACT) {
-                    __builtin_amdgcn_sched_barrier(0);
+                if constexpr (EXACT) {
+                    if constexpr (n % 2 == 0)
+                        block_sums2(part[n % RING], part[(n + 1) % RING], bf[j], bf[j + 1], af[i & 1]);
+                    if constexpr (j == 1)
+                        af[(i + 1) & 1].template convert<0>(ar[(i + 1) & 3].lo);
+                    if constexpr (j == 3)
+                        af[(i + 1) & 1].template convert<1>(ar[(i + 1) & 3].hi);
+                    if constexpr (n < 2)
+                        bf[n + 2] = Fp8Frag<EXACT>(br[n + 2].lo, br[n + 2].hi);
+                    if constexpr (n >= NM - 2)
+                        bf[n - (NM - 2)] = Fp8Frag<EXACT>(br[n - (NM - 2)].lo, br[n - (NM - 2)].hi);
                 } else {
-                    // Fragments are converted a few MFMAs before their use, when
-                    // their predecessors have had theirs: B's next column in the
-                    // first pair, A's rows about the turn of each pair.
-                    if constexpr (n < PAIR && j + 1 < C::FN) {
-                        if constexpr (n % 2 == 0)
-                            bf[j + 1].template convert<0>(br[j + 1].lo);
-                        else
-                            bf[j + 1].template convert<1>(br[j + 1].hi);
-                    }
-                    if constexpr (n == NM - 2)
-                        bf[0] = Fp8Frag<EXACT>(br[0].lo, br[0].hi);
-                    if constexpr (n % PAIR == PAIR - 1)
-                        af[0] = Fp8Frag<EXACT>(ar[(i + 1) & 3].lo, ar[(i + 1) & 3].hi);
-                    if constexpr (n % PAIR == 0)
-                        af[1] = Fp8Frag<EXACT>(ar[(i + 1) & 3].lo, ar[(i + 1) & 3].hi);
+                    if constexpr (j == 0)
+                        af[i & 1] = Fp8Frag<EXACT>(ar[i & 3].lo, ar[i & 3].hi);
+                    part[n % RING] = block_sums(bf[j], af[i & 1]);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
                 if constexpr (j == 0)
                     read_a(n < TAIL ? s : s ^ 1, (i + 2) % C::FM);
                 if constexpr (n >= TAIL && n % 2 == 1)
-                    read_b(s ^ 1, j);
+                    read_b(s ^ 1, (n - TAIL) / 2);
                 if constexpr (f >= 0)
                     ld.fire(ld.cur, f, stage_at(n < TAIL ? s ^ 1 : s), w);
                 // The step's scales: read at its start, needed LAG MFMAs on.
@@ -459,15 +476,17 @@ __global__ void __launch_bounds__(C::THREADS, 2) k_gemm_fp8(Params p, Fp8Params 
                     add(n - LAG, sc[row_of(n - LAG)], sbr[ROWB ? col_of(n - LAG) : 0]);
                 else if constexpr (!ROWB)
                     add(NM - LAG + n, held[row_of(NM - LAG + n) & 1], f32x4_t{});
-                if constexpr (EXACT) {
-                    // Four dependent MFMAs with the vector work between them.
+                if constexpr (!EXACT) {
+                    __builtin_amdgcn_sched_barrier(0);
+                } else if constexpr (n % 2 == 1) {
+                    // The two slots' 8 MFMAs with the vector work between them.
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
+                    for (int x = 0; x < 8; ++x) {
                         __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-                        __builtin_amdgcn_sched_group_barrier(0x002, 6, 0);
+                        __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
                     }
+                    __builtin_amdgcn_sched_barrier(0);
                 }
-                __builtin_amdgcn_sched_barrier(0);
             };
             [&]<int... NS>(std::integer_sequence<int, NS...>) {
                 (slot.template operator()<NS>(), ...);
