@@ -57,27 +57,23 @@ struct Fp8Frag {
     }
 };
 
+// 8 e4m3 bytes as bf16.
+__device__ __forceinline__ bf16x8_t bf16_of(uint32_t w0, uint32_t w1)
+{
+    const bf16x2_t a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, 1.0f, false);
+    const bf16x2_t b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, 1.0f, true);
+    const bf16x2_t c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, 1.0f, false);
+    const bf16x2_t d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, 1.0f, true);
+    return bf16x8_t{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
 template <>
 struct Fp8Frag<true> {
     bf16x8_t v[4];
     __device__ __forceinline__ Fp8Frag() {}
     __device__ __forceinline__ Fp8Frag(u32x4_t lo, u32x4_t hi)
+        : v{bf16_of(lo[0], lo[1]), bf16_of(lo[2], lo[3]), bf16_of(hi[0], hi[1]), bf16_of(hi[2], hi[3])}
     {
-        convert<0>(lo);
-        convert<1>(hi);
-    }
-    // Half HALF of the fragment from its 16 bytes.
-    template <int HALF>
-    __device__ __forceinline__ void convert(u32x4_t x)
-    {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const bf16x2_t a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[2 * i], 1.0f, false);
-            const bf16x2_t b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[2 * i], 1.0f, true);
-            const bf16x2_t c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[2 * i + 1], 1.0f, false);
-            const bf16x2_t d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[2 * i + 1], 1.0f, true);
-            v[2 * HALF + i] = bf16x8_t{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
-        }
     }
 };
 
@@ -93,19 +89,6 @@ __device__ __forceinline__ f32x4_t block_sums(const Fp8Frag<true>& b, const Fp8F
     for (int i = 0; i < 4; ++i)
         d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b.v[i], a.v[i], d, 0, 0, 0);
     return d;
-}
-
-// Two blocks against one: the two chains of dependent MFMAs take turns, so that
-// neither waits for its own last result.
-__device__ __forceinline__ void block_sums2(f32x4_t& d0, f32x4_t& d1, const Fp8Frag<true>& b0, const Fp8Frag<true>& b1,
-                                            const Fp8Frag<true>& a)
-{
-    d0 = d1 = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        d0 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b0.v[i], a.v[i], d0, 0, 0, 0);
-        d1 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b1.v[i], a.v[i], d1, 0, 0, 0);
-    }
 }
 
 // 4 consecutive values of a row of C at column n (any alignment).
@@ -139,16 +122,21 @@ __device__ __forceinline__ void store_c4(const Fp8Params& q, int64_t m, int64_t 
 // ---------------------------------------------------------------------------
 // Large products: 128-byte k-steps through the two-stage LDS ring.
 // ---------------------------------------------------------------------------
-template <int BM, int BN, int WM, int WN>
-using Fp8Cfg = Cfg<BM, BN, 64, 2, WM, WN, SYNC_BARRIER, true, 0, false, 16>;
+template <int BM, int BN, int WM, int WN, int MF = 16>
+using Fp8Cfg = Cfg<BM, BN, 64, 2, WM, WN, SYNC_BARRIER, true, 0, false, MF>;
 
-// The column of the wave's tile that MFMA row i of fragment j holds: a lane's 4
-// rows of each fragment follow one another, so that the lane ends up with 4 * FN
-// consecutive columns of C.
+// The column of a wave's strip that LDS row `row` of the strip holds.  An MFMA
+// leaves a lane 4 consecutive rows of B's fragment at a time (16 x 16: rows 4 g
+// .. of each fragment; 32 x 32: rows 8 q + 4 h .. for q = 0 .. 3).  The map
+// strings them together, so that a lane ends up with RUN consecutive columns of
+// C: 4 of each of the FN fragments, or the 16 of one.
 template <class C>
-__device__ __forceinline__ int fp8_col(int j, int i)
+__device__ __forceinline__ int fp8_col(int row)
 {
-    return (i >> 2) * (4 * C::FN) + j * 4 + (i & 3);
+    if constexpr (C::MF == 32)
+        return (row & ~31) + ((row >> 2) & 1) * 16 + ((row >> 3) & 3) * 4 + (row & 3);
+    else
+        return ((row & 15) >> 2) * (4 * C::FN) + (row >> 4) * 4 + (row & 3);
 }
 
 // The load stream of one workgroup: positions (output tile, k-step), each an A
@@ -176,14 +164,14 @@ struct Fp8Loader {
     // periods of the swizzle), a scalar distance for A and, fp8_col being
     // additive in them, for B.
     static constexpr int RSTEP = C::NLW * 8;
-    static_assert(RSTEP % 16 == 0 && (RSTEP % C::TN == 0 || C::TN % RSTEP == 0), "loads of a lane");
+    static_assert(RSTEP % C::MF == 0 && (RSTEP % C::TN == 0 || C::TN % RSTEP == 0), "loads of a lane");
     uint32_t voffA, voffB, voffS;
     uint32_t ldaB, ldbB;                    // row strides in bytes
     int32_t kofs;                           // of the lane's chunk within the k-step, bytes
     static constexpr int rows_a(int t) { return t * RSTEP; }
     static constexpr int cols_b(int t)
     {
-        return RSTEP % C::TN == 0 ? t * RSTEP : t * RSTEP / C::TN * C::TN + t * RSTEP % C::TN / 16 * 4;
+        return C::MF == 32 || RSTEP % C::TN == 0 ? t * RSTEP : t * RSTEP / C::TN * C::TN + t * RSTEP % C::TN / 16 * 4;
     }
     struct Position {
         const char* a;
@@ -202,12 +190,12 @@ struct Fp8Loader {
         const int row = w * 8 + lane / 8;
         kofs = ((lane % 8) ^ swz_k<64>(row)) * 16;
         voffA = (uint32_t)row * ldaB + (uint32_t)kofs;
-        voffB = (uint32_t)(row / C::TN * C::TN + fp8_col<C>(row % C::TN / 16, row & 15)) * ldbB + (uint32_t)kofs;
+        voffB = (uint32_t)(row / C::TN * C::TN + fp8_col<C>(row % C::TN)) * ldbB + (uint32_t)kofs;
         const bool a = w < AW;
         // A's scales in the order a lane reads them: word FM * r + i of a wave's
-        // rows holds row 16 * i + r.
+        // rows holds row MF * i + r.
         const int at = (a ? w : w - AW) * 64 + lane, in = at % C::TM;
-        voffS = (uint32_t)(a ? at - in + in % C::FM * 16 + in / C::FM : at >> q.sb_shift) * 4u;
+        voffS = (uint32_t)(a ? at - in + in % C::FM * C::MF + in / C::FM : at >> q.sb_shift) * 4u;
         sstep = (a ? q.ldsa : q.ldsb) * 4;
     }
 
@@ -268,34 +256,36 @@ struct Fp8Loader {
     }
 };
 
-// Columns of C that lane group g of a wave holds of one row: 4 * FN consecutive
-// ones from n on.
-template <class C>
-__device__ __forceinline__ void store_row(const Fp8Params& q, int64_t m, int64_t n, int64_t N, const f32x4_t (&v)[C::FN])
+// 16 consecutive columns of a row of C from n on: v(x) is the x-th 4 of them.
+template <class V>
+__device__ __forceinline__ void store_c16(const Fp8Params& q, int64_t m, int64_t n, int64_t N, V&& v)
 {
-    if (n + 4 * C::FN <= N) {
+    if (n + 16 <= N) {
         if (q.c_fp32) {
             float* c = (float*)q.c + m * q.ldc + n;
 #pragma unroll
-            for (int j = 0; j < C::FN; ++j)
-                __builtin_memcpy(c + j * 4, &v[j], 16);
+            for (int x = 0; x < 4; ++x) {
+                const f32x4_t y = v(x);
+                __builtin_memcpy(c + x * 4, &y, 16);
+            }
         } else {
             uint16_t* c = (uint16_t*)q.c + m * q.ldc + n;
 #pragma unroll
-            for (int j = 0; j < C::FN; j += 2) {
-                const u32x4_t x = {pack_bf16x2(v[j][0], v[j][1]), pack_bf16x2(v[j][2], v[j][3]),
-                                   pack_bf16x2(v[j + 1][0], v[j + 1][1]), pack_bf16x2(v[j + 1][2], v[j + 1][3])};
-                __builtin_memcpy(c + j * 4, &x, 16);
+            for (int x = 0; x < 4; x += 2) {
+                const f32x4_t y = v(x), z = v(x + 1);
+                const u32x4_t w = {pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(z[0], z[1]),
+                                   pack_bf16x2(z[2], z[3])};
+                __builtin_memcpy(c + x * 4, &w, 16);
             }
         }
     } else {
 #pragma unroll
-        for (int j = 0; j < C::FN; ++j)
-            store_c4(q, m, n + j * 4, N, v[j]);
+        for (int x = 0; x < 4; ++x)
+            store_c4(q, m, n + x * 4, N, v(x));
     }
 }
 
-template <class C, bool ROWB, bool EXACT>
+template <class C, bool ROWB>
 __global__ void __launch_bounds__(C::THREADS, 2) k_gemm_fp8(Params p, Fp8Params q)
 {
     using LD = Fp8Loader<C>;
@@ -365,28 +355,21 @@ __global__ void __launch_bounds__(C::THREADS, 2) k_gemm_fp8(Params p, Fp8Params 
     for (int j = 0; j < C::FN; ++j)
         read_b(0, j);
 
-    // The k-step's schedule, NM slots of one block product each.  Both ways:
-    // the barrier stands before the last two fragment rows' slots (TAIL); by
-    // then the wave has read every fragment of the stage, so the stage can be
+    // The MFMAs of a k-step go by pairs of fragment rows, column by column.  So in
+    // the last pair a fragment of B has its last use two MFMAs before the next
+    // one's, and its successor, the next k-step's, is read in between; it is
+    // needed only after as many MFMAs, 2 * FN, whose time covers the read.  A's
+    // fragments are read a pair ahead.  The barrier stands before the last pair:
+    // by then the wave has read every fragment of the stage, so the stage can be
     // refilled and the next one be read.  The refill's loads go out one every
-    // GAP slots, into the next k-step.  A's fragments are read two rows ahead.
-    // The partial sums of slot n are added to the running sums LAG slots later,
-    // when they are sure to be there; the last LAG of a k-step in the next one,
-    // with the scales they belong to (`held`).
+    // GAP MFMAs, into the next k-step.
     //
-    // Fast: pairs of fragment rows, column by column.  So in the last pair a
-    // fragment of B has its last use two MFMAs before the next one's, and its
-    // successor, the next k-step's, is read in between; it is needed only after
-    // as many MFMAs, 2 * FN, whose time covers the read.
-    //
-    // Exact: row by row, two columns at a time (block_sums2).  A fragment is
-    // converted when its predecessor has had its last use and before its own
-    // first: A's next row during a row, B's first two columns at the end of a
-    // k-step and its last two at the start of the next.
-    constexpr int NM = C::FM * C::FN, PAIR = 2 * C::FN, TAIL = NM - PAIR, LAG = EXACT ? 2 : 3, RING = 4, GAP = 2;
-    constexpr auto row_of = [](int n) { return EXACT ? n / C::FN : n / PAIR * 2 + n % 2; };
-    constexpr auto col_of = [](int n) { return EXACT ? n % C::FN : n % PAIR / 2; };
-    static_assert(C::FN == 4, "B's fragments are converted in halves of a row");
+    // The partial sums of MFMA n are added to the running sums after MFMA n +
+    // LAG, when they are sure to be there; the last LAG of a k-step in the next
+    // one, with the scales they belong to (`held`).
+    constexpr int NM = C::FM * C::FN, PAIR = 2 * C::FN, TAIL = NM - PAIR, LAG = 3, RING = 4, GAP = 2;
+    constexpr auto row_of = [](int n) { return n / PAIR * 2 + n % 2; };
+    constexpr auto col_of = [](int n) { return n % PAIR / 2; };
     // The load that goes out at MFMA n, counted from the barrier on; none: -1.
     constexpr auto load_at = [](int n) {
         const int t = n >= TAIL ? n - TAIL : n + PAIR;
@@ -398,12 +381,7 @@ __global__ void __launch_bounds__(C::THREADS, 2) k_gemm_fp8(Params p, Fp8Params 
         ((load_at(TAIL + NS) >= 0 ? ld.fire(ld.cur, load_at(TAIL + NS), stage_at(1), w) : (void)0), ...);
     }(std::make_integer_sequence<int, PAIR>{});
     f32x4_t part[RING];
-    Fp8Frag<EXACT> bf[C::FN], af[2];
-    if constexpr (EXACT) {
-        bf[0] = Fp8Frag<EXACT>(br[0].lo, br[0].hi);
-        bf[1] = Fp8Frag<EXACT>(br[1].lo, br[1].hi);
-        af[0] = Fp8Frag<EXACT>(ar[0].lo, ar[0].hi);
-    }
+    Fp8Frag<false> bf[C::FN], af[2];
     int s = 0;
     for (int32_t it = 0; it < n_tiles; ++it) {
         int32_t tm, tn, sp, u;
@@ -430,34 +408,18 @@ __global__ void __launch_bounds__(C::THREADS, 2) k_gemm_fp8(Params p, Fp8Params 
         // would then be for everything instead of for the fragments they need.
         wait_lgkm0();
         for (int32_t kt = 0; kt < p.k_steps; ++kt) {
-            if constexpr (!EXACT) {
 #pragma unroll
-                for (int j = 0; j < C::FN; ++j)
-                    bf[j] = Fp8Frag<EXACT>(br[j].lo, br[j].hi);
-            }
+            for (int j = 0; j < C::FN; ++j)
+                bf[j] = Fp8Frag<false>(br[j].lo, br[j].hi);
             float sc[C::FM];
-            // One slot of the schedule: a block product (two of them in every
-            // other slot of the exact way), what is loaded beside it, and the sums
-            // of an earlier one.
+            // One slot of the schedule: an MFMA, what is loaded beside it, and
+            // the sums of an earlier MFMA.
             auto slot = [&]<int n>() {
                 constexpr int i = row_of(n), j = col_of(n), f = load_at(n);
-                if constexpr (EXACT) {
-                    if constexpr (n % 2 == 0)
-                        block_sums2(part[n % RING], part[(n + 1) % RING], bf[j], bf[j + 1], af[i & 1]);
-                    if constexpr (j == 1)
-                        af[(i + 1) & 1].template convert<0>(ar[(i + 1) & 3].lo);
-                    if constexpr (j == 3)
-                        af[(i + 1) & 1].template convert<1>(ar[(i + 1) & 3].hi);
-                    if constexpr (n < 2)
-                        bf[n + 2] = Fp8Frag<EXACT>(br[n + 2].lo, br[n + 2].hi);
-                    if constexpr (n >= NM - 2)
-                        bf[n - (NM - 2)] = Fp8Frag<EXACT>(br[n - (NM - 2)].lo, br[n - (NM - 2)].hi);
-                } else {
-                    if constexpr (j == 0)
-                        af[i & 1] = Fp8Frag<EXACT>(ar[i & 3].lo, ar[i & 3].hi);
-                    part[n % RING] = block_sums(bf[j], af[i & 1]);
-                    __builtin_amdgcn_sched_barrier(0);
-                }
+                if constexpr (j == 0)
+                    af[i & 1] = Fp8Frag<false>(ar[i & 3].lo, ar[i & 3].hi);
+                part[n % RING] = block_sums(bf[j], af[i & 1]);
+                __builtin_amdgcn_sched_barrier(0);
                 if constexpr (j == 0)
                     read_a(n < TAIL ? s : s ^ 1, (i + 2) % C::FM);
                 if constexpr (n >= TAIL && n % 2 == 1)
@@ -476,17 +438,7 @@ __global__ void __launch_bounds__(C::THREADS, 2) k_gemm_fp8(Params p, Fp8Params 
                     add(n - LAG, sc[row_of(n - LAG)], sbr[ROWB ? col_of(n - LAG) : 0]);
                 else if constexpr (!ROWB)
                     add(NM - LAG + n, held[row_of(NM - LAG + n) & 1], f32x4_t{});
-                if constexpr (!EXACT) {
-                    __builtin_amdgcn_sched_barrier(0);
-                } else if constexpr (n % 2 == 1) {
-                    // The two slots' 8 MFMAs with the vector work between them.
-#pragma unroll
-                    for (int x = 0; x < 8; ++x) {
-                        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-                        __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
-                    }
-                    __builtin_amdgcn_sched_barrier(0);
-                }
+                __builtin_amdgcn_sched_barrier(0);
             };
             [&]<int... NS>(std::integer_sequence<int, NS...>) {
                 (slot.template operator()<NS>(), ...);
@@ -518,18 +470,189 @@ __global__ void __launch_bounds__(C::THREADS, 2) k_gemm_fp8(Params p, Fp8Params 
                 add(n, held[row_of(n) & 1], f32x4_t{});
         }
         if (p.splits > 1) {
+            // Fragments of rows past M are not stored (nor read back).
             float* part = p.partial + (int64_t)(sp * p.span + u) * (C::BM * C::BN);
+            const int64_t left = p.M - ((int64_t)tm * C::BM + wm * C::TM);
 #pragma unroll
             for (int i = 0; i < C::FM; ++i)
 #pragma unroll
                 for (int j = 0; j < C::FN; ++j)
-                    *(f32x4_t*)(part + (((w * C::FM + i) * C::FN + j) * 64 + lane) * 4) = acc[i][j];
+                    if (i * C::MF < left)
+                        *(f32x4_t*)(part + (((w * C::FM + i) * C::FN + j) * 64 + lane) * 4) = acc[i][j];
         } else {
 #pragma unroll
             for (int i = 0; i < C::FM; ++i) {
                 const int64_t m = (int64_t)tm * C::BM + wm * C::TM + i * 16 + r16;
                 if (m < p.M)
-                    store_row<C>(q, m, (int64_t)tn * C::BN + wn * C::TN + g * (4 * C::FN), p.N, acc[i]);
+                    store_c16(q, m, (int64_t)tn * C::BN + wn * C::TN + g * 16, p.N, [&](int x) { return acc[i][x]; });
+            }
+        }
+    }
+    wait_vmcnt<0>();   // the last, empty position's loads still write LDS
+    clock_end(p);
+}
+
+// The exact way: 128 x 128 tiles, 4 waves of 64 x 64 each, two workgroups on a
+// compute unit.  What bounds it is instruction issue: beside its MFMAs, each of
+// which takes about 11 clocks of its SIMD's vector issue, a k-step costs a wave
+// 128 conversions and 64 or, with row scales, 128 scalings (0.47 MFMA busy at
+// 8192^3 with row scales, 0.54 with block scales; the same kernel with a quarter
+// of the MFMAs and conversions takes 63% of the time, without its loads 80%).
+// One wave's conversions overlap another's MFMAs through the two workgroups,
+// which do not wait for each other; spreading them between the MFMAs of 16 x 16
+// fragments by hand gave the same time (1040 us against 1060 at 8192^3).  A
+// k-step goes in two halves of 64, so that the converted fragments of a half,
+// the partial sums and the running sums fit the wave's 256 registers.
+template <class C, bool ROWB>
+__global__ void __launch_bounds__(C::THREADS, 2) k_gemm_fp8_exact(Params p, Fp8Params q)
+{
+    using LD = Fp8Loader<C>;
+    static_assert(C::MF == 32, "32 x 32 MFMAs");
+    __shared__ __attribute__((aligned(1024))) char smem_raw[C::RING_BYTES + 2 * LD::SCALE_BYTES];
+    lds_char* smem = (lds_char*)smem_raw;
+    const int lane = threadIdx.x & 63, r32 = lane & 31, h = lane >> 5;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = w / C::WN, wn = w % C::WN;
+
+    const int32_t G = gridDim.x, b = blockIdx.x;
+    const int32_t n_tiles = (b < p.tiles) ? (p.tiles - 1 - b) / G + 1 : 0;
+    if (n_tiles == 0)
+        return;
+    clock_begin(p);
+    LD ld;
+    ld.init(p, q, w, lane);
+    ld.cur = ld.first(p, q, 0, n_tiles, w);
+    auto stage_at = [&](int st) { return smem + st * C::STAGE_BYTES; };
+    auto scales_at = [&](int st) { return smem + C::RING_BYTES + st * LD::SCALE_BYTES; };
+    auto fire_all = [&](int st) {
+        ld.fire_scales(ld.cur, scales_at(st), w);
+#pragma unroll
+        for (int t = 0; t < C::LOADS; ++t)
+            ld.fire(ld.cur, t, stage_at(st), w);
+    };
+
+    // Lane (r32, h) reads chunks 4 k + 2 h and the next one of row r32 in half k.
+    const int swz = swz_k<64>(r32);
+    uint32_t at[2][2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+            at[k][x] = (uint32_t)r32 * 128u + (uint32_t)(((4 * k + 2 * h + x) ^ swz) * 16);
+    struct Raw {
+        u32x4_t lo, hi;
+    };
+    auto read = [&](const lds_char* t, int k) {
+        return Raw{*(const LDS_AS u32x4_t*)(t + at[k][0]), *(const LDS_AS u32x4_t*)(t + at[k][1])};
+    };
+
+    fire_all(0);
+    int s = 0;
+    for (int32_t it = 0; it < n_tiles; ++it) {
+        int32_t tm, tn, sp, u;
+        tile_coords(p, b + it * G, G, tm, tn, sp, u);
+        ld.nxt = ld.first(p, q, it + 1, n_tiles, w);
+        f32x16_t acc[C::FM][C::FN];
+#pragma unroll
+        for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+            for (int j = 0; j < C::FN; ++j)
+                acc[i][j] = f32x16_t{};
+        for (int32_t kt = 0; kt < p.k_steps; ++kt) {
+            // As in the fast kernel: this position has landed and the other
+            // stage has been read, in every wave.
+            wait_vmcnt<0>();
+            wait_lgkm0();
+            block_barrier();
+            ld.step(kt == p.k_steps - 1);
+            fire_all(s ^ 1);
+            const lds_char* ta = stage_at(s) + wm * C::TM * 128;
+            const lds_char* tb = stage_at(s) + C::A_BYTES + wn * C::TN * 128;
+            f32x16_t part[C::FM][C::FN];
+            Raw ar[C::FM], br[C::FN];
+#pragma unroll
+            for (int i = 0; i < C::FM; ++i)
+                ar[i] = read(ta + i * 4096, 0);
+#pragma unroll
+            for (int j = 0; j < C::FN; ++j)
+                br[j] = read(tb + j * 4096, 0);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                Fp8Frag<true> af[C::FM], bf[C::FN];
+#pragma unroll
+                for (int i = 0; i < C::FM; ++i)
+                    af[i] = Fp8Frag<true>(ar[i].lo, ar[i].hi);
+#pragma unroll
+                for (int j = 0; j < C::FN; ++j)
+                    bf[j] = Fp8Frag<true>(br[j].lo, br[j].hi);
+                __builtin_amdgcn_sched_barrier(0);
+                if (k == 0) {
+#pragma unroll
+                    for (int i = 0; i < C::FM; ++i)
+                        ar[i] = read(ta + i * 4096, 1);
+#pragma unroll
+                    for (int j = 0; j < C::FN; ++j)
+                        br[j] = read(tb + j * 4096, 1);
+                }
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+#pragma unroll
+                    for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+                        for (int j = 0; j < C::FN; ++j)
+                            part[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                                bf[j].v[x], af[i].v[x], k == 0 && x == 0 ? f32x16_t{} : part[i][j], 0, 0, 0);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            // A's scales: one for each of the lane's rows.  B's: one, or those of
+            // the lane's 16 columns in each fragment.
+            const lds_f32* sa = (const lds_f32*)scales_at(s) + wm * C::TM + r32 * C::FM;
+            const lds_f32* sb = (const lds_f32*)scales_at(s) + C::BM + wn * C::TN;
+            float sai[C::FM];
+#pragma unroll
+            for (int i = 0; i < C::FM; ++i)
+                sai[i] = ROWB ? sa[i] : sa[i] * sb[0];
+#pragma unroll
+            for (int j = 0; j < C::FN; ++j) {
+                f32x4_t sbj[ROWB ? 4 : 1];
+                if constexpr (ROWB) {
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        sbj[x] = *(const LDS_AS f32x4_t*)(sb + j * 32 + h * 16 + x * 4);
+                }
+#pragma unroll
+                for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        acc[i][j][e] = __builtin_fmaf(ROWB ? part[i][j][e] * sbj[e / 4][e % 4] : part[i][j][e], sai[i],
+                                                      acc[i][j][e]);
+            }
+            s ^= 1;
+        }
+        if (p.splits > 1) {
+            float* out = p.partial + (int64_t)(sp * p.span + u) * (C::BM * C::BN);
+            const int64_t left = p.M - ((int64_t)tm * C::BM + wm * C::TM);
+#pragma unroll
+            for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+                for (int j = 0; j < C::FN; ++j)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        if (i * C::MF < left)
+                            *(f32x4_t*)(out + ((((w * C::FM + i) * C::FN + j) * 4 + x) * 64 + lane) * 4) =
+                            f32x4_t{acc[i][j][4 * x], acc[i][j][4 * x + 1], acc[i][j][4 * x + 2], acc[i][j][4 * x + 3]};
+        } else {
+#pragma unroll
+            for (int i = 0; i < C::FM; ++i) {
+                const int64_t m = (int64_t)tm * C::BM + wm * C::TM + i * 32 + r32;
+                if (m < p.M) {
+#pragma unroll
+                    for (int j = 0; j < C::FN; ++j)
+                        store_c16(q, m, (int64_t)tn * C::BN + wn * C::TN + j * 32 + h * 16, p.N, [&](int x) {
+                            return f32x4_t{acc[i][j][4 * x], acc[i][j][4 * x + 1], acc[i][j][4 * x + 2],
+                                           acc[i][j][4 * x + 3]};
+                        });
+                }
             }
         }
     }
@@ -538,7 +661,8 @@ __global__ void __launch_bounds__(C::THREADS, 2) k_gemm_fp8(Params p, Fp8Params 
 }
 
 // Sums the k chunks' partial tiles in chunk order and stores C.  A thread takes
-// 4 consecutive columns, in the order the partial tiles are stored in.
+// 4 consecutive columns, in the order the partial tiles are stored in: the
+// waves' fragments, for 32 x 32 MFMAs 4 quarters each, then the lanes.
 template <class C>
 __global__ void __launch_bounds__(256) k_reduce_fp8(Params p, Fp8Params q)
 {
@@ -547,16 +671,20 @@ __global__ void __launch_bounds__(256) k_reduce_fp8(Params p, Fp8Params q)
     for (int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x; id < total; id += (int64_t)gridDim.x * 256) {
         const int32_t u = (int32_t)(id / QUADS);
         const int at = (int)(id % QUADS);
+        constexpr int QF = C::MF == 32 ? 4 : 1;
+        const int lane = at & 63, x = at / 64 % QF, f = at / (64 * QF);
+        const int j = f % C::FN, i = f / C::FN % C::FM, w = f / (C::FN * C::FM);
+        int32_t tm, tn;
+        raster_tile(p, u, tm, tn);
+        const int64_t m = (int64_t)tm * C::BM + w / C::WN * C::TM + i * C::MF + lane % C::MF;
+        const int64_t n = (int64_t)tn * C::BN + w % C::WN * C::TN +
+                          (C::MF == 32 ? j * 32 + (lane >> 5) * 16 + x * 4 : (lane >> 4) * (4 * C::FN) + j * 4);
+        if (m >= p.M)
+            continue;
         f32x4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
         for (int32_t sp = 0; sp < p.splits; ++sp)
             v += *(const f32x4_t*)(p.partial + (int64_t)(sp * p.span + u) * (C::BM * C::BN) + at * 4);
-        const int lane = at & 63, j = at / 64 % C::FN, i = at / (64 * C::FN) % C::FM, w = at / (64 * C::FN * C::FM);
-        int32_t tm, tn;
-        raster_tile(p, u, tm, tn);
-        const int64_t m = (int64_t)tm * C::BM + w / C::WN * C::TM + i * 16 + (lane & 15);
-        const int64_t n = (int64_t)tn * C::BN + w % C::WN * C::TN + (lane >> 4) * (4 * C::FN) + j * 4;
-        if (m < p.M)
-            store_c4(q, m, n, p.N, v);
+        store_c4(q, m, n, p.N, v);
     }
 }
 
@@ -795,7 +923,7 @@ int64_t tiles_time(const TileTimes& t, int64_t tile, int per_cu, int64_t M, int6
     const int64_t run = items <= cus ? steps * t.alone
                         : per_cu == 1 ? ceil_div(items, cus) * steps * t.alone
                                       : ceil_div(items, 2 * (int64_t)cus) * steps * t.shared;
-    return run + (splits > 1 ? kSplitLaunch + kSplitTile * items : 0);
+    return run + (splits > 1 ? kSplitLaunch + kSplitTile * items * (M < tile ? M : tile) / tile : 0);
 }
 
 // The number of k chunks that is estimated fastest, among those that leave a
@@ -816,7 +944,7 @@ int64_t choose_fp8_splits(const TileTimes& t, int64_t M, int64_t N, int64_t kblo
     return best;
 }
 
-template <class C, bool EXACT>
+template <class C>
 int launch_tiles(Params p, const Fp8Params& q, int64_t splits, int cus, int per_cu, TempMem& tm, hipStream_t s)
 {
     p.tiles_m = (int32_t)((p.M + C::BM - 1) / C::BM);
@@ -846,10 +974,17 @@ int launch_tiles(Params p, const Fp8Params& q, int64_t splits, int cus, int per_
     }
     const dim3 grid((unsigned)(p.tiles < slots ? p.tiles : slots)), block(C::THREADS);
     const bool rowb = q.sb_shift == 0;
-    if (rowb)
-        hipLaunchKernelGGL(HIP_KERNEL_NAME(k_gemm_fp8<C, true, EXACT>), grid, block, 0, s, p, q);
-    else
-        hipLaunchKernelGGL(HIP_KERNEL_NAME(k_gemm_fp8<C, false, EXACT>), grid, block, 0, s, p, q);
+    if constexpr (C::MF == 32) {
+        if (rowb)
+            hipLaunchKernelGGL(HIP_KERNEL_NAME(k_gemm_fp8_exact<C, true>), grid, block, 0, s, p, q);
+        else
+            hipLaunchKernelGGL(HIP_KERNEL_NAME(k_gemm_fp8_exact<C, false>), grid, block, 0, s, p, q);
+    } else {
+        if (rowb)
+            hipLaunchKernelGGL(HIP_KERNEL_NAME(k_gemm_fp8<C, true>), grid, block, 0, s, p, q);
+        else
+            hipLaunchKernelGGL(HIP_KERNEL_NAME(k_gemm_fp8<C, false>), grid, block, 0, s, p, q);
+    }
     int rc = launched();
     if (p.splits > 1) {
         if (rc == GEMM_OK) {
@@ -911,12 +1046,12 @@ int gemm_fp8_direct(int64_t M, int64_t N, const char* A, int64_t lda, const char
     p.ldb = ldb / 2;
     p.clock_on = g_clock_on.load(std::memory_order_relaxed) ? 1u : 0u;
     // The exact way takes 128 x 128 tiles at any size: its fragments are twice
-    // as large, and beside 128 running sums they do not fit a wave's registers.
+    // as large, and beside more running sums they do not fit a wave's registers.
     if (exact)
-        return launch_tiles<Fp8Cfg<128, 128, 2, 2>, true>(p, q, splits, cus, 2, tm, s);
+        return launch_tiles<Fp8Cfg<128, 128, 2, 2, 32>>(p, q, splits, cus, 2, tm, s);
     if (tiles_time(kFast256, 256, 1, M, N, q.kblocks, 1, cus) < time128)
-        return launch_tiles<Fp8Cfg<256, 256, 2, 4>, false>(p, q, 1, cus, 1, tm, s);
-    return launch_tiles<Fp8Cfg<128, 128, 2, 2>, false>(p, q, splits, cus, 2, tm, s);
+        return launch_tiles<Fp8Cfg<256, 256, 2, 4>>(p, q, 1, cus, 1, tm, s);
+    return launch_tiles<Fp8Cfg<128, 128, 2, 2>>(p, q, splits, cus, 2, tm, s);
 }
 
 }  // namespace
