@@ -292,7 +292,8 @@ def _matrix(name, x, dtype):
 
 
 def _shaped(name, x, rows, cols):
-    if x.shape != (rows, cols):
+    r, c = x.shape
+    if r != rows or c != cols:
         raise ValueError("%s must have shape %s, not %s" % (name, (rows, cols), tuple(x.shape)))
 
 
@@ -310,8 +311,9 @@ def _current(torch, x, *others):
     for t in others:
         if t is not None and t.get_device() != d:
             raise ValueError("tensors on different devices: cuda:%d and %s" % (d, t.device))
-    if d != torch.cuda.current_device():
-        raise ValueError("tensors on cuda:%d, but the current device is cuda:%d" % (d, torch.cuda.current_device()))
+    current = torch._C._cuda_getDevice()
+    if d != current:
+        raise ValueError("tensors on cuda:%d, but the current device is cuda:%d" % (d, current))
     return torch._C._cuda_getCurrentRawStream(d)
 
 

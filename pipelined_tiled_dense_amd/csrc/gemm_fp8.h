@@ -348,7 +348,6 @@ __global__ void __launch_bounds__(C::THREADS, 2) k_gemm_fp8(Params p, Fp8Params 
     ld.step(false);
     wait_vmcnt<0>();
     block_barrier();
-    ld.fire_scales(ld.cur, scales_at(1), w);
     read_a(0, 0);
     read_a(0, 1);
 #pragma unroll
@@ -429,6 +428,8 @@ __global__ void __launch_bounds__(C::THREADS, 2) k_gemm_fp8(Params p, Fp8Params 
                 // The step's scales: read at its start, needed LAG MFMAs on.
                 if constexpr (n == 0)
                     read_scales(s);
+                if constexpr (n == TAIL / 2 - 1)
+                    ld.fire_scales(ld.cur, scales_at(s ^ 1), w);
                 if constexpr (n == LAG) {
 #pragma unroll
                     for (int x = 0; x < C::FM; ++x)
@@ -450,7 +451,6 @@ __global__ void __launch_bounds__(C::THREADS, 2) k_gemm_fp8(Params p, Fp8Params 
             wait_lgkm0();
             wait_vmcnt<0>();
             block_barrier();
-            ld.fire_scales(ld.cur, scales_at(s), w);
             [&]<int... NS>(std::integer_sequence<int, NS...>) {
                 (slot.template operator()<TAIL + NS>(), ...);
             }(std::make_integer_sequence<int, PAIR>{});

@@ -354,13 +354,20 @@ int gemm_rms_norm_bwd(int64_t M, int64_t D, const void* dY, int64_t lddy, const 
     int64_t grid = (int64_t)cus * ((8 + rs.nw - 1) / rs.nw);
     if (grid > (M + 3) / 4)
         grid = (M + 3) / 4;
+    // A few rows: one workgroup, whose sums are the weight's gradient, in one launch.
+    if (M <= 8)
+        grid = M > 0 ? 1 : 0;
     void* ws = nullptr;
-    if (M > 0) {
-        rc = temp_take(tm, grid * D * 4, st, &ws);
+    hipEvent_t done = nullptr;
+    if (grid > 1) {
+        rc = temp_take(tm, grid * D * 4, st, &ws, &done);
         if (rc != GEMM_OK)
             return rc;
+    }
+    if (grid > 0) {
         NormBwdParams p{(const uint16_t*)dY, (const uint16_t*)H, (const uint16_t*)weight, rstd, (const uint16_t*)dres,
-                        (uint16_t*)dX, (float*)ws, M, lddy, ldh, lddr, lddx, (int32_t)D, 1.0f / (float)D};
+                        (uint16_t*)dX, grid > 1 ? (float*)ws : dweight, M, lddy, ldh, lddr, lddx, (int32_t)D,
+                        1.0f / (float)D};
         const dim3 g((unsigned)grid), b((unsigned)(rs.nw * 64));
         if (rs.nch == 1)
             hipLaunchKernelGGL(k_rms_norm_bwd<1>, g, b, 0, st, p, rs.nw);
@@ -370,12 +377,13 @@ int gemm_rms_norm_bwd(int64_t M, int64_t D, const void* dY, int64_t lddy, const 
             hipLaunchKernelGGL(k_rms_norm_bwd<4>, g, b, 0, st, p, rs.nw);
         rc = launched();
     }
-    if (rc == GEMM_OK) {
-        hipLaunchKernelGGL(k_norm_weight_grad, dim3((unsigned)((D + 15) / 16)), dim3(1024), 0, st, (const float*)ws,
-                           (int32_t)grid, (int32_t)D, dweight);
+    if (rc == GEMM_OK && grid != 1) {
+        // The shares' last use: its completion records the block's event.
+        hipExtLaunchKernelGGL(k_norm_weight_grad, dim3((unsigned)((D + 15) / 16)), dim3(1024), 0, st, nullptr, done, 0,
+                              (const float*)ws, (int32_t)grid, (int32_t)D, dweight);
         rc = launched();
     }
-    const int frc = temp_give(tm, ws, st);
+    const int frc = temp_give(tm, ws, st, rc == GEMM_OK && done != nullptr);
     return rc != GEMM_OK ? rc : frc;
 }
 
