@@ -696,6 +696,12 @@ __global__ void __launch_bounds__(256) k_reduce_fp8(Params p, Fp8Params q)
 // and add their sums through LDS in wave order.  So every compute unit has loads
 // in flight over the whole of k even where C gives few workgroups, with no
 // second launch.
+//
+// ANY takes operands of any alignment and stride and any K >= 16 (otherwise rows
+// start on 16-byte boundaries and K is a multiple of 16): a chunk that reaches
+// past the row's end is read from its last 16 bytes and shifted into place, so
+// nothing past the row is read, and rows past the matrix repeat its last one,
+// whose sums no one stores.
 // ---------------------------------------------------------------------------
 struct SkinnyParams {
     const char* a;
@@ -706,7 +712,26 @@ struct SkinnyParams {
 
 constexpr int kSkinnyWaves = 8;
 
-template <int MF, int NF, int DEPTH, bool ROWB, bool EXACT>
+// 16 bytes at p (any alignment) without their first `cut`, zeros after the rest;
+// `tail` (uniform) is false where cut is 0 in every lane.
+__device__ __forceinline__ u32x4_t load_from(const char* p, int cut, bool tail)
+{
+    uint64_t x[2];
+    __builtin_memcpy(x, p, 16);
+    if (tail) {
+        const int s = (cut & 7) * 8;
+        const uint64_t lo = cut >= 8 ? x[1] : x[0], hi = cut >= 8 ? 0u : x[1];
+        x[0] = s ? (lo >> s) | (hi << (64 - s)) : lo;
+        x[1] = hi >> s;
+        if (cut >= 16)
+            x[0] = x[1] = 0;
+    }
+    u32x4_t v;
+    __builtin_memcpy(&v, x, 16);
+    return v;
+}
+
+template <int MF, int NF, int DEPTH, bool ROWB, bool EXACT, bool ANY>
 __global__ void __launch_bounds__(kSkinnyWaves * 64) k_gemm_fp8_skinny(SkinnyParams p, Fp8Params q)
 {
     __shared__ __attribute__((aligned(16))) f32x4_t sums[kSkinnyWaves][MF * NF][64];
@@ -725,12 +750,23 @@ __global__ void __launch_bounds__(kSkinnyWaves * 64) k_gemm_fp8_skinny(SkinnyPar
     const __amdgpu_buffer_rsrc_t ra = make_rsrc(p.a + m0 * p.lda, (a_rows - 1) * p.lda + q.K);
     const __amdgpu_buffer_rsrc_t rb = make_rsrc(p.b + n0 * p.ldb, (b_rows - 1) * p.ldb + q.K);
     uint32_t va[MF], vb[NF];
+    const char *pa[MF], *pb[NF];
 #pragma unroll
-    for (int i = 0; i < MF; ++i)
-        va[i] = i * 16 + r16 < a_rows ? (uint32_t)(i * 16 + r16) * (uint32_t)p.lda + g * 16 : kOOB;
+    for (int i = 0; i < MF; ++i) {
+        const int row = i * 16 + r16;
+        if constexpr (ANY)
+            pa[i] = p.a + (m0 + min(row, (int)a_rows - 1)) * p.lda;
+        else
+            va[i] = row < a_rows ? (uint32_t)row * (uint32_t)p.lda + g * 16 : kOOB;
+    }
 #pragma unroll
-    for (int j = 0; j < NF; ++j)
-        vb[j] = j * 16 + r16 < b_rows ? (uint32_t)(j * 16 + r16) * (uint32_t)p.ldb + g * 16 : kOOB;
+    for (int j = 0; j < NF; ++j) {
+        const int row = j * 16 + r16;
+        if constexpr (ANY)
+            pb[j] = p.b + (n0 + min(row, (int)b_rows - 1)) * p.ldb;
+        else
+            vb[j] = row < b_rows ? (uint32_t)row * (uint32_t)p.ldb + g * 16 : kOOB;
+    }
 
     struct Block {
         u32x4_t a[MF][2], b[NF][2];
@@ -739,16 +775,27 @@ __global__ void __launch_bounds__(kSkinnyWaves * 64) k_gemm_fp8_skinny(SkinnyPar
     auto load = [&](Block& v, int32_t kb) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const bool ok = kb * kBlock + (h * 4 + g) * 16 < (int32_t)q.K;
-            const uint32_t k = (uint32_t)kb * kBlock + h * 64;
+            const int32_t k = kb * kBlock + (h * 4 + g) * 16;
+            if constexpr (ANY) {
+                const int32_t at = min(k, (int32_t)q.K - 16), cut = min(k - at, 16);
 #pragma unroll
-            for (int j = 0; j < NF; ++j)
-                v.b[j][h] = __builtin_bit_cast(
-                    u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rb, ok ? vb[j] : kOOB, (int)k, 0));
+                for (int j = 0; j < NF; ++j)
+                    v.b[j][h] = load_from(pb[j] + at, cut, (kb + 1) * kBlock > q.K);
 #pragma unroll
-            for (int i = 0; i < MF; ++i)
-                v.a[i][h] = __builtin_bit_cast(
-                    u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(ra, ok ? va[i] : kOOB, (int)k, 0));
+                for (int i = 0; i < MF; ++i)
+                    v.a[i][h] = load_from(pa[i] + at, cut, (kb + 1) * kBlock > q.K);
+            } else {
+                const bool ok = k < (int32_t)q.K;
+                const uint32_t so = (uint32_t)kb * kBlock + h * 64;
+#pragma unroll
+                for (int j = 0; j < NF; ++j)
+                    v.b[j][h] = __builtin_bit_cast(
+                        u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rb, ok ? vb[j] : kOOB, (int)so, 0));
+#pragma unroll
+                for (int i = 0; i < MF; ++i)
+                    v.a[i][h] = __builtin_bit_cast(
+                        u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(ra, ok ? va[i] : kOOB, (int)so, 0));
+            }
         }
         // The scales, each checked against the end of its array.
         const bool in = kb < q.kblocks;
@@ -837,15 +884,21 @@ __global__ void __launch_bounds__(kSkinnyWaves * 64) k_gemm_fp8_skinny(SkinnyPar
     }
 }
 
-// A byte matrix copied to rows of `dst_cols` bytes (a multiple of 16), zeros
-// past src_cols; any source stride and alignment.
-__global__ void __launch_bounds__(256) k_pad_copy8(const uint8_t* src, int64_t rows, int64_t src_cols, int64_t ld_src,
-                                                   uint8_t* dst, int64_t dst_cols)
+// Zero-padded copies, dst_cols bytes (a multiple of 16) a row, of the operands
+// that do not fit the tiles' loads: those with rows, one launch for both.
+struct PadParams {
+    const uint8_t* src[2];
+    uint8_t* dst[2];
+    int64_t rows[2], ld[2];
+};
+
+__global__ void __launch_bounds__(256) k_pad_copy8(PadParams p, int64_t src_cols, int64_t dst_cols)
 {
-    const int64_t per_row = dst_cols / 16, total = rows * per_row;
+    const int64_t per_row = dst_cols / 16, first = p.rows[0] * per_row, total = first + p.rows[1] * per_row;
     for (int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x; id < total; id += (int64_t)gridDim.x * 256) {
-        const int64_t r = id / per_row, c = (id - r * per_row) * 16;
-        const uint8_t* s = src + r * ld_src + c;
+        const int o = id >= first;
+        const int64_t at = o ? id - first : id, r = at / per_row, c = (at - r * per_row) * 16;
+        const uint8_t* s = p.src[o] + r * p.ld[o] + c;
         u32x4_t v = {0u, 0u, 0u, 0u};
         if (c + 16 <= src_cols) {
             __builtin_memcpy(&v, s, 16);
@@ -855,7 +908,7 @@ __global__ void __launch_bounds__(256) k_pad_copy8(const uint8_t* src, int64_t r
                 if (c + e < src_cols)
                     v[e >> 2] |= (uint32_t)s[e] << (8 * (e & 3));
         }
-        *(u32x4_t*)(dst + r * dst_cols + c) = v;
+        *(u32x4_t*)(p.dst[o] + r * dst_cols + c) = v;
     }
 }
 
@@ -876,20 +929,29 @@ unsigned flat_grid(int64_t threads)
 }
 
 template <int MF, int NF, int DEPTH>
-int launch_skinny(SkinnyParams p, const Fp8Params& q, bool exact, hipStream_t s)
+int launch_skinny(SkinnyParams p, const Fp8Params& q, bool exact, bool any, hipStream_t s)
 {
     p.tiles_m = (int32_t)((p.M + MF * 16 - 1) / (MF * 16));
     p.tiles_n = (int32_t)((p.N + NF * 16 - 1) / (NF * 16));
     const dim3 g((unsigned)((p.tiles_n + 7) / 8 * 8 * p.tiles_m)), b(kSkinnyWaves * 64);
+    // Operands of any alignment take wider addresses: half the depth leaves them
+    // the registers.
+    auto run = [&]<bool ROWB, bool EXACT>() {
+        if (any)
+            hipLaunchKernelGGL(HIP_KERNEL_NAME(k_gemm_fp8_skinny<MF, NF, (DEPTH + 1) / 2, ROWB, EXACT, true>), g, b, 0,
+                               s, p, q);
+        else
+            hipLaunchKernelGGL(HIP_KERNEL_NAME(k_gemm_fp8_skinny<MF, NF, DEPTH, ROWB, EXACT, false>), g, b, 0, s, p, q);
+    };
     const bool rowb = q.sb_shift == 0;
     if (rowb && exact)
-        hipLaunchKernelGGL(HIP_KERNEL_NAME(k_gemm_fp8_skinny<MF, NF, DEPTH, true, true>), g, b, 0, s, p, q);
+        run.template operator()<true, true>();
     else if (rowb)
-        hipLaunchKernelGGL(HIP_KERNEL_NAME(k_gemm_fp8_skinny<MF, NF, DEPTH, true, false>), g, b, 0, s, p, q);
+        run.template operator()<true, false>();
     else if (exact)
-        hipLaunchKernelGGL(HIP_KERNEL_NAME(k_gemm_fp8_skinny<MF, NF, DEPTH, false, true>), g, b, 0, s, p, q);
+        run.template operator()<false, true>();
     else
-        hipLaunchKernelGGL(HIP_KERNEL_NAME(k_gemm_fp8_skinny<MF, NF, DEPTH, false, false>), g, b, 0, s, p, q);
+        run.template operator()<false, false>();
     return launched();
 }
 
@@ -913,6 +975,10 @@ constexpr int64_t kSplitLaunch = 6500, kSplitTile = 38;
 // Few-rows kernel: bytes a compute unit's workgroup reads per ns, all of them
 // reading (12.8 us for one token and 8192 x 8192, 28 us for 64 rows).
 constexpr int64_t kSkinnyBytes = 33;
+
+// The padded copies of operands that do not fit the tiles' loads, beside their
+// bytes: a launch and the memory's event.
+constexpr int64_t kPadLaunch = 5000;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -998,10 +1064,34 @@ int launch_tiles(Params p, const Fp8Params& q, int64_t splits, int cus, int per_
     return rc;
 }
 
-// The product on operands whose rows start on 16-byte boundaries, K a multiple
-// of 16.
-int gemm_fp8_direct(int64_t M, int64_t N, const char* A, int64_t lda, const char* B, int64_t ldb, const Fp8Params& q,
-                    int cus, TempMem& tm, hipStream_t s)
+// The product in tiles, on operands whose rows start on 16-byte boundaries, K a
+// multiple of 16.
+int run_tiles(int64_t M, int64_t N, const char* A, int64_t lda, const char* B, int64_t ldb, const Fp8Params& q,
+              int64_t splits, int64_t time128, bool exact, int cus, TempMem& tm, hipStream_t s)
+{
+    Params p;
+    memset(&p, 0, sizeof p);
+    p.A = A;
+    p.B = B;
+    p.M = M;
+    p.N = N;
+    p.K = q.K / 2;
+    p.lda = lda / 2;
+    p.ldb = ldb / 2;
+    p.clock_on = g_clock_on.load(std::memory_order_relaxed) ? 1u : 0u;
+    // The exact way takes 128 x 128 tiles at any size: its fragments are twice
+    // as large, and beside more running sums they do not fit a wave's registers.
+    if (exact)
+        return launch_tiles<Fp8Cfg<128, 128, 2, 2, 32>>(p, q, splits, cus, 2, tm, s);
+    if (tiles_time(kFast256, 256, 1, M, N, q.kblocks, 1, cus) < time128)
+        return launch_tiles<Fp8Cfg<256, 256, 2, 4>>(p, q, 1, cus, 1, tm, s);
+    return launch_tiles<Fp8Cfg<128, 128, 2, 2>>(p, q, splits, cus, 2, tm, s);
+}
+
+// The product of operands whose rows fit the tiles' loads (16-byte boundaries, K
+// a multiple of 16), or, marked by a_fits and b_fits, do not.
+int run_fp8(int64_t M, int64_t N, const char* A, int64_t lda, bool a_fits, const char* B, int64_t ldb, bool b_fits,
+            Fp8Params q, int cus, TempMem& tm, hipStream_t s)
 {
     const bool exact = q.c_fp32 || q.kblocks <= kShortBlocks;
     const TileTimes& t128 = exact ? kExact128 : kFast128;
@@ -1026,32 +1116,44 @@ int gemm_fp8_direct(int64_t M, int64_t N, const char* A, int64_t lda, const char
             skinny = v;
         }
     }
-    if (shape >= 0 && skinny < time128) {
+    const bool any = !a_fits || !b_fits;
+    if (shape >= 0 && skinny < time128 + (any ? kPadLaunch : 0) && (!any || q.K >= 16)) {
         const SkinnyParams p{A, B, M, N, lda, ldb, 0, 0};
         switch (shape) {
-        case 0: return launch_skinny<1, 1, 2>(p, q, exact, s);
-        case 1: return launch_skinny<1, 2, 2>(p, q, exact, s);
-        case 2: return launch_skinny<2, 2, 2>(p, q, exact, s);
-        default: return launch_skinny<4, 2, 1>(p, q, exact, s);
+        case 0: return launch_skinny<1, 1, 2>(p, q, exact, any, s);
+        case 1: return launch_skinny<1, 2, 2>(p, q, exact, any, s);
+        case 2: return launch_skinny<2, 2, 2>(p, q, exact, any, s);
+        default: return launch_skinny<4, 2, 1>(p, q, exact, any, s);
         }
     }
-    Params p;
-    memset(&p, 0, sizeof p);
-    p.A = A;
-    p.B = B;
-    p.M = M;
-    p.N = N;
-    p.K = q.K / 2;
-    p.lda = lda / 2;
-    p.ldb = ldb / 2;
-    p.clock_on = g_clock_on.load(std::memory_order_relaxed) ? 1u : 0u;
-    // The exact way takes 128 x 128 tiles at any size: its fragments are twice
-    // as large, and beside more running sums they do not fit a wave's registers.
-    if (exact)
-        return launch_tiles<Fp8Cfg<128, 128, 2, 2, 32>>(p, q, splits, cus, 2, tm, s);
-    if (tiles_time(kFast256, 256, 1, M, N, q.kblocks, 1, cus) < time128)
-        return launch_tiles<Fp8Cfg<256, 256, 2, 4>>(p, q, 1, cus, 1, tm, s);
-    return launch_tiles<Fp8Cfg<128, 128, 2, 2>>(p, q, splits, cus, 2, tm, s);
+
+    void* ws = nullptr;
+    int rc = GEMM_OK;
+    if (any) {
+        const int64_t K16 = (q.K + 15) & ~(int64_t)15;
+        const int64_t a_pad = a_fits ? 0 : align256(M * K16), b_pad = b_fits ? 0 : align256(N * K16);
+        rc = temp_take(tm, a_pad + b_pad, s, &ws);
+        if (rc != GEMM_OK)
+            return rc;
+        const PadParams c{{(const uint8_t*)A, (const uint8_t*)B}, {(uint8_t*)ws, (uint8_t*)ws + a_pad},
+                          {a_fits ? 0 : M, b_fits ? 0 : N}, {lda, ldb}};
+        hipLaunchKernelGGL(k_pad_copy8, dim3(flat_grid((c.rows[0] + c.rows[1]) * (K16 / 16))), dim3(256), 0, s, c, q.K,
+                           K16);
+        rc = launched();
+        if (!a_fits) {
+            A = (const char*)c.dst[0];
+            lda = K16;
+        }
+        if (!b_fits) {
+            B = (const char*)c.dst[1];
+            ldb = K16;
+        }
+        q.K = K16;   // the copies' zeros extend K to the 16-byte grid
+    }
+    if (rc == GEMM_OK)
+        rc = run_tiles(M, N, A, lda, B, ldb, q, splits, time128, exact, cus, tm, s);
+    const int frc = temp_give(tm, ws, s);
+    return rc != GEMM_OK ? rc : frc;
 }
 
 }  // namespace
@@ -1100,32 +1202,5 @@ extern "C" int gemm_fp8_bt(int64_t M, int64_t N, int64_t K, const void* A, int64
     auto fits = [&](const void* ptr, int64_t ld) {
         return K % 16 == 0 && ld % 16 == 0 && ld <= 2 * kMaxLd && ((uintptr_t)ptr & 15) == 0;
     };
-    const int64_t a_pad = fits(A, lda) ? 0 : align256(M * K16), b_pad = fits(B, ldb) ? 0 : align256(N * K16);
-    void* ws = nullptr;
-    if (a_pad + b_pad > 0) {
-        rc = temp_take(tm, a_pad + b_pad, s, &ws);
-        if (rc != GEMM_OK)
-            return rc;
-        auto copy = [&](const void* src, int64_t rows, int64_t ld, char* dst) {
-            hipLaunchKernelGGL(k_pad_copy8, dim3(flat_grid(rows * (K16 / 16))), dim3(256), 0, s, (const uint8_t*)src,
-                               rows, K, ld, (uint8_t*)dst, K16);
-            return launched();
-        };
-        if (a_pad) {
-            rc = copy(A, M, lda, (char*)ws);
-            A = ws;
-            lda = K16;
-        }
-        if (b_pad && rc == GEMM_OK) {
-            rc = copy(B, N, ldb, (char*)ws + a_pad);
-            B = (char*)ws + a_pad;
-            ldb = K16;
-        }
-        // The copies' zeros extend K to the 16-byte grid.
-        q.K = K16;
-    }
-    if (rc == GEMM_OK)
-        rc = gemm_fp8_direct(M, N, (const char*)A, lda, (const char*)B, ldb, q, cus, tm, s);
-    const int frc = temp_give(tm, ws, s);
-    return rc != GEMM_OK ? rc : frc;
+    return run_fp8(M, N, (const char*)A, lda, fits(A, lda), (const char*)B, ldb, fits(B, ldb), q, cus, tm, s);
 }
