@@ -434,9 +434,11 @@ enum { GEMM_NORM_MAX_WIDTH = 32768 };
  * operand.
  *
  * M, N, K >= 0, N and K at most 2^22, M below 2^31.  M == 0 or N == 0 is a
- * no-op, K == 0 writes +0.  K and the leading dimensions of A and B multiples
- * of 16 with 16-byte aligned A and B run directly; any other call copies the
- * operands that need it, zero-padded, into temporary memory first.  Split k
+ * no-op, K == 0 writes +0.  Operands of any alignment and stride run directly
+ * where C has few rows or tiles (K >= 16).  Larger products run directly with K
+ * and the leading dimensions of A and B multiples of 16 and 16-byte aligned A and
+ * B; otherwise they copy the operands that need it, zero-padded, into temporary
+ * memory first.  Split k
  * ranges (few output tiles, long K) put fp32 partial tiles there, summed in a
  * fixed order.  Temporary memory is gemm_bf16's (kept blocks, see there).
  * Results are deterministic for given sizes, strides and alignment.

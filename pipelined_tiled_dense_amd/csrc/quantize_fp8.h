@@ -4,7 +4,7 @@
 // Bound by memory: 2 bytes in and 1 out per value.  Row scales of X itself need
 // only a maximum over 16 lanes (k_quantize_rows).  Blocks of 128 x 128, and the
 // transpose, take a 128 x 128 tile of X in one workgroup's registers
-// (k_quantize_tile).
+// (k_quantize_tile): 8192 x 4096 transposed, 101 MB, 21 us, 4.8 TB/s.
 #pragma once
 
 namespace {
@@ -18,6 +18,7 @@ struct QuantParams {
     int32_t per_row;     // ceil(K / 128)
 };
 
+template <bool EVEN>
 __global__ void __launch_bounds__(256) k_quantize_rows(QuantParams p)
 {
     for (int64_t u0 = (int64_t)blockIdx.x * kUnits; u0 < p.units; u0 += (int64_t)gridDim.x * kUnits) {
@@ -26,13 +27,13 @@ __global__ void __launch_bounds__(256) k_quantize_rows(QuantParams p)
         int64_t row, c;
         unit_place(u0, p.per_row, row, c);
         const int n = left(p.K, c);
-        const u32x4_t v = load_chunk(p.x + row * p.ldx + c, n);
+        const u32x4_t v = load_chunk<EVEN>(p.x + row * p.ldx + c, n, c);
         float y[kChunk];
 #pragma unroll
         for (int e = 0; e < kChunk; ++e)
             y[e] = chunk_at(v, e);
         const BlockScale b = block_scale(block_top(y));
-        store_chunk8(p.q + row * p.ldq + c, n, chunk_fp8(y, b));
+        store_chunk8<EVEN>(p.q + row * p.ldq + c, n, chunk_fp8(y, b));
         if ((threadIdx.x & (kLanes - 1)) == 0)
             p.scale[c / kBlock * p.lds + row] = b.scale;
     }
@@ -74,8 +75,8 @@ __global__ void __launch_bounds__(256, 4) k_quantize_tile(QuantParams p)
         u32x4_t v[kChunk];
 #pragma unroll
         for (int i = 0; i < kChunk; ++i)
-            v[i] = load_chunk(p.x + (r0 + min(r8 + i, nr - 1)) * p.ldx + c0 + min(c8, nc - 1),
-                              r8 + i < nr ? nc - c8 : 0);
+            v[i] = load_chunk<false>(p.x + (r0 + min(r8 + i, nr - 1)) * p.ldx + c0 + min(c8, nc - 1),
+                              r8 + i < nr ? nc - c8 : 0, c0 + c8);
         BlockScale b[kChunk];   // of each column; of the tile in b[0]
         if constexpr (BLOCKS) {
             uint32_t m = 0;
@@ -133,7 +134,7 @@ __global__ void __launch_bounds__(256, 4) k_quantize_tile(QuantParams p)
             for (int i = 0; i < kChunk; ++i) {
                 const int c = i * 16 + (t >> 4);
                 if (c < nc)
-                    store_chunk8(p.q + (c0 + c) * p.ldq + r0 + c8, nr - c8,
+                    store_chunk8<false>(p.q + (c0 + c) * p.ldq + r0 + c8, nr - c8,
                                  *(const u32x2_t*)(tile + tile_at(c, c8)));
             }
         } else {
@@ -144,7 +145,7 @@ __global__ void __launch_bounds__(256, 4) k_quantize_tile(QuantParams p)
                 for (int e = 0; e < kChunk; ++e)
                     y[e] = chunk_at(v[i], e);
                 if (r8 + i < nr)
-                    store_chunk8(p.q + (r0 + r8 + i) * p.ldq + c0 + c8, nc - c8, chunk_fp8(y, b[0]));
+                    store_chunk8<false>(p.q + (r0 + r8 + i) * p.ldq + c0 + c8, nc - c8, chunk_fp8(y, b[0]));
             }
         }
         __syncthreads();   // tops and tile are free for the next unit
@@ -179,7 +180,10 @@ int gemm_quantize_fp8(int64_t M, int64_t K, const void* X, int64_t ldx, void* Q,
     hipStream_t st = (hipStream_t)stream;
     if (block_rows == 1 && !transposed) {
         p.units = M * p.per_row;
-        hipLaunchKernelGGL(k_quantize_rows, dim3(unit_grid(p.units)), dim3(256), 0, st, p);
+        if (K % kChunk == 0)
+            hipLaunchKernelGGL(k_quantize_rows<true>, dim3(unit_grid(p.units)), dim3(256), 0, st, p);
+        else
+            hipLaunchKernelGGL(k_quantize_rows<false>, dim3(unit_grid(p.units)), dim3(256), 0, st, p);
         return launched();
     }
     p.units = (M + kBlock - 1) / kBlock * p.per_row;
