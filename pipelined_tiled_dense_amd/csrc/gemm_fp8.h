@@ -708,9 +708,10 @@ __global__ void __launch_bounds__(256) k_reduce_fp8(Params p, Fp8Params q)
 // memory straight into registers, DEPTH blocks in use and DEPTH more in flight,
 // and add their sums through LDS in wave order.  So every compute unit has loads
 // in flight over the whole of k even where C gives few workgroups, with no
-// second launch.  Bound by B's bytes where there are many columns (1 x 8192 x
-// 8192: 12.8 us, 5.3 TB/s), by the latency of a wave's blocks where there are few
-// (300 x 1000 x 4112, 4 blocks a wave: 12 us).
+// second launch; only a long k against very few columns is split over several
+// workgroups, whose sums a second launch adds in order.  Bound by B's bytes where there are many columns (1 x 8192 x
+// 8192: 13.0 us, 5.2 TB/s), by the latency of a wave's blocks where there are few
+// (300 x 1000 x 4112, 4 blocks a wave: 10.8 us).
 //
 // ANY takes operands of any alignment and stride and any K >= 16 (otherwise rows
 // start on 16-byte boundaries and K is a multiple of 16): a chunk that reaches
@@ -723,26 +724,50 @@ struct SkinnyParams {
     const char* b;
     int64_t M, N, lda, ldb;
     int32_t tiles_m, tiles_n;
+    int32_t chunk;           // k blocks per workgroup: all, or a k chunk's (blockIdx.y counts the chunks)
+    float* partial;          // with several chunks: M x N sums of each
 };
 
 constexpr int kSkinnyWaves = 8;
 
-// 16 bytes at p (any alignment) without their first `cut`, zeros after the rest;
-// `tail` (uniform) is false where cut is 0 in every lane.
-__device__ __forceinline__ u32x4_t load_from(const char* p, int cut, bool tail)
+// 16 bytes at any address as the dwords that hold them, so that no lane's access
+// crosses a dword: byte-aligned 16-byte loads of rows at odd addresses took 2.5
+// times as long (4 x 528 x 5249).  Every dword holds a byte of the 16, so none
+// lies outside the operand's pages.  Where four dwords are enough, the fifth is
+// read from `spare`, one place for all lanes, which costs next to nothing.
+struct Bytes16 {
+    u32x4_t v;
+    uint32_t end;
+};
+
+__device__ __forceinline__ Bytes16 load_any(const char* p, const float* spare)
 {
-    uint64_t x[2];
-    __builtin_memcpy(x, p, 16);
+    Bytes16 r;
+    const uint32_t by = (uint32_t)(uintptr_t)p & 3u;
+    const char* lo = p - by;
+    __builtin_memcpy(&r.v, __builtin_assume_aligned(lo, 4), 16);
+    __builtin_memcpy(&r.end, __builtin_assume_aligned(by ? lo + 16 : (const char*)spare, 4), 4);
+    return r;
+}
+
+// The 16 bytes that load_any(p) read, without their first `cut` and with zeros
+// after the rest; `tail` (uniform) is false where cut is 0 in every lane.
+__device__ __forceinline__ u32x4_t bytes_of(const Bytes16& r, const char* p, int cut, bool tail)
+{
+    const uint32_t by = (uint32_t)(uintptr_t)p & 3u;
+    u32x4_t v = {__builtin_amdgcn_alignbyte(r.v[1], r.v[0], by), __builtin_amdgcn_alignbyte(r.v[2], r.v[1], by),
+                 __builtin_amdgcn_alignbyte(r.v[3], r.v[2], by), __builtin_amdgcn_alignbyte(r.end, r.v[3], by)};
     if (tail) {
+        uint64_t x[2];
+        __builtin_memcpy(x, &v, 16);
         const int s = (cut & 7) * 8;
         const uint64_t lo = cut >= 8 ? x[1] : x[0], hi = cut >= 8 ? 0u : x[1];
         x[0] = s ? (lo >> s) | (hi << (64 - s)) : lo;
         x[1] = hi >> s;
         if (cut >= 16)
             x[0] = x[1] = 0;
+        __builtin_memcpy(&v, x, 16);
     }
-    u32x4_t v;
-    __builtin_memcpy(&v, x, 16);
     return v;
 }
 
@@ -759,61 +784,83 @@ __global__ void __launch_bounds__(kSkinnyWaves * 64) k_gemm_fp8_skinny(SkinnyPar
     if (tn >= p.tiles_n)
         return;
     const int64_t m0 = (int64_t)tm * (MF * 16), n0 = (int64_t)tn * (NF * 16);
+    const int32_t kb_first = blockIdx.y * p.chunk, kb_end = min(kb_first + p.chunk, q.kblocks);
+    if (p.partial) {
+        q.c = (char*)(p.partial + blockIdx.y * p.M * p.N);
+        q.ldc = p.N;
+        q.c_fp32 = 1;
+    }
 
     // Rows past the end read as zeros: their offset is past the resource.
     const int64_t a_rows = min(p.M - m0, (int64_t)MF * 16), b_rows = min(p.N - n0, (int64_t)NF * 16);
     const __amdgpu_buffer_rsrc_t ra = make_rsrc(p.a + m0 * p.lda, (a_rows - 1) * p.lda + q.K);
     const __amdgpu_buffer_rsrc_t rb = make_rsrc(p.b + n0 * p.ldb, (b_rows - 1) * p.ldb + q.K);
-    uint32_t va[MF], vb[NF];
-    const char *pa[MF], *pb[NF];
+    // Lanes 4 i .. 4 i + 3 read 64 consecutive bytes of a row: the cache takes four
+    // such lanes at a time, lanes of four rows one by one (64 rows of 4096 x 4096:
+    // 10.5 us in the MFMA's own order, 7.0 without a lane's way to it).  An MFMA's
+    // lane (r16, g) then takes chunk g of row r16 from the lane that read it.
+    const int lr = (lane >> 2 & 3) * 4 + (lane >> 4), lc = lane & 3;
+    const int from = ((lane & 3) * 16 + (lane & 12) + g) * 4;
+    auto mfma_order = [&](u32x4_t v) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            v[e] = (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)v[e]);
+        return v;
+    };
+    uint32_t va[MF] = {}, vb[NF] = {};
+    const char *pa[MF] = {}, *pb[NF] = {};
 #pragma unroll
     for (int i = 0; i < MF; ++i) {
-        const int row = i * 16 + r16;
+        const int row = i * 16 + lr;
         if constexpr (ANY)
             pa[i] = p.a + (m0 + min(row, (int)a_rows - 1)) * p.lda;
         else
-            va[i] = row < a_rows ? (uint32_t)row * (uint32_t)p.lda + g * 16 : kOOB;
+            va[i] = row < a_rows ? (uint32_t)row * (uint32_t)p.lda + lc * 16 : kOOB;
     }
 #pragma unroll
     for (int j = 0; j < NF; ++j) {
-        const int row = j * 16 + r16;
+        const int row = j * 16 + lr;
         if constexpr (ANY)
             pb[j] = p.b + (n0 + min(row, (int)b_rows - 1)) * p.ldb;
         else
-            vb[j] = row < b_rows ? (uint32_t)row * (uint32_t)p.ldb + g * 16 : kOOB;
+            vb[j] = row < b_rows ? (uint32_t)row * (uint32_t)p.ldb + lc * 16 : kOOB;
     }
 
+    using Raw = std::conditional_t<ANY, Bytes16, u32x4_t>;
     struct Block {
-        u32x4_t a[MF][2], b[NF][2];
+        Raw a[MF][2], b[NF][2];
         float sa[MF], sb[ROWB ? NF * 4 : 1];
     };
+    // ANY: where half h of block kb is read, and how many of its bytes precede it.
+    auto place = [&](int32_t kb, int h, int32_t& at) {
+        const int32_t k = kb * kBlock + (h * 4 + lc) * 16;
+        at = min(k, (int32_t)q.K - 16);
+        return min(k - at, 16);
+    };
     auto load = [&](Block& v, int32_t kb) {
+        // The halves of a line one after the other, while the line is in the L1.
+        auto halves = [&](Raw (&to)[2], const char* row, const __amdgpu_buffer_rsrc_t& rsrc, uint32_t voff) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int32_t k = kb * kBlock + (h * 4 + g) * 16;
-            if constexpr (ANY) {
-                const int32_t at = min(k, (int32_t)q.K - 16), cut = min(k - at, 16);
-#pragma unroll
-                for (int j = 0; j < NF; ++j)
-                    v.b[j][h] = load_from(pb[j] + at, cut, (kb + 1) * kBlock > q.K);
-#pragma unroll
-                for (int i = 0; i < MF; ++i)
-                    v.a[i][h] = load_from(pa[i] + at, cut, (kb + 1) * kBlock > q.K);
-            } else {
-                const bool ok = k < (int32_t)q.K;
-                const uint32_t so = (uint32_t)kb * kBlock + h * 64;
-#pragma unroll
-                for (int j = 0; j < NF; ++j)
-                    v.b[j][h] = __builtin_bit_cast(
-                        u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rb, ok ? vb[j] : kOOB, (int)so, 0));
-#pragma unroll
-                for (int i = 0; i < MF; ++i)
-                    v.a[i][h] = __builtin_bit_cast(
-                        u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(ra, ok ? va[i] : kOOB, (int)so, 0));
+            for (int h = 0; h < 2; ++h) {
+                if constexpr (ANY) {
+                    int32_t at;
+                    place(kb, h, at);
+                    to[h] = load_any(row + at, q.sa);
+                } else {
+                    const bool ok = kb * kBlock + (h * 4 + lc) * 16 < (int32_t)q.K;
+                    to[h] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
+                                                            rsrc, ok ? voff : kOOB, kb * kBlock + h * 64, 0));
+                }
             }
-        }
+        };
+#pragma unroll
+        for (int j = 0; j < NF; ++j)
+            halves(v.b[j], pb[j], rb, vb[j]);
+#pragma unroll
+        for (int i = 0; i < MF; ++i)
+            halves(v.a[i], pa[i], ra, va[i]);
         // The scales, each checked against the end of its array.
-        const bool in = kb < q.kblocks;
+        const bool in = kb < kb_end;
         const __amdgpu_buffer_rsrc_t rsa = make_rsrc(q.sa + (in ? kb * q.ldsa : 0) + m0, in ? a_rows * 4 : 0);
 #pragma unroll
         for (int i = 0; i < MF; ++i)
@@ -832,14 +879,28 @@ __global__ void __launch_bounds__(kSkinnyWaves * 64) k_gemm_fp8_skinny(SkinnyPar
 #pragma unroll
         for (int j = 0; j < NF; ++j)
             acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-    auto compute = [&](const Block& v) {
+    auto compute = [&](const Block& v, int32_t kb) {
+        auto frag = [&](const Raw (&raw)[2], const char* row) {
+            if constexpr (ANY) {
+                u32x4_t x[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    int32_t at;
+                    const int cut = place(kb, h, at);
+                    x[h] = mfma_order(bytes_of(raw[h], row + at, cut, (kb + 1) * kBlock > q.K));
+                }
+                return Fp8Frag<EXACT>(x[0], x[1]);
+            } else {
+                return Fp8Frag<EXACT>(mfma_order(raw[0]), mfma_order(raw[1]));
+            }
+        };
         Fp8Frag<EXACT> bf[NF];
 #pragma unroll
         for (int j = 0; j < NF; ++j)
-            bf[j] = Fp8Frag<EXACT>(v.b[j][0], v.b[j][1]);
+            bf[j] = frag(v.b[j], pb[j]);
 #pragma unroll
         for (int i = 0; i < MF; ++i) {
-            const Fp8Frag<EXACT> af(v.a[i][0], v.a[i][1]);
+            const Fp8Frag<EXACT> af = frag(v.a[i], pa[i]);
 #pragma unroll
             for (int j = 0; j < NF; ++j) {
                 const f32x4_t d = block_sums(bf[j], af);
@@ -855,7 +916,7 @@ __global__ void __launch_bounds__(kSkinnyWaves * 64) k_gemm_fp8_skinny(SkinnyPar
     Block cur[DEPTH], nxt[DEPTH];
     constexpr int STEP = kSkinnyWaves * DEPTH;
     auto load_all = [&](Block (&v)[DEPTH], int32_t kb0) {
-        if (kb0 < q.kblocks) {
+        if (kb0 < kb_end) {
 #pragma unroll
             for (int d = 0; d < DEPTH; ++d)
                 load(v[d], kb0 + d * kSkinnyWaves);
@@ -864,15 +925,15 @@ __global__ void __launch_bounds__(kSkinnyWaves * 64) k_gemm_fp8_skinny(SkinnyPar
     auto compute_all = [&](const Block (&v)[DEPTH], int32_t kb0) {
 #pragma unroll
         for (int d = 0; d < DEPTH; ++d)
-            if (kb0 + d * kSkinnyWaves < q.kblocks)
-                compute(v[d]);
+            if (kb0 + d * kSkinnyWaves < kb_end)
+                compute(v[d], kb0 + d * kSkinnyWaves);
     };
     // Workgroups start at different places along k: with a power-of-two row
     // stride, all of them reading the same columns at once fall on the same few
     // memory channels (8192 x 8192 weight, one token: 18.4 us, and 12.8 so).
-    const int32_t rounds = (q.kblocks + STEP - 1) / STEP, rot = (int32_t)(blockIdx.x % (unsigned)rounds);
+    const int32_t rounds = (kb_end - kb_first + STEP - 1) / STEP, rot = (int32_t)(blockIdx.x % (unsigned)rounds);
     auto at = [&](int32_t t) {
-        return t < rounds ? w + (t + rot < rounds ? t + rot : t + rot - rounds) * STEP : q.kblocks;
+        return t < rounds ? kb_first + w + (t + rot < rounds ? t + rot : t + rot - rounds) * STEP : kb_end;
     };
     load_all(cur, at(0));
     for (int32_t t = 0; t < rounds; t += 2) {
@@ -943,31 +1004,81 @@ unsigned flat_grid(int64_t threads)
     return (unsigned)(n < 65536 ? n : 65536);
 }
 
+// C from the k chunks' sums, added in chunk order, 4 columns a thread.
+__global__ void __launch_bounds__(256) k_reduce_chunks(SkinnyParams p, Fp8Params q, int32_t chunks)
+{
+    const int64_t per_row = (p.N + 3) / 4, step = (int64_t)gridDim.x * 256;
+    for (int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x; t < p.M * per_row; t += step) {
+        const int64_t m = t / per_row, n = t % per_row * 4;
+        f32x4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int32_t z = 0; z < chunks; ++z) {
+            const float* x = p.partial + (z * p.M + m) * p.N + n;
+            f32x4_t y = {0.0f, 0.0f, 0.0f, 0.0f};
+            if (n + 4 <= p.N) {
+                __builtin_memcpy(&y, x, 16);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 3; ++e)
+                    if (n + e < p.N)
+                        y[e] = x[e];
+            }
+            v += y;
+        }
+        store_c4(q, m, n, p.N, v);
+    }
+}
+
 template <int MF, int NF, int DEPTH>
-int launch_skinny(SkinnyParams p, const Fp8Params& q, bool exact, bool any, hipStream_t s)
+int launch_skinny(SkinnyParams p, const Fp8Params& q, bool exact, bool any, int64_t chunks, TempMem& tm, hipStream_t s)
 {
     p.tiles_m = (int32_t)((p.M + MF * 16 - 1) / (MF * 16));
     p.tiles_n = (int32_t)((p.N + NF * 16 - 1) / (NF * 16));
-    const dim3 g((unsigned)((p.tiles_n + 7) / 8 * 8 * p.tiles_m)), b(kSkinnyWaves * 64);
-    // Operands of any alignment take wider addresses: half the depth leaves them
-    // the registers.
+    p.chunk = (int32_t)((q.kblocks + chunks - 1) / chunks);
+    chunks = (q.kblocks + p.chunk - 1) / p.chunk;
+    void* ws = nullptr;
+    hipEvent_t done = nullptr;
+    if (chunks > 1) {
+        const int rc = temp_take(tm, chunks * p.M * p.N * 4, s, &ws, &done);
+        if (rc != GEMM_OK)
+            return rc;
+    }
+    p.partial = (float*)ws;
+    const dim3 g((unsigned)((p.tiles_n + 7) / 8 * 8 * p.tiles_m), (unsigned)chunks), b(kSkinnyWaves * 64);
+    // Operands of any alignment take wider addresses and a dword more: less depth
+    // leaves them the registers.
     auto run = [&]<bool ROWB, bool EXACT>() {
-        if (any)
-            hipLaunchKernelGGL(HIP_KERNEL_NAME(k_gemm_fp8_skinny<MF, NF, (DEPTH + 1) / 2, ROWB, EXACT, true>), g, b, 0,
-                               s, p, q);
-        else
-            hipLaunchKernelGGL(HIP_KERNEL_NAME(k_gemm_fp8_skinny<MF, NF, DEPTH, ROWB, EXACT, false>), g, b, 0, s, p, q);
+        if constexpr (MF * NF < 16) {
+            if (any) {
+                hipLaunchKernelGGL(HIP_KERNEL_NAME(k_gemm_fp8_skinny<MF, NF, 1, ROWB, EXACT, true>), g, b, 0, s, p, q);
+                return;
+            }
+        }
+        hipLaunchKernelGGL(HIP_KERNEL_NAME(k_gemm_fp8_skinny<MF, NF, DEPTH, ROWB, EXACT, false>), g, b, 0, s, p, q);
     };
     const bool rowb = q.sb_shift == 0;
-    if (rowb && exact)
-        run.template operator()<true, true>();
-    else if (rowb)
-        run.template operator()<true, false>();
-    else if (exact)
-        run.template operator()<false, true>();
-    else
-        run.template operator()<false, false>();
-    return launched();
+    if constexpr (MF * NF < 16) {
+        if (rowb && exact)
+            run.template operator()<true, true>();
+        else if (rowb)
+            run.template operator()<true, false>();
+        else if (exact)
+            run.template operator()<false, true>();
+        else
+            run.template operator()<false, false>();
+    } else {
+        run.template operator()<false, false>();   // the others do not fit the registers
+    }
+    int rc = launched();
+    if (chunks > 1) {
+        if (rc == GEMM_OK) {
+            hipExtLaunchKernelGGL(k_reduce_chunks, dim3(flat_grid(p.M * ((p.N + 3) / 4))), dim3(256), 0, s, nullptr,
+                                  done, 0, p, q, (int32_t)chunks);
+            rc = launched();
+        }
+        const int frc = temp_give(tm, ws, s, rc == GEMM_OK && done != nullptr);
+        rc = rc != GEMM_OK ? rc : frc;
+    }
+    return rc;
 }
 
 // Sums of up to this many blocks are computed exactly (see the top).
@@ -988,8 +1099,12 @@ constexpr TileTimes kExact128{1300, 2200};      // the same shape, 80 us with 8 
 // (128 x 4096 x 4096: 20.2 us with 4 splits, 22.2 with 8, 27.9 with none).
 constexpr int64_t kSplitLaunch = 6500, kSplitTile = 38;
 // Few-rows kernel: bytes a compute unit's workgroup reads per ns, all of them
-// reading (12.8 us for one token and 8192 x 8192, 28 us for 64 rows).
-constexpr int64_t kSkinnyBytes = 33;
+// reading (64 x 8192 x 8192 in 64 x 32: 20 us; fp32 C converts every byte), in
+// fragments of 4 x 4 (256 x 4096 x 4096: 16 us), and what another workgroup in
+// turn costs beside its bytes, for each of its fragments (1039 x 1792 x 256 to
+// fp32, 4 turns of 8 fragments: 12.5 us, where tiles take 9.7).
+constexpr int64_t kSkinnyBytes[2] = {45, 40}, kSkinnyBytes44 = 37, kSkinnyTurn = 190;
+constexpr int64_t kChunkBytes = 2000;   // k chunks: bytes per ns of their sums, written and read
 
 // The padded copies of operands that do not fit the tiles' loads, beside their
 // bytes: a launch and the memory's event.
@@ -1114,31 +1229,44 @@ int run_fp8(int64_t M, int64_t N, const char* A, int64_t lda, bool a_fits, const
     const int64_t splits = choose_fp8_splits(t128, M, N, q.kblocks, cus, &time128);
 
     // The few-rows kernel's shapes: rows in fragments of 16, and as many columns
-    // as keep the most compute units busy for the fewest bytes.
+    // as keep the most compute units busy for the fewest bytes; k chunks where
+    // that leaves compute units idle, each with two blocks or more a wave (32 x 624
+    // x 13056: 17 us, 8.9 with chunks).  Not in the shape of 4 x 4 fragments, whose
+    // few waves with much each do not keep up with memory (32 x 3264 x 18176: 32 us
+    // in 5 chunks, tiles 17.5).
     constexpr struct {
         int mf, nf;
-    } kShapes[] = {{1, 1}, {1, 2}, {2, 2}, {4, 2}};
+    } kShapes[] = {{1, 1}, {1, 2}, {2, 2}, {4, 2}, {4, 4}};
+    const bool any = !a_fits || !b_fits;
     int shape = -1;
-    int64_t skinny = 0;
-    for (int i = 0; i < 4; ++i) {
+    int64_t skinny = 0, chunks = 1;
+    for (int i = 0; i < (exact || any || q.sb_shift == 0 ? 4 : 5); ++i) {
         const int64_t rows = kShapes[i].mf * 16, cols = kShapes[i].nf * 16;
         const int64_t groups = ceil_div(M, rows) * ceil_div(N, cols);
         if (groups >= (int64_t)1 << 22)
             continue;   // far from few rows, and past what a launch takes
-        const int64_t v = ceil_div(groups, cus) * ((M < rows ? M : rows) + cols) * q.kblocks * kBlock / kSkinnyBytes;
-        if (shape < 0 || v < skinny) {
-            shape = i;
-            skinny = v;
+        for (int64_t c = 1; c <= kMaxSplits; ++c) {
+            if (c > 1 && (i == 4 || groups * c > cus || q.kblocks < c * 2 * kSkinnyWaves))
+                break;
+            const int64_t turns = ceil_div(groups * c, cus), rate = i == 4 ? kSkinnyBytes44 : kSkinnyBytes[exact];
+            const int64_t v = turns * ((M < rows ? M : rows) + cols) * ceil_div(q.kblocks, c) * kBlock / rate +
+                              (turns - 1) * kSkinnyTurn * kShapes[i].mf * kShapes[i].nf +
+                              (c > 1 ? kSplitLaunch + c * M * N * 8 / kChunkBytes : 0);
+            if (shape < 0 || v < skinny) {
+                shape = i;
+                skinny = v;
+                chunks = c;
+            }
         }
     }
-    const bool any = !a_fits || !b_fits;
     if (shape >= 0 && skinny < time128 + (any ? kPadLaunch : 0) && (!any || q.K >= 16)) {
-        const SkinnyParams p{A, B, M, N, lda, ldb, 0, 0};
+        const SkinnyParams p{A, B, M, N, lda, ldb, 0, 0, 0, nullptr};
         switch (shape) {
-        case 0: return launch_skinny<1, 1, 2>(p, q, exact, any, s);
-        case 1: return launch_skinny<1, 2, 2>(p, q, exact, any, s);
-        case 2: return launch_skinny<2, 2, 2>(p, q, exact, any, s);
-        default: return launch_skinny<4, 2, 1>(p, q, exact, any, s);
+        case 0: return launch_skinny<1, 1, 2>(p, q, exact, any, chunks, tm, s);
+        case 1: return launch_skinny<1, 2, 2>(p, q, exact, any, chunks, tm, s);
+        case 2: return launch_skinny<2, 2, 2>(p, q, exact, any, chunks, tm, s);
+        case 3: return launch_skinny<4, 2, 1>(p, q, exact, any, chunks, tm, s);
+        default: return launch_skinny<4, 4, 1>(p, q, exact, any, chunks, tm, s);
         }
     }
 

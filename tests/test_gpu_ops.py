@@ -332,6 +332,25 @@ def test_gemm_fp8_exact(M, N, K, b_rows):
     assert torch.equal(bd.gemm_fp8(a, sa, b, sb, out_dtype=torch.float32).double(), want)
 
 
+@pytest.mark.parametrize("M,N,K,b_rows", [(5, 130, 13952, 128), (33, 99, 9001, 1), (1, 250, 20000, 128), (64, 32, 32768, 1),
+                                          (250, 2600, 1040, 128)])
+def test_gemm_fp8_few_rows_split_k(M, N, K, b_rows):
+    """A long k against a few columns, whose k range several workgroups share, and
+    a C of as many tiles as the device has compute units: whole numbers again, so
+    every order of the sums gives the same; twice, for the kept memory."""
+    g = gen(K + N)
+    a = torch.randint(-4, 5, (M, K), generator=g, device="cuda").float().to(FP8)
+    b = torch.randint(-4, 5, (N, K), generator=g, device="cuda").float().to(FP8)
+    sa = 2.0 ** torch.randint(-1, 1, (ref.nblocks(K), M), generator=g, device="cuda").float()
+    sb = 2.0 ** torch.randint(-1, 1, (ref.nblocks(K), -(-N // b_rows)), generator=g, device="cuda").float()
+    want, _ = ref.gemm(a, sa, b, sb, b_rows)
+    for _ in range(2):
+        buf = torch.full((M, N + 3), 7.0, device="cuda")
+        assert torch.equal(bd.gemm_fp8(a, sa, b, sb, out=buf[:, :N]).double(), want)
+        assert (buf[:, N:] == 7.0).all()
+        assert torch.equal(bd.gemm_fp8(a, sa, b, sb), want.float().to(BF16))
+
+
 def test_gemm_fp8_nonfinite_operands_stay_in_their_rows():
     """NaN in one row of A and one of B, and an infinite scale: they reach the
     row and columns they belong to and nothing else."""
