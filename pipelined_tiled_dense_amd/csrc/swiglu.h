@@ -3,8 +3,8 @@
 // Bound by memory: every value is read once and written once, 8 at a time.  A
 // unit of work is 128 columns of a row, 16 lanes of one chunk, so that an 8-bit
 // output's scale is a maximum over one DPP row.  8192 x 8192 to 8 bits, 335 MB:
-// 68 us, 4.9 TB/s; the gradient at 2047 x 5005, 102 MB, whose odd rows start at
-// any byte: 21 us, 4.8 TB/s (a large copy reaches 5.1).
+// 71 us, 4.7 TB/s; the gradient at 2047 x 5005, 102 MB, whose odd rows start at
+// any byte: 20 us, 5.1 TB/s (a large copy reaches 5.1).
 #pragma once
 
 namespace {
@@ -45,7 +45,9 @@ __device__ __forceinline__ Sigmoid sigmoid(float x)
 // vector instructions as much as by memory): x u / (1 + exp(-x)) with e =
 // exp(-x) up to 2^127.9, beyond which silu is below 2^-120 of x and the bound
 // keeps e finite.  The denominator is taken times 1/4, so that its reciprocal
-// (1 ulp) stays a normal number, which v_rcp_f32 needs.
+// stays a normal number, which v_rcp_f32 needs; a Newton step corrects it (its
+// ulp alone turned twice as many 8-bit roundings as the other steps; 3 us of 71
+// at 8192 x 8192).
 __device__ __forceinline__ float silu_times(float x, float u)
 {
     constexpr float kLog2e = 0x1.715476p+0f, kLog2eRest = 0x1.4ae0cp-26f, kLn2 = 0x1.62e430p-1f;
@@ -54,7 +56,8 @@ __device__ __forceinline__ float silu_times(float x, float u)
     const float rest = __builtin_fmaf(nx, kLog2eRest, __builtin_fmaf(nx, kLog2e, -p));
     const float e0 = __builtin_amdgcn_exp2f(p);
     const float e = __builtin_fmaf(e0, rest * kLn2, e0);
-    const float r = __builtin_amdgcn_rcpf(__builtin_fmaf(e, 0.25f, 0.25f));
+    const float d = __builtin_fmaf(e, 0.25f, 0.25f), r0 = __builtin_amdgcn_rcpf(d);
+    const float r = __builtin_fmaf(__builtin_fmaf(-d, r0, 1.0f), r0, r0);
     return x * r * (0.25f * u);
 }
 
