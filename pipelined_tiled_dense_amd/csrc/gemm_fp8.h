@@ -796,9 +796,9 @@ __global__ void __launch_bounds__(kSkinnyWaves * 64) k_gemm_fp8_skinny(SkinnyPar
     const __amdgpu_buffer_rsrc_t ra = make_rsrc(p.a + m0 * p.lda, (a_rows - 1) * p.lda + q.K);
     const __amdgpu_buffer_rsrc_t rb = make_rsrc(p.b + n0 * p.ldb, (b_rows - 1) * p.ldb + q.K);
     // Lanes 4 i .. 4 i + 3 read 64 consecutive bytes of a row: the cache takes four
-    // such lanes at a time, lanes of four rows one by one (64 rows of 4096 x 4096:
-    // 10.5 us in the MFMA's own order, 7.0 without a lane's way to it).  An MFMA's
-    // lane (r16, g) then takes chunk g of row r16 from the lane that read it.
+    // such lanes at a time, lanes of four rows one by one.  An MFMA's lane (r16, g)
+    // then takes chunk g of row r16 from the lane that read it (64 x 4096 x 4096:
+    // 10.5 us read in the MFMA's order, 8.1 so; the exchange is 1.1 of it).
     const int lr = (lane >> 2 & 3) * 4 + (lane >> 4), lc = lane & 3;
     const int from = ((lane & 3) * 16 + (lane & 12) + g) * 4;
     auto mfma_order = [&](u32x4_t v) {
