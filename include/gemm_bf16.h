@@ -503,7 +503,9 @@ int gemm_rms_norm_bwd(int64_t M, int64_t D, const void* dY, int64_t lddy,
 /*
  * gemm_swiglu: y = g / (1 + exp(-g)) * u for bf16 GU (M x 2F, ldgu >= 2F; row
  * i holds g in columns 0 .. F-1 and u in F .. 2F-1).  Y is M x F, bf16 or 8
- * bits with row scales (lds >= M) by y_type.  M == 0 or F == 0 is a no-op.
+ * bits with row scales (lds >= M) by y_type.  It is right for every gate, up to
+ * the rounding of fp32: small ones under a large u, and large ones, too; minus
+ * infinity and NaN give NaN.  M == 0 or F == 0 is a no-op.
  */
 int gemm_swiglu(int64_t M, int64_t F, const void* GU, int64_t ldgu,
                 void* Y, int64_t ldy, int y_type, float* scale, int64_t lds, void* stream);

@@ -3,7 +3,7 @@
 // Bound by memory: every value is read once and written once, 8 at a time.  A
 // unit of work is 128 columns of a row, 16 lanes of one chunk, so that an 8-bit
 // output's scale is a maximum over one DPP row.  8192 x 8192 to 8 bits, 335 MB:
-// 71 us, 4.7 TB/s; the gradient at 2047 x 5005, 102 MB, whose odd rows start at
+// 68 us, 4.9 TB/s; the gradient at 2047 x 5005, 102 MB, whose odd rows start at
 // any byte: 20 us, 5.1 TB/s (a large copy reaches 5.1).
 #pragma once
 
@@ -42,23 +42,64 @@ __device__ __forceinline__ Sigmoid sigmoid(float x)
 }
 
 // silu(x) * u alone, in fewer steps (the 8-bit forward kernel is bound by its
-// vector instructions as much as by memory): x u / (1 + exp(-x)) with e =
-// exp(-x) up to 2^127.9, beyond which silu is below 2^-120 of x and the bound
-// keeps e finite.  The denominator is taken times 1/4, so that its reciprocal
-// stays a normal number, which v_rcp_f32 needs; a Newton step corrects it (its
-// ulp alone turned twice as many 8-bit roundings as the other steps; 3 us of 71
-// at 8192 x 8192).
+// vector instructions as much as by memory): x u / (1 + exp(-x)) for x from
+// kLowGate on, where exp(-x) stays below 2^127.7.  The denominator is taken times
+// 1/4, so that its reciprocal stays a normal number, which v_rcp_f32 needs, and x
+// with it, so that no product passes |x|; a Newton step corrects the reciprocal
+// (its ulp alone turned twice as many 8-bit roundings as the other steps; 3 us at
+// 8192 x 8192).
+constexpr float kLowGate = -88.5f;
+
 __device__ __forceinline__ float silu_times(float x, float u)
 {
     constexpr float kLog2e = 0x1.715476p+0f, kLog2eRest = 0x1.4ae0cp-26f, kLn2 = 0x1.62e430p-1f;
-    const float nx = x < -88.6f ? 88.6f : (x > 150.0f ? -150.0f : -x);
+    const float nx = x > 150.0f ? -150.0f : -x;
     const float p = nx * kLog2e;
     const float rest = __builtin_fmaf(nx, kLog2eRest, __builtin_fmaf(nx, kLog2e, -p));
     const float e0 = __builtin_amdgcn_exp2f(p);
     const float e = __builtin_fmaf(e0, rest * kLn2, e0);
     const float d = __builtin_fmaf(e, 0.25f, 0.25f), r0 = __builtin_amdgcn_rcpf(d);
     const float r = __builtin_fmaf(__builtin_fmaf(-d, r0, 1.0f), r0, r0);
-    return x * r * (0.25f * u);
+    return (0.25f * x) * r * u;
+}
+
+// The same below kLowGate, where 1 + exp(-x) is exp(-x) to fp32: x u exp(x), with
+// exp(x) as the third power of f = exp(x / 3), a normal number, and f taken to u
+// and to x first, so that a large u meets the small factors before anything
+// overflows or is lost.  From -216 on down |x u exp(x)| is below bf16's smallest
+// value for every u, and a zero comes out; minus infinity is -inf / inf.
+__device__ __forceinline__ float silu_times_low(float x, float u)
+{
+    constexpr float kThird = 0x1.ec709ep-2f, kThirdRest = -0x1.e2fe02p-29f, kLn2 = 0x1.62e430p-1f;   // (log2 e) / 3
+    const float xc = x < -216.0f ? -216.0f : x;
+    const float p = xc * kThird;
+    const float rest = __builtin_fmaf(xc, kThirdRest, __builtin_fmaf(xc, kThird, -p));
+    const float f0 = __builtin_amdgcn_exp2f(p);
+    const float f = __builtin_fmaf(f0, rest * kLn2, f0);
+    const float y = (u * f) * (xc * f) * f;
+    return x == -__builtin_inff() ? __builtin_nanf("") : y;
+}
+
+// 8 gates and their u.  Gates below kLowGate are rare: a branch that no lane of
+// most waves takes, with both ways whole (8192 x 8192 to 8 bits: 68 us; 73 with the
+// low gates corrected after the others).
+__device__ __forceinline__ void silu_chunk(u32x4_t gv, u32x4_t uv, float (&y)[kChunk])
+{
+    float low = 0.0f;
+#pragma unroll
+    for (int e = 0; e < kChunk; ++e)
+        low = __builtin_fminf(low, chunk_at(gv, e));
+    if (__builtin_expect(low < kLowGate, 0)) {
+#pragma unroll
+        for (int e = 0; e < kChunk; ++e) {
+            const float g = chunk_at(gv, e), u = chunk_at(uv, e);
+            y[e] = g < kLowGate ? silu_times_low(g, u) : silu_times(g, u);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < kChunk; ++e)
+            y[e] = silu_times(chunk_at(gv, e), chunk_at(uv, e));
+    }
 }
 
 struct SwigluParams {
@@ -83,11 +124,7 @@ __global__ void __launch_bounds__(256) k_swiglu(SwigluParams p)
         const uint16_t* src = p.gu + row * p.ldgu + c;
         const u32x4_t gv = load_chunk<EVEN>(src, n, c), uv = load_chunk<EVEN>(src + p.F, n, c);
         float y[kChunk];
-#pragma unroll
-        for (int e = 0; e < kChunk; ++e) {
-            const float g = chunk_at(gv, e);
-            y[e] = silu_times(g, chunk_at(uv, e));
-        }
+        silu_chunk(gv, uv, y);
         if constexpr (FP8) {
             const BlockScale b = block_scale(block_top(y));
             store_chunk8<EVEN>((uint8_t*)p.y + row * p.ldy + c, n, chunk_fp8(y, b));

@@ -1,0 +1,80 @@
+"""The 8-bit operators at the ends of their number ranges, against their 64-bit
+formulas."""
+import pytest
+import torch
+
+import ops_reference as ref
+from pipelined_tiled_dense_amd import binding as bd
+
+pytestmark = pytest.mark.gpu
+
+BF16, FP8 = torch.bfloat16, torch.float8_e4m3fn
+BF16_MAX = float(torch.finfo(BF16).max)
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gpu():
+    if not torch.cuda.is_available():
+        pytest.fail("no GPU visible")
+    bd.library()
+    yield
+
+
+@pytest.fixture(autouse=True)
+def named(request):
+    print("  %s" % request.node.name, flush=True)
+    yield
+    torch.cuda.synchronize()
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+# -- gated unit --------------------------------------------------------------------
+GATES = [-3.3e38, -1e30, -1e20, -1000.0, -217.0, -216.0, -200.0, -190.0, -177.0, -150.0, -128.0, -104.0, -100.0, -95.0, -90.0,
+         -89.0, -88.5, -88.0, -87.0, -20.0, -1.0, -1e-3, -1e-38, 0.0, 1e-38, 1.0, 20.0, 88.0, 150.0, 151.0, 1e30, 8e37, 1e38,
+         3.3e38]
+
+
+@pytest.mark.parametrize("size", [1.0, -1e-3, 1e-30, 1e18, 3e38])
+def test_swiglu_over_the_whole_range_of_gates(size):
+    """Every gate against many u of one magnitude.  The kernel's steps are three
+    exponentials of an ulp and a correction each, and five products: 16 U32.
+    What passes bf16's largest value becomes an infinity."""
+    g = torch.tensor(GATES, device="cuda").to(BF16)[:, None].expand(-1, 200)
+    u = ((torch.rand(len(GATES), 200, generator=gen(1), device="cuda") * 0.9 + 0.1) * size).to(BF16)
+    gu = torch.cat([g, u], 1)
+    want = ref.swiglu(gu.double())
+    rel = 16 * ref.U32
+    y = bd.swiglu(gu).double()
+    big = want.abs() > BF16_MAX * (1 - ref.U16)
+    assert ((y - want).abs() <= (ref.U16 + rel) * want.abs() + ref.TINY16)[~big].all()
+    assert (y[big].abs() >= BF16_MAX * (1 - ref.U16)).all() and (y[big].sign() == want[big].sign()).all()
+    # Rows whose products pass fp32's range have no 8-bit form.
+    fine = (want.abs().amax(1) < float(torch.finfo(torch.float32).max))
+    q, scale = bd.swiglu(gu[fine].contiguous(), quantize=True)
+    ref.check_quantized(q, scale, want[fine], 1, rel)
+
+
+def test_swiglu_nonfinite_gates():
+    """The formula's own values: an infinite gate passes u's sign on, minus
+    infinity and NaN are not numbers."""
+    g = torch.tensor([float("inf"), float("-inf"), float("nan"), -300.0])
+    y = bd.swiglu(torch.cat([g, torch.full_like(g, -2.0)]).to(BF16).cuda()[None])[0]
+    assert y[0] == float("-inf") and y[1].isnan() and y[2].isnan() and y[3] == 0
+
+
+def test_swiglu_one_low_gate_among_others():
+    """A single gate below the exponential's range in a chunk, at each place of a
+    row, leaves its neighbours as they are."""
+    F = 150
+    gu = torch.randn(F, 2 * F, generator=gen(2), device="cuda").to(BF16)
+    low = gu.clone()
+    i = torch.arange(F, device="cuda")
+    low[i, i] = -100.0
+    low[i, F + i] = 1e38
+    a, b, want = bd.swiglu(gu), bd.swiglu(low), ref.swiglu(low.double())
+    keep = ~torch.eye(F, dtype=torch.bool, device="cuda")
+    assert torch.equal(a[keep], b[keep])
+    assert ((b[i, i].double() - want[i, i]).abs() <= (ref.U16 + 16 * ref.U32) * want[i, i].abs()).all()
