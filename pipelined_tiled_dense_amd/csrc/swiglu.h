@@ -49,6 +49,8 @@ __device__ __forceinline__ Sigmoid sigmoid(float x)
 // (its ulp alone turned twice as many 8-bit roundings as the other steps; 3 us at
 // 8192 x 8192).
 constexpr float kLowGate = -88.5f;
+// The gradients': higher, so that u s stays a normal number for every u that matters.
+constexpr float kLowGateGrad = -40.0f;
 
 __device__ __forceinline__ float silu_times(float x, float u)
 {
@@ -63,21 +65,39 @@ __device__ __forceinline__ float silu_times(float x, float u)
     return (0.25f * x) * r * u;
 }
 
-// The same below kLowGate, where 1 + exp(-x) is exp(-x) to fp32: x u exp(x), with
-// exp(x) as the third power of f = exp(x / 3), a normal number, and f taken to u
-// and to x first, so that a large u meets the small factors before anything
-// overflows or is lost.  From -216 on down |x u exp(x)| is below bf16's smallest
-// value for every u, and a zero comes out; minus infinity is -inf / inf.
-__device__ __forceinline__ float silu_times_low(float x, float u)
+// Below these gates 1 + exp(-x) is exp(-x) to fp32, and exp(x) the third power of f =
+// exp(x / 3), a normal number: each of the factors beside exp(x) takes an f first,
+// so that a large one meets a small one before anything overflows or is lost.
+// v_exp_f32 makes f zero from -262 on down, where what is left is below bf16's
+// smallest value (beside one large factor; beside two, below 2^-114).  The bound
+// on x keeps infinities out of the products; minus infinity is left to the formula.
+struct LowGate {
+    float x, f;
+};
+
+__device__ __forceinline__ LowGate low_gate(float x)
 {
     constexpr float kThird = 0x1.ec709ep-2f, kThirdRest = -0x1.e2fe02p-29f, kLn2 = 0x1.62e430p-1f;   // (log2 e) / 3
-    const float xc = x < -216.0f ? -216.0f : x;
+    const float xc = x < -1000.0f ? -1000.0f : x;
     const float p = xc * kThird;
     const float rest = __builtin_fmaf(xc, kThirdRest, __builtin_fmaf(xc, kThird, -p));
     const float f0 = __builtin_amdgcn_exp2f(p);
-    const float f = __builtin_fmaf(f0, rest * kLn2, f0);
-    const float y = (u * f) * (xc * f) * f;
-    return x == -__builtin_inff() ? __builtin_nanf("") : y;
+    return {x == -__builtin_inff() ? __builtin_nanf("") : xc, __builtin_fmaf(f0, rest * kLn2, f0)};
+}
+
+__device__ __forceinline__ float silu_times_low(float x, float u)
+{
+    const LowGate l = low_gate(x);
+    return (u * l.f) * (l.x * l.f) * l.f;
+}
+
+__device__ __forceinline__ float lowest(u32x4_t gv)
+{
+    float low = 0.0f;
+#pragma unroll
+    for (int e = 0; e < kChunk; ++e)
+        low = __builtin_fminf(low, chunk_at(gv, e));
+    return low;
 }
 
 // 8 gates and their u.  Gates below kLowGate are rare: a branch that no lane of
@@ -85,11 +105,7 @@ __device__ __forceinline__ float silu_times_low(float x, float u)
 // low gates corrected after the others).
 __device__ __forceinline__ void silu_chunk(u32x4_t gv, u32x4_t uv, float (&y)[kChunk])
 {
-    float low = 0.0f;
-#pragma unroll
-    for (int e = 0; e < kChunk; ++e)
-        low = __builtin_fminf(low, chunk_at(gv, e));
-    if (__builtin_expect(low < kLowGate, 0)) {
+    if (__builtin_expect(lowest(gv) < kLowGate, 0)) {
 #pragma unroll
         for (int e = 0; e < kChunk; ++e) {
             const float g = chunk_at(gv, e), u = chunk_at(uv, e);
@@ -149,12 +165,28 @@ __global__ void __launch_bounds__(256) k_swiglu_bwd(SwigluParams p)
         const u32x4_t gv = load_chunk<EVEN>(src, n, c), uv = load_chunk<EVEN>(src + p.F, n, c);
         const u32x4_t dv = load_chunk<EVEN>(p.dy + row * p.lddy + c, n, c);
         float dg[kChunk], du[kChunk];
-#pragma unroll
-        for (int e = 0; e < kChunk; ++e) {
+        auto gradient = [&](int e) {
             const float g = chunk_at(gv, e), d = chunk_at(dv, e);
             const Sigmoid s = sigmoid(g);
             du[e] = d * (g * s.s);
-            dg[e] = d * chunk_at(uv, e) * (s.s * __builtin_fmaf(g, s.c, 1.0f));
+            dg[e] = d * (chunk_at(uv, e) * (s.s * __builtin_fmaf(g, s.c, 1.0f)));   // d * u alone may overflow
+        };
+        if (__builtin_expect(lowest(gv) < kLowGateGrad, 0)) {
+#pragma unroll
+            for (int e = 0; e < kChunk; ++e) {
+                if (chunk_at(gv, e) < kLowGateGrad) {
+                    const LowGate l = low_gate(chunk_at(gv, e));
+                    const float d = chunk_at(dv, e) * l.f;
+                    du[e] = d * (l.x * l.f) * l.f;
+                    dg[e] = d * (chunk_at(uv, e) * l.f) * ((1.0f + l.x) * l.f);
+                } else {
+                    gradient(e);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < kChunk; ++e)
+                gradient(e);
         }
         uint16_t* dst = (uint16_t*)p.y + row * p.ldy + c;
         store_chunk<EVEN>(dst, n, chunk_bf16(dg));

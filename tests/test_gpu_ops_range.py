@@ -78,3 +78,25 @@ def test_swiglu_one_low_gate_among_others():
     keep = ~torch.eye(F, dtype=torch.bool, device="cuda")
     assert torch.equal(a[keep], b[keep])
     assert ((b[i, i].double() - want[i, i]).abs() <= (ref.U16 + 16 * ref.U32) * want[i, i].abs()).all()
+
+
+@pytest.mark.parametrize("dy_size", [1e-3, 1.0, 1e18, 1e30])
+def test_swiglu_backward_over_the_whole_range_of_gates(dy_size):
+    """The gradients by the same gates, under gradients and u of any magnitude
+    whose formula stays inside bf16's range.  Bounds as for ordinary gates: 32
+    U32 of the terms' magnitudes, and the rounding."""
+    gates = [g for g in GATES if abs(g) < 1e36 or g < 0]
+    g = torch.tensor(gates, device="cuda").to(BF16)[:, None].expand(-1, 200)
+    rand = lambda seed: torch.rand(len(gates), 200, generator=gen(seed), device="cuda") * 0.9 + 0.1  # noqa: E731
+    dy = (rand(3) * dy_size).to(BF16)
+    for size in (1.0, -1e-3, 1e25):
+        u = (rand(4) * size).to(BF16)
+        want = ref.swiglu_bwd(dy.double(), torch.cat([g, u], 1).double())
+        s = 1.0 / (1.0 + torch.exp(-g.double()))
+        d = dy.double().abs()
+        # t e^g with the exponential's argument bounded: no infinity times zero.
+        dg_mag = d * u.double().abs() * s * (1.0 + (g.double().abs() * (1.0 - s)).clamp_max(1e300))
+        mag = torch.cat([dg_mag, d * g.double().abs() * s], 1)
+        got = bd.swiglu_backward(dy, torch.cat([g, u], 1)).double()
+        fine = mag < float(torch.finfo(BF16).max) / 4
+        assert ((got - want).abs() <= ref.U16 * want.abs() + 32 * ref.U32 * mag + ref.TINY16)[fine].all()
