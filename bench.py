@@ -7,7 +7,8 @@ Every (sync scheme, ring stages) configuration of the library is timed on it
 -- barrier sync at 2, 3 and 4 stages and over the split-window ring
 (stages 5), flag sync at 2, 3 and 4, the wave-specialised and the ping-pong
 kernels at 2, 3 and 4 -- and ``value`` is the fastest.  The other four
-workloads get the same matrix under ``workloads``.  Prints one JSON line.
+workloads get the same matrix under ``workloads``, with throughput and % of
+peak there and the other fields on stderr.  Prints one JSON line.
 
 Also reports:
   roofline      achieved matrix-core TFLOP/s of the fastest configuration's
@@ -462,6 +463,14 @@ def measure_workload(bd, w, configs, args, torch, A=None, B=None):
     return res, (A, B, dA, dB, C)
 
 
+def short_configs(results):
+    """What the result line keeps of each configuration of a workload other than
+    the headline one: readers of the line's last 16,000 characters get all of it
+    this way (it was 30,600 long with every field).  The other fields of these
+    configurations are on stderr, a line each as they are measured."""
+    return {cfg: {k: e[k] for k in ("tflops", "pct_of_peak")} for cfg, e in results.items()}
+
+
 # Untimed calls before torch.matmul is timed: measured at 8192^3, hipBLASLt's
 # kernel needs about 50 calls after another kernel ran before its throughput
 # settles (its first 25 ran ~13% below its steady state), against about 20
@@ -807,7 +816,7 @@ def main():
             b = max(res, key=lambda k: res[k]["tflops"])
             entry = {"M": ow.M, "N": ow.N, "K": ow.K, "b_layout": "N x K" if ow.b_transposed else "K x N",
                      "best": b, "tflops": res[b]["tflops"], "pct_of_peak": res[b]["pct_of_peak"],
-                     "configs": res}
+                     "configs": short_configs(res)}
             if not args.no_reference:
                 entry["reference_tflops"] = reference_matmul(odA, odB, oC, ow, args.steps, args.warmup,
                                                              torch)["tflops"]
