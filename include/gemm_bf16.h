@@ -473,7 +473,9 @@ int gemm_quantize_fp8(int64_t M, int64_t K, const void* X, int64_t ldx,
  * GEMM_TYPE_BF16: Y is bf16, and may be the very memory of x unless H is;
  * scale is ignored.  GEMM_TYPE_FP8: Y is 8 bits
  * with row scales (lds >= M).  The statistics and y use h before its rounding
- * to bf16.  rstd (M fp32 values) is written unless NULL.
+ * to bf16.  rstd (M fp32 values) is written unless NULL.  The mean is right for
+ * rows of any magnitude, also where the squares leave fp32's range; a row of
+ * zeros with eps 0 gives NaN, and one of subnormal values an infinite rstd.
  * M == 0 is a no-op.  D is 1 .. GEMM_NORM_MAX_WIDTH (GEMM_ERR_INVALID_VALUE
  * below, GEMM_ERR_UNSUPPORTED_SHAPE above); eps must be >= 0 and finite.
  */

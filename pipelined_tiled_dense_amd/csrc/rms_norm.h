@@ -44,8 +44,16 @@ __device__ __forceinline__ float group_sum(float x, float* red, int nw)
     return s;
 }
 
+// Where a mean square is sure to hold no subnormal or lost squares, and a sum no
+// infinite ones.
+constexpr float kLeastMean = 0x1p-100f, kMostSum = 0x1.fffffep127f;
+
+// Six waves per SIMD where the registers would allow five for the sake of a few
+// values (6220 x 5001 to bf16: 63.7 us, 67.4 with five); four, as 1024 threads have
+// at the least, leaves the other forms as they come out.
 template <int NCH, bool FP8, bool EVEN>
-__global__ void __launch_bounds__(1024) k_rms_norm(NormParams p, int nw)
+__global__ void __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(NCH == 2 && !FP8 && !EVEN ? 6 : 4)))
+k_rms_norm(NormParams p, int nw)
 {
     __shared__ float red[2][16];
     const int lane_t = nw == 1 ? (threadIdx.x & 63) : threadIdx.x;
@@ -79,7 +87,25 @@ __global__ void __launch_bounds__(1024) k_rms_norm(NormParams p, int nw)
             }
         ss = group_sum(ss, red[parity], nw);
         parity ^= 1;
-        const float rstd = 1.0f / __builtin_sqrtf(ss * p.inv_d + p.eps);
+        float mean = ss * p.inv_d + p.eps, size = 1.0f;
+        // Squares beyond fp32's range, from |h| = 2^64 / sqrt(D) up or, with eps near
+        // zero, below 2^-50: the row's sum again, of values times a power of two.
+        // Every lane of the row holds the same sum, so the row's lanes branch together.
+        if (__builtin_expect(!(mean >= kLeastMean && ss <= kMostSum), 0)) {
+            size = mean < 1.0f ? 0x1p80f : 0x1p-80f;
+            ss = 0.0f;
+#pragma unroll
+            for (int i = 0; i < NCH; ++i)
+#pragma unroll
+                for (int e = 0; e < kChunk; ++e) {
+                    const float v = size * (r ? chunk_at(xv[i], e) + chunk_at(rv[i], e) : chunk_at(xv[i], e));
+                    ss = __builtin_fmaf(v, v, ss);
+                }
+            ss = group_sum(ss, red[parity], nw);
+            parity ^= 1;
+            mean = ss * p.inv_d + p.eps * size * size;
+        }
+        const float rstd = size / __builtin_sqrtf(mean);
         if (p.rstd && lane_t == 0)
             p.rstd[row] = rstd;
 #pragma unroll

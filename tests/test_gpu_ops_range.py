@@ -100,3 +100,37 @@ def test_swiglu_backward_over_the_whole_range_of_gates(dy_size):
         got = bd.swiglu_backward(dy, torch.cat([g, u], 1)).double()
         fine = mag < float(torch.finfo(BF16).max) / 4
         assert ((got - want).abs() <= ref.U16 * want.abs() + 32 * ref.U32 * mag + ref.TINY16)[fine].all()
+
+
+# -- norm ------------------------------------------------------------------------
+def rows_of(sizes, D, seed):
+    """A bf16 row of D normal values, limited to 4, for each size."""
+    x = torch.randn(len(sizes), D, generator=gen(seed), device="cuda").clamp(-4, 4)
+    return (x * torch.tensor(sizes, device="cuda")[:, None]).to(BF16)
+
+
+@pytest.mark.parametrize("quantize", [False, True], ids=["bf16", "fp8"])
+@pytest.mark.parametrize("residual", [False, True], ids=["plain", "residual"])
+@pytest.mark.parametrize("D", [1, 300, 2048, 5005, 9001, 16384, 32761])
+def test_rms_norm_rows_of_any_magnitude(D, residual, quantize):
+    """Rows whose squares leave fp32's range at either end, with ordinary rows
+    between them: the same bounds as anywhere else."""
+    sizes = [1e-36, 1.0, 1e-25, 1e-19, 1e18, 1e20, 3.0, 1e30, 2e37]
+    eps = 0.0
+    x, w = rows_of(sizes, D, D), rows_of([1.0], D, 5)[0].abs() + 0.5
+    r = rows_of(sizes, D, D + 1) if residual else None
+    out = bd.rms_norm(x, w, residual=r, eps=eps, quantize=quantize, return_rstd=True)
+    h, rstd, y = ref.rms_norm(x.double(), None if r is None else r.double(), w.double(), eps)
+    rel = (D / 2 + 8) * ref.U32
+    # rstd itself is below fp32's normal range where a row's values are at its top: its steps there are 2^-149.
+    assert ((out.rstd.double() - rstd).abs() <= rel * rstd + 2.0 ** -149).all()
+    rel += 2.0 ** -149 / float(rstd.min())
+    if quantize:
+        ref.check_quantized(out.y, out.scale, y, 1, rel)
+    else:
+        assert ((out.y.double() - y).abs() <= (ref.U16 + rel) * y.abs() + ref.TINY16).all()
+    # Mixed magnitudes within a row: the large values carry the sum.
+    m = x[:3].repeat(1, 1)
+    m[:, D // 2] = 1e38
+    got, want = bd.rms_norm(m, w, eps=1e-6).y.double(), ref.rms_norm(m.double(), None, w.double(), 1e-6)[2]
+    assert ((got - want).abs() <= (ref.U16 + rel) * want.abs() + ref.TINY16)[:, D // 2].all()
