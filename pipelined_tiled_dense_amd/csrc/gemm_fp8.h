@@ -11,15 +11,19 @@
 //
 // Two ways to contract a block of 128:
 //   fast    one v_mfma_f32_16x16x128_f8f6f4, twice the rate of bf16.  It adds
-//           each run of 8 products on a grid set by the largest of them: a share
-//           of about 2^-13 is lost (measured: 65536 + 1 = 65536 within a run,
-//           and an error of 1.5e-5 of the result's norm on random operands).
-//           That is a hundredth of bf16's rounding.
+//           each run of 8 consecutive products on a grid of 2^-13 of the run's
+//           largest: what a product has below the grid is cut off (measured: beside
+//           2^16 a product of 2^3 counts, 1.5 * 2^3 counts as 2^3, and 2^2 is
+//           lost; the sums of runs add up as fp32 sums do).  On random operands
+//           that is 1.5e-5 of the result's norm, a hundredth of bf16's rounding;
+//           where products cancel within a run it is whatever they leave.
 //   exact   the bytes converted to bf16, which holds every e4m3 value, and four
-//           v_mfma_f32_16x16x32_bf16, whose sums are fp32's (1e-8 on the same
-//           operands).  Half the matrix rate, and 16 conversions a fragment.
-// An fp32 C is computed exactly.  So is whatever does not wait for the matrix
-// cores: few rows (bound by B's bytes) and short sums (bound by C's).
+//           v_mfma_f32_16x16x32_bf16, whose sums are fp32's (0.7 to 1.1e-7 of the
+//           result's norm).  Half the matrix rate, and 16 conversions a fragment.
+// A bf16 C takes the fast way unless the caller asks for the exact one, which
+// costs 0.4 us at 1 x 8192 x 8192 (13.2), 0.9 at 64 x 8192 x 8192 (19.5), 65 at
+// 4096^3 (59) and 590 at 8192^3 (405).  An fp32 C and short sums (bound by C's
+// bytes) are computed exactly.
 //
 // A tile row of 128 bytes is what the bf16 product calls a row of 64 elements:
 // the tile configurations, the LDS ring with its swizzle and the raster are the
@@ -1221,9 +1225,9 @@ int run_tiles(int64_t M, int64_t N, const char* A, int64_t lda, const char* B, i
 // The product of operands whose rows fit the tiles' loads (16-byte boundaries, K
 // a multiple of 16), or, marked by a_fits and b_fits, do not.
 int run_fp8(int64_t M, int64_t N, const char* A, int64_t lda, bool a_fits, const char* B, int64_t ldb, bool b_fits,
-            Fp8Params q, int cus, TempMem& tm, hipStream_t s)
+            Fp8Params q, bool exact, int cus, TempMem& tm, hipStream_t s)
 {
-    const bool exact = q.c_fp32 || q.kblocks <= kShortBlocks;
+    exact = exact || q.kblocks <= kShortBlocks;
     const TileTimes& t128 = exact ? kExact128 : kFast128;
     int64_t time128 = 0;
     const int64_t splits = choose_fp8_splits(t128, M, N, q.kblocks, cus, &time128);
@@ -1305,6 +1309,8 @@ extern "C" int gemm_fp8_bt(int64_t M, int64_t N, int64_t K, const void* A, int64
                            const void* B, int64_t ldb, const float* SB, int64_t ldsb, int b_block_rows, void* C,
                            int64_t ldc, int c_type, void* stream)
 {
+    const bool exact = c_type & GEMM_FP8_EXACT || c_type == GEMM_TYPE_FP32;
+    c_type &= ~GEMM_FP8_EXACT;
     if (M < 0 || N < 0 || K < 0 || (b_block_rows != 1 && b_block_rows != kBlock) ||
         (c_type != GEMM_TYPE_BF16 && c_type != GEMM_TYPE_FP32))
         return GEMM_ERR_INVALID_VALUE;
@@ -1345,5 +1351,6 @@ extern "C" int gemm_fp8_bt(int64_t M, int64_t N, int64_t K, const void* A, int64
     auto fits = [&](const void* ptr, int64_t ld) {
         return K % 16 == 0 && ld % 16 == 0 && ld <= 2 * kMaxLd && ((uintptr_t)ptr & 15) == 0;
     };
-    return run_fp8(M, N, (const char*)A, lda, fits(A, lda), (const char*)B, ldb, fits(B, ldb), q, cus, tm, s);
+    return run_fp8(M, N, (const char*)A, lda, fits(A, lda), (const char*)B, ldb, fits(B, ldb), q, exact, cus, tm,
+                   s);
 }

@@ -25,10 +25,11 @@ class Gradients(NamedTuple):
 class FeedForward:
     """The block with bfloat16 weights ``norm`` (D,), ``gate_up`` (2F, D) and
     ``down`` (D, F).  ``training`` also keeps the transposed weights that the
-    gradients of the activations read."""
+    gradients of the activations read; ``exact`` computes every product with
+    fp32's sums (see ``binding.gemm_fp8``)."""
 
-    def __init__(self, norm, gate_up, down, *, eps=1e-6, training=False):
-        self.eps, self.training = eps, training
+    def __init__(self, norm, gate_up, down, *, eps=1e-6, training=False, exact=False):
+        self.eps, self.training, self.exact = eps, training, exact
         self.set_weights(norm, gate_up, down)
 
     def set_weights(self, norm, gate_up, down):
@@ -44,15 +45,15 @@ class FeedForward:
         """(out, h) for x (M, D), any M: the block's output and the residual
         stream it is to be added to (x itself without a residual)."""
         n = binding.rms_norm(x, self.norm, residual=residual, eps=self.eps, quantize=True)
-        gu = binding.gemm_fp8(n.y, n.scale, *self.gate_up)
-        out = binding.gemm_fp8(*binding.swiglu(gu, quantize=True), *self.down)
+        gu = binding.gemm_fp8(n.y, n.scale, *self.gate_up, exact=self.exact)
+        out = binding.gemm_fp8(*binding.swiglu(gu, quantize=True), *self.down, exact=self.exact)
         return out, (x if residual is None else n.h)
 
     def forward(self, x, residual=None):
         """As the call, and what ``backward`` reads: (out, h, saved)."""
         n = binding.rms_norm(x, self.norm, residual=residual, eps=self.eps, quantize=True, return_rstd=True)
-        gu = binding.gemm_fp8(n.y, n.scale, *self.gate_up)
-        out = binding.gemm_fp8(*binding.swiglu(gu, quantize=True), *self.down)
+        gu = binding.gemm_fp8(n.y, n.scale, *self.gate_up, exact=self.exact)
+        out = binding.gemm_fp8(*binding.swiglu(gu, quantize=True), *self.down, exact=self.exact)
         h = x if residual is None else n.h
         return out, h, (h, n.rstd, gu)
 
@@ -67,11 +68,11 @@ class FeedForward:
         quantize, product, f32 = binding.quantize_fp8, binding.gemm_fp8, torch.float32
         h, rstd, gu = saved
         ddown = product(*quantize(dout, transposed=True), *quantize(binding.swiglu(gu), transposed=True), out_dtype=f32)
-        dgu = binding.swiglu_backward(product(*quantize(dout), *self.down_t), gu)
+        dgu = binding.swiglu_backward(product(*quantize(dout), *self.down_t, exact=self.exact), gu)
         n = binding.rms_norm(h, self.norm, eps=self.eps).y
         dgate_up = product(*quantize(dgu, transposed=True), *quantize(n, transposed=True), out_dtype=f32)
-        dx, dnorm = binding.rms_norm_backward(product(*quantize(dgu), *self.gate_up_t), h, self.norm, rstd,
-                                              dresidual=dh)
+        dx, dnorm = binding.rms_norm_backward(product(*quantize(dgu), *self.gate_up_t, exact=self.exact), h, self.norm,
+                                              rstd, dresidual=dh)
         return Gradients(dx, dnorm, dgate_up, ddown)
 
 

@@ -172,3 +172,15 @@ def test_quantized_check_accepts_the_nearest_values_and_nothing_else(block_rows)
         ref.check_quantized(q, scale * 1.001, y, block_rows, 0.0)
     with pytest.raises(AssertionError):
         ref.check_quantized(q, scale.flip(0), y, block_rows, 0.0)
+
+
+def test_exact_sums_are_a_flag_of_the_product_alone():
+    """GEMM_FP8_EXACT goes with both of the product's types and with nothing else."""
+    import os
+    import re
+    text = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "gemm_bf16.h")).read()
+    assert int(re.search(r"GEMM_FP8_EXACT = (\d+)", text).group(1)) == bd.FP8_EXACT
+    assert gemm(ctype=bd.TYPE_FP8 | bd.FP8_EXACT) == BAD and gemm(ctype=bd.FP8_EXACT * 2) == BAD
+    assert norm(yt=bd.TYPE_BF16 | bd.FP8_EXACT) == BAD and swiglu(yt=bd.TYPE_FP8 | bd.FP8_EXACT) == BAD
+    if not torch.cuda.is_available():
+        assert gemm(ctype=bd.TYPE_BF16 | bd.FP8_EXACT) == DEVICE and gemm(ctype=bd.TYPE_FP32 | bd.FP8_EXACT) == DEVICE
