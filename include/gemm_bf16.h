@@ -428,6 +428,11 @@ enum { GEMM_NORM_MAX_WIDTH = 32768 };
  * the rounding to bf16, and at most 7 * 2^-13 of each run's largest product;
  * where large products cancel within a run, a small one beside them is lost.
  *
+ * The products SA * SB are formed in fp32 and have to be 0 or between 2^-126 and
+ * 2^127 in magnitude: below, bits of the block's share of C are lost, and above,
+ * it is infinite, NaN where the block's sum is 0.  (Scales of blocks of zeros may
+ * be anything finite that does not make an infinity.)
+ *
  * b_block_rows is 128 (a weight's blocks, ldsb >= ceil(N / 128)) or 1 (row
  * scales, ldsb >= N); ldsa >= M.  c_type is GEMM_TYPE_BF16 or GEMM_TYPE_FP32,
  * either with GEMM_FP8_EXACT (which an fp32 C implies) added; ldc >= N.  A bf16 C

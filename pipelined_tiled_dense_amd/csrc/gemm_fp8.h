@@ -4,7 +4,9 @@
 //   C[i][j] = sum_kb sa[kb][i] * sb[kb][j or j / 128] * sum_{k in kb} A[i][k] * B[j][k]
 //
 // A block's partial sums start from zero and enter the running sums by one fused
-// multiply-add each, times the product of the two scales.  The MFMA's rows are
+// multiply-add each, times the product of the two scales, which has to be a normal
+// number: one scale after the other would take any pair whose result fits, at
+// four more products beside each MFMA's four multiply-adds.  The MFMA's rows are
 // B's (n) and its columns A's (m): a lane then holds 4 consecutive columns of one
 // row of C, so a block's scale product is one value per lane and fragment,
 // shared by every fragment of that row against the same 128 columns.
@@ -641,7 +643,7 @@ __global__ void __launch_bounds__(C::THREADS, 2) k_gemm_fp8_exact(Params p, Fp8P
                 for (int i = 0; i < C::FM; ++i)
 #pragma unroll
                     for (int e = 0; e < 16; ++e)
-                        acc[i][j][e] = __builtin_fmaf(ROWB ? part[i][j][e] * sbj[e / 4][e % 4] : part[i][j][e], sai[i],
+                        acc[i][j][e] = __builtin_fmaf(part[i][j][e], ROWB ? sai[i] * sbj[e / 4][e % 4] : sai[i],
                                                       acc[i][j][e]);
             }
             s ^= 1;

@@ -112,3 +112,23 @@ def test_the_block_takes_the_way_it_is_given():
         grads.append(dx)
         assert torch.equal(b.backward(saved, dout).x, dx)
     assert not torch.equal(*grads)
+
+
+@pytest.mark.parametrize("exact", [False, True], ids=["fast", "exact"])
+@pytest.mark.parametrize("b_rows", [128, 1])
+@pytest.mark.parametrize("M,N,K", [(1, 200, 512), (60, 300, 520), (2000, 2030, 1040), (300, 260, 200)])
+def test_scales_whose_product_is_a_normal_number(M, N, K, b_rows, exact):
+    """One scale large and the other small, and both small or large, up to a
+    product at either end of the stated range: whole numbers and powers of two,
+    so the result is the exact one in every kernel."""
+    g = gen(K)
+    a = torch.randint(-4, 5, (M, K), generator=g, device="cuda").float().to(FP8)
+    b = torch.randint(-4, 5, (N, K), generator=g, device="cuda").float().to(FP8)
+    kb, cols = ref.nblocks(K), -(-N // b_rows)
+    for ea, eb in ((-110, 125), (125, -110), (-120, 100), (100, -120), (-63, -63), (-126, 0), (60, 50), (110, 0)):
+        sa, sb = torch.full((kb, M), 2.0 ** ea, device="cuda"), torch.full((kb, cols), 2.0 ** eb, device="cuda")
+        want, _ = ref.gemm(a, sa, b, sb, b_rows)
+        c = bd.gemm_fp8(a, sa, b, sb, exact=exact)
+        assert torch.equal(c, want.float().to(BF16)), (ea, eb)
+        if exact:
+            assert torch.equal(bd.gemm_fp8(a, sa, b, sb, out_dtype=F32).double(), want), (ea, eb)
