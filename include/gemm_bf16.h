@@ -459,6 +459,32 @@ int gemm_fp8_bt(int64_t M, int64_t N, int64_t K,
                 const void* B, int64_t ldb, const float* SB, int64_t ldsb, int b_block_rows,
                 void* C, int64_t ldc, int c_type, void* stream);
 
+/* How gemm_fp8_bt computes a product (see gemm_fp8_plan_cus). */
+typedef struct gemm_fp8_plan {
+    int32_t rows, cols;       /* of C, that a workgroup computes at a time */
+    int32_t few_rows;         /* 1: the waves of a workgroup share k, operands of any alignment;
+                                 0: tiles through LDS */
+    int32_t exact;            /* 1: fp32's sums */
+    int32_t threads;          /* per workgroup */
+    int32_t reserved;
+    int64_t tiles;            /* ceil(M / rows) * ceil(N / cols) */
+    int64_t k_splits;         /* chunks of k, summed by a second launch where there are several */
+    int64_t k_blocks;         /* blocks of 128 per chunk, the last one's may be fewer */
+    int64_t grid;             /* workgroups of the main launch */
+    int64_t workspace_bytes;  /* the chunks' sums (0 with one chunk) */
+    int64_t pad_bytes;        /* zero-padded copies of operands that the tiles cannot read */
+} gemm_fp8_plan_t;
+
+/*
+ * gemm_fp8_plan_cus: what gemm_fp8_bt does on a device with `compute_units`
+ * compute units (256 on an MI355X), without querying one.  a_aligned, b_aligned:
+ * whether the operand's rows start on 16-byte boundaries.  Sizes, b_block_rows and
+ * c_type are checked as in gemm_fp8_bt; a null `out` or compute_units < 1 is
+ * GEMM_ERR_INVALID_VALUE.  With an empty product every field is 0.
+ */
+int gemm_fp8_plan_cus(int64_t M, int64_t N, int64_t K, int b_block_rows, int c_type, int a_aligned, int b_aligned,
+                      int compute_units, gemm_fp8_plan_t* out);
+
 /*
  * gemm_quantize_fp8: quantises bf16 X (M x K, ldx >= K) into Q and scales.
  * block_rows 1: a scale for each row and k block; 128: for each 128 x 128

@@ -57,6 +57,16 @@ class Plan(ctypes.Structure):
         return {name: getattr(self, name) for name, _ in self._fields_}
 
 
+class Fp8Plan(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("cols", ctypes.c_int32), ("few_rows", ctypes.c_int32),
+                ("exact", ctypes.c_int32), ("threads", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("tiles", ctypes.c_int64), ("k_splits", ctypes.c_int64), ("k_blocks", ctypes.c_int64),
+                ("grid", ctypes.c_int64), ("workspace_bytes", ctypes.c_int64), ("pad_bytes", ctypes.c_int64)]
+
+    def as_dict(self):
+        return {name: getattr(self, name) for name, _ in self._fields_ if name != "reserved"}
+
+
 _lib = None
 
 
@@ -100,7 +110,8 @@ def library() -> ctypes.CDLL:
         lib.gemm_rms_norm_bwd.argtypes = [i64, i64, p, i64, p, i64, p, p, p, i64, p, i64, p, p]
         lib.gemm_swiglu.argtypes = [i64, i64, p, i64, p, i64, i32, p, i64, p]
         lib.gemm_swiglu_bwd.argtypes = [i64, i64, p, i64, p, i64, p, i64, p]
-        for name in ("gemm_fp8_bt", "gemm_quantize_fp8", "gemm_rms_norm", "gemm_rms_norm_bwd", "gemm_swiglu",
+        lib.gemm_fp8_plan_cus.argtypes = [i64, i64, i64, i32, i32, i32, i32, i32, ctypes.POINTER(Fp8Plan)]
+        for name in ("gemm_fp8_bt", "gemm_fp8_plan_cus", "gemm_quantize_fp8", "gemm_rms_norm", "gemm_rms_norm_bwd", "gemm_swiglu",
                      "gemm_swiglu_bwd"):
             getattr(lib, name).restype = i32
         _lib = lib
@@ -194,6 +205,15 @@ def gemm_bf16_clock_samples(reset: bool = False) -> dict:
 
 def gemm_fp8_bt(M, N, K, A, lda, SA, ldsa, B, ldb, SB, ldsb, b_block_rows, C, ldc, c_type, stream) -> int:
     return library().gemm_fp8_bt(M, N, K, A, lda, SA, ldsa, B, ldb, SB, ldsb, b_block_rows, C, ldc, c_type, stream)
+
+
+def gemm_fp8_plan_cus(M, N, K, b_block_rows, c_type, a_aligned, b_aligned, compute_units) -> dict:
+    out = Fp8Plan()
+    rc = library().gemm_fp8_plan_cus(M, N, K, b_block_rows, c_type, int(bool(a_aligned)), int(bool(b_aligned)),
+                                     compute_units, ctypes.byref(out))
+    if rc != GEMM_OK:
+        raise GemmError(rc, "gemm_fp8_plan_cus")
+    return out.as_dict()
 
 
 def gemm_quantize_fp8(M, K, X, ldx, Q, ldq, scale, lds, block_rows, transposed, stream) -> int:

@@ -1035,21 +1035,22 @@ __global__ void __launch_bounds__(256) k_reduce_chunks(SkinnyParams p, Fp8Params
 }
 
 template <int MF, int NF, int DEPTH>
-int launch_skinny(SkinnyParams p, const Fp8Params& q, bool exact, bool any, int64_t chunks, TempMem& tm, hipStream_t s)
+int launch_skinny(SkinnyParams p, const Fp8Params& q, const gemm_fp8_plan_t& pl, bool any, TempMem& tm, hipStream_t s)
 {
     p.tiles_m = (int32_t)((p.M + MF * 16 - 1) / (MF * 16));
     p.tiles_n = (int32_t)((p.N + NF * 16 - 1) / (NF * 16));
-    p.chunk = (int32_t)((q.kblocks + chunks - 1) / chunks);
-    chunks = (q.kblocks + p.chunk - 1) / p.chunk;
+    p.chunk = (int32_t)pl.k_blocks;
+    const bool exact = pl.exact;
+    const int64_t chunks = pl.k_splits;
     void* ws = nullptr;
     hipEvent_t done = nullptr;
     if (chunks > 1) {
-        const int rc = temp_take(tm, chunks * p.M * p.N * 4, s, &ws, &done);
+        const int rc = temp_take(tm, pl.workspace_bytes, s, &ws, &done);
         if (rc != GEMM_OK)
             return rc;
     }
     p.partial = (float*)ws;
-    const dim3 g((unsigned)((p.tiles_n + 7) / 8 * 8 * p.tiles_m), (unsigned)chunks), b(kSkinnyWaves * 64);
+    const dim3 g((unsigned)(pl.grid / chunks), (unsigned)chunks), b(kSkinnyWaves * 64);
     // Operands of any alignment take wider addresses and a dword more: less depth
     // leaves them the registers.
     auto run = [&]<bool ROWB, bool EXACT>() {
@@ -1147,21 +1148,16 @@ int64_t choose_fp8_splits(const TileTimes& t, int64_t M, int64_t N, int64_t kblo
 }
 
 template <class C>
-int launch_tiles(Params p, const Fp8Params& q, int64_t splits, int cus, int per_cu, TempMem& tm, hipStream_t s)
+int launch_tiles(Params p, const Fp8Params& q, const gemm_fp8_plan_t& pl, TempMem& tm, hipStream_t s)
 {
     p.tiles_m = (int32_t)((p.M + C::BM - 1) / C::BM);
     p.tiles_n = (int32_t)((p.N + C::BN - 1) / C::BN);
-    const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n, slots = (int64_t)cus * per_cu;
-    if (tiles * kMaxSplits > INT32_MAX)
-        return GEMM_ERR_UNSUPPORTED_SHAPE;
-    p.k_steps = (int32_t)((q.kblocks + splits - 1) / splits);
-    p.splits = (int32_t)((q.kblocks + p.k_steps - 1) / p.k_steps);   // no empty chunk
+    p.splits = (int32_t)pl.k_splits;
     // The load cursor runs two positions ahead and crosses at most one tile
     // border: a single k-step is followed by one that reads zeros.
-    if (p.k_steps < 2)
-        p.k_steps = 2;
+    p.k_steps = pl.k_blocks < 2 ? 2 : (int32_t)pl.k_blocks;
     p.ksplit = (int64_t)p.k_steps * (kBlock / 2);
-    p.tiles_mn = p.span = (int32_t)tiles;
+    p.tiles_mn = p.span = (int32_t)pl.tiles;
     p.tile_base = 0;
     p.tiles = p.span * p.splits;
     p.group_m = 4;
@@ -1169,12 +1165,12 @@ int launch_tiles(Params p, const Fp8Params& q, int64_t splits, int cus, int per_
     void* ws = nullptr;
     hipEvent_t done = nullptr;
     if (p.splits > 1) {
-        const int rc = temp_take(tm, (int64_t)p.tiles * C::BM * C::BN * 4, s, &ws, &done);
+        const int rc = temp_take(tm, pl.workspace_bytes, s, &ws, &done);
         if (rc != GEMM_OK)
             return rc;
         p.partial = (float*)ws;
     }
-    const dim3 grid((unsigned)(p.tiles < slots ? p.tiles : slots)), block(C::THREADS);
+    const dim3 grid((unsigned)pl.grid), block(C::THREADS);
     const bool rowb = q.sb_shift == 0;
     if constexpr (C::MF == 32) {
         if (rowb)
@@ -1190,7 +1186,7 @@ int launch_tiles(Params p, const Fp8Params& q, int64_t splits, int cus, int per_
     int rc = launched();
     if (p.splits > 1) {
         if (rc == GEMM_OK) {
-            hipExtLaunchKernelGGL(k_reduce_fp8<C>, dim3(flat_grid(tiles * (C::BM * C::BN / 4))), dim3(256), 0, s,
+            hipExtLaunchKernelGGL(k_reduce_fp8<C>, dim3(flat_grid(pl.tiles * (C::BM * C::BN / 4))), dim3(256), 0, s,
                                   nullptr, done, 0, p, q);
             rc = launched();
         }
@@ -1203,7 +1199,7 @@ int launch_tiles(Params p, const Fp8Params& q, int64_t splits, int cus, int per_
 // The product in tiles, on operands whose rows start on 16-byte boundaries, K a
 // multiple of 16.
 int run_tiles(int64_t M, int64_t N, const char* A, int64_t lda, const char* B, int64_t ldb, const Fp8Params& q,
-              int64_t splits, int64_t time128, bool exact, int cus, TempMem& tm, hipStream_t s)
+              const gemm_fp8_plan_t& pl, TempMem& tm, hipStream_t s)
 {
     Params p;
     memset(&p, 0, sizeof p);
@@ -1215,47 +1211,50 @@ int run_tiles(int64_t M, int64_t N, const char* A, int64_t lda, const char* B, i
     p.lda = lda / 2;
     p.ldb = ldb / 2;
     p.clock_on = g_clock_on.load(std::memory_order_relaxed) ? 1u : 0u;
-    // The exact way takes 128 x 128 tiles at any size: its fragments are twice
-    // as large, and beside more running sums they do not fit a wave's registers.
-    if (exact)
-        return launch_tiles<Fp8Cfg<128, 128, 2, 2, 32>>(p, q, splits, cus, 2, tm, s);
-    if (tiles_time(kFast256, 256, 1, M, N, q.kblocks, 1, cus) < time128)
-        return launch_tiles<Fp8Cfg<256, 256, 2, 4>>(p, q, 1, cus, 1, tm, s);
-    return launch_tiles<Fp8Cfg<128, 128, 2, 2>>(p, q, splits, cus, 2, tm, s);
+    if (pl.exact)
+        return launch_tiles<Fp8Cfg<128, 128, 2, 2, 32>>(p, q, pl, tm, s);
+    if (pl.rows == 256)
+        return launch_tiles<Fp8Cfg<256, 256, 2, 4>>(p, q, pl, tm, s);
+    return launch_tiles<Fp8Cfg<128, 128, 2, 2>>(p, q, pl, tm, s);
 }
 
-// The product of operands whose rows fit the tiles' loads (16-byte boundaries, K
-// a multiple of 16), or, marked by a_fits and b_fits, do not.
-int run_fp8(int64_t M, int64_t N, const char* A, int64_t lda, bool a_fits, const char* B, int64_t ldb, bool b_fits,
-            Fp8Params q, bool exact, int cus, TempMem& tm, hipStream_t s)
+// The few-rows kernel's shapes: rows in fragments of 16, and as many columns as
+// keep the most compute units busy for the fewest bytes.
+constexpr struct {
+    int mf, nf;
+} kShapes[] = {{1, 1}, {1, 2}, {2, 2}, {4, 2}, {4, 4}};
+
+// The kernel, k chunks and launch of a product, from its sizes alone: `rowb` for
+// row scales of B, a_fits and b_fits for operands whose rows start on 16-byte
+// boundaries.  The call runs what stands here.
+int plan_fp8(int64_t M, int64_t N, int64_t K, bool rowb, bool exact, bool a_fits, bool b_fits, int cus,
+             gemm_fp8_plan_t* out)
 {
-    exact = exact || q.kblocks <= kShortBlocks;
+    const int64_t kblocks = ceil_div(K, kBlock);
+    exact = exact || kblocks <= kShortBlocks;
+    a_fits = a_fits && K % 16 == 0;
+    b_fits = b_fits && K % 16 == 0;
     const TileTimes& t128 = exact ? kExact128 : kFast128;
     int64_t time128 = 0;
-    const int64_t splits = choose_fp8_splits(t128, M, N, q.kblocks, cus, &time128);
+    const int64_t splits = choose_fp8_splits(t128, M, N, kblocks, cus, &time128);
 
-    // The few-rows kernel's shapes: rows in fragments of 16, and as many columns
-    // as keep the most compute units busy for the fewest bytes; k chunks where
-    // that leaves compute units idle, each with two blocks or more a wave (32 x 624
-    // x 13056: 17 us, 8.9 with chunks).  Not in the shape of 4 x 4 fragments, whose
-    // few waves with much each do not keep up with memory (32 x 3264 x 18176: 32 us
-    // in 5 chunks, tiles 17.5).
-    constexpr struct {
-        int mf, nf;
-    } kShapes[] = {{1, 1}, {1, 2}, {2, 2}, {4, 2}, {4, 4}};
+    // k chunks where few columns leave compute units idle, each with two blocks or
+    // more a wave (32 x 624 x 13056: 17 us, 8.9 with chunks).  Not in the shape of 4
+    // x 4 fragments, whose few waves with much each do not keep up with memory (32 x
+    // 3264 x 18176: 32 us in 5 chunks, tiles 17.5).
     const bool any = !a_fits || !b_fits;
     int shape = -1;
     int64_t skinny = 0, chunks = 1;
-    for (int i = 0; i < (exact || any || q.sb_shift == 0 ? 4 : 5); ++i) {
+    for (int i = 0; i < (exact || any || rowb ? 4 : 5); ++i) {
         const int64_t rows = kShapes[i].mf * 16, cols = kShapes[i].nf * 16;
         const int64_t groups = ceil_div(M, rows) * ceil_div(N, cols);
         if (groups >= (int64_t)1 << 22)
             continue;   // far from few rows, and past what a launch takes
         for (int64_t c = 1; c <= kMaxSplits; ++c) {
-            if (c > 1 && (i == 4 || groups * c > cus || q.kblocks < c * 2 * kSkinnyWaves))
+            if (c > 1 && (i == 4 || groups * c > cus || kblocks < c * 2 * kSkinnyWaves))
                 break;
             const int64_t turns = ceil_div(groups * c, cus), rate = i == 4 ? kSkinnyBytes44 : kSkinnyBytes[exact];
-            const int64_t v = turns * ((M < rows ? M : rows) + cols) * ceil_div(q.kblocks, c) * kBlock / rate +
+            const int64_t v = turns * ((M < rows ? M : rows) + cols) * ceil_div(kblocks, c) * kBlock / rate +
                               (turns - 1) * kSkinnyTurn * kShapes[i].mf * kShapes[i].nf +
                               (c > 1 ? kSplitLaunch + c * M * N * 8 / kChunkBytes : 0);
             if (shape < 0 || v < skinny) {
@@ -1265,14 +1264,56 @@ int run_fp8(int64_t M, int64_t N, const char* A, int64_t lda, bool a_fits, const
             }
         }
     }
-    if (shape >= 0 && skinny < time128 + (any ? kPadLaunch : 0) && (!any || q.K >= 16)) {
+
+    gemm_fp8_plan_t p;
+    memset(&p, 0, sizeof p);
+    p.exact = exact;
+    p.few_rows = shape >= 0 && skinny < time128 + (any ? kPadLaunch : 0) && (!any || K >= 16);
+    if (p.few_rows) {
+        p.rows = kShapes[shape].mf * 16;
+        p.cols = kShapes[shape].nf * 16;
+        p.threads = kSkinnyWaves * 64;
+        p.k_blocks = ceil_div(kblocks, chunks);
+        p.k_splits = ceil_div(kblocks, p.k_blocks);   // no empty chunk
+        p.tiles = ceil_div(M, p.rows) * ceil_div(N, p.cols);
+        // A multiple of 8 column tiles: each goes to one of the 8 XCDs.
+        p.grid = ceil_div(M, p.rows) * ceil_div(ceil_div(N, p.cols), 8) * 8 * p.k_splits;
+        p.workspace_bytes = p.k_splits > 1 ? p.k_splits * M * N * 4 : 0;
+        *out = p;
+        return GEMM_OK;
+    }
+    // The exact way takes 128 x 128 tiles at any size: its fragments are twice
+    // as large, and beside more running sums they do not fit a wave's registers.
+    const bool big = !exact && tiles_time(kFast256, 256, 1, M, N, kblocks, 1, cus) < time128;
+    p.rows = p.cols = big ? 256 : 128;
+    p.threads = big ? 512 : 256;
+    p.k_blocks = ceil_div(kblocks, big ? 1 : splits);
+    p.k_splits = ceil_div(kblocks, p.k_blocks);
+    p.tiles = ceil_div(M, p.rows) * ceil_div(N, p.cols);
+    if (p.tiles * kMaxSplits > INT32_MAX)
+        return GEMM_ERR_UNSUPPORTED_SHAPE;
+    const int64_t slots = (int64_t)cus * (big ? 1 : 2);
+    p.grid = p.tiles * p.k_splits < slots ? p.tiles * p.k_splits : slots;
+    p.workspace_bytes = p.k_splits > 1 ? p.tiles * p.k_splits * p.rows * p.cols * 4 : 0;
+    const int64_t K16 = (K + 15) & ~(int64_t)15;
+    p.pad_bytes = (a_fits ? 0 : align256(M * K16)) + (b_fits ? 0 : align256(N * K16));
+    *out = p;
+    return GEMM_OK;
+}
+
+// The product by its plan.
+int run_fp8(int64_t M, int64_t N, const char* A, int64_t lda, bool a_fits, const char* B, int64_t ldb, bool b_fits,
+            Fp8Params q, const gemm_fp8_plan_t& pl, TempMem& tm, hipStream_t s)
+{
+    const bool any = !a_fits || !b_fits;
+    if (pl.few_rows) {
         const SkinnyParams p{A, B, M, N, lda, ldb, 0, 0, 0, nullptr};
-        switch (shape) {
-        case 0: return launch_skinny<1, 1, 2>(p, q, exact, any, chunks, tm, s);
-        case 1: return launch_skinny<1, 2, 2>(p, q, exact, any, chunks, tm, s);
-        case 2: return launch_skinny<2, 2, 2>(p, q, exact, any, chunks, tm, s);
-        case 3: return launch_skinny<4, 2, 1>(p, q, exact, any, chunks, tm, s);
-        default: return launch_skinny<4, 4, 1>(p, q, exact, any, chunks, tm, s);
+        switch (pl.rows * 64 + pl.cols) {
+        case 16 * 64 + 16: return launch_skinny<1, 1, 2>(p, q, pl, any, tm, s);
+        case 16 * 64 + 32: return launch_skinny<1, 2, 2>(p, q, pl, any, tm, s);
+        case 32 * 64 + 32: return launch_skinny<2, 2, 2>(p, q, pl, any, tm, s);
+        case 64 * 64 + 32: return launch_skinny<4, 2, 1>(p, q, pl, any, tm, s);
+        default: return launch_skinny<4, 4, 1>(p, q, pl, any, tm, s);
         }
     }
 
@@ -1280,8 +1321,8 @@ int run_fp8(int64_t M, int64_t N, const char* A, int64_t lda, bool a_fits, const
     int rc = GEMM_OK;
     if (any) {
         const int64_t K16 = (q.K + 15) & ~(int64_t)15;
-        const int64_t a_pad = a_fits ? 0 : align256(M * K16), b_pad = b_fits ? 0 : align256(N * K16);
-        rc = temp_take(tm, a_pad + b_pad, s, &ws);
+        const int64_t a_pad = a_fits ? 0 : align256(M * K16);
+        rc = temp_take(tm, pl.pad_bytes, s, &ws);
         if (rc != GEMM_OK)
             return rc;
         const PadParams c{{(const uint8_t*)A, (const uint8_t*)B}, {(uint8_t*)ws, (uint8_t*)ws + a_pad},
@@ -1300,9 +1341,20 @@ int run_fp8(int64_t M, int64_t N, const char* A, int64_t lda, bool a_fits, const
         q.K = K16;   // the copies' zeros extend K to the 16-byte grid
     }
     if (rc == GEMM_OK)
-        rc = run_tiles(M, N, A, lda, B, ldb, q, splits, time128, exact, cus, tm, s);
+        rc = run_tiles(M, N, A, lda, B, ldb, q, pl, tm, s);
     const int frc = temp_give(tm, ws, s);
     return rc != GEMM_OK ? rc : frc;
+}
+
+bool fp8_exact(int c_type) { return (c_type & GEMM_FP8_EXACT) != 0 || c_type == GEMM_TYPE_FP32; }
+
+int fp8_shape(int64_t M, int64_t N, int64_t K, int b_block_rows, int c_type)
+{
+    const int type = c_type & ~GEMM_FP8_EXACT;
+    if (M < 0 || N < 0 || K < 0 || (b_block_rows != 1 && b_block_rows != kBlock) ||
+        (type != GEMM_TYPE_BF16 && type != GEMM_TYPE_FP32))
+        return GEMM_ERR_INVALID_VALUE;
+    return M > kMaxRows || N > kMaxLd || K > kMaxLd ? GEMM_ERR_UNSUPPORTED_SHAPE : GEMM_OK;
 }
 
 }  // namespace
@@ -1311,13 +1363,10 @@ extern "C" int gemm_fp8_bt(int64_t M, int64_t N, int64_t K, const void* A, int64
                            const void* B, int64_t ldb, const float* SB, int64_t ldsb, int b_block_rows, void* C,
                            int64_t ldc, int c_type, void* stream)
 {
-    const bool exact = c_type & GEMM_FP8_EXACT || c_type == GEMM_TYPE_FP32;
+    if (const int rc = fp8_shape(M, N, K, b_block_rows, c_type))
+        return rc;
+    const bool exact = fp8_exact(c_type);
     c_type &= ~GEMM_FP8_EXACT;
-    if (M < 0 || N < 0 || K < 0 || (b_block_rows != 1 && b_block_rows != kBlock) ||
-        (c_type != GEMM_TYPE_BF16 && c_type != GEMM_TYPE_FP32))
-        return GEMM_ERR_INVALID_VALUE;
-    if (M > kMaxRows || N > kMaxLd || K > kMaxLd)
-        return GEMM_ERR_UNSUPPORTED_SHAPE;
     if (M == 0 || N == 0)
         return GEMM_OK;
     const int64_t kblocks = (K + kBlock - 1) / kBlock, sb_cols = b_block_rows == 1 ? N : (N + kBlock - 1) / kBlock;
@@ -1353,6 +1402,24 @@ extern "C" int gemm_fp8_bt(int64_t M, int64_t N, int64_t K, const void* A, int64
     auto fits = [&](const void* ptr, int64_t ld) {
         return K % 16 == 0 && ld % 16 == 0 && ld <= 2 * kMaxLd && ((uintptr_t)ptr & 15) == 0;
     };
-    return run_fp8(M, N, (const char*)A, lda, fits(A, lda), (const char*)B, ldb, fits(B, ldb), q, exact, cus, tm,
-                   s);
+    const bool a_fits = fits(A, lda), b_fits = fits(B, ldb);
+    gemm_fp8_plan_t pl;
+    rc = plan_fp8(M, N, K, b_block_rows == 1, exact, a_fits, b_fits, cus, &pl);
+    if (rc != GEMM_OK)
+        return rc;
+    return run_fp8(M, N, (const char*)A, lda, a_fits, (const char*)B, ldb, b_fits, q, pl, tm, s);
+}
+
+extern "C" int gemm_fp8_plan_cus(int64_t M, int64_t N, int64_t K, int b_block_rows, int c_type, int a_aligned,
+                                 int b_aligned, int compute_units, gemm_fp8_plan_t* out)
+{
+    if (!out || compute_units < 1)
+        return GEMM_ERR_INVALID_VALUE;
+    if (const int rc = fp8_shape(M, N, K, b_block_rows, c_type))
+        return rc;
+    if (M == 0 || N == 0 || K == 0) {
+        memset(out, 0, sizeof *out);
+        return GEMM_OK;
+    }
+    return plan_fp8(M, N, K, b_block_rows == 1, fp8_exact(c_type), a_aligned != 0, b_aligned != 0, compute_units, out);
 }
