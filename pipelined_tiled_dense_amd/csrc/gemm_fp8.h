@@ -1224,6 +1224,13 @@ constexpr struct {
     int mf, nf;
 } kShapes[] = {{1, 1}, {1, 2}, {2, 2}, {4, 2}, {4, 4}};
 
+// Workgroups of a k chunk: a multiple of 8 column tiles, each for one of the 8
+// XCDs.  A launch's threads have to stay below 2^32, 2^23 workgroups.
+int64_t skinny_grid(int64_t M, int64_t N, int64_t rows, int64_t cols)
+{
+    return ceil_div(M, rows) * ceil_div(ceil_div(N, cols), 8) * 8;
+}
+
 // The kernel, k chunks and launch of a product, from its sizes alone: `rowb` for
 // row scales of B, a_fits and b_fits for operands whose rows start on 16-byte
 // boundaries.  The call runs what stands here.
@@ -1248,7 +1255,7 @@ int plan_fp8(int64_t M, int64_t N, int64_t K, bool rowb, bool exact, bool a_fits
     for (int i = 0; i < (exact || any || rowb ? 4 : 5); ++i) {
         const int64_t rows = kShapes[i].mf * 16, cols = kShapes[i].nf * 16;
         const int64_t groups = ceil_div(M, rows) * ceil_div(N, cols);
-        if (groups >= (int64_t)1 << 22)
+        if (skinny_grid(M, N, rows, cols) >= (int64_t)1 << 22)
             continue;   // far from few rows, and past what a launch takes
         for (int64_t c = 1; c <= kMaxSplits; ++c) {
             if (c > 1 && (i == 4 || groups * c > cus || kblocks < c * 2 * kSkinnyWaves))
@@ -1276,8 +1283,7 @@ int plan_fp8(int64_t M, int64_t N, int64_t K, bool rowb, bool exact, bool a_fits
         p.k_blocks = ceil_div(kblocks, chunks);
         p.k_splits = ceil_div(kblocks, p.k_blocks);   // no empty chunk
         p.tiles = ceil_div(M, p.rows) * ceil_div(N, p.cols);
-        // A multiple of 8 column tiles: each goes to one of the 8 XCDs.
-        p.grid = ceil_div(M, p.rows) * ceil_div(ceil_div(N, p.cols), 8) * 8 * p.k_splits;
+        p.grid = skinny_grid(M, N, p.rows, p.cols) * p.k_splits;
         p.workspace_bytes = p.k_splits > 1 ? p.k_splits * M * N * 4 : 0;
         *out = p;
         return GEMM_OK;

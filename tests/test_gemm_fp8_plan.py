@@ -78,6 +78,17 @@ def test_plans_are_sound():
         assert p["exact"] or kb > 2
 
 
+def test_launches_fit():
+    """A launch's threads are a 32-bit number, also for the most rows and for few
+    columns, whose tiles the few-rows kernel rounds up to a multiple of 8."""
+    rng = random.Random(5)
+    sizes = [random_size(rng) for _ in range(20000)]
+    sizes += [(int(2 ** rng.uniform(20, 31)) - 1, rng.randint(1, 300), int(2 ** rng.uniform(0, 12))) for _ in range(20000)]
+    for M, N, K in sizes:
+        p = plan(M, N, K, rng.choice((1, 128)), rng.random() < 0.5, rng.random() < 0.5, True)
+        assert p["grid"] * p["threads"] < 1 << 32, (M, N, K, p)
+
+
 def test_plan_refuses_what_the_product_refuses():
     for kw, code in (({"M": -1}, bd.GEMM_ERR_INVALID_VALUE), ({"b_rows": 2}, bd.GEMM_ERR_INVALID_VALUE),
                      ({"cus": 0}, bd.GEMM_ERR_INVALID_VALUE), ({"N": (1 << 22) + 1}, bd.GEMM_ERR_UNSUPPORTED_SHAPE)):
