@@ -249,8 +249,14 @@ struct Operand {
     int esz;
 
     bool ok_ld() const { return rows <= 1 || (ld >= cols && ld <= kMaxRows); }
-    // ld and rows are below 2^31, cols below 2^32 and esz at most 4: no overflow.
-    int64_t bytes() const { return rows <= 0 || cols <= 0 ? 0 : (rows > 1 ? (rows - 1) * ld + cols : cols) * esz; }
+    // Its extent, at most 2^62 (ld and rows are below 2^31 and cols below 2^32, so
+    // that the elements are countable, but not always their bytes).
+    int64_t bytes() const
+    {
+        constexpr int64_t kMost = (int64_t)1 << 62;
+        const int64_t n = rows <= 0 || cols <= 0 ? 0 : rows > 1 ? (rows - 1) * ld + cols : cols;
+        return n > kMost / esz ? kMost : n * esz;
+    }
 };
 
 // The status of one operand with values to read or write.

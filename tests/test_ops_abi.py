@@ -184,3 +184,12 @@ def test_exact_sums_are_a_flag_of_the_product_alone():
     assert norm(yt=bd.TYPE_BF16 | bd.FP8_EXACT) == BAD and swiglu(yt=bd.TYPE_FP8 | bd.FP8_EXACT) == BAD
     if not torch.cuda.is_available():
         assert gemm(ctype=bd.TYPE_BF16 | bd.FP8_EXACT) == DEVICE and gemm(ctype=bd.TYPE_FP32 | bd.FP8_EXACT) == DEVICE
+
+
+def test_overlap_of_the_largest_strides():
+    """An output whose rows span more bytes than 63 bits count still meets what lies
+    behind it."""
+    m = (1 << 31) - 1
+    assert gemm(M=m, ldsa=m, C=A0 // 2, ldc=m, ctype=bd.TYPE_FP32) == ALIAS
+    assert gemm(M=m, ldsa=m, C=A0 // 2, ldc=m) == ALIAS
+    assert quantize(M=m, x=A0 // 2, ldx=m, lds=m) == ALIAS
