@@ -720,10 +720,12 @@ __global__ void __launch_bounds__(256) k_reduce_fp8(Params p, Fp8Params q)
 // (300 x 1000 x 4112, 4 blocks a wave: 10.8 us).
 //
 // ANY takes operands of any alignment and stride and any K >= 16 (otherwise rows
-// start on 16-byte boundaries and K is a multiple of 16): a chunk that reaches
-// past the row's end is read from its last 16 bytes and shifted into place, so
-// nothing past the row is read, and rows past the matrix repeat its last one,
-// whose sums no one stores.
+// start on 16-byte boundaries and K is a multiple of 16), by the same 16-byte
+// loads at any byte (4 x 4096 x 4096 rows 4100 apart 5.8 us and 4097 apart 7.2; as
+// aligned dwords put together, 6.5 and 6.8, with a register more for each load): a
+// chunk that reaches past the row's end is read from its last 16 bytes and shifted
+// into place, so nothing past the row is read, and rows past the matrix repeat its
+// last one, whose sums no one stores.
 // ---------------------------------------------------------------------------
 struct SkinnyParams {
     const char* a;
@@ -736,44 +738,18 @@ struct SkinnyParams {
 
 constexpr int kSkinnyWaves = 8;
 
-// 16 bytes at any address as the dwords that hold them, so that no lane's access
-// crosses a dword: byte-aligned 16-byte loads of rows at odd addresses took 2.5
-// times as long (4 x 528 x 5249).  Every dword holds a byte of the 16, so none
-// lies outside the operand's pages.  Where four dwords are enough, the fifth is
-// read from `spare`, one place for all lanes, which costs next to nothing.
-struct Bytes16 {
-    u32x4_t v;
-    uint32_t end;
-};
-
-__device__ __forceinline__ Bytes16 load_any(const char* p, const float* spare)
+// 16 bytes without their first `cut` (0 .. 16), zeros after the rest.
+__device__ __forceinline__ u32x4_t without_first(u32x4_t v, int cut)
 {
-    Bytes16 r;
-    const uint32_t by = (uint32_t)(uintptr_t)p & 3u;
-    const char* lo = p - by;
-    __builtin_memcpy(&r.v, __builtin_assume_aligned(lo, 4), 16);
-    __builtin_memcpy(&r.end, __builtin_assume_aligned(by ? lo + 16 : (const char*)spare, 4), 4);
-    return r;
-}
-
-// The 16 bytes that load_any(p) read, without their first `cut` and with zeros
-// after the rest; `tail` (uniform) is false where cut is 0 in every lane.
-__device__ __forceinline__ u32x4_t bytes_of(const Bytes16& r, const char* p, int cut, bool tail)
-{
-    const uint32_t by = (uint32_t)(uintptr_t)p & 3u;
-    u32x4_t v = {__builtin_amdgcn_alignbyte(r.v[1], r.v[0], by), __builtin_amdgcn_alignbyte(r.v[2], r.v[1], by),
-                 __builtin_amdgcn_alignbyte(r.v[3], r.v[2], by), __builtin_amdgcn_alignbyte(r.end, r.v[3], by)};
-    if (tail) {
-        uint64_t x[2];
-        __builtin_memcpy(x, &v, 16);
-        const int s = (cut & 7) * 8;
-        const uint64_t lo = cut >= 8 ? x[1] : x[0], hi = cut >= 8 ? 0u : x[1];
-        x[0] = s ? (lo >> s) | (hi << (64 - s)) : lo;
-        x[1] = hi >> s;
-        if (cut >= 16)
-            x[0] = x[1] = 0;
-        __builtin_memcpy(&v, x, 16);
-    }
+    uint64_t x[2];
+    __builtin_memcpy(x, &v, 16);
+    const int s = (cut & 7) * 8;
+    const uint64_t lo = cut >= 8 ? x[1] : x[0], hi = cut >= 8 ? 0u : x[1];
+    x[0] = s ? (lo >> s) | (hi << (64 - s)) : lo;
+    x[1] = hi >> s;
+    if (cut >= 16)
+        x[0] = x[1] = 0;
+    __builtin_memcpy(&v, x, 16);
     return v;
 }
 
@@ -832,9 +808,8 @@ __global__ void __launch_bounds__(kSkinnyWaves * 64) k_gemm_fp8_skinny(SkinnyPar
             vb[j] = row < b_rows ? (uint32_t)row * (uint32_t)p.ldb + lc * 16 : kOOB;
     }
 
-    using Raw = std::conditional_t<ANY, Bytes16, u32x4_t>;
     struct Block {
-        Raw a[MF][2], b[NF][2];
+        u32x4_t a[MF][2], b[NF][2];
         float sa[MF], sb[ROWB ? NF * 4 : 1];
     };
     // ANY: where half h of block kb is read, and how many of its bytes precede it.
@@ -845,13 +820,13 @@ __global__ void __launch_bounds__(kSkinnyWaves * 64) k_gemm_fp8_skinny(SkinnyPar
     };
     auto load = [&](Block& v, int32_t kb) {
         // The halves of a line one after the other, while the line is in the L1.
-        auto halves = [&](Raw (&to)[2], const char* row, const __amdgpu_buffer_rsrc_t& rsrc, uint32_t voff) {
+        auto halves = [&](u32x4_t (&to)[2], const char* row, const __amdgpu_buffer_rsrc_t& rsrc, uint32_t voff) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 if constexpr (ANY) {
                     int32_t at;
                     place(kb, h, at);
-                    to[h] = load_any(row + at, q.sa);
+                    __builtin_memcpy(&to[h], row + at, 16);
                 } else {
                     const bool ok = kb * kBlock + (h * 4 + lc) * 16 < (int32_t)q.K;
                     to[h] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
@@ -886,27 +861,27 @@ __global__ void __launch_bounds__(kSkinnyWaves * 64) k_gemm_fp8_skinny(SkinnyPar
         for (int j = 0; j < NF; ++j)
             acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
     auto compute = [&](const Block& v, int32_t kb) {
-        auto frag = [&](const Raw (&raw)[2], const char* row) {
-            if constexpr (ANY) {
-                u32x4_t x[2];
+        const bool tail = ANY && (kb + 1) * kBlock > q.K;
+        auto frag = [&](const u32x4_t (&raw)[2]) {
+            u32x4_t x[2];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
+            for (int h = 0; h < 2; ++h) {
+                x[h] = raw[h];
+                if (tail) {
                     int32_t at;
-                    const int cut = place(kb, h, at);
-                    x[h] = mfma_order(bytes_of(raw[h], row + at, cut, (kb + 1) * kBlock > q.K));
+                    x[h] = without_first(x[h], place(kb, h, at));
                 }
-                return Fp8Frag<EXACT>(x[0], x[1]);
-            } else {
-                return Fp8Frag<EXACT>(mfma_order(raw[0]), mfma_order(raw[1]));
+                x[h] = mfma_order(x[h]);
             }
+            return Fp8Frag<EXACT>(x[0], x[1]);
         };
         Fp8Frag<EXACT> bf[NF];
 #pragma unroll
         for (int j = 0; j < NF; ++j)
-            bf[j] = frag(v.b[j], pb[j]);
+            bf[j] = frag(v.b[j]);
 #pragma unroll
         for (int i = 0; i < MF; ++i) {
-            const Fp8Frag<EXACT> af = frag(v.a[i], pa[i]);
+            const Fp8Frag<EXACT> af = frag(v.a[i]);
 #pragma unroll
             for (int j = 0; j < NF; ++j) {
                 const f32x4_t d = block_sums(bf[j], af);
@@ -1051,8 +1026,8 @@ int launch_skinny(SkinnyParams p, const Fp8Params& q, const gemm_fp8_plan_t& pl,
     }
     p.partial = (float*)ws;
     const dim3 g((unsigned)(pl.grid / chunks), (unsigned)chunks), b(kSkinnyWaves * 64);
-    // Operands of any alignment take wider addresses and a dword more: less depth
-    // leaves them the registers.
+    // Operands of any alignment take 64-bit addresses: less depth leaves them the
+    // registers.
     auto run = [&]<bool ROWB, bool EXACT>() {
         if constexpr (MF * NF < 16) {
             if (any) {
@@ -1073,7 +1048,8 @@ int launch_skinny(SkinnyParams p, const Fp8Params& q, const gemm_fp8_plan_t& pl,
         else
             run.template operator()<false, false>();
     } else {
-        run.template operator()<false, false>();   // the others do not fit the registers
+        // This form spills 8 registers, the others 65 to 146: they take other shapes.
+        run.template operator()<false, false>();
     }
     int rc = launched();
     if (chunks > 1) {
