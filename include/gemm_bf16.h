@@ -408,8 +408,8 @@ enum {
 /* Added to gemm_fp8_bt's c_type: the sums of a bf16 C are those of an fp32 C. */
 enum { GEMM_FP8_EXACT = 256 };
 
-/* The widest row gemm_rms_norm and gemm_rms_norm_bwd take (a row stays in one
- * workgroup's registers). */
+/* The widest row gemm_rms_norm and gemm_rms_norm_bwd take: one workgroup holds a
+ * row across its sum. */
 enum { GEMM_NORM_MAX_WIDTH = 32768 };
 
 /*

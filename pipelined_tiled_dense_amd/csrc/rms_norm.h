@@ -3,10 +3,11 @@
 //
 //   h = x + residual,  rstd = 1 / sqrt(mean(h^2) + eps),  y = h * rstd * weight
 //
-// Bound by memory: a row is read once, held in registers across the row's sum
-// of squares, and written once (8192 x 8192 with residual to 8 bits, 470 MB: 85
-// us, 5.5 TB/s; a large copy reaches 5.1).  One row: 2.5 us, the latency of two
-// loads, the row's sum and a store.
+// Bound by memory: a row is read once, held in registers across the row's sum of
+// squares, and written once (8192 x 8192 with residual to 8 bits, 470 MB: 84 us, 5.6
+// TB/s; a large copy reaches 5.1).  Off the multiple of 8 over 16384 wide, 5 registers
+// (8 to bf16) of a lane's go through scratch memory: 2048 x 32761 to 8 bits 134 us,
+// 32768 105.  One row: 2.7 us, the latency of two loads, the row's sum and a store.
 #pragma once
 
 namespace {
@@ -141,7 +142,11 @@ k_rms_norm(NormParams p, int nw)
 // are in flight together), keeps each row in registers across the mean, and sums
 // its rows' share of dweight in registers; the workgroups' shares go to temporary
 // memory and a second, small launch adds them in workgroup order, so the sum does
-// not depend on timing.  Bound by memory (8191 x 4096, 268 MB: 54 us, 5.0 TB/s).
+// not depend on timing.  Bound by memory (8191 x 4096, 268 MB: 54 us, 5.0 TB/s; 4096 x
+// 16384 90 us).  Over 16384 wide a lane's four chunks of dy, h, dres, the weight and
+// its sums do not fit 128 registers, what 1024 threads leave, and 116 of them (103 off
+// the multiple of 8) go through scratch memory: 2048 x 32768 274 us, three times as
+// long as the same bytes at 16384.
 // ---------------------------------------------------------------------------
 struct NormBwdParams {
     const uint16_t* dy;
@@ -266,8 +271,10 @@ __global__ void __launch_bounds__(1024) k_norm_weight_grad(const float* part, in
     }
 }
 
-// Waves per row and chunks per lane for D values: few chunks per lane as long
-// as the row fits 16 waves.
+// Waves per row and chunks per lane for D values: 4 waves before a lane takes
+// another chunk (8192 x 4096 forward 39.0 us, with 8 waves of one chunk 41.2; 8192 x
+// 2048 20.3, with 2 waves of two 19.5), up to max_nch chunks as long as the row fits
+// 16 waves, and then as many as it needs.
 struct RowShape {
     int nch, nw;
 };
@@ -351,6 +358,10 @@ int gemm_rms_norm(int64_t M, int64_t D, const void* X, int64_t ldx, const void* 
         return rc;
     NormParams p{(const uint16_t*)X, (const uint16_t*)residual, (const uint16_t*)weight, (uint16_t*)H, Y, scale, rstd,
                  M, ldx, ldr, ldh, ldy, lds, (int32_t)D, eps, 1.0f / (float)D};
+    // With rows for every compute unit twice over, two chunks a lane: more of a row
+    // in flight from fewer waves (2048 x 8192 20.6 us, with one 23.1); with fewer rows
+    // one, which has each lane's work done sooner (1 x 4096 2.7 us, with two 3.0; 512
+    // rows are level).
     const RowShape rs = row_shape(D, M < 2 * cus ? 1 : 2);
     const int threads = rs.nw == 1 ? 256 : rs.nw * 64;
     const int64_t groups = rs.nw == 1 ? (M + 3) / 4 : M;
@@ -406,7 +417,9 @@ int gemm_rms_norm_bwd(int64_t M, int64_t D, const void* dY, int64_t lddy, const 
     int64_t grid = (int64_t)cus * ((8 + rs.nw - 1) / rs.nw);
     if (grid > (M + 1) / 2)
         grid = (M + 1) / 2;
-    // A few rows: one workgroup, whose sums are the weight's gradient, in one launch.
+    // A few rows: one workgroup, whose sums are the weight's gradient, in one launch
+    // (3 x 4096 5.5 us, in two launches 9.2; 8 rows are level at 4096 wide, 20.1 against
+    // 17.5 at 16384).
     if (M <= 4)
         grid = M > 0 ? 1 : 0;
     void* ws = nullptr;
