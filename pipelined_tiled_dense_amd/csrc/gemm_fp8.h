@@ -300,7 +300,7 @@ __device__ __forceinline__ void store_c16(const Fp8Params& q, int64_t m, int64_t
 //
 // 256 x 256 tiles (8 waves of 128 x 64) read each operand least often and 128 x
 // 128 (4 waves of 64 x 64, two workgroups a compute unit) fill the device with
-// smaller C.  What bounds 8192^3 (411 to 460 us, 2.4 to 2.7 PFLOP/s; a product
+// smaller C.  What bounds 8192^3 (405 to 478 us, 2.3 to 2.7 PFLOP/s; a product
 // without block scales reaches 3.0): the matrix cores are busy 0.65 to 0.72 of
 // the time, and the clock falls to 1.75 GHz under the load; without its loads
 // the kernel reaches 0.78.
