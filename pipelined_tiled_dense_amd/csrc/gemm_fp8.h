@@ -715,9 +715,9 @@ __global__ void __launch_bounds__(256) k_reduce_fp8(Params p, Fp8Params q)
 // and add their sums through LDS in wave order.  So every compute unit has loads
 // in flight over the whole of k even where C gives few workgroups, with no
 // second launch; only a long k against very few columns is split over several
-// workgroups, whose sums a second launch adds in order.  Bound by B's bytes where there are many columns (1 x 8192 x
-// 8192: 13.0 us, 5.2 TB/s), by the latency of a wave's blocks where there are few
-// (300 x 1000 x 4112, 4 blocks a wave: 10.8 us).
+// workgroups, whose sums a second launch adds in order.  Bound by B's bytes where
+// there are many columns (1 x 8192 x 8192: 13.0 us, 5.2 TB/s), by the latency of a
+// wave's blocks where there are few (300 x 1000 x 4112, 4 blocks a wave: 11.0 us).
 //
 // ANY takes operands of any alignment and stride and any K >= 16 (otherwise rows
 // start on 16-byte boundaries and K is a multiple of 16), by the same 16-byte
