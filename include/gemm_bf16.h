@@ -560,6 +560,105 @@ int gemm_swiglu(int64_t M, int64_t F, const void* GU, int64_t ldgu,
 int gemm_swiglu_bwd(int64_t M, int64_t F, const void* dY, int64_t lddy,
                     const void* GU, int64_t ldgu, void* dGU, int64_t lddgu, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Linear layers on bf16 operands: the product with bias, activation, residual or
+ * gate in its epilogue, and the products of the backward pass.
+ *
+ * A weight has one row per output, W (N x K): y = x W^T.  Everything is bf16 unless
+ * it says fp32; sums and the elementwise work are fp32, rounded once to each
+ * output.  Entry points are asynchronous on `stream`, validate as gemm_bf16 does and
+ * return the same status codes; leading dimensions, alignment and overlaps are as
+ * for the 8-bit operators above.  Optional operands are NULL where absent (their
+ * leading dimension is then ignored).  M is 0 .. 2^31 - 1, the other sizes 0 .. 2^22
+ * (GEMM_ERR_UNSUPPORTED_SHAPE above).
+ *
+ * The products run on operands whose rows are multiples of 8 long, start on 16-byte
+ * boundaries and are at most 2^22 elements apart; they copy any other, zero-padded,
+ * into temporary memory first (but not where M <= 64 and both operands are read
+ * along their rows).  Few output tiles and a long sum are split into chunks along
+ * it, whose fp32 sums a second launch adds in a fixed order.  Temporary memory is
+ * gemm_bf16's (kept blocks, see there).  Results are deterministic for given sizes,
+ * strides and alignment.
+ *
+ * Activations and their slopes follow these formulas for every z, up to the rounding
+ * of fp32; an infinity or a NaN gives what the formula gives.
+ * ------------------------------------------------------------------------- */
+enum {
+    GEMM_ACT_NONE = 0,       /* z */
+    GEMM_ACT_RELU = 1,       /* max(z, 0); slope 0 at 0 */
+    GEMM_ACT_GELU = 2,       /* z Phi(z), Phi the normal distribution function */
+    GEMM_ACT_GELU_TANH = 3,  /* z / (1 + exp(-2 sqrt(2 / pi) (z + 0.044715 z^3))) */
+    GEMM_ACT_SILU = 4        /* z / (1 + exp(-z)) */
+};
+
+/*
+ * gemm_linear: for X (M x K, ldx >= K), W (N x K, ldw >= K), bias (N values) and
+ * residual (M x N):
+ *
+ *     z = X W^T + bias,   Y = act(z) + residual
+ *
+ * bias, residual and Z may be NULL.  Z (M x N) receives z, which the backward pass
+ * of the activation reads; Y uses z before its rounding.  Y may be the very memory
+ * of residual.  M == 0 or N == 0 is a no-op; with K == 0 the product is 0.
+ */
+int gemm_linear(int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, const void* W, int64_t ldw,
+                const void* bias, int act, const void* residual, int64_t ldr, void* Z, int64_t ldz,
+                void* Y, int64_t ldy, void* stream);
+
+/*
+ * gemm_linear_bwd_input: the gradient of a layer's input X (M x K) from that of its
+ * output, dY (M x N), and, where X is act(Z), of Z instead:
+ *
+ *     dX = (dY W + dres) * act'(Z)
+ *
+ * dres (M x K, may be NULL) is the gradient that reaches X in other ways.  Z (M x
+ * K) is ignored with GEMM_ACT_NONE, whose slope is 1.  dX (M x K) may be the very
+ * memory of Z or of dres.  M == 0 or K == 0 is a no-op; with N == 0 the product is 0.
+ */
+int gemm_linear_bwd_input(int64_t M, int64_t N, int64_t K, const void* dY, int64_t lddy, const void* W, int64_t ldw,
+                          int act, const void* Z, int64_t ldz, const void* dres, int64_t lddr,
+                          void* dX, int64_t lddx, void* stream);
+
+/*
+ * gemm_linear_bwd_weight: the gradients of a layer's weight and bias:
+ *
+ *     dW = dY^T X  (N x K),   dbias[n] = sum over rows of dY[.][n]
+ *
+ * dW is fp32 or bf16 by dw_type (GEMM_TYPE_FP32, GEMM_TYPE_BF16); dbias (N fp32
+ * values) may be NULL.  Both are overwritten; M == 0 gives zeros.
+ */
+int gemm_linear_bwd_weight(int64_t M, int64_t N, int64_t K, const void* dY, int64_t lddy, const void* X, int64_t ldx,
+                           void* dW, int64_t lddw, int dw_type, float* dbias, void* stream);
+
+/*
+ * gemm_gated_linear: both projections of a gated unit, the activation and their
+ * product in one: W is 2F x K, the F rows of the gate and then the F rows of the other
+ * factor, bias (2F values, may be NULL) likewise:
+ *
+ *     [g, u] = X W^T + bias,   Y = act(g) * u   (M x F)
+ *
+ * GU (M x 2F, may be NULL) receives g in columns 0 .. F-1 and u in F .. 2F-1, as
+ * gemm_swiglu reads them and the backward pass does; Y uses them before rounding.
+ * M == 0 or F == 0 is a no-op.
+ */
+int gemm_gated_linear(int64_t M, int64_t F, int64_t K, const void* X, int64_t ldx, const void* W, int64_t ldw,
+                      const void* bias, int act, void* GU, int64_t ldgu, void* Y, int64_t ldy, void* stream);
+
+/*
+ * gemm_gated_linear_bwd_input: the gradients of g and u, side by side in dGU (M x
+ * 2F), through the layer that reads the unit's output: dY (M x N) is the gradient of
+ * that layer's output, W (N x F) its weight:
+ *
+ *     t = dY W,   dg = t * u * act'(g),   du = t * act(g)
+ *
+ * Y (M x F, may be NULL) receives act(g) * u again, which the gradient of W
+ * contracts with dY, so that the forward pass need not keep it.  dGU may be the
+ * very memory of GU.  M == 0 or F == 0 is a no-op; with N == 0 the product is 0.
+ */
+int gemm_gated_linear_bwd_input(int64_t M, int64_t F, int64_t N, const void* dY, int64_t lddy, const void* W, int64_t ldw,
+                                int act, const void* GU, int64_t ldgu, void* dGU, int64_t lddgu,
+                                void* Y, int64_t ldy, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

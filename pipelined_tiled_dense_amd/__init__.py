@@ -9,7 +9,8 @@ from __future__ import annotations
 import importlib
 
 _FROM_BINDING = ("gemm", "gemm_fp8", "quantize_fp8", "rms_norm", "rms_norm_backward", "swiglu", "swiglu_backward",
-                 "RmsNorm", "GemmError", "SYNC_MODES")
+                 "linear", "linear_backward_input", "linear_backward_weight", "gated_linear",
+                 "gated_linear_backward_input", "RmsNorm", "GemmError", "SYNC_MODES")
 __all__ = ["binding", "inputs", "mlp", *_FROM_BINDING, "FeedForward"]
 
 

@@ -31,6 +31,7 @@ TYPE_BF16 = 0
 TYPE_FP8 = 1
 TYPE_FP32 = 2
 FP8_EXACT = 256             # GEMM_FP8_EXACT, added to gemm_fp8_bt's c_type
+ACTIVATIONS = {None: 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}   # GEMM_ACT_*
 BLOCK = 128                 # values along k (and rows of a block) that share a scale
 NORM_MAX_WIDTH = 32768      # GEMM_NORM_MAX_WIDTH
 
@@ -111,8 +112,14 @@ def library() -> ctypes.CDLL:
         lib.gemm_swiglu.argtypes = [i64, i64, p, i64, p, i64, i32, p, i64, p]
         lib.gemm_swiglu_bwd.argtypes = [i64, i64, p, i64, p, i64, p, i64, p]
         lib.gemm_fp8_plan_cus.argtypes = [i64, i64, i64, i32, i32, i32, i32, i32, ctypes.POINTER(Fp8Plan)]
+        lib.gemm_linear.argtypes = [i64, i64, i64, p, i64, p, i64, p, i32, p, i64, p, i64, p, i64, p]
+        lib.gemm_linear_bwd_input.argtypes = [i64, i64, i64, p, i64, p, i64, i32, p, i64, p, i64, p, i64, p]
+        lib.gemm_linear_bwd_weight.argtypes = [i64, i64, i64, p, i64, p, i64, p, i64, i32, p, p]
+        lib.gemm_gated_linear.argtypes = [i64, i64, i64, p, i64, p, i64, p, i32, p, i64, p, i64, p]
+        lib.gemm_gated_linear_bwd_input.argtypes = [i64, i64, i64, p, i64, p, i64, i32, p, i64, p, i64, p, i64, p]
         for name in ("gemm_fp8_bt", "gemm_fp8_plan_cus", "gemm_quantize_fp8", "gemm_rms_norm", "gemm_rms_norm_bwd", "gemm_swiglu",
-                     "gemm_swiglu_bwd"):
+                     "gemm_swiglu_bwd", "gemm_linear", "gemm_linear_bwd_input", "gemm_linear_bwd_weight",
+                     "gemm_gated_linear", "gemm_gated_linear_bwd_input"):
             getattr(lib, name).restype = i32
         _lib = lib
     return _lib
@@ -235,6 +242,26 @@ def gemm_swiglu(M, F, GU, ldgu, Y, ldy, y_type, scale, lds, stream) -> int:
 
 def gemm_swiglu_bwd(M, F, dY, lddy, GU, ldgu, dGU, lddgu, stream) -> int:
     return library().gemm_swiglu_bwd(M, F, dY, lddy, GU, ldgu, dGU, lddgu, stream)
+
+
+def gemm_linear(M, N, K, X, ldx, W, ldw, bias, act, residual, ldr, Z, ldz, Y, ldy, stream) -> int:
+    return library().gemm_linear(M, N, K, X, ldx, W, ldw, bias, act, residual, ldr, Z, ldz, Y, ldy, stream)
+
+
+def gemm_linear_bwd_input(M, N, K, dY, lddy, W, ldw, act, Z, ldz, dres, lddr, dX, lddx, stream) -> int:
+    return library().gemm_linear_bwd_input(M, N, K, dY, lddy, W, ldw, act, Z, ldz, dres, lddr, dX, lddx, stream)
+
+
+def gemm_linear_bwd_weight(M, N, K, dY, lddy, X, ldx, dW, lddw, dw_type, dbias, stream) -> int:
+    return library().gemm_linear_bwd_weight(M, N, K, dY, lddy, X, ldx, dW, lddw, dw_type, dbias, stream)
+
+
+def gemm_gated_linear(M, F, K, X, ldx, W, ldw, bias, act, GU, ldgu, Y, ldy, stream) -> int:
+    return library().gemm_gated_linear(M, F, K, X, ldx, W, ldw, bias, act, GU, ldgu, Y, ldy, stream)
+
+
+def gemm_gated_linear_bwd_input(M, F, N, dY, lddy, W, ldw, act, GU, ldgu, dGU, lddgu, Y, ldy, stream) -> int:
+    return library().gemm_gated_linear_bwd_input(M, F, N, dY, lddy, W, ldw, act, GU, ldgu, dGU, lddgu, Y, ldy, stream)
 
 
 strerror = gemm_bf16_strerror
@@ -531,3 +558,156 @@ def swiglu_backward(dy, gu, *, stream=None):
     _done(library().gemm_swiglu_bwd(M, F, dy.data_ptr(), lddy, gu.data_ptr(), ldgu, dgu.data_ptr(), 2 * F, s),
           "gemm_swiglu_bwd")
     return dgu
+
+
+# -- linear layers on bf16 operands -------------------------------------------------
+# A weight has one row per output: (N, K), for x (M, K).  An activation is None,
+# "relu", "gelu", "gelu_tanh" or "silu".  Streams and devices as above.
+def _activation(name):
+    if name not in ACTIVATIONS:
+        raise ValueError("activation must be one of %s" % [a for a in ACTIVATIONS])
+    return ACTIVATIONS[name]
+
+
+def _optional(name, x, dtype, rows, cols):
+    """(pointer, leading dimension) of an operand that may be None."""
+    if x is None:
+        return None, 0
+    ld = _matrix(name, x, dtype)
+    _shaped(name, x, rows, cols)
+    return x.data_ptr(), ld
+
+
+def linear(x, weight, *, bias=None, activation=None, residual=None, return_preactivation=False, stream=None):
+    """act(z) + residual with z = x @ weight.T + bias for x (M, K) and weight (N,
+    K), the whole of it in the product's epilogue; with ``return_preactivation``
+    the pair of it and z, which ``linear_backward_input`` reads.  All bfloat16."""
+    import torch
+
+    if stream is not None:
+        return _on_stream(stream, (x, weight, bias, residual),
+                          lambda: linear(x, weight, bias=bias, activation=activation, residual=residual,
+                                         return_preactivation=return_preactivation))
+    bf16, act = torch.bfloat16, _activation(activation)
+    ldx, ldw = _matrix("x", x, bf16), _matrix("weight", weight, bf16)
+    (M, K), (N, KW) = x.shape, weight.shape
+    if KW != K:
+        raise ValueError("inner dimensions differ: %d vs %d" % (K, KW))
+    if bias is not None:
+        _vector("bias", bias, bf16, N)
+    r, ldr = _optional("residual", residual, bf16, M, N)
+    s, dev = _current(torch, x, weight, bias, residual), x.device
+    y = torch.empty(M, N, dtype=bf16, device=dev)
+    z = torch.empty(M, N, dtype=bf16, device=dev) if return_preactivation else None
+    _done(library().gemm_linear(M, N, K, x.data_ptr(), ldx, weight.data_ptr(), ldw,
+                                None if bias is None else bias.data_ptr(), act, r, ldr,
+                                None if z is None else z.data_ptr(), N, y.data_ptr(), N, s), "gemm_linear")
+    return (y, z) if return_preactivation else y
+
+
+def linear_backward_input(dy, weight, *, preactivation=None, activation=None, dresidual=None, stream=None):
+    """The gradient of ``linear``'s x (M, K) for the gradient dy (M, N) of its y,
+    plus ``dresidual``, the gradient that reaches x in other ways; with an
+    activation, x being act(preactivation), the gradient of preactivation:
+    (dy @ weight + dresidual) * act'(preactivation).  bfloat16."""
+    import torch
+
+    if stream is not None:
+        return _on_stream(stream, (dy, weight, preactivation, dresidual),
+                          lambda: linear_backward_input(dy, weight, preactivation=preactivation, activation=activation,
+                                                        dresidual=dresidual))
+    bf16, act = torch.bfloat16, _activation(activation)
+    lddy, ldw = _matrix("dy", dy, bf16), _matrix("weight", weight, bf16)
+    (M, N), (NW, K) = dy.shape, weight.shape
+    if NW != N:
+        raise ValueError("dy has %d columns, weight %d rows" % (N, NW))
+    if (preactivation is None) != (activation is None):
+        raise ValueError("an activation and its preactivation come together")
+    z, ldz = _optional("preactivation", preactivation, bf16, M, K)
+    r, ldr = _optional("dresidual", dresidual, bf16, M, K)
+    s = _current(torch, dy, weight, preactivation, dresidual)
+    dx = torch.empty(M, K, dtype=bf16, device=dy.device)
+    _done(library().gemm_linear_bwd_input(M, N, K, dy.data_ptr(), lddy, weight.data_ptr(), ldw, act, z, ldz, r, ldr,
+                                          dx.data_ptr(), K, s), "gemm_linear_bwd_input")
+    return dx
+
+
+def linear_backward_weight(dy, x, *, bias=False, out_dtype=None, stream=None):
+    """The gradient dy.T @ x (N, K) of ``linear``'s weight for the gradient dy (M,
+    N) of its z and its x (M, K), in ``out_dtype``, float32 (the default) or
+    bfloat16; with ``bias`` the pair of it and the bias's, float32 (N,)."""
+    import torch
+
+    if stream is not None:
+        return _on_stream(stream, (dy, x), lambda: linear_backward_weight(dy, x, bias=bias, out_dtype=out_dtype))
+    bf16, f32 = torch.bfloat16, torch.float32
+    if out_dtype is None:
+        out_dtype = f32
+    if out_dtype is not bf16 and out_dtype is not f32:
+        raise TypeError("out_dtype must be bfloat16 or float32")
+    lddy, ldx = _matrix("dy", dy, bf16), _matrix("x", x, bf16)
+    (M, N), (MX, K) = dy.shape, x.shape
+    if MX != M:
+        raise ValueError("dy has %d rows, x %d" % (M, MX))
+    s, dev = _current(torch, dy, x), dy.device
+    dw = torch.empty(N, K, dtype=out_dtype, device=dev)
+    db = torch.empty(N, dtype=f32, device=dev) if bias else None
+    _done(library().gemm_linear_bwd_weight(M, N, K, dy.data_ptr(), lddy, x.data_ptr(), ldx, dw.data_ptr(), K,
+                                           TYPE_FP32 if out_dtype is f32 else TYPE_BF16,
+                                           None if db is None else db.data_ptr(), s), "gemm_linear_bwd_weight")
+    return (dw, db) if bias else dw
+
+
+def gated_linear(x, weight, *, bias=None, activation="silu", return_gu=False, stream=None):
+    """act(g) * u with [g, u] = x @ weight.T + bias for x (M, K) and weight (2F, K),
+    the F rows of g and then the F rows of u: both projections and the gate in one
+    kernel.  y (M, F); with ``return_gu`` the pair of it and [g, u] side by side (M,
+    2F), which ``gated_linear_backward_input`` reads.  All bfloat16."""
+    import torch
+
+    if stream is not None:
+        return _on_stream(stream, (x, weight, bias),
+                          lambda: gated_linear(x, weight, bias=bias, activation=activation, return_gu=return_gu))
+    bf16, act = torch.bfloat16, _activation(activation)
+    ldx, ldw = _matrix("x", x, bf16), _matrix("weight", weight, bf16)
+    (M, K), (F2, KW) = x.shape, weight.shape
+    if KW != K:
+        raise ValueError("inner dimensions differ: %d vs %d" % (K, KW))
+    if F2 % 2:
+        raise ValueError("weight must have an even number of rows")
+    if bias is not None:
+        _vector("bias", bias, bf16, F2)
+    s, dev, F = _current(torch, x, weight, bias), x.device, F2 // 2
+    y = torch.empty(M, F, dtype=bf16, device=dev)
+    gu = torch.empty(M, F2, dtype=bf16, device=dev) if return_gu else None
+    _done(library().gemm_gated_linear(M, F, K, x.data_ptr(), ldx, weight.data_ptr(), ldw,
+                                      None if bias is None else bias.data_ptr(), act,
+                                      None if gu is None else gu.data_ptr(), F2, y.data_ptr(), F, s),
+          "gemm_gated_linear")
+    return (y, gu) if return_gu else y
+
+
+def gated_linear_backward_input(dy, weight, gu, *, activation="silu", return_y=False, stream=None):
+    """The gradient of gu = [g, u] (M, 2F) through the layer that reads ``gated_linear``'s
+    y: dy (M, N) is the gradient of that layer's output and weight (N, F) its weight.
+    With t = dy @ weight it is [t * u * act'(g), t * act(g)]; with ``return_y`` the
+    pair of it and y again, which that weight's gradient reads.  bfloat16."""
+    import torch
+
+    if stream is not None:
+        return _on_stream(stream, (dy, weight, gu),
+                          lambda: gated_linear_backward_input(dy, weight, gu, activation=activation, return_y=return_y))
+    bf16, act = torch.bfloat16, _activation(activation)
+    lddy, ldw, ldgu = _matrix("dy", dy, bf16), _matrix("weight", weight, bf16), _matrix("gu", gu, bf16)
+    (M, N), (NW, F) = dy.shape, weight.shape
+    if NW != N:
+        raise ValueError("dy has %d columns, weight %d rows" % (N, NW))
+    _shaped("gu", gu, M, 2 * F)
+    s, dev = _current(torch, dy, weight, gu), dy.device
+    dgu = torch.empty(M, 2 * F, dtype=bf16, device=dev)
+    y = torch.empty(M, F, dtype=bf16, device=dev) if return_y else None
+    _done(library().gemm_gated_linear_bwd_input(M, F, N, dy.data_ptr(), lddy, weight.data_ptr(), ldw, act,
+                                                gu.data_ptr(), ldgu, dgu.data_ptr(), 2 * F,
+                                                None if y is None else y.data_ptr(), F, s),
+          "gemm_gated_linear_bwd_input")
+    return (dgu, y) if return_y else dgu

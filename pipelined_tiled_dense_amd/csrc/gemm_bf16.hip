@@ -92,6 +92,7 @@
 #include <stdint.h>
 #include <string.h>
 
+#include <algorithm>
 #include <atomic>
 #include <mutex>
 #include <type_traits>
@@ -198,6 +199,10 @@ struct Cfg {
     static constexpr int BM = BM_, BN = BN_, BK = BK_, S = S_, WM = WM_, WN = WN_;
     static constexpr int SYNC = SYNC_;
     static constexpr bool BT = BT_;                 // B stored N x K
+    // What the linear layers' configurations override: A stored K x M; a B of
+    // two factors of p.N rows each, whose 16-row blocks alternate in the tile;
+    // sizes that need not be multiples of 8 (see Loader::init).
+    static constexpr bool AT = false, PAIRED = false, ANY_SIZE = false;
     // Split-window ring: the LDS holds NWIN windows of one operand tile each
     // (a position's A tile and its B tile occupy two windows), instead of S
     // whole stages; the epilogue stages through a drained window.
@@ -246,6 +251,7 @@ struct Cfg {
     static constexpr int LOADS = A_LOADS + B_LOADS;
     static constexpr int CPR_K = BK / 8;                             // 16-byte chunks per K-contiguous row
     static constexpr int CPR_N = BN / 8;                             // chunks per row of a K x N B tile
+    static constexpr int CPR_M = BM / 8;                             // chunks per row of a K x M A tile
     static constexpr int RING_BYTES = WIN ? NWIN * A_BYTES : PIPES * S * STAGE_BYTES;
     // Ring counters (2 x S 32-bit words, or S 64-bit signal words) and the
     // workgroup's poison word (SyncState), padded to 8 bytes.
@@ -689,6 +695,7 @@ struct Loader {
     // N (B stored N x K) and k-rows past K (B stored K x N).
     const char* a_end;
     const char* b_end;
+    const char* b_base;   // p.B, or with a paired B the factor that this wave loads
 
     __device__ __forceinline__ static int slot(int t, int lw, int lane) { return (t * C::NLW + lw) * 64 + lane; }
     // K-contiguous tiles with 32-wide k-steps and 16 x 16 blocks permute the
@@ -717,6 +724,19 @@ struct Loader {
         const int row = s / C::CPR_N;
         return ((s % C::CPR_N) ^ swz_n<C::MF>(row)) * 8;
     }
+    // The same in a K x M tile of A.
+    __device__ __forceinline__ static int mofs_m(int s)
+    {
+        const int row = s / C::CPR_M;
+        return ((s % C::CPR_M) ^ swz_n<C::MF>(row)) * 8;
+    }
+    // Row of B, from the tile's first, of a K-contiguous slot.  Paired: blocks of 16
+    // tile rows take 16 rows of one factor and the same 16 of the other in turn.
+    __device__ __forceinline__ static int brow(int s)
+    {
+        const int row = krow(s);
+        return C::PAIRED ? (row >> 5) * 16 + (row & 15) : row;
+    }
 
     __device__ __forceinline__ void init(const Params& p, int32_t ntiles, int lw, int lane, int32_t first = 0,
                                          int32_t stride = 1)
@@ -727,22 +747,37 @@ struct Loader {
 #pragma unroll
         for (int t = 0; t < C::A_LOADS; ++t) {
             const int s = slot(t, lw, lane);
-            voffA[t] = (uint32_t)krow(s) * lda2 + (uint32_t)kofs_k(s) * 2u;
+            if constexpr (C::AT)
+                voffA[t] = (uint32_t)(s / C::CPR_M) * lda2 + (uint32_t)mofs_m(s) * 2u;
+            else
+                voffA[t] = (uint32_t)krow(s) * lda2 + (uint32_t)kofs_k(s) * 2u;
         }
 #pragma unroll
         for (int t = 0; t < C::B_LOADS; ++t) {
             const int s = slot(t, lw, lane);
             if constexpr (C::BT)
-                voffB[t] = (uint32_t)krow(s) * ldb2 + (uint32_t)kofs_k(s) * 2u;
+                voffB[t] = (uint32_t)brow(s) * ldb2 + (uint32_t)kofs_k(s) * 2u;
             else
                 voffB[t] = (uint32_t)(s / C::CPR_N) * ldb2 + (uint32_t)nofs_n(s) * 2u;
         }
-        a_end = p.A + ((p.M - 1) * p.lda + p.K) * 2;
-        b_end = C::BT ? p.B + ((p.N - 1) * p.ldb + p.K) * 2 : p.B + ((p.K - 1) * p.ldb + p.N) * 2;
+        b_base = p.B;
+        if constexpr (C::PAIRED) {
+            // A wave's DMA instructions cover 8 tile rows each, NLW * 8 apart: all of
+            // them in blocks of one parity, so in one factor.
+            static_assert(C::BT && C::BK == 64 && C::NLW % 4 == 0, "whole blocks of one factor per wave");
+            b_base += (int64_t)((lw >> 1) & 1) * p.N * p.ldb * 2;
+        }
+        // ANY_SIZE: the operands' memory holds rows of whole 16-byte chunks (leading
+        // dimensions are multiples of 8), so the last row's last chunk counts whole.
+        auto width = [](int64_t n) { return C::ANY_SIZE ? (n + 7) & ~(int64_t)7 : n; };
+        a_end = C::AT ? p.A + ((p.K - 1) * p.lda + width(p.M)) * 2 : p.A + ((p.M - 1) * p.lda + width(p.K)) * 2;
+        b_end = C::BT ? b_base + ((p.N - 1) * p.ldb + width(p.K)) * 2 : b_base + ((p.K - 1) * p.ldb + width(p.N)) * 2;
         n_tiles = ntiles;
         total = ntiles * p.k_steps;
         if constexpr (LONGK) {
             bstep = C::BT ? (uint32_t)C::BK * 2u : (uint32_t)C::BK * 2u * (uint32_t)p.ldb;
+            if constexpr (C::AT)
+                astep = (uint32_t)C::BK * 2u * (uint32_t)p.lda;
             cur = tile_prep(p, 0);
             prefetch_next_tile(p, 1);
         } else {
@@ -762,9 +797,10 @@ struct Loader {
         int32_t tm = 0, tn = 0, sp = 0, u = 0;
         tile_coords(p, (int32_t)blockIdx.x + (t_first + min(t, n_tiles - 1) * t_stride) * (int32_t)gridDim.x,
                     (int32_t)gridDim.x, tm, tn, sp, u);
-        const int64_t m0 = (int64_t)tm * C::BM, n0 = (int64_t)tn * C::BN, k0 = (int64_t)sp * p.ksplit;
-        a = p.A + (m0 * p.lda + k0) * 2;
-        b = C::BT ? p.B + (n0 * p.ldb + k0) * 2 : p.B + (k0 * p.ldb + n0) * 2;
+        const int64_t m0 = (int64_t)tm * C::BM, n0 = (int64_t)tn * (C::PAIRED ? C::BN / 2 : C::BN);
+        const int64_t k0 = (int64_t)sp * p.ksplit;
+        a = C::AT ? p.A + (k0 * p.lda + m0) * 2 : p.A + (m0 * p.lda + k0) * 2;
+        b = C::BT ? b_base + (n0 * p.ldb + k0) * 2 : b_base + (k0 * p.ldb + n0) * 2;
         n_left = (int32_t)(p.N - n0);
         k_left = (int32_t)(p.K - k0);
     }
@@ -788,8 +824,8 @@ struct Loader {
         Prep r;
         tile_origin(p, t, a, b, r.nrem, r.krem);
         const bool live = t < n_tiles;
-        r.ra = rsrc_n(a, live ? (uint32_t)(a_end - a) : 0u);
-        r.rb = rsrc_n(b, live ? (uint32_t)(b_end - b) : 0u);
+        r.ra = rsrc_n(a, live && (!C::ANY_SIZE || a < a_end) ? (uint32_t)(a_end - a) : 0u);
+        r.rb = rsrc_n(b, live && (!C::ANY_SIZE || b < b_end) ? (uint32_t)(b_end - b) : 0u);
         r.soa = 0;
         r.sob = 0;
         return r;
@@ -811,7 +847,7 @@ struct Loader {
     // Stepping cursor: the current position and the next tile's origin, and
     // the scalar-offset step of B per k-step.
     Prep cur, nxt;
-    uint32_t bstep;
+    uint32_t astep, bstep;   // of A only where it is stored K x M
 
     // Rebuilding cursor: position q, k-step kt within its tile, the operand
     // origins at that position, and the k / n extents left for the edge masks.
@@ -827,7 +863,7 @@ struct Loader {
         constexpr uint32_t kstep = (uint32_t)C::BK * 2u;
         if constexpr (LONGK) {
             const Prep r = cur;
-            cur.soa += kstep;
+            cur.soa += C::AT ? astep : kstep;
             cur.sob += bstep;
             cur.krem -= C::BK;
             return r;
@@ -836,8 +872,8 @@ struct Loader {
             Prep r;
             r.krem = krem;
             r.nrem = nrem;
-            r.ra = rsrc_n(pa, live ? records((uint64_t)(a_end - pa)) : 0u);
-            r.rb = rsrc_n(pb, live ? records((uint64_t)(b_end - pb)) : 0u);
+            r.ra = rsrc_n(pa, live && (!C::ANY_SIZE || pa < a_end) ? records((uint64_t)(a_end - pa)) : 0u);
+            r.rb = rsrc_n(pb, live && (!C::ANY_SIZE || pb < b_end) ? records((uint64_t)(b_end - pb)) : 0u);
             r.soa = 0;
             r.sob = 0;
             ++q;
@@ -846,7 +882,7 @@ struct Loader {
                 tile_origin(p, ++ti, pa, pb, nrem, krem);
             } else {
                 krem -= C::BK;
-                pa += kstep;
+                pa += C::AT ? (int64_t)kstep * p.lda : (int64_t)kstep;
                 pb += C::BT ? (int64_t)kstep : (int64_t)kstep * p.ldb;
             }
             return r;
@@ -859,7 +895,9 @@ struct Loader {
                                              int lane) const
     {
         if (t < C::A_LOADS) {
-            const bool ok = !EDGE || kofs_k(slot(t, lw, lane)) < r.krem;
+            // A stored K x M: k-rows past K lie past the resource, and columns past M
+            // only reach rows of C that are not stored.
+            const bool ok = !EDGE || C::AT || kofs_k(slot(t, lw, lane)) < r.krem;
             lds_dma16(r.ra, a_tile + (t * C::NLW + lw) * 1024, ok ? voffA[t] : kOOB, r.soa);
         } else {
             const int tb = t - C::A_LOADS;
@@ -901,12 +939,13 @@ struct Loader {
 template <class C>
 struct Frags {
     bf16x8_t a[C::FM];
+    i16x4_t ah[C::AT ? C::FM : 1][2];   // A stored K x M: the two transposing reads per block
     bf16x8_t b[C::FN];       // B stored N x K
     i16x4_t bh[C::FN][2];    // B stored K x N: the two transposing reads per block
 };
 
 template <class C>
-constexpr int frag_reads() { return C::FM + (C::BT ? 1 : 2) * C::FN; }
+constexpr int frag_reads() { return (C::AT ? 2 : 1) * C::FM + (C::BT ? 1 : 2) * C::FN; }
 
 // The frag_reads<C>() LDS read instructions of MFMA k-step kk, one at a time.
 // The MFMA runs with the B fragment as its first operand, so accumulator
@@ -938,9 +977,11 @@ template <class C>
 struct FragReader {
     uint32_t a_off, b_off;
     int r;
+    int a_block;   // A stored K x M: the wave's first block
 
     __device__ __forceinline__ FragReader(int wm, int wn, int lane, int kk)
     {
+        a_block = wm * C::FM;
         if constexpr (C::MF == 16) {
             const int h = lane >> 4, r16 = lane & 15;
             // 64-wide k-steps: row r16 in place, chunk swizzled; 32-wide: the
@@ -948,8 +989,13 @@ struct FragReader {
             const uint32_t in_block = (C::BK == 32) ? (uint32_t)kperm_slot(lane) << 4
                                                      : (uint32_t)(r16 * (C::BK * 2)) +
                                                            (uint32_t)(((4 * kk + h) ^ swz_k<C::BK>(r16)) << 4);
-            a_off = opaque((uint32_t)(wm * C::TM * (C::BK * 2)) + in_block);
+            if constexpr (C::AT)
+                a_off = opaque((uint32_t)(32 * kk + 8 * h + (r16 >> 2)) * (C::BM * 2) +
+                               (uint32_t)(((r16 & 3) >> 1) * 16 + (r16 & 1) * 8));
+            else
+                a_off = opaque((uint32_t)(wm * C::TM * (C::BK * 2)) + in_block);
             if constexpr (C::BT) {
+                static_assert(!C::AT, "r serves both operands");
                 b_off = opaque((uint32_t)(wn * C::TN * (C::BK * 2)) + in_block);
                 r = 0;
             } else {
@@ -997,7 +1043,20 @@ struct FragReader {
     {
         if constexpr (C::MF == 16) {
             constexpr int NB = (C::BT ? 1 : 2) * C::FN;   // B reads
-            if (d == 0 || d > NB) {
+            if constexpr (C::AT) {
+                static_assert(!C::BT, "K x M with K x N");
+                const bool of_a = d < 2 || d >= NB + 2;
+                const int x = d < 2 ? d : of_a ? d - NB : d - 2;
+                const int hh = x & 1, J = of_a ? a_block + (x >> 1) : wn * C::FN + (x >> 1);
+                const lds_char* tile = of_a ? a_tile + a_off : b_tile + b_off;
+                const uint32_t row = of_a ? C::BM * 2 : C::BN * 2;
+                const i16x4_t v = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                    (LDS_AS i16x4_t*)(tile + (uint32_t)(4 * hh) * row + (uint32_t)(2 * (J ^ r)) * 16u));
+                if (of_a)
+                    f.ah[x >> 1][hh] = v;
+                else
+                    f.bh[x >> 1][hh] = v;
+            } else if (d == 0 || d > NB) {
                 const int i = (d == 0) ? 0 : d - NB;
                 f.a[i] = *(const LDS_AS bf16x8_t*)(a_tile + a_off + i * (16 * C::BK * 2));
             } else if constexpr (C::BT) {
@@ -1144,6 +1203,15 @@ __device__ __forceinline__ bf16x8_t b_frag(const Frags<C>& f, int j)
     return __builtin_bit_cast(bf16x8_t, v);
 }
 
+template <class C>
+__device__ __forceinline__ bf16x8_t a_frag(const Frags<C>& f, int i)
+{
+    if constexpr (!C::AT)
+        return f.a[i];
+    const i16x8_t v = __builtin_shufflevector(f.ah[i][0], f.ah[i][1], 0, 1, 2, 3, 4, 5, 6, 7);
+    return __builtin_bit_cast(bf16x8_t, v);
+}
+
 // MFMAs LO .. HI-1 of one k-step (block x = i * FN + j).
 template <class C, int LO, int HI>
 __device__ __forceinline__ void mfma_range(f32x16_t (&acc)[C::FM][C::FN], const Frags<C>& f)
@@ -1171,7 +1239,7 @@ __device__ __forceinline__ void region_mfma(typename C::Acc (&acc)[C::FM][C::FN]
 #pragma unroll
         for (int x = LO; x < HI; ++x)
             acc[I0 + x / C::FN][x % C::FN] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                b_frag<C>(f, x % C::FN), f.a[I0 + x / C::FN], acc[I0 + x / C::FN][x % C::FN], 0, 0, 0);
+                b_frag<C>(f, x % C::FN), a_frag<C>(f, I0 + x / C::FN), acc[I0 + x / C::FN][x % C::FN], 0, 0, 0);
     } else {
         mfma_range<C, LO, HI>(acc, fr[KKI & 1]);
     }
@@ -1557,8 +1625,11 @@ __device__ __forceinline__ void poison_tile(typename C::Acc (&acc)[C::FM][C::FN]
 // ---------------------------------------------------------------------------
 // Kernel: every wave loads and computes (GEMM_SYNC_BARRIER, GEMM_SYNC_FLAGS).
 // ---------------------------------------------------------------------------
-template <class C, bool LONGK, bool EDGE>
-__global__ void __launch_bounds__(C::THREADS) k_gemm(Params p)
+//
+// P: Params, whose tiles are rounded and stored as they are, or a type derived
+// from it with a store_tile of its own (the linear layers' epilogues).
+template <class C, bool LONGK, bool EDGE, class P = Params>
+__global__ void __launch_bounds__(C::THREADS) k_gemm(P p)
 {
     static_assert(!C::PRODUCERS, "configs with loader waves use k_gemm_ws / k_gemm_pp");
     __shared__ __attribute__((aligned(1024))) char smem_raw[C::LDS_BYTES];
@@ -1760,7 +1831,9 @@ __global__ void __launch_bounds__(C::THREADS) k_gemm(Params p)
         }
         if constexpr (C::SYNC == SYNC_FLAGS)
             poison_tile<C>(acc, st);
-        if (p.splits > 1)
+        if constexpr (!std::is_same_v<P, Params>)
+            p.template store_tile<C>(acc, strip, tm, tn, sp * p.span + u, wm, wn, lane);
+        else if (p.splits > 1)
             store_partial<C>(p, acc, sp * p.span + u, wm, wn, lane);
         else
             store_tile<C>(p, acc, strip, tm * C::BM, tn * C::BN, wm, wn, lane);
@@ -1790,8 +1863,8 @@ __global__ void __launch_bounds__(C::THREADS) k_gemm(Params p)
 //             loads may still be outstanding); barrier; first half of
 //             B(c+2); fragments of k-step 0 of position c+1
 // ---------------------------------------------------------------------------
-template <class C, bool LONGK, bool EDGE>
-__global__ void __launch_bounds__(C::THREADS) k_gemm_win(Params p)
+template <class C, bool LONGK, bool EDGE, class P = Params>
+__global__ void __launch_bounds__(C::THREADS) k_gemm_win(P p)
 {
     static_assert(C::WIN && C::SYNC == SYNC_BARRIER, "window-ring configs only");
     __shared__ __attribute__((aligned(1024))) char smem_raw[C::LDS_BYTES];
@@ -1893,7 +1966,11 @@ __global__ void __launch_bounds__(C::THREADS) k_gemm_win(Params p)
             prep_b = prep_a;
             wa = step5(wa, 2);
         }
-        if (p.splits > 1) {
+        if constexpr (!std::is_same_v<P, Params>) {
+            p.template store_tile<C>(acc, win(step5(wa, 4)) + w * C::EPI_WAVE_BYTES, tm, tn, sp * p.span + u, wm, wn, lane);
+            wait_lgkm0();
+            block_barrier();
+        } else if (p.splits > 1) {
             store_partial<C>(p, acc, sp * p.span + u, wm, wn, lane);
         } else {
             // The window of the last position's B tile is free until region 1

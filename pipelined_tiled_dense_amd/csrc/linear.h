@@ -1,0 +1,967 @@
+// Linear layers on the bf16 product (part of library.hip): bias, activation,
+// residual and gate in the product's epilogue, and the products of the backward
+// pass.
+//
+//   linear                y = act(x w^T + bias) + residual
+//   linear, input's grad  dx = (dy w + dres) act'(z)
+//   linear, weight's grad dw = dy^T x,  dbias = column sums of dy
+//   gated                 y = act(g) u,  [g, u] = x [wg; wu]^T + bias
+//   gated, input's grad   dg = t u act'(g),  du = t act(g),  t = dy w
+//
+// The main loops are the bf16 product's (k_gemm_win, k_gemm): these operators are
+// parameter types with a store_tile of their own, and configurations that load A
+// stored K x M (the weight's gradient contracts over the rows of both operands)
+// and B as two factors whose 16-row blocks alternate, so that one wave holds g and
+// u of the same elements.
+#pragma once
+
+namespace {
+
+enum { FUSE_LINEAR, FUSE_DX, FUSE_DW, FUSE_GATED, FUSE_DGATED };
+
+constexpr bool fuse_paired(int mode) { return mode == FUSE_GATED; }
+
+// What an epilogue reads and writes, row-major with `ld` elements between rows.
+//   LINEAR  in0 residual, out0 y, out1 z              (bias)
+//   DX      in0 z, in1 dres, out0 dx
+//   DW      out0 dw (fp32 or bf16)
+//   GATED   out0 y, out1 [g, u]                       (bias)
+//   DGATED  in0 [g, u], out0 [dg, du], out1 y
+// All but LINEAR's y, DX's dx, DW's dw, GATED's y and DGATED's in0 and out0 may be
+// null.
+struct Epilogue {
+    const uint16_t* bias;
+    const uint16_t* in0;
+    const uint16_t* in1;
+    void* out0;
+    uint16_t* out1;
+    int64_t ld_in0, ld_in1, ld_out0, ld_out1;
+    int64_t M, N;            // of the output (a gated unit's N: of one factor)
+    int32_t act;
+    int32_t fp32;            // DW: dw is fp32
+};
+
+// ---------------------------------------------------------------------------
+// The elementwise part: 8 consecutive columns of one row, from fp32 sums.
+// ---------------------------------------------------------------------------
+struct EpilogueIn {
+    u32x4_t a, b;
+};
+
+// What element (row, c) .. (row, c + 7) reads, the n (<= 8) columns that exist.
+template <int MODE>
+__device__ __forceinline__ EpilogueIn epilogue_load(const Epilogue& e, int64_t row, int64_t c, int n)
+{
+    EpilogueIn in{};
+    if (row >= e.M)
+        n = 0;
+    if constexpr (MODE == FUSE_LINEAR || MODE == FUSE_DX) {
+        if (e.in0)
+            in.a = load_chunk<false>(e.in0 + row * e.ld_in0 + c, n, c);
+    }
+    if constexpr (MODE == FUSE_DX) {
+        if (e.in1)
+            in.b = load_chunk<false>(e.in1 + row * e.ld_in1 + c, n, c);
+    }
+    if constexpr (MODE == FUSE_DGATED) {
+        const uint16_t* gu = e.in0 + row * e.ld_in0 + c;
+        in.a = load_chunk<false>(gu, n, c);
+        in.b = load_chunk<false>(gu + e.N, n, c);
+    }
+    return in;
+}
+
+__device__ __forceinline__ void store_bf16(void* base, int64_t at, int n, const float (&v)[kChunk])
+{
+    store_chunk<false>((uint16_t*)base + at, n, chunk_bf16(v));
+}
+
+__device__ __forceinline__ void add_chunk(float (&v)[kChunk], u32x4_t x)
+{
+#pragma unroll
+    for (int e = 0; e < kChunk; ++e)
+        v[e] += chunk_at(x, e);
+}
+
+// s: the sums (GATED: of the gate, and t those of the other factor).
+template <int MODE>
+__device__ __forceinline__ void epilogue_finish(const Epilogue& e, const EpilogueIn& in, int64_t row, int64_t c, int n,
+                                                float (&s)[kChunk], float (&t)[kChunk])
+{
+    if (row >= e.M || n <= 0)
+        return;
+    if constexpr (MODE == FUSE_LINEAR) {
+        if (e.bias)
+            add_chunk(s, load_chunk<false>(e.bias + c, n, c));
+        if (e.out1)
+            store_bf16(e.out1, row * e.ld_out1 + c, n, s);
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i)
+            s[i] = activated<false>(e.act, s[i]).times(1.0f);
+        if (e.in0)
+            add_chunk(s, in.a);
+        store_bf16(e.out0, row * e.ld_out0 + c, n, s);
+    }
+    if constexpr (MODE == FUSE_DX) {
+        if (e.in1)
+            add_chunk(s, in.b);
+        if (e.in0) {
+#pragma unroll
+            for (int i = 0; i < kChunk; ++i)
+                s[i] = activated<true>(e.act, chunk_at(in.a, i)).slope_times(s[i]);
+        }
+        store_bf16(e.out0, row * e.ld_out0 + c, n, s);
+    }
+    if constexpr (MODE == FUSE_DW) {
+        if (e.fp32) {
+            float* p = (float*)e.out0 + row * e.ld_out0 + c;
+            if (n >= kChunk) {
+                __builtin_memcpy(p, s, 32);
+            } else {
+#pragma unroll
+                for (int i = 0; i < kChunk - 1; ++i)
+                    if (i < n)
+                        p[i] = s[i];
+            }
+        } else {
+            store_bf16(e.out0, row * e.ld_out0 + c, n, s);
+        }
+    }
+    if constexpr (MODE == FUSE_GATED) {
+        if (e.bias) {
+            add_chunk(s, load_chunk<false>(e.bias + c, n, c));
+            add_chunk(t, load_chunk<false>(e.bias + e.N + c, n, c));
+        }
+        if (e.out1) {
+            store_bf16(e.out1, row * e.ld_out1 + c, n, s);
+            store_bf16(e.out1, row * e.ld_out1 + e.N + c, n, t);
+        }
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i)
+            s[i] = activated<false>(e.act, s[i]).times(t[i]);
+        store_bf16(e.out0, row * e.ld_out0 + c, n, s);
+    }
+    if constexpr (MODE == FUSE_DGATED) {
+        float dg[kChunk], du[kChunk], y[kChunk];
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i) {
+            const float u = chunk_at(in.b, i);
+            const Activated a = activated<true>(e.act, chunk_at(in.a, i));
+            dg[i] = a.slope_times(s[i], u);
+            du[i] = a.times(s[i]);
+            y[i] = a.times(u);
+        }
+        store_bf16(e.out0, row * e.ld_out0 + c, n, dg);
+        store_bf16(e.out0, row * e.ld_out0 + e.N + c, n, du);
+        if (e.out1)
+            store_bf16(e.out1, row * e.ld_out1 + c, n, y);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Tiles.
+// ---------------------------------------------------------------------------
+// 256 x 256 tiles on the split-window ring, 8 waves: the bf16 product's default.
+// 128 x 128 tiles on a two-stage ring, 4 waves: two workgroups share a compute
+// unit, so that one's epilogue runs beside the other's main loop and small outputs
+// give more workgroups.  A paired B needs both factors' 64 columns in a wave.
+template <bool BT_, bool AT_, bool PAIRED_, bool BIG_>
+struct LinearCfg;
+
+template <bool BT_, bool AT_, bool PAIRED_>
+struct LinearCfg<BT_, AT_, PAIRED_, true>
+    : Cfg<256, 256, 64, 2, PAIRED_ ? 4 : 2, PAIRED_ ? 2 : 4, SYNC_BARRIER, BT_, 0, true, 16> {
+    static constexpr bool AT = AT_, PAIRED = PAIRED_, ANY_SIZE = true;
+    static constexpr int PER_CU = 1;
+};
+
+template <bool BT_, bool AT_, bool PAIRED_>
+struct LinearCfg<BT_, AT_, PAIRED_, false>
+    : Cfg<128, 128, 64, 2, PAIRED_ ? 4 : 2, PAIRED_ ? 1 : 2, SYNC_BARRIER, BT_, 0, false, 16> {
+    static constexpr bool AT = AT_, PAIRED = PAIRED_, ANY_SIZE = true;
+    static constexpr int PER_CU = 2;
+};
+
+// Sums of the k chunks: chunk sp's of the launch's u-th tile are piece sp * span +
+// u of the workspace, a tile's rows (of both factors, one after the other) in fp32.
+template <int MODE>
+struct LinearParams : Params {
+    Epilogue e;
+
+    // The accumulators, 16 rows by 64 columns at a time, through the wave's strip of
+    // LDS into rows, 8 consecutive columns a lane.  A rolled loop, whose passes differ
+    // only in the accumulators that a uniform switch picks, so that the elementwise
+    // part is there once, with every activation in it.
+    //
+    // Strip: 16 rows of 256 bytes, the 16-byte chunk XORed with the row.  A write's 16
+    // lanes of one column group hold 16 rows, a read's 16 lanes two rows at chunks of
+    // one parity: either way all chunks differ, and with them all banks.
+    template <class C>
+    __device__ __forceinline__ void store_tile(typename C::Acc (&acc)[C::FM][C::FN], lds_char* strip, int32_t tm,
+                                               int32_t tn, int32_t piece, int wm, int wn, int lane_in) const
+    {
+        constexpr bool PAIR = fuse_paired(MODE);
+        static_assert(C::PAIRED == PAIR && C::EPI_WAVE_BYTES == 16 * 64 * 4, "the strip");
+        constexpr int FACTORS = PAIR ? 2 : 1, JB = 4 * FACTORS, PER_I = C::FN / JB, PASSES = C::FM * PER_I;
+        constexpr int BNO = C::BN / FACTORS;   // output columns of a tile
+        const int lane = (int)opaque((uint32_t)lane_in);
+        const int wrow = lane & 15, wq = lane >> 4, rrow = lane >> 3, c8 = lane & 7;
+        const int64_t c0 = (int64_t)tn * BNO + wn * (C::TN / FACTORS) + c8 * 8;
+        const int64_t r0 = (int64_t)tm * C::BM + wm * C::TM + rrow;
+        auto row_of = [&](int pass, int step) { return r0 + (pass / PER_I) * 16 + step * 8; };
+        auto col_of = [&](int pass) { return c0 + (pass % PER_I) * 64; };
+        const bool whole = splits == 1;
+        EpilogueIn in[2];
+        auto fetch = [&](int pass) {
+            if (whole) {
+#pragma unroll
+                for (int step = 0; step < 2; ++step)
+                    in[step] = epilogue_load<MODE>(e, row_of(pass, step), col_of(pass), left(e.N, col_of(pass)));
+            }
+        };
+        fetch(0);
+#pragma clang loop unroll(disable)
+        for (int pass = 0; pass < PASSES; ++pass) {
+            float v[FACTORS][2][kChunk];
+#pragma unroll
+            for (int h = 0; h < FACTORS; ++h) {
+                [&]<int... P>(std::integer_sequence<int, P...>) {
+                    (
+                        [&] {
+                            if (pass == P) {
+#pragma unroll
+                                for (int jj = 0; jj < 4; ++jj)
+                                    *(LDS_AS f32x4_t*)(strip + wrow * 256 + (((4 * jj + wq) ^ wrow) << 4)) =
+                                        acc[P / PER_I][(P % PER_I) * JB + jj * FACTORS + h];
+                            }
+                        }(),
+                        ...);
+                }(std::make_integer_sequence<int, PASSES>{});
+                wait_lgkm0();
+#pragma unroll
+                for (int step = 0; step < 2; ++step) {
+                    const int row = rrow + 8 * step;
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const f32x4_t x = *(const LDS_AS f32x4_t*)(strip + row * 256 + (((2 * c8 + q) ^ row) << 4));
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            v[h][step][4 * q + i] = x[i];
+                    }
+                }
+                wait_lgkm0();
+            }
+            const int64_t c = col_of(pass);
+            if (whole) {
+                const EpilogueIn now[2] = {in[0], in[1]};
+                if (pass + 1 < PASSES)
+                    fetch(pass + 1);
+#pragma unroll
+                for (int step = 0; step < 2; ++step)
+                    epilogue_finish<MODE>(e, now[step], row_of(pass, step), c, left(e.N, c), v[0][step],
+                                          v[FACTORS - 1][step]);
+            } else {
+                float* to = partial + (int64_t)piece * (C::BM * BNO * FACTORS);
+#pragma unroll
+                for (int h = 0; h < FACTORS; ++h)
+#pragma unroll
+                    for (int step = 0; step < 2; ++step)
+                        __builtin_memcpy(to + (h * C::BM + (int)(row_of(pass, step) - (int64_t)tm * C::BM)) * BNO +
+                                             (int)(c - (int64_t)tn * BNO),
+                                         v[h][step], 32);
+            }
+        }
+    }
+};
+
+// The epilogue over the sums of k chunks, added in chunk order (with no chunk, K ==
+// 0: over zeros), for the launch's span of tiles of bm x bn outputs.
+template <int MODE>
+__global__ void __launch_bounds__(256) k_linear_finish(LinearParams<MODE> p, int32_t bm, int32_t bn)
+{
+    constexpr int FACTORS = fuse_paired(MODE) ? 2 : 1;
+    const int32_t per_row = bn / kChunk, units = bm * per_row;
+    const int64_t total = (int64_t)p.span * units, piece = (int64_t)bm * bn * FACTORS;
+    for (int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x; q < total; q += (int64_t)gridDim.x * 256) {
+        const int32_t u = (int32_t)(q / units), at = (int32_t)(q - (int64_t)u * units), r = at / per_row;
+        const int32_t cc = (at - r * per_row) * kChunk;
+        int32_t tm, tn;
+        raster_tile(p, p.tile_base + u, tm, tn);
+        const int64_t row = (int64_t)tm * bm + r, c = (int64_t)tn * bn + cc;
+        const int n = left(p.e.N, c);
+        if (row >= p.e.M || n <= 0)
+            continue;
+        const EpilogueIn in = epilogue_load<MODE>(p.e, row, c, n);
+        float v[2][kChunk] = {};
+        for (int32_t sp = 0; sp < p.splits; ++sp) {
+            const float* src = p.partial + (sp * (int64_t)p.span + u) * piece + (int64_t)r * bn + cc;
+#pragma unroll
+            for (int h = 0; h < FACTORS; ++h) {
+                float x[kChunk];
+                __builtin_memcpy(x, src + (int64_t)h * bm * bn, 32);
+#pragma unroll
+                for (int i = 0; i < kChunk; ++i)
+                    v[h][i] += x[i];
+            }
+        }
+        epilogue_finish<MODE>(p.e, in, row, c, n, v[0], v[1]);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Few rows: bound by the weight's bytes and by latency.  As for 8-bit operands
+// (gemm_fp8.h): a workgroup of 8 waves takes 16 MF rows by 16 NF columns (of both
+// factors), its waves share out the 128-byte blocks along k and stream fragments
+// from global memory into registers, DEPTH blocks in use and DEPTH in flight; their
+// sums meet in LDS, in wave order.  ANY: operands of any alignment and stride, K >=
+// 8, by 16-byte loads at any byte; a chunk that reaches past the row's end is read
+// from its last 16 bytes and shifted into place.
+// ---------------------------------------------------------------------------
+template <int MODE, int MF, int NF, int DEPTH, bool ANY>
+__global__ void __launch_bounds__(kSkinnyWaves * 64) k_linear_few(LinearParams<MODE> p, int32_t chunk, int32_t kblocks)
+{
+    constexpr int FACTORS = fuse_paired(MODE) ? 2 : 1, NB = NF * FACTORS, FR = MF * NB;
+    __shared__ __attribute__((aligned(16))) f32x4_t sums[kSkinnyWaves][FR][64];
+    const int lane = threadIdx.x & 63, r16 = lane & 15, g = lane >> 4;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    // The row tiles of one column tile go to one XCD, which then reads the weight once.
+    const int32_t x = blockIdx.x & 7, y = blockIdx.x >> 3;
+    const int32_t tm = y % p.tiles_m, tn = y / p.tiles_m * 8 + x;
+    if (tn >= p.tiles_n)
+        return;
+    const int64_t m0 = (int64_t)tm * (MF * 16), n0 = (int64_t)tn * (NF * 16);
+    const int32_t kb_first = blockIdx.y * chunk, kb_end = min(kb_first + chunk, kblocks);
+    const int64_t lda = p.lda * 2, ldb = p.ldb * 2;
+    const int32_t kbytes = (int32_t)p.K * 2;
+
+    // Rows past the end read as zeros: their offset is past the resource.
+    const int64_t a_rows = min(p.M - m0, (int64_t)MF * 16), b_rows = min(p.N - n0, (int64_t)NF * 16);
+    const char* a0 = p.A + m0 * lda;
+    const char* b0[FACTORS];
+    __amdgpu_buffer_rsrc_t rb[FACTORS];
+    const __amdgpu_buffer_rsrc_t ra = make_rsrc(a0, (a_rows - 1) * lda + kbytes);
+#pragma unroll
+    for (int h = 0; h < FACTORS; ++h) {
+        b0[h] = p.B + (n0 + h * p.N) * ldb;
+        rb[h] = make_rsrc(b0[h], (b_rows - 1) * ldb + kbytes);
+    }
+    // Lanes 4 i .. 4 i + 3 read 64 consecutive bytes of a row; an MFMA's lane (r16, g)
+    // then takes chunk g of row r16 from the lane that read it.
+    const int lr = (lane >> 2 & 3) * 4 + (lane >> 4), lc = lane & 3;
+    const int from = ((lane & 3) * 16 + (lane & 12) + g) * 4;
+    auto mfma_order = [&](u32x4_t v) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            v[i] = (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)v[i]);
+        return v;
+    };
+    uint32_t va[MF] = {}, vb[NF] = {};
+#pragma unroll
+    for (int i = 0; i < MF; ++i)
+        va[i] = i * 16 + lr < a_rows ? (uint32_t)(i * 16 + lr) * (uint32_t)lda + lc * 16 : kOOB;
+#pragma unroll
+    for (int j = 0; j < NF; ++j)
+        vb[j] = j * 16 + lr < b_rows ? (uint32_t)(j * 16 + lr) * (uint32_t)ldb + lc * 16 : kOOB;
+
+    struct Block {
+        u32x4_t a[MF][2], b[NB][2];
+    };
+    // ANY: where half h of block kb is read, and how many of its bytes precede it.
+    auto place = [&](int32_t kb, int h, int32_t& at) {
+        const int32_t k = kb * 128 + (h * 4 + lc) * 16;
+        at = min(k, kbytes - 16);
+        return min(k - at, 16);
+    };
+    auto load = [&](Block& v, int32_t kb) {
+        // The halves of a line one after the other, while the line is in the L1.
+        auto halves = [&](u32x4_t (&to)[2], const char* base, int64_t row, int64_t rows, int64_t ld,
+                          const __amdgpu_buffer_rsrc_t& rsrc, uint32_t voff) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if constexpr (ANY) {
+                    int32_t at;
+                    place(kb, h, at);
+                    // Rows past the last repeat it; no one stores their sums.
+                    __builtin_memcpy(&to[h], base + min(row, rows - 1) * ld + at, 16);
+                } else {
+                    const bool ok = kb * 128 + (h * 4 + lc) * 16 < kbytes;
+                    to[h] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
+                                                            rsrc, ok ? voff : kOOB, kb * 128 + h * 64, 0));
+                }
+            }
+        };
+#pragma unroll
+        for (int h = 0; h < FACTORS; ++h)
+#pragma unroll
+            for (int j = 0; j < NF; ++j)
+                halves(v.b[h * NF + j], b0[h], j * 16 + lr, b_rows, ldb, rb[h], vb[j]);
+#pragma unroll
+        for (int i = 0; i < MF; ++i)
+            halves(v.a[i], a0, i * 16 + lr, a_rows, lda, ra, va[i]);
+    };
+
+    f32x4_t acc[MF][NB];
+#pragma unroll
+    for (int i = 0; i < MF; ++i)
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+            acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    auto compute = [&](const Block& v, int32_t kb) {
+        const bool tail = ANY && (kb + 1) * 128 > kbytes;
+        auto frag = [&](const u32x4_t (&raw)[2], bf16x8_t (&to)[2]) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                u32x4_t q = raw[h];
+                if (tail) {
+                    int32_t at;
+                    q = without_first(q, place(kb, h, at));
+                }
+                to[h] = __builtin_bit_cast(bf16x8_t, mfma_order(q));
+            }
+        };
+        bf16x8_t bf[NB][2];
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+            frag(v.b[j], bf[j]);
+#pragma unroll
+        for (int i = 0; i < MF; ++i) {
+            bf16x8_t af[2];
+            frag(v.a[i], af);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int j = 0; j < NB; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf[j][h], af[h], acc[i][j], 0, 0, 0);
+        }
+    };
+
+    Block cur[DEPTH], nxt[DEPTH];
+    constexpr int STEP = kSkinnyWaves * DEPTH;
+    auto load_all = [&](Block (&v)[DEPTH], int32_t kb0) {
+        if (kb0 < kb_end) {
+#pragma unroll
+            for (int d = 0; d < DEPTH; ++d)
+                load(v[d], kb0 + d * kSkinnyWaves);
+        }
+    };
+    auto compute_all = [&](const Block (&v)[DEPTH], int32_t kb0) {
+#pragma unroll
+        for (int d = 0; d < DEPTH; ++d)
+            if (kb0 + d * kSkinnyWaves < kb_end)
+                compute(v[d], kb0 + d * kSkinnyWaves);
+    };
+    // Workgroups start at different places along k: with a power-of-two row stride,
+    // all of them reading the same columns at once fall on the same few channels.
+    const int32_t rounds = (kb_end - kb_first + STEP - 1) / STEP, rot = (int32_t)(blockIdx.x % (unsigned)rounds);
+    auto at = [&](int32_t t) {
+        return t < rounds ? kb_first + w + (t + rot < rounds ? t + rot : t + rot - rounds) * STEP : kb_end;
+    };
+    load_all(cur, at(0));
+    for (int32_t t = 0; t < rounds; t += 2) {
+        load_all(nxt, at(t + 1));
+        compute_all(cur, at(t));
+        load_all(cur, at(t + 2));
+        compute_all(nxt, at(t + 1));
+    }
+
+#pragma unroll
+    for (int i = 0; i < MF; ++i)
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+            sums[w][i * NB + j][lane] = acc[i][j];
+    __syncthreads();
+    // Wave w finishes fragments w, w + 8, ... of one factor with the other's beside
+    // them.  Lanes of even g hold columns 8 (g / 2) .. + 3 and get + 4 .. + 7 from the
+    // lane 16 further.
+    for (int f = w; f < MF * NF; f += kSkinnyWaves) {
+        const int i = f / NF, j = f % NF;
+        float v[2][kChunk];
+#pragma unroll
+        for (int h = 0; h < FACTORS; ++h) {
+            f32x4_t s = sums[0][i * NB + h * NF + j][lane];
+#pragma unroll
+            for (int z = 1; z < kSkinnyWaves; ++z)
+                s += sums[z][i * NB + h * NF + j][lane];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                v[h][q] = s[q];
+                v[h][4 + q] = __shfl_xor(s[q], 16);
+            }
+        }
+        if (g & 1)
+            continue;
+        const int r = i * 16 + r16, cc = j * 16 + g * 4;
+        const int64_t row = m0 + r, c = n0 + cc;
+        if (p.splits > 1) {
+            const int64_t piece = (int64_t)blockIdx.y * p.span + (tn * p.tiles_m + tm);
+            float* to = p.partial + piece * (MF * 16 * NF * 16 * FACTORS) + r * (NF * 16) + cc;
+#pragma unroll
+            for (int h = 0; h < FACTORS; ++h)
+                __builtin_memcpy(to + h * (MF * 16 * NF * 16), v[h], 32);
+        } else {
+            const int n = left(p.e.N, c);
+            epilogue_finish<MODE>(p.e, epilogue_load<MODE>(p.e, row, c, n), row, c, n, v[0], v[1]);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Column sums of bf16 X (rows x cols) in fp32: dbias.  A workgroup sums 256 columns
+// of a run of rows, 8 rows at a time; a second launch adds the runs in order.
+// ---------------------------------------------------------------------------
+__global__ void __launch_bounds__(256) k_column_sums(const uint16_t* x, int64_t rows, int64_t cols, int64_t ld,
+                                                     int64_t run, float* to)
+{
+    __shared__ float sums[8][32][kChunk];
+    const int cl = threadIdx.x & 31, rl = threadIdx.x >> 5;
+    const int64_t c = ((int64_t)blockIdx.x * 32 + cl) * kChunk;
+    const int n = left(cols, c);
+    const int64_t first = (int64_t)blockIdx.y * run, end = min(first + run, rows);
+    float s[kChunk] = {};
+    for (int64_t r = first + rl; r < end; r += 8)
+        add_chunk(s, load_chunk<false>(x + r * ld + c, n, c));
+#pragma unroll
+    for (int i = 0; i < kChunk; ++i)
+        sums[rl][cl][i] = s[i];
+    __syncthreads();
+    const int col = threadIdx.x;
+    float t = 0.0f;
+#pragma unroll
+    for (int r = 0; r < 8; ++r)
+        t += sums[r][col / kChunk][col % kChunk];
+    if ((int64_t)blockIdx.x * 256 + col < cols)
+        to[blockIdx.y * cols + (int64_t)blockIdx.x * 256 + col] = t;
+}
+
+__global__ void __launch_bounds__(256) k_column_sums_join(const float* part, int64_t cols, int32_t runs, float* to)
+{
+    const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (c >= cols)
+        return;
+    float t = 0.0f;
+    for (int32_t r = 0; r < runs; ++r)
+        t += part[r * cols + c];
+    to[c] = t;
+}
+
+// Zero-padded copies of the operands whose rows do not start on 16-byte boundaries
+// or end inside a 16-byte chunk, one launch for both.
+struct LinearPad {
+    const uint16_t* src[2];
+    uint16_t* dst[2];
+    int64_t rows[2], cols[2], ld[2], dst_ld[2];
+};
+
+__global__ void __launch_bounds__(256) k_linear_pad(LinearPad p)
+{
+    const int64_t first = p.rows[0] * (p.dst_ld[0] / kChunk), total = first + p.rows[1] * (p.dst_ld[1] / kChunk);
+    for (int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x; id < total; id += (int64_t)gridDim.x * 256) {
+        const int o = id >= first;
+        const int64_t per_row = p.dst_ld[o] / kChunk, at = o ? id - first : id, r = at / per_row;
+        const int64_t c = (at - r * per_row) * kChunk;
+        *(u32x4_t*)(p.dst[o] + r * p.dst_ld[o] + c) = load_chunk<false>(p.src[o] + r * p.ld[o] + c, left(p.cols[o], c), c);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Host side.
+// ---------------------------------------------------------------------------
+// A product C (M x N, N of one factor) over K, as the kernels see it.
+struct LinearShape {
+    int64_t M, N, K;
+    bool bt, at;             // B stored N x K; A stored K x M
+    int factors;
+};
+
+enum { TILES_BIG, TILES_SMALL, TILES_FEW };
+
+// Rows of few-row workgroups and their columns of one factor.
+constexpr int kFewCols = 32;
+
+struct LinearPlan {
+    int kind;
+    int mf;                  // TILES_FEW: row fragments
+    int bm, bn;              // outputs per workgroup
+    int64_t tiles, splits, chunk, grid, workspace;   // chunk: k elements
+};
+
+// k chunks for `tiles` work items on `slots` places: chunks of whole 64-wide k-steps,
+// each at least `least` long, all of them with work.
+int64_t linear_splits(int64_t tiles, int64_t K, int64_t slots, int64_t least, int64_t& chunk)
+{
+    chunk = K;
+    if (2 * tiles > slots)
+        return 1;
+    int64_t s = slots / tiles;
+    if (s > kMaxSplits)
+        s = kMaxSplits;
+    if (s > K / least)
+        s = K / least;
+    if (s <= 1)
+        return 1;
+    chunk = ceil_div(ceil_div(K, s), 64) * 64;
+    return ceil_div(K, chunk);
+}
+
+LinearPlan linear_plan(const LinearShape& q, int cus)
+{
+    LinearPlan pl{};
+    if (q.bt && !q.at && q.M <= 64 && q.K >= kChunk) {
+        pl.kind = TILES_FEW;
+        pl.mf = q.M <= 16 ? 1 : q.M <= 32 ? 2 : 4;
+        pl.bm = pl.mf * 16;
+        pl.bn = kFewCols;
+        pl.tiles = ceil_div(q.M, pl.bm) * ceil_div(q.N, pl.bn);
+        pl.splits = linear_splits(pl.tiles, q.K, cus, 2048, pl.chunk);
+        pl.grid = ceil_div(ceil_div(q.N, pl.bn), 8) * 8 * ceil_div(q.M, pl.bm);
+    } else {
+        const int64_t big = ceil_div(q.M, 256) * ceil_div(q.N * q.factors, 256);
+        const int edge = big >= cus ? 256 : 128;
+        pl.kind = edge == 256 ? TILES_BIG : TILES_SMALL;
+        pl.bm = edge;
+        pl.bn = edge / q.factors;
+        pl.tiles = ceil_div(q.M, pl.bm) * ceil_div(q.N, pl.bn);
+        const int64_t slots = (int64_t)cus * (edge == 256 ? 1 : 2);
+        pl.splits = linear_splits(pl.tiles, q.K, slots, 512, pl.chunk);
+        pl.grid = pl.tiles * pl.splits < slots ? pl.tiles * pl.splits : slots;
+    }
+    pl.workspace = pl.splits > 1 ? pl.tiles * pl.splits * pl.bm * pl.bn * q.factors * 4 : 0;
+    return pl;
+}
+
+template <class C, int MODE>
+int launch_linear(const LinearParams<MODE>& p, int64_t grid, hipStream_t s)
+{
+    // Masks per lane only where a position may be partial: the k tail inside rows,
+    // and columns past N of a K x N B.
+    const bool edge = (!C::AT && (p.K % C::BK != 0 || p.K % p.ksplit != 0)) || (!C::BT && p.N % C::BN != 0);
+    const bool longk = p.k_steps >= C::LONGK_MIN_KT && p.small_span;
+    const dim3 g((unsigned)grid), b(C::THREADS);
+    auto run = [&]<bool LONGK, bool EDGE>() {
+        if constexpr (C::WIN)
+            hipLaunchKernelGGL(HIP_KERNEL_NAME(k_gemm_win<C, LONGK, EDGE, LinearParams<MODE>>), g, b, 0, s, p);
+        else
+            hipLaunchKernelGGL(HIP_KERNEL_NAME(k_gemm<C, LONGK, EDGE, LinearParams<MODE>>), g, b, 0, s, p);
+    };
+    if (longk && !edge)
+        run.template operator()<true, false>();
+    else if (longk)
+        run.template operator()<true, true>();
+    else
+        run.template operator()<false, true>();
+    return launched();
+}
+
+template <int MODE>
+int launch_few(const LinearParams<MODE>& p, const LinearPlan& pl, bool any, hipStream_t s)
+{
+    const int32_t kblocks = (int32_t)ceil_div(p.K, 64), chunk = (int32_t)ceil_div(pl.chunk, 64);
+    const dim3 g((unsigned)pl.grid, (unsigned)pl.splits), b(kSkinnyWaves * 64);
+    auto run = [&]<int MF, int DEPTH>() {
+        if (any)
+            hipLaunchKernelGGL(HIP_KERNEL_NAME(k_linear_few<MODE, MF, 2, DEPTH, true>), g, b, 0, s, p, chunk, kblocks);
+        else
+            hipLaunchKernelGGL(HIP_KERNEL_NAME(k_linear_few<MODE, MF, 2, DEPTH, false>), g, b, 0, s, p, chunk, kblocks);
+    };
+    if (pl.mf == 1)
+        run.template operator()<1, 2>();
+    else if (pl.mf == 2)
+        run.template operator()<2, 2>();
+    else
+        run.template operator()<4, 1>();
+    return launched();
+}
+
+// The product of A and B into epilogue e.  The caller has checked everything but
+// the device.
+template <int MODE>
+int linear_run(const LinearShape& q, const void* A, int64_t lda, const void* B, int64_t ldb, const Epilogue& e,
+               TempMem& tm, int cus, hipStream_t s)
+{
+    constexpr bool PAIR = fuse_paired(MODE), BT = MODE == FUSE_LINEAR || PAIR, AT = MODE == FUSE_DW;
+    LinearParams<MODE> p;
+    memset((void*)&p, 0, sizeof p);
+    p.e = e;
+    const LinearPlan pl = q.K > 0 ? linear_plan(q, cus) : LinearPlan{TILES_SMALL, 0, 128, 128 / q.factors, 0, 0, 0, 0, 0};
+    p.A = (const char*)A;
+    p.B = (const char*)B;
+    p.M = q.M;
+    p.N = q.N;
+    p.K = q.K;
+    p.lda = lda;
+    p.ldb = ldb;
+    p.tiles_m = (int32_t)ceil_div(q.M, pl.bm);
+    p.tiles_n = (int32_t)ceil_div(q.N, pl.bn);
+    const int64_t tiles = ceil_div(q.M, pl.bm) * ceil_div(q.N, pl.bn);
+    const int64_t steps = ceil_div(pl.chunk, 64);
+    if (tiles > ((int64_t)1 << 30) || tiles * (pl.splits ? pl.splits : 1) * (steps ? steps : 1) > ((int64_t)1 << 30))
+        return GEMM_ERR_UNSUPPORTED_SHAPE;
+    p.tiles_mn = p.span = (int32_t)tiles;
+    p.splits = (int32_t)pl.splits;
+    p.tiles = (int32_t)(tiles * pl.splits);
+    p.ksplit = pl.chunk;
+    p.k_steps = (int32_t)steps;
+    p.group_m = pl.kind == TILES_FEW ? p.tiles_m : 4;
+    p.spin_limit = kSpinLimit;
+    p.clock_on = g_clock_on.load(std::memory_order_relaxed) ? 1u : 0u;
+    auto finish = [&]() {
+        const int64_t units = (int64_t)p.span * pl.bm * pl.bn / kChunk;
+        hipLaunchKernelGGL(k_linear_finish<MODE>, dim3(flat_grid(units)), dim3(256), 0, s, p, pl.bm, pl.bn);
+        return launched();
+    };
+    if (q.K == 0)
+        return finish();
+
+    // Operands as the tiles read them: rows on 16-byte boundaries, of whole 16-byte
+    // chunks, at most 2^22 elements apart.  The few-row kernel takes any.
+    const int64_t a_rows = AT ? q.K : q.M, a_cols = AT ? q.M : q.K;
+    const int64_t b_rows = BT ? q.N * q.factors : q.K, b_cols = BT ? q.K : q.N;
+    auto fits = [](const void* ptr, int64_t rows, int64_t cols, int64_t ld) {
+        return ((uintptr_t)ptr & 15) == 0 && cols % kChunk == 0 && (rows <= 1 || (ld % kChunk == 0 && ld <= kMaxLd));
+    };
+    const bool a_ok = fits(A, a_rows, a_cols, lda), b_ok = fits(B, b_rows, b_cols, ldb);
+    const bool few = pl.kind == TILES_FEW;
+    const bool pad_a = !few && !a_ok, pad_b = !few && !b_ok;
+    const int64_t a_ld = round8(a_cols), b_ld = round8(b_cols);
+    const int64_t a_bytes = pad_a ? align256(a_rows * a_ld * 2) : 0, b_bytes = pad_b ? align256(b_rows * b_ld * 2) : 0;
+    const int64_t bytes = a_bytes + b_bytes + pl.workspace;
+    void* ws = nullptr;
+    int rc = GEMM_OK;
+    if (bytes > 0 && (rc = temp_take(tm, bytes, s, &ws)) != GEMM_OK)
+        return rc;
+    if (pad_a || pad_b) {
+        LinearPad c{{(const uint16_t*)A, (const uint16_t*)B},
+                    {(uint16_t*)ws, (uint16_t*)((char*)ws + a_bytes)},
+                    {pad_a ? a_rows : 0, pad_b ? b_rows : 0},
+                    {a_cols, b_cols},
+                    {lda, ldb},
+                    {a_ld, b_ld}};
+        if (pad_a) {
+            p.A = (const char*)c.dst[0];
+            p.lda = a_ld;
+        }
+        if (pad_b) {
+            p.B = (const char*)c.dst[1];
+            p.ldb = b_ld;
+        }
+        hipLaunchKernelGGL(k_linear_pad, dim3(flat_grid(a_bytes / 16 + b_bytes / 16)), dim3(256), 0, s, c);
+        rc = launched();
+    }
+    if (pl.splits > 1)
+        p.partial = (float*)((char*)ws + a_bytes + b_bytes);
+    // A single row's stride is never used, but enters sizes and offsets.
+    if (a_rows <= 1)
+        p.lda = a_ld;
+    if (b_rows <= 1)
+        p.ldb = b_ld;
+    p.small_span = ((a_rows - 1) * p.lda + a_ld) * 2 < (int64_t)kMaxRecords &&
+                   ((b_rows / q.factors - 1) * p.ldb + b_ld) * 2 < (int64_t)kMaxRecords;
+    if (rc == GEMM_OK) {
+        if constexpr (BT) {
+            if (few)
+                rc = launch_few<MODE>(p, pl, !(a_ok && b_ok), s);
+        }
+        if (pl.kind == TILES_BIG)
+            rc = launch_linear<LinearCfg<BT, AT, PAIR, true>, MODE>(p, pl.grid, s);
+        else if (pl.kind == TILES_SMALL)
+            rc = launch_linear<LinearCfg<BT, AT, PAIR, false>, MODE>(p, pl.grid, s);
+    }
+    if (rc == GEMM_OK && pl.splits > 1)
+        rc = finish();
+    const int frc = temp_give(tm, ws, s);
+    return rc != GEMM_OK ? rc : frc;
+}
+
+int linear_sizes(int64_t M, int64_t N, int64_t K)
+{
+    if (M < 0 || N < 0 || K < 0)
+        return GEMM_ERR_INVALID_VALUE;
+    return M > kMaxRows || N > kMaxLd || K > kMaxLd ? GEMM_ERR_UNSUPPORTED_SHAPE : GEMM_OK;
+}
+
+bool known_act(int act) { return act >= GEMM_ACT_NONE && act <= GEMM_ACT_SILU; }
+
+// An operand of a call: whether it has to be there, and, of an output, which input's
+// very memory it may be (its elements are read before they are written, by the
+// lane that writes them).
+struct LinearOperand {
+    Operand o;
+    bool needed;
+    const void* in_place;
+};
+
+int check_linear(const LinearOperand* ins, int n_ins, const LinearOperand* outs, int n_outs)
+{
+    for (int i = 0; i < n_ins + n_outs; ++i) {
+        const LinearOperand& x = i < n_ins ? ins[i] : outs[i - n_ins];
+        if (!x.needed && !x.o.p)
+            continue;
+        if (const int rc = check_operand(x.o))
+            return rc;
+    }
+    for (int i = 0; i < n_outs; ++i) {
+        for (int j = 0; j < n_ins; ++j)
+            if (meet(outs[i].o, ins[j].o) && !(outs[i].in_place == ins[j].o.p && ins[j].in_place == ins[j].o.p &&
+                                               same_memory(outs[i].o, ins[j].o)))
+                return GEMM_ERR_ALIAS;
+        for (int j = 0; j < i; ++j)
+            if (meet(outs[i].o, outs[j].o))
+                return GEMM_ERR_ALIAS;
+    }
+    return GEMM_OK;
+}
+
+// The device, then the product.
+template <int MODE>
+int linear_enqueue(const LinearShape& q, const void* A, int64_t lda, const void* B, int64_t ldb, const Epilogue& e,
+                   void* stream)
+{
+    int cus = 0;
+    TempMem tm;
+    if (const int rc = device_info(&cus, &tm.pool, nullptr, &tm.info))
+        return rc;
+    return linear_run<MODE>(q, A, lda, B, ldb, e, tm, cus, (hipStream_t)stream);
+}
+
+// dbias: the column sums of dY.
+int column_sums(const void* X, int64_t rows, int64_t cols, int64_t ld, float* to, TempMem& tm, int cus, hipStream_t s)
+{
+    const int64_t groups = ceil_div(cols, 256);
+    int64_t runs = std::max<int64_t>(1, std::min(4 * (int64_t)cus / groups, rows / 64));
+    const int64_t run = ceil_div(rows, runs);
+    runs = rows > 0 ? ceil_div(rows, run) : 1;
+    void* ws = nullptr;
+    int rc = GEMM_OK;
+    if (runs > 1 && (rc = temp_take(tm, runs * cols * 4, s, &ws)) != GEMM_OK)
+        return rc;
+    hipLaunchKernelGGL(k_column_sums, dim3((unsigned)groups, (unsigned)runs), dim3(256), 0, s, (const uint16_t*)X, rows,
+                       cols, ld, run, runs > 1 ? (float*)ws : to);
+    rc = launched();
+    if (rc == GEMM_OK && runs > 1) {
+        hipLaunchKernelGGL(k_column_sums_join, dim3((unsigned)groups), dim3(256), 0, s, (const float*)ws, cols,
+                           (int32_t)runs, to);
+        rc = launched();
+    }
+    const int frc = temp_give(tm, ws, s);
+    return rc != GEMM_OK ? rc : frc;
+}
+
+}  // namespace
+
+extern "C" {
+
+int gemm_linear(int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, const void* W, int64_t ldw,
+                const void* bias, int act, const void* residual, int64_t ldr, void* Z, int64_t ldz, void* Y, int64_t ldy,
+                void* stream)
+{
+    if (const int rc = linear_sizes(M, N, K))
+        return rc;
+    if (!known_act(act))
+        return GEMM_ERR_INVALID_VALUE;
+    if (M == 0 || N == 0)
+        return GEMM_OK;
+    const LinearOperand ins[] = {{{K > 0 ? X : nullptr, M, K, ldx, 2}, K > 0, nullptr},
+                                 {{K > 0 ? W : nullptr, N, K, ldw, 2}, K > 0, nullptr},
+                                 {{bias, 1, N, N, 2}, false, nullptr},
+                                 {{residual, M, N, ldr, 2}, false, residual}};
+    const LinearOperand outs[] = {{{Y, M, N, ldy, 2}, true, residual}, {{Z, M, N, ldz, 2}, false, nullptr}};
+    if (const int rc = check_linear(ins, 4, outs, 2))
+        return rc;
+    const Epilogue e{(const uint16_t*)bias, (const uint16_t*)residual, nullptr, Y, (uint16_t*)Z, ldr, 0, ldy, ldz,
+                     M, N, act, 0};
+    return linear_enqueue<FUSE_LINEAR>({M, N, K, true, false, 1}, X, ldx, W, ldw, e, stream);
+}
+
+int gemm_linear_bwd_input(int64_t M, int64_t N, int64_t K, const void* dY, int64_t lddy, const void* W, int64_t ldw,
+                          int act, const void* Z, int64_t ldz, const void* dres, int64_t lddr, void* dX, int64_t lddx,
+                          void* stream)
+{
+    if (const int rc = linear_sizes(M, N, K))
+        return rc;
+    if (!known_act(act))
+        return GEMM_ERR_INVALID_VALUE;
+    if (M == 0 || K == 0)
+        return GEMM_OK;
+    if (act == GEMM_ACT_NONE)
+        Z = nullptr;
+    const LinearOperand ins[] = {{{N > 0 ? dY : nullptr, M, N, lddy, 2}, N > 0, nullptr},
+                                 {{N > 0 ? W : nullptr, N, K, ldw, 2}, N > 0, nullptr},
+                                 {{Z, M, K, ldz, 2}, act != GEMM_ACT_NONE, Z},
+                                 {{dres, M, K, lddr, 2}, false, dres}};
+    const LinearOperand outs[] = {{{dX, M, K, lddx, 2}, true, dX == Z ? Z : dres}};
+    if (const int rc = check_linear(ins, 4, outs, 1))
+        return rc;
+    const Epilogue e{nullptr, (const uint16_t*)Z, (const uint16_t*)dres, dX, nullptr, ldz, lddr, lddx, 0, M, K, act, 0};
+    return linear_enqueue<FUSE_DX>({M, K, N, false, false, 1}, dY, lddy, W, ldw, e, stream);
+}
+
+int gemm_linear_bwd_weight(int64_t M, int64_t N, int64_t K, const void* dY, int64_t lddy, const void* X, int64_t ldx,
+                           void* dW, int64_t lddw, int dw_type, float* dbias, void* stream)
+{
+    if (const int rc = linear_sizes(M, N, K))
+        return rc;
+    const bool fp32 = dw_type == GEMM_TYPE_FP32;
+    if (!fp32 && dw_type != GEMM_TYPE_BF16)
+        return GEMM_ERR_INVALID_VALUE;
+    const bool weight = N > 0 && K > 0, bias = dbias && N > 0;
+    if (!weight && !bias)
+        return GEMM_OK;
+    const LinearOperand ins[] = {{{M > 0 ? dY : nullptr, M, N, lddy, 2}, M > 0, nullptr},
+                                 {{M > 0 && weight ? X : nullptr, M, K, ldx, 2}, M > 0 && weight, nullptr}};
+    const LinearOperand outs[] = {{{weight ? dW : nullptr, N, K, lddw, fp32 ? 4 : 2}, weight, nullptr},
+                                  {{dbias, 1, N, N, 4}, false, nullptr}};
+    if (const int rc = check_linear(ins, 2, outs, 2))
+        return rc;
+    int cus = 0;
+    TempMem tm;
+    if (const int rc = device_info(&cus, &tm.pool, nullptr, &tm.info))
+        return rc;
+    if (bias)
+        if (const int rc = column_sums(dY, M, N, lddy, dbias, tm, cus, (hipStream_t)stream))
+            return rc;
+    if (!weight)
+        return GEMM_OK;
+    const Epilogue e{nullptr, nullptr, nullptr, dW, nullptr, 0, 0, lddw, 0, N, K, GEMM_ACT_NONE, fp32 ? 1 : 0};
+    return linear_run<FUSE_DW>({N, K, M, false, true, 1}, dY, lddy, X, ldx, e, tm, cus, (hipStream_t)stream);
+}
+
+int gemm_gated_linear(int64_t M, int64_t F, int64_t K, const void* X, int64_t ldx, const void* W, int64_t ldw,
+                      const void* bias, int act, void* GU, int64_t ldgu, void* Y, int64_t ldy, void* stream)
+{
+    if (const int rc = linear_sizes(M, F, K))
+        return rc;
+    if (!known_act(act))
+        return GEMM_ERR_INVALID_VALUE;
+    if (M == 0 || F == 0)
+        return GEMM_OK;
+    const LinearOperand ins[] = {{{K > 0 ? X : nullptr, M, K, ldx, 2}, K > 0, nullptr},
+                                 {{K > 0 ? W : nullptr, 2 * F, K, ldw, 2}, K > 0, nullptr},
+                                 {{bias, 1, 2 * F, 2 * F, 2}, false, nullptr}};
+    const LinearOperand outs[] = {{{Y, M, F, ldy, 2}, true, nullptr}, {{GU, M, 2 * F, ldgu, 2}, false, nullptr}};
+    if (const int rc = check_linear(ins, 3, outs, 2))
+        return rc;
+    const Epilogue e{(const uint16_t*)bias, nullptr, nullptr, Y, (uint16_t*)GU, 0, 0, ldy, ldgu, M, F, act, 0};
+    return linear_enqueue<FUSE_GATED>({M, F, K, true, false, 2}, X, ldx, W, ldw, e, stream);
+}
+
+int gemm_gated_linear_bwd_input(int64_t M, int64_t F, int64_t N, const void* dY, int64_t lddy, const void* W, int64_t ldw,
+                                int act, const void* GU, int64_t ldgu, void* dGU, int64_t lddgu, void* Y, int64_t ldy,
+                                void* stream)
+{
+    if (const int rc = linear_sizes(M, F, N))
+        return rc;
+    if (!known_act(act))
+        return GEMM_ERR_INVALID_VALUE;
+    if (M == 0 || F == 0)
+        return GEMM_OK;
+    const LinearOperand ins[] = {{{N > 0 ? dY : nullptr, M, N, lddy, 2}, N > 0, nullptr},
+                                 {{N > 0 ? W : nullptr, N, F, ldw, 2}, N > 0, nullptr},
+                                 {{GU, M, 2 * F, ldgu, 2}, true, GU}};
+    const LinearOperand outs[] = {{{dGU, M, 2 * F, lddgu, 2}, true, GU}, {{Y, M, F, ldy, 2}, false, nullptr}};
+    if (const int rc = check_linear(ins, 3, outs, 2))
+        return rc;
+    const Epilogue e{nullptr, (const uint16_t*)GU, nullptr, dGU, (uint16_t*)Y, ldgu, 0, lddgu, ldy, M, F, act, 0};
+    return linear_enqueue<FUSE_DGATED>({M, F, N, false, false, 1}, dY, lddy, W, ldw, e, stream);
+}
+
+}  // extern "C"
