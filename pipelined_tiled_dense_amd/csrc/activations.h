@@ -1,35 +1,44 @@
-// Activations and their slopes for the linear layers' epilogues (part of library.hip).
+// Activations and their slopes, 8 values at a time, for the linear layers'
+// epilogues (part of library.hip).
+//
+// Those epilogues are bound by their vector instructions (a tile's 128 values a
+// lane, while the matrix cores wait), so the usual way has as few as bf16 results
+// need: one exponential and one reciprocal a value, off by an ulp each, and for the
+// normal distribution a polynomial right to 1.6e-5, a hundredth of bf16's rounding.
+// Very negative z, whose exponential or its reciprocal leaves fp32's normal range,
+// take another: a branch that no lane of most waves takes.
 #pragma once
 
 namespace {
 
-// An activation a(z) and its slope a'(z) as value * f^3 and slope * f^3.  f is 1,
-// except where a and a' are too small for fp32 (very negative z): then it is the
-// third root of what they hold of an exponential, a normal number, and each factor
-// beside the activation takes an f first, so that a large one meets a small one
-// before anything overflows or is lost.
+// a(z) and a'(z) as value * f^3 and slope * f^3.  f is 1, except where the two are
+// too small for fp32: then it is the third root of what they hold of an
+// exponential, a normal number, and each factor beside the activation takes an f
+// first, so that a large one meets a small one before anything overflows or is lost.
 struct Activated {
     float f, value, slope;
 
     __device__ __forceinline__ float times(float x) const { return (x * f) * (value * f) * f; }
+    __device__ __forceinline__ float slope_times(float x) const { return (x * f) * (slope * f) * f; }
     // x y alone may overflow beside a small slope, y times a slope be lost beside a large x.
     __device__ __forceinline__ float slope_times(float x, float y) const
     {
         const float xf = x * f, yf = y * f, sf = slope * f;
         return f > 0.01f ? xf * (yf * sf) : xf * yf * sf;
     }
-    __device__ __forceinline__ float slope_times(float x) const { return (x * f) * (slope * f) * f; }
 };
 
-// z times the logistic function of v(z), with z v'(z) for the slope: silu (v = z)
-// and gelu's usual approximation (v = z (a + b z^2)).  Where s(v) is exp(v) to
-// fp32, it is f^3 (low_gate).
+// z times the logistic function p of v(z): silu (v = z) and gelu's usual
+// approximation (v = z (a + b z^2)).
+constexpr float kTanhA = 1.59576912f, kTanhB = 0.0713548163f;   // 2 sqrt(2 / pi), that times 0.044715
+
+// zdv: z v'(z), which the slope p + p (1 - p) z v'(z) takes.
 template <bool SLOPE>
 __device__ __forceinline__ Activated z_logistic(float z, float v, float zdv)
 {
     if (v < (SLOPE ? kLowGateGrad : kLowGate)) {
+        // p is exp(v) to fp32.
         const LowGate l = low_gate(v);
-        // Minus infinity times zero: NaN, as the formula has it.
         return {l.f, z == -__builtin_inff() ? __builtin_nanf("") : z, 1.0f + zdv};
     }
     if constexpr (SLOPE) {
@@ -39,54 +48,131 @@ __device__ __forceinline__ Activated z_logistic(float z, float v, float zdv)
     return {1.0f, logistic_times(v, z), 0.0f};
 }
 
-// z times the normal distribution function Phi(z).  With a = |z| the tail is
+// The normal distribution's tail, with a >= 0:
 //
 //   Phi(-a) = h(a) exp(-a^2 / 2),   h(a) = exp(a^2 / 2) erfc(a / sqrt 2) / 2
 //
-// and h a polynomial in t = 1 / (1 + 0.275 a), fitted by weighted least squares for
-// the smallest relative error over 0 <= a <= 60 (2.5e-6 in fp32, a thousandth of
-// bf16's step).  exp(-a^2 / 2) is f^3.  The slope is Phi(z) + z phi(z), phi the
-// density exp(-a^2 / 2) / sqrt(2 pi).
-template <bool SLOPE>
-__device__ __forceinline__ Activated z_normal(float z)
+// h as a polynomial in t = 1 / (1 + 0.325 a), fitted by weighted least squares for
+// the smallest relative error over 0 <= a <= 60.
+__device__ __forceinline__ float normal_tail(float a)
 {
-    constexpr float kThird = 0x1.ec709ep-3f;   // log2(e) / 6
-    constexpr float kDensity = 0.398942280f;   // 1 / sqrt(2 pi)
-    const float a = __builtin_fabsf(z) > 40.0f ? 40.0f : __builtin_fabsf(z);   // keeps NaN
-    const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.275f, a, 1.0f));
-    float h = -0.0551880188f;
-    h = __builtin_fmaf(h, t, 0.129638717f);
-    h = __builtin_fmaf(h, t, 0.00414652424f);
-    h = __builtin_fmaf(h, t, 0.103499249f);
-    h = __builtin_fmaf(h, t, 0.0982339233f);
-    h = __builtin_fmaf(h, t, 0.109967098f);
-    h = __builtin_fmaf(h, t, 0.109701574f);
-    h *= t;
-    const float f = __builtin_amdgcn_exp2f(-kThird * (a * a));
-    const float bump = __builtin_fmaf(-kDensity, a, h);   // the slope's tail over f^3
-    if (z <= 0.0f)
-        return {f, z == -__builtin_inff() ? __builtin_nanf("") : z * h, bump};
-    const float f3 = f * f * f;
-    return {1.0f, __builtin_fmaf(-z * f3, h, z), __builtin_fmaf(-f3, bump, 1.0f)};
+    const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.325f, a, 1.0f));
+    float h = -0.0636566505f;
+    h = __builtin_fmaf(h, t, 0.122516617f);
+    h = __builtin_fmaf(h, t, 0.0615336969f);
+    h = __builtin_fmaf(h, t, 0.120580301f);
+    h = __builtin_fmaf(h, t, 0.129357710f);
+    h = __builtin_fmaf(h, t, 0.129660428f);
+    return h * t;
 }
 
-// Activation `act` (uniform), with its slope where SLOPE.
-template <bool SLOPE>
-__device__ __forceinline__ Activated activated(int act, float z)
+constexpr float kDensity = 0.398942280f;   // 1 / sqrt(2 pi)
+constexpr float kLog2e = 1.44269504f;
+
+// z Phi(z) for z < 0, with exp(-z^2 / 2) as f^3.  Its slope is Phi(z) + z phi(z), phi
+// the density exp(-z^2 / 2) / sqrt(2 pi).
+__device__ __forceinline__ Activated z_normal_low(float z)
 {
+    const float a = __builtin_fminf(-z, 40.0f), h = normal_tail(a);
+    const float f = __builtin_amdgcn_exp2f((-kLog2e / 6.0f) * (a * a));
+    return {f, z == -__builtin_inff() ? __builtin_nanf("") : z * h, __builtin_fmaf(-kDensity, a, h)};
+}
+
+// Any z, by the careful way.
+template <bool SLOPE>
+__device__ __forceinline__ Activated activated_low(int act, float z)
+{
+    if (act == GEMM_ACT_GELU) {
+        if (z < -5.0f)
+            return z_normal_low(z);
+        const float a = __builtin_fminf(__builtin_fabsf(z), 40.0f), h = normal_tail(a);
+        const float e = __builtin_amdgcn_exp2f((-0.5f * kLog2e) * (z * z));
+        const float tail = e * __builtin_fmaf(-kDensity, a, h);
+        return {1.0f, __builtin_fmaf(-a, h * e, __builtin_fmaxf(z, 0.0f)), z > 0.0f ? 1.0f - tail : tail};
+    }
     if (act == GEMM_ACT_SILU)
         return z_logistic<SLOPE>(z, z, z);
-    if (act == GEMM_ACT_GELU_TANH) {
-        constexpr float kA = 1.59576912f, kB = 0.0713548163f;   // 2 sqrt(2 / pi), that times 0.044715
-        // Past 30 the logistic function is 0 or 1 and z^3 may overflow.
-        const float c = z > 30.0f ? 30.0f : z < -30.0f ? -30.0f : z, c2 = c * c;
-        return z_logistic<SLOPE>(z, c * __builtin_fmaf(kB, c2, kA), c * __builtin_fmaf(3.0f * kB, c2, kA));
+    // Past 30 the logistic function is 0 or 1 and z^3 may overflow.
+    const float c = z > 30.0f ? 30.0f : z < -30.0f ? -30.0f : z, c2 = c * c;
+    return z_logistic<SLOPE>(z, c * __builtin_fmaf(kTanhB, c2, kTanhA), c * __builtin_fmaf(3.0f * kTanhB, c2, kTanhA));
+}
+
+// The z below which the usual way does not go: exp(-v), or exp(-z^2 / 2), within 2^120.
+__device__ __forceinline__ float lowest_usual(int act)
+{
+    return act == GEMM_ACT_SILU ? -80.0f : act == GEMM_ACT_GELU ? -12.5f : -9.5f;
+}
+
+template <bool SLOPE>
+__device__ __forceinline__ void logistic_usual(float z, float minus_v, float zdv, float& value, float& slope)
+{
+    const float e = __builtin_amdgcn_exp2f(minus_v * kLog2e), p = __builtin_amdgcn_rcpf(1.0f + e);
+    value = z * p;
+    if constexpr (SLOPE)
+        slope = __builtin_fmaf(zdv * (e * p), p, p);
+}
+
+// f(i, a) for the activation a of z[i], i = 0 .. 7; `act` is uniform.
+template <bool SLOPE, class F>
+__device__ __forceinline__ void activate(int act, const float (&z)[kChunk], F&& f)
+{
+    struct Usual {
+        float value, slope;
+        __device__ __forceinline__ float times(float x) const { return x * value; }
+        __device__ __forceinline__ float slope_times(float x) const { return x * slope; }
+        __device__ __forceinline__ float slope_times(float x, float y) const { return x * (y * slope); }
+    };
+    Usual u;
+    if (act == GEMM_ACT_NONE) {
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i)
+            f(i, Usual{z[i], 1.0f});
+        return;
     }
-    if (act == GEMM_ACT_GELU)
-        return z_normal<SLOPE>(z);
-    if (act == GEMM_ACT_RELU)   // NaN stays
-        return {1.0f, z < 0.0f ? 0.0f : z, z > 0.0f ? 1.0f : z <= 0.0f ? 0.0f : z};
-    return {1.0f, z, 1.0f};
+    if (act == GEMM_ACT_RELU) {   // NaN stays
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i)
+            f(i, Usual{z[i] < 0.0f ? 0.0f : z[i], z[i] > 0.0f ? 1.0f : z[i] <= 0.0f ? 0.0f : z[i]});
+        return;
+    }
+    float low = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kChunk; ++i)
+        low = __builtin_fminf(low, z[i]);
+    if (__builtin_expect(low < lowest_usual(act), 0)) {
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i)
+            f(i, activated_low<SLOPE>(act, z[i]));
+        return;
+    }
+    if (act == GEMM_ACT_SILU) {
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i) {
+            logistic_usual<SLOPE>(z[i], -z[i], z[i], u.value, u.slope);
+            f(i, u);
+        }
+    } else if (act == GEMM_ACT_GELU_TANH) {
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i) {
+            const float z2 = z[i] * z[i];
+            const float c = __builtin_fminf(z[i], 30.0f);   // the slope is 1 there, and z^3 may overflow
+            logistic_usual<SLOPE>(z[i], z[i] * __builtin_fmaf(-kTanhB, z2, -kTanhA),
+                                  c * __builtin_fmaf(3.0f * kTanhB * c, c, kTanhA), u.value, u.slope);
+            f(i, u);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i) {
+            const float a = __builtin_fminf(__builtin_fabsf(z[i]), 30.0f), h = normal_tail(a);
+            const float e = __builtin_amdgcn_exp2f((-0.5f * kLog2e) * (z[i] * z[i]));
+            u.value = __builtin_fmaf(-a, h * e, __builtin_fmaxf(z[i], 0.0f));
+            if constexpr (SLOPE) {
+                const float tail = e * __builtin_fmaf(-kDensity, a, h);
+                u.slope = z[i] > 0.0f ? 1.0f - tail : tail;
+            }
+            f(i, u);
+        }
+    }
 }
 
 }  // namespace

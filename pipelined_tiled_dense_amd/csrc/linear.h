@@ -71,9 +71,25 @@ __device__ __forceinline__ EpilogueIn epilogue_load(const Epilogue& e, int64_t r
     return in;
 }
 
+// Outputs go out non-temporal, as the product's C does (see Cfg::STORE_C).
+typedef u32x4_t __attribute__((aligned(2))) u32x4_any_t;
+typedef f32x4_t __attribute__((aligned(4))) f32x4_any_t;
+
 __device__ __forceinline__ void store_bf16(void* base, int64_t at, int n, const float (&v)[kChunk])
 {
-    store_chunk<false>((uint16_t*)base + at, n, chunk_bf16(v));
+    uint16_t* p = (uint16_t*)base + at;
+    const u32x4_t x = chunk_bf16(v);
+    if (n >= kChunk)
+        __builtin_nontemporal_store(x, (u32x4_any_t*)p);
+    else
+        store_chunk<false>(p, n, x);
+}
+
+__device__ __forceinline__ void chunk_values(float (&v)[kChunk], u32x4_t x)
+{
+#pragma unroll
+    for (int e = 0; e < kChunk; ++e)
+        v[e] = chunk_at(x, e);
 }
 
 __device__ __forceinline__ void add_chunk(float (&v)[kChunk], u32x4_t x)
@@ -95,9 +111,7 @@ __device__ __forceinline__ void epilogue_finish(const Epilogue& e, const Epilogu
             add_chunk(s, load_chunk<false>(e.bias + c, n, c));
         if (e.out1)
             store_bf16(e.out1, row * e.ld_out1 + c, n, s);
-#pragma unroll
-        for (int i = 0; i < kChunk; ++i)
-            s[i] = activated<false>(e.act, s[i]).times(1.0f);
+        activate<false>(e.act, s, [&](int i, const auto& a) { s[i] = a.times(1.0f); });
         if (e.in0)
             add_chunk(s, in.a);
         store_bf16(e.out0, row * e.ld_out0 + c, n, s);
@@ -106,9 +120,9 @@ __device__ __forceinline__ void epilogue_finish(const Epilogue& e, const Epilogu
         if (e.in1)
             add_chunk(s, in.b);
         if (e.in0) {
-#pragma unroll
-            for (int i = 0; i < kChunk; ++i)
-                s[i] = activated<true>(e.act, chunk_at(in.a, i)).slope_times(s[i]);
+            float z[kChunk];
+            chunk_values(z, in.a);
+            activate<true>(e.act, z, [&](int i, const auto& a) { s[i] = a.slope_times(s[i]); });
         }
         store_bf16(e.out0, row * e.ld_out0 + c, n, s);
     }
@@ -116,7 +130,8 @@ __device__ __forceinline__ void epilogue_finish(const Epilogue& e, const Epilogu
         if (e.fp32) {
             float* p = (float*)e.out0 + row * e.ld_out0 + c;
             if (n >= kChunk) {
-                __builtin_memcpy(p, s, 32);
+                __builtin_nontemporal_store(f32x4_t{s[0], s[1], s[2], s[3]}, (f32x4_any_t*)p);
+                __builtin_nontemporal_store(f32x4_t{s[4], s[5], s[6], s[7]}, (f32x4_any_t*)(p + 4));
             } else {
 #pragma unroll
                 for (int i = 0; i < kChunk - 1; ++i)
@@ -136,21 +151,18 @@ __device__ __forceinline__ void epilogue_finish(const Epilogue& e, const Epilogu
             store_bf16(e.out1, row * e.ld_out1 + c, n, s);
             store_bf16(e.out1, row * e.ld_out1 + e.N + c, n, t);
         }
-#pragma unroll
-        for (int i = 0; i < kChunk; ++i)
-            s[i] = activated<false>(e.act, s[i]).times(t[i]);
+        activate<false>(e.act, s, [&](int i, const auto& a) { s[i] = a.times(t[i]); });
         store_bf16(e.out0, row * e.ld_out0 + c, n, s);
     }
     if constexpr (MODE == FUSE_DGATED) {
-        float dg[kChunk], du[kChunk], y[kChunk];
-#pragma unroll
-        for (int i = 0; i < kChunk; ++i) {
+        float g[kChunk], dg[kChunk], du[kChunk], y[kChunk];
+        chunk_values(g, in.a);
+        activate<true>(e.act, g, [&](int i, const auto& a) {
             const float u = chunk_at(in.b, i);
-            const Activated a = activated<true>(e.act, chunk_at(in.a, i));
             dg[i] = a.slope_times(s[i], u);
             du[i] = a.times(s[i]);
             y[i] = a.times(u);
-        }
+        });
         store_bf16(e.out0, row * e.ld_out0 + c, n, dg);
         store_bf16(e.out0, row * e.ld_out0 + e.N + c, n, du);
         if (e.out1)
@@ -188,87 +200,85 @@ template <int MODE>
 struct LinearParams : Params {
     Epilogue e;
 
-    // The accumulators, 16 rows by 64 columns at a time, through the wave's strip of
-    // LDS into rows, 8 consecutive columns a lane.  A rolled loop, whose passes differ
-    // only in the accumulators that a uniform switch picks, so that the elementwise
-    // part is there once, with every activation in it.
+    // The accumulators, 8 rows by 64 columns of each factor at a time, through the
+    // wave's strip of LDS into rows, 8 consecutive columns a lane.  A rolled loop,
+    // whose rounds differ only in the accumulators that a uniform switch picks, so
+    // that the elementwise part is there once, with every activation in it.
     //
-    // Strip: 16 rows of 256 bytes, the 16-byte chunk XORed with the row.  A write's 16
-    // lanes of one column group hold 16 rows, a read's 16 lanes two rows at chunks of
-    // one parity: either way all chunks differ, and with them all banks.
+    // Strip: 16 rows of 256 bytes, the 16-byte chunk XORed with the row: 16 rows of
+    // one factor, written every other round, or 8 rows of both.  A write's 16 lanes
+    // of one column group hold 16 rows (8 of both), a read's 16 lanes two rows at
+    // chunks of one parity: either way all chunks differ, and with them all banks.
     template <class C>
     __device__ __forceinline__ void store_tile(typename C::Acc (&acc)[C::FM][C::FN], lds_char* strip, int32_t tm,
                                                int32_t tn, int32_t piece, int wm, int wn, int lane_in) const
     {
         constexpr bool PAIR = fuse_paired(MODE);
         static_assert(C::PAIRED == PAIR && C::EPI_WAVE_BYTES == 16 * 64 * 4, "the strip");
-        constexpr int FACTORS = PAIR ? 2 : 1, JB = 4 * FACTORS, PER_I = C::FN / JB, PASSES = C::FM * PER_I;
+        constexpr int FACTORS = PAIR ? 2 : 1, JB = 4 * FACTORS, PER_I = C::FN / JB, ROUNDS = C::FM * PER_I * 2;
         constexpr int BNO = C::BN / FACTORS;   // output columns of a tile
         const int lane = (int)opaque((uint32_t)lane_in);
         const int wrow = lane & 15, wq = lane >> 4, rrow = lane >> 3, c8 = lane & 7;
         const int64_t c0 = (int64_t)tn * BNO + wn * (C::TN / FACTORS) + c8 * 8;
         const int64_t r0 = (int64_t)tm * C::BM + wm * C::TM + rrow;
-        auto row_of = [&](int pass, int step) { return r0 + (pass / PER_I) * 16 + step * 8; };
-        auto col_of = [&](int pass) { return c0 + (pass % PER_I) * 64; };
+        auto row_of = [&](int round) { return r0 + (round / (2 * PER_I)) * 16 + (round & 1) * 8; };
+        auto col_of = [&](int round) { return c0 + (round / 2 % PER_I) * 64; };
         const bool whole = splits == 1;
-        EpilogueIn in[2];
-        auto fetch = [&](int pass) {
-            if (whole) {
-#pragma unroll
-                for (int step = 0; step < 2; ++step)
-                    in[step] = epilogue_load<MODE>(e, row_of(pass, step), col_of(pass), left(e.N, col_of(pass)));
-            }
+        EpilogueIn in{};
+        auto fetch = [&](int round) {
+            if (whole)
+                in = epilogue_load<MODE>(e, row_of(round), col_of(round), left(e.N, col_of(round)));
         };
         fetch(0);
 #pragma clang loop unroll(disable)
-        for (int pass = 0; pass < PASSES; ++pass) {
-            float v[FACTORS][2][kChunk];
-#pragma unroll
-            for (int h = 0; h < FACTORS; ++h) {
+        for (int round = 0; round < ROUNDS; ++round) {
+            // The blocks of `round`, this round's lanes of them.
+            const int half = round & 1;
+            if (PAIR ? (wrow >> 3) == half : half == 0) {
                 [&]<int... P>(std::integer_sequence<int, P...>) {
                     (
                         [&] {
-                            if (pass == P) {
+                            if (round / 2 == P) {
 #pragma unroll
-                                for (int jj = 0; jj < 4; ++jj)
-                                    *(LDS_AS f32x4_t*)(strip + wrow * 256 + (((4 * jj + wq) ^ wrow) << 4)) =
-                                        acc[P / PER_I][(P % PER_I) * JB + jj * FACTORS + h];
+                                for (int h = 0; h < FACTORS; ++h)
+#pragma unroll
+                                    for (int jj = 0; jj < 4; ++jj) {
+                                        const int row = PAIR ? (wrow & 7) + 8 * h : wrow;
+                                        *(LDS_AS f32x4_t*)(strip + row * 256 + (((4 * jj + wq) ^ row) << 4)) =
+                                            acc[P / PER_I][(P % PER_I) * JB + jj * FACTORS + h];
+                                    }
                             }
                         }(),
                         ...);
-                }(std::make_integer_sequence<int, PASSES>{});
-                wait_lgkm0();
-#pragma unroll
-                for (int step = 0; step < 2; ++step) {
-                    const int row = rrow + 8 * step;
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        const f32x4_t x = *(const LDS_AS f32x4_t*)(strip + row * 256 + (((2 * c8 + q) ^ row) << 4));
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            v[h][step][4 * q + i] = x[i];
-                    }
-                }
-                wait_lgkm0();
+                }(std::make_integer_sequence<int, ROUNDS / 2>{});
             }
-            const int64_t c = col_of(pass);
-            if (whole) {
-                const EpilogueIn now[2] = {in[0], in[1]};
-                if (pass + 1 < PASSES)
-                    fetch(pass + 1);
+            wait_lgkm0();
+            float v[FACTORS][kChunk];
 #pragma unroll
-                for (int step = 0; step < 2; ++step)
-                    epilogue_finish<MODE>(e, now[step], row_of(pass, step), c, left(e.N, c), v[0][step],
-                                          v[FACTORS - 1][step]);
+            for (int h = 0; h < FACTORS; ++h) {
+                const int row = rrow + 8 * (PAIR ? h : half);
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const f32x4_t x = *(const LDS_AS f32x4_t*)(strip + row * 256 + (((2 * c8 + q) ^ row) << 4));
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        v[h][4 * q + i] = x[i];
+                }
+            }
+            wait_lgkm0();
+            const int64_t row = row_of(round), c = col_of(round);
+            if (whole) {
+                const EpilogueIn now = in;
+                if (round + 1 < ROUNDS)
+                    fetch(round + 1);
+                epilogue_finish<MODE>(e, now, row, c, left(e.N, c), v[0], v[FACTORS - 1]);
             } else {
                 float* to = partial + (int64_t)piece * (C::BM * BNO * FACTORS);
 #pragma unroll
                 for (int h = 0; h < FACTORS; ++h)
-#pragma unroll
-                    for (int step = 0; step < 2; ++step)
-                        __builtin_memcpy(to + (h * C::BM + (int)(row_of(pass, step) - (int64_t)tm * C::BM)) * BNO +
-                                             (int)(c - (int64_t)tn * BNO),
-                                         v[h][step], 32);
+                    __builtin_memcpy(to + (h * C::BM + (int)(row - (int64_t)tm * C::BM)) * BNO +
+                                         (int)(c - (int64_t)tn * BNO),
+                                     v[h], 32);
             }
         }
     }
@@ -535,13 +545,24 @@ __global__ void __launch_bounds__(256) k_column_sums(const uint16_t* x, int64_t 
 
 __global__ void __launch_bounds__(256) k_column_sums_join(const float* part, int64_t cols, int32_t runs, float* to)
 {
-    const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (c >= cols)
-        return;
+    __shared__ float sums[16][16];
+    const int cl = threadIdx.x & 15, rl = threadIdx.x >> 4;
+    const int64_t c = (int64_t)blockIdx.x * 16 + cl;
     float t = 0.0f;
-    for (int32_t r = 0; r < runs; ++r)
-        t += part[r * cols + c];
-    to[c] = t;
+    if (c < cols) {
+#pragma unroll 4
+        for (int32_t r = rl; r < runs; r += 16)
+            t += part[r * cols + c];
+    }
+    sums[rl][cl] = t;
+    __syncthreads();
+    if (rl == 0 && c < cols) {
+        t = 0.0f;
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+            t += sums[r][cl];
+        to[c] = t;
+    }
 }
 
 // Zero-padded copies of the operands whose rows do not start on 16-byte boundaries
@@ -838,7 +859,7 @@ int column_sums(const void* X, int64_t rows, int64_t cols, int64_t ld, float* to
                        cols, ld, run, runs > 1 ? (float*)ws : to);
     rc = launched();
     if (rc == GEMM_OK && runs > 1) {
-        hipLaunchKernelGGL(k_column_sums_join, dim3((unsigned)groups), dim3(256), 0, s, (const float*)ws, cols,
+        hipLaunchKernelGGL(k_column_sums_join, dim3((unsigned)ceil_div(cols, 16)), dim3(256), 0, s, (const float*)ws, cols,
                            (int32_t)runs, to);
         rc = launched();
     }

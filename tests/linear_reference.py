@@ -9,8 +9,8 @@ what its own evaluation in fp32 may add:
   logistic   z p(v) with an exponential whose argument is right to 8 U32 |v| and 16
              roundings beside it: the share (16 + 8 |v| (1 - p)) U32, since where p
              is near 1 the exponential hardly enters;
-  normal     the tail h exp(-a^2 / 2) from a polynomial right to 2.5e-6 = 42 U32, an
-             argument right to 2 U32 a^2 and a few roundings: (64 + 2 a^2) U32 of
+  normal     the tail h exp(-a^2 / 2) from a polynomial right to 1.6e-5 = 269 U32, an
+             argument right to 2 U32 a^2 and a few roundings: (300 + 2 a^2) U32 of
              the tail, beside roundings of the whole."""
 import math
 
@@ -33,7 +33,7 @@ def activation(z, act):
         a = z.abs()
         phi = torch.exp(-z * z / 2) / math.sqrt(2 * math.pi)
         tail, cdf = 0.5 * torch.erfc(a / math.sqrt(2)), 0.5 * torch.erfc(-z / math.sqrt(2))
-        share = (64 + 2 * a * a) * U32
+        share = (300 + 2 * a * a) * U32
         value, slope = z * cdf, cdf + z * phi
         return value, slope, a * tail * share + 4 * U32 * value.abs(), (tail + a * phi) * share + 4 * U32 * slope.abs()
     if act == "gelu_tanh":
