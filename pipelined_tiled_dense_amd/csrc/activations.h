@@ -155,7 +155,7 @@ __device__ __forceinline__ void activate(int act, const float (&z)[kChunk], F&& 
 #pragma unroll
         for (int i = 0; i < kChunk; ++i) {
             const float z2 = z[i] * z[i];
-            const float c = __builtin_fminf(z[i], 30.0f);   // the slope is 1 there, and z^3 may overflow
+            const float c = __builtin_amdgcn_fmed3f(z[i], -10.0f, 30.0f);   // the slope is 1 there, and z^3 may overflow
             logistic_usual<SLOPE>(z[i], z[i] * __builtin_fmaf(-kTanhB, z2, -kTanhA),
                                   c * __builtin_fmaf(3.0f * kTanhB * c, c, kTanhA), u.value, u.slope);
             f(i, u);
@@ -163,9 +163,10 @@ __device__ __forceinline__ void activate(int act, const float (&z)[kChunk], F&& 
     } else {
 #pragma unroll
         for (int i = 0; i < kChunk; ++i) {
-            const float a = __builtin_fminf(__builtin_fabsf(z[i]), 30.0f), h = normal_tail(a);
+            // The bounds keep infinity out of a product with zero; NaN comes through e.
+            const float a = __builtin_amdgcn_fmed3f(__builtin_fabsf(z[i]), 0.0f, 30.0f), h = normal_tail(a);
             const float e = __builtin_amdgcn_exp2f((-0.5f * kLog2e) * (z[i] * z[i]));
-            u.value = __builtin_fmaf(-a, h * e, __builtin_fmaxf(z[i], 0.0f));
+            u.value = __builtin_fmaf(-a, h * e, __builtin_amdgcn_fmed3f(z[i], 0.0f, __builtin_inff()));
             if constexpr (SLOPE) {
                 const float tail = e * __builtin_fmaf(-kDensity, a, h);
                 u.slope = z[i] > 0.0f ? 1.0f - tail : tail;

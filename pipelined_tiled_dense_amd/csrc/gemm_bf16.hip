@@ -1831,9 +1831,10 @@ __global__ void __launch_bounds__(C::THREADS, 2) k_gemm(P p)
         }
         if constexpr (C::SYNC == SYNC_FLAGS)
             poison_tile<C>(acc, st);
-        if constexpr (!std::is_same_v<P, Params>)
+        if constexpr (!std::is_same_v<P, Params>) {
             p.template store_tile<C>(acc, strip, tm, tn, sp * p.span + u, wm, wn, lane);
-        else if (p.splits > 1)
+            read_frags<C>(fr[0], stage_at(s_cur), wm, wn, lane, 0);   // again: see k_gemm_win
+        } else if (p.splits > 1)
             store_partial<C>(p, acc, sp * p.span + u, wm, wn, lane);
         else
             store_tile<C>(p, acc, strip, tm * C::BM, tn * C::BN, wm, wn, lane);
@@ -1970,6 +1971,12 @@ __global__ void __launch_bounds__(C::THREADS) k_gemm_win(P p)
             p.template store_tile<C>(acc, win(step5(wa, 4)) + w * C::EPI_WAVE_BYTES, tm, tn, sp * p.span + u, wm, wn, lane);
             wait_lgkm0();
             block_barrier();
+            // The next tile's first fragments again: held through a longer epilogue, their
+            // registers would push it into spills.
+            const FragReader<C> rd(wm, wn, lane, 0);
+#pragma unroll
+            for (int d = 0; d < frag_reads<C>(); ++d)
+                rd.read(fr[0], win(wa), win(step5(wa, 1)), wn, d);
         } else if (p.splits > 1) {
             store_partial<C>(p, acc, sp * p.span + u, wm, wn, lane);
         } else {

@@ -48,23 +48,37 @@ struct EpilogueIn {
     u32x4_t a, b;
 };
 
-// What element (row, c) .. (row, c + 7) reads, the n (<= 8) columns that exist.
+// A chunk of 8 columns from c on, the n (<= 8) of them that exist, of row first +
+// lane_row: `first` is uniform, so that a loop over rows keeps what a lane adds to a
+// matrix's address and moves the uniform part.
+struct EpilogueAt {
+    int64_t first, c;
+    int32_t lane_row, n;
+
+    __device__ __forceinline__ bool in(int64_t M) const { return lane_row < M - first; }
+    template <class T>
+    __device__ __forceinline__ T* of(T* base, int64_t ld) const
+    {
+        return base + first * ld + (lane_row * ld + c);
+    }
+};
+
 template <int MODE>
-__device__ __forceinline__ EpilogueIn epilogue_load(const Epilogue& e, int64_t row, int64_t c, int n)
+__device__ __forceinline__ EpilogueIn epilogue_load(const Epilogue& e, const EpilogueAt& at)
 {
     EpilogueIn in{};
-    if (row >= e.M)
-        n = 0;
+    const int n = at.in(e.M) ? at.n : 0;
+    const int64_t c = at.c;
     if constexpr (MODE == FUSE_LINEAR || MODE == FUSE_DX) {
         if (e.in0)
-            in.a = load_chunk<false>(e.in0 + row * e.ld_in0 + c, n, c);
+            in.a = load_chunk<false>(at.of(e.in0, e.ld_in0), n, c);
     }
     if constexpr (MODE == FUSE_DX) {
         if (e.in1)
-            in.b = load_chunk<false>(e.in1 + row * e.ld_in1 + c, n, c);
+            in.b = load_chunk<false>(at.of(e.in1, e.ld_in1), n, c);
     }
     if constexpr (MODE == FUSE_DGATED) {
-        const uint16_t* gu = e.in0 + row * e.ld_in0 + c;
+        const uint16_t* gu = at.of(e.in0, e.ld_in0);
         in.a = load_chunk<false>(gu, n, c);
         in.b = load_chunk<false>(gu + e.N, n, c);
     }
@@ -75,9 +89,8 @@ __device__ __forceinline__ EpilogueIn epilogue_load(const Epilogue& e, int64_t r
 typedef u32x4_t __attribute__((aligned(2))) u32x4_any_t;
 typedef f32x4_t __attribute__((aligned(4))) f32x4_any_t;
 
-__device__ __forceinline__ void store_bf16(void* base, int64_t at, int n, const float (&v)[kChunk])
+__device__ __forceinline__ void store_bf16(uint16_t* p, int n, const float (&v)[kChunk])
 {
-    uint16_t* p = (uint16_t*)base + at;
     const u32x4_t x = chunk_bf16(v);
     if (n >= kChunk)
         __builtin_nontemporal_store(x, (u32x4_any_t*)p);
@@ -101,20 +114,23 @@ __device__ __forceinline__ void add_chunk(float (&v)[kChunk], u32x4_t x)
 
 // s: the sums (GATED: of the gate, and t those of the other factor).
 template <int MODE>
-__device__ __forceinline__ void epilogue_finish(const Epilogue& e, const EpilogueIn& in, int64_t row, int64_t c, int n,
+__device__ __forceinline__ void epilogue_finish(const Epilogue& e, const EpilogueIn& in, const EpilogueAt& at,
                                                 float (&s)[kChunk], float (&t)[kChunk])
 {
-    if (row >= e.M || n <= 0)
+    const int n = at.n;
+    const int64_t c = at.c;
+    if (!at.in(e.M) || n <= 0)
         return;
+    uint16_t* out = at.of((uint16_t*)e.out0, e.ld_out0);   // not DW's, which may be fp32
     if constexpr (MODE == FUSE_LINEAR) {
         if (e.bias)
             add_chunk(s, load_chunk<false>(e.bias + c, n, c));
         if (e.out1)
-            store_bf16(e.out1, row * e.ld_out1 + c, n, s);
+            store_bf16(at.of(e.out1, e.ld_out1), n, s);
         activate<false>(e.act, s, [&](int i, const auto& a) { s[i] = a.times(1.0f); });
         if (e.in0)
             add_chunk(s, in.a);
-        store_bf16(e.out0, row * e.ld_out0 + c, n, s);
+        store_bf16(out, n, s);
     }
     if constexpr (MODE == FUSE_DX) {
         if (e.in1)
@@ -124,11 +140,11 @@ __device__ __forceinline__ void epilogue_finish(const Epilogue& e, const Epilogu
             chunk_values(z, in.a);
             activate<true>(e.act, z, [&](int i, const auto& a) { s[i] = a.slope_times(s[i]); });
         }
-        store_bf16(e.out0, row * e.ld_out0 + c, n, s);
+        store_bf16(out, n, s);
     }
     if constexpr (MODE == FUSE_DW) {
         if (e.fp32) {
-            float* p = (float*)e.out0 + row * e.ld_out0 + c;
+            float* p = at.of((float*)e.out0, e.ld_out0);
             if (n >= kChunk) {
                 __builtin_nontemporal_store(f32x4_t{s[0], s[1], s[2], s[3]}, (f32x4_any_t*)p);
                 __builtin_nontemporal_store(f32x4_t{s[4], s[5], s[6], s[7]}, (f32x4_any_t*)(p + 4));
@@ -139,7 +155,7 @@ __device__ __forceinline__ void epilogue_finish(const Epilogue& e, const Epilogu
                         p[i] = s[i];
             }
         } else {
-            store_bf16(e.out0, row * e.ld_out0 + c, n, s);
+            store_bf16(out, n, s);
         }
     }
     if constexpr (MODE == FUSE_GATED) {
@@ -148,11 +164,11 @@ __device__ __forceinline__ void epilogue_finish(const Epilogue& e, const Epilogu
             add_chunk(t, load_chunk<false>(e.bias + e.N + c, n, c));
         }
         if (e.out1) {
-            store_bf16(e.out1, row * e.ld_out1 + c, n, s);
-            store_bf16(e.out1, row * e.ld_out1 + e.N + c, n, t);
+            store_bf16(at.of(e.out1, e.ld_out1), n, s);
+            store_bf16(at.of(e.out1, e.ld_out1) + e.N, n, t);
         }
         activate<false>(e.act, s, [&](int i, const auto& a) { s[i] = a.times(t[i]); });
-        store_bf16(e.out0, row * e.ld_out0 + c, n, s);
+        store_bf16(out, n, s);
     }
     if constexpr (MODE == FUSE_DGATED) {
         float g[kChunk], dg[kChunk], du[kChunk], y[kChunk];
@@ -163,10 +179,10 @@ __device__ __forceinline__ void epilogue_finish(const Epilogue& e, const Epilogu
             du[i] = a.times(s[i]);
             y[i] = a.times(u);
         });
-        store_bf16(e.out0, row * e.ld_out0 + c, n, dg);
-        store_bf16(e.out0, row * e.ld_out0 + e.N + c, n, du);
+        store_bf16(out, n, dg);
+        store_bf16(out + e.N, n, du);
         if (e.out1)
-            store_bf16(e.out1, row * e.ld_out1 + c, n, y);
+            store_bf16(at.of(e.out1, e.ld_out1), n, y);
     }
 }
 
@@ -219,40 +235,45 @@ struct LinearParams : Params {
         constexpr int BNO = C::BN / FACTORS;   // output columns of a tile
         const int lane = (int)opaque((uint32_t)lane_in);
         const int wrow = lane & 15, wq = lane >> 4, rrow = lane >> 3, c8 = lane & 7;
-        const int64_t c0 = (int64_t)tn * BNO + wn * (C::TN / FACTORS) + c8 * 8;
-        const int64_t r0 = (int64_t)tm * C::BM + wm * C::TM + rrow;
-        auto row_of = [&](int round) { return r0 + (round / (2 * PER_I)) * 16 + (round & 1) * 8; };
-        auto col_of = [&](int round) { return c0 + (round / 2 % PER_I) * 64; };
+        static_assert(PER_I == 1 && ROUNDS <= 16, "64 columns of a factor per wave");
+        const int64_t c = (int64_t)tn * BNO + wn * (C::TN / FACTORS) + c8 * 8;
+        const int32_t r0 = wm * C::TM;
+        EpilogueAt at{(int64_t)tm * C::BM + r0, c, rrow, left(e.N, c)};
         const bool whole = splits == 1;
         EpilogueIn in{};
-        auto fetch = [&](int round) {
-            if (whole)
-                in = epilogue_load<MODE>(e, row_of(round), col_of(round), left(e.N, col_of(round)));
-        };
-        fetch(0);
+        if (whole)
+            in = epilogue_load<MODE>(e, at);
+        float* part = partial + (int64_t)piece * (C::BM * BNO * FACTORS) + (r0 + rrow) * BNO + (int)(c - (int64_t)tn * BNO);
 #pragma clang loop unroll(disable)
         for (int round = 0; round < ROUNDS; ++round) {
-            // The blocks of `round`, this round's lanes of them.
+            // This round's lanes of its blocks.  A wave's LDS operations complete in
+            // order, so neither its writes nor its reads are waited for before the others.
             const int half = round & 1;
             if (PAIR ? (wrow >> 3) == half : half == 0) {
-                [&]<int... P>(std::integer_sequence<int, P...>) {
-                    (
-                        [&] {
-                            if (round / 2 == P) {
+                auto write = [&]<int P>() {
+                    if constexpr (P < ROUNDS / 2) {
 #pragma unroll
-                                for (int h = 0; h < FACTORS; ++h)
+                        for (int h = 0; h < FACTORS; ++h)
 #pragma unroll
-                                    for (int jj = 0; jj < 4; ++jj) {
-                                        const int row = PAIR ? (wrow & 7) + 8 * h : wrow;
-                                        *(LDS_AS f32x4_t*)(strip + row * 256 + (((4 * jj + wq) ^ row) << 4)) =
-                                            acc[P / PER_I][(P % PER_I) * JB + jj * FACTORS + h];
-                                    }
+                            for (int jj = 0; jj < 4; ++jj) {
+                                const int row = PAIR ? (wrow & 7) + 8 * h : wrow;
+                                *(LDS_AS f32x4_t*)(strip + row * 256 + (((4 * jj + wq) ^ row) << 4)) =
+                                    acc[P][jj * FACTORS + h];
                             }
-                        }(),
-                        ...);
-                }(std::make_integer_sequence<int, ROUNDS / 2>{});
+                    }
+                };
+                switch (round >> 1) {
+                case 0: write.template operator()<0>(); break;
+                case 1: write.template operator()<1>(); break;
+                case 2: write.template operator()<2>(); break;
+                case 3: write.template operator()<3>(); break;
+                case 4: write.template operator()<4>(); break;
+                case 5: write.template operator()<5>(); break;
+                case 6: write.template operator()<6>(); break;
+                default: write.template operator()<7>(); break;
+                }
             }
-            wait_lgkm0();
+            COMPILER_FENCE();
             float v[FACTORS][kChunk];
 #pragma unroll
             for (int h = 0; h < FACTORS; ++h) {
@@ -265,20 +286,19 @@ struct LinearParams : Params {
                         v[h][4 * q + i] = x[i];
                 }
             }
-            wait_lgkm0();
-            const int64_t row = row_of(round), c = col_of(round);
+            COMPILER_FENCE();
             if (whole) {
                 const EpilogueIn now = in;
+                const EpilogueAt here = at;
+                at.first += 8;
                 if (round + 1 < ROUNDS)
-                    fetch(round + 1);
-                epilogue_finish<MODE>(e, now, row, c, left(e.N, c), v[0], v[FACTORS - 1]);
+                    in = epilogue_load<MODE>(e, at);
+                epilogue_finish<MODE>(e, now, here, v[0], v[FACTORS - 1]);
             } else {
-                float* to = partial + (int64_t)piece * (C::BM * BNO * FACTORS);
 #pragma unroll
                 for (int h = 0; h < FACTORS; ++h)
-                    __builtin_memcpy(to + (h * C::BM + (int)(row - (int64_t)tm * C::BM)) * BNO +
-                                         (int)(c - (int64_t)tn * BNO),
-                                     v[h], 32);
+                    __builtin_memcpy(part + h * (C::BM * BNO), v[h], 32);
+                part += 8 * BNO;
             }
         }
     }
@@ -297,11 +317,11 @@ __global__ void __launch_bounds__(256) k_linear_finish(LinearParams<MODE> p, int
         const int32_t cc = (at - r * per_row) * kChunk;
         int32_t tm, tn;
         raster_tile(p, p.tile_base + u, tm, tn);
-        const int64_t row = (int64_t)tm * bm + r, c = (int64_t)tn * bn + cc;
-        const int n = left(p.e.N, c);
-        if (row >= p.e.M || n <= 0)
+        const int64_t c = (int64_t)tn * bn + cc;
+        const EpilogueAt here{(int64_t)tm * bm, c, r, left(p.e.N, c)};
+        if (!here.in(p.e.M) || here.n <= 0)
             continue;
-        const EpilogueIn in = epilogue_load<MODE>(p.e, row, c, n);
+        const EpilogueIn in = epilogue_load<MODE>(p.e, here);
         float v[2][kChunk] = {};
         for (int32_t sp = 0; sp < p.splits; ++sp) {
             const float* src = p.partial + (sp * (int64_t)p.span + u) * piece + (int64_t)r * bn + cc;
@@ -314,7 +334,7 @@ __global__ void __launch_bounds__(256) k_linear_finish(LinearParams<MODE> p, int
                     v[h][i] += x[i];
             }
         }
-        epilogue_finish<MODE>(p.e, in, row, c, n, v[0], v[1]);
+        epilogue_finish<MODE>(p.e, in, here, v[0], v[1]);
     }
 }
 
@@ -501,7 +521,6 @@ __global__ void __launch_bounds__(kSkinnyWaves * 64) k_linear_few(LinearParams<M
         if (g & 1)
             continue;
         const int r = i * 16 + r16, cc = j * 16 + g * 4;
-        const int64_t row = m0 + r, c = n0 + cc;
         if (p.splits > 1) {
             const int64_t piece = (int64_t)blockIdx.y * p.span + (tn * p.tiles_m + tm);
             float* to = p.partial + piece * (MF * 16 * NF * 16 * FACTORS) + r * (NF * 16) + cc;
@@ -509,8 +528,8 @@ __global__ void __launch_bounds__(kSkinnyWaves * 64) k_linear_few(LinearParams<M
             for (int h = 0; h < FACTORS; ++h)
                 __builtin_memcpy(to + h * (MF * 16 * NF * 16), v[h], 32);
         } else {
-            const int n = left(p.e.N, c);
-            epilogue_finish<MODE>(p.e, epilogue_load<MODE>(p.e, row, c, n), row, c, n, v[0], v[1]);
+            const EpilogueAt here{m0, n0 + cc, r, left(p.e.N, n0 + cc)};
+            epilogue_finish<MODE>(p.e, epilogue_load<MODE>(p.e, here), here, v[0], v[1]);
         }
     }
 }
