@@ -205,9 +205,9 @@ struct LinearCfg<BT_, AT_, PAIRED_, true>
 
 template <bool BT_, bool AT_, bool PAIRED_>
 struct LinearCfg<BT_, AT_, PAIRED_, false>
-    : Cfg<128, 128, 64, 2, PAIRED_ ? 4 : 2, PAIRED_ ? 1 : 2, SYNC_BARRIER, BT_, 0, false, 16> {
+    : Cfg<128, 128, 64, 4, 4, PAIRED_ ? 1 : 2, SYNC_BARRIER, BT_, 0, false, 16> {
     static constexpr bool AT = AT_, PAIRED = PAIRED_, ANY_SIZE = true;
-    static constexpr int PER_CU = 2;
+    static constexpr int PER_CU = 1;
 };
 
 // Sums of the k chunks: chunk sp's of the launch's u-th tile are piece sp * span +
@@ -243,7 +243,13 @@ struct LinearParams : Params {
         EpilogueIn in{};
         if (whole)
             in = epilogue_load<MODE>(e, at);
-        float* part = partial + (int64_t)piece * (C::BM * BNO * FACTORS) + (r0 + rrow) * BNO + (int)(c - (int64_t)tn * BNO);
+        // fp32 sums go out as they are, 4 columns a lane, whole 128-byte lines a store:
+        // columns 4 c8 .. and, 32 further, the others, in this order in even rows (whose
+        // reads then meet the odd rows' on no bank).
+        const bool plain = !whole || (MODE == FUSE_DW && e.fp32);
+        const int64_t ld = whole ? e.ld_out0 : BNO, cq = whole ? c - 4 * c8 : c - 4 * c8 - (int64_t)tn * BNO;
+        float* out = whole ? (float*)e.out0 + at.first * ld
+                           : partial + (int64_t)piece * (C::BM * BNO * FACTORS) + (int64_t)r0 * ld;
 #pragma clang loop unroll(disable)
         for (int round = 0; round < ROUNDS; ++round) {
             // This round's lanes of its blocks.  A wave's LDS operations complete in
@@ -260,6 +266,8 @@ struct LinearParams : Params {
                                 *(LDS_AS f32x4_t*)(strip + row * 256 + (((4 * jj + wq) ^ row) << 4)) =
                                     acc[P][jj * FACTORS + h];
                             }
+                        // Tells the cases apart: merged, they would index the accumulators.
+                        asm volatile("; rows %0" ::"n"(P));
                     }
                 };
                 switch (round >> 1) {
@@ -274,6 +282,35 @@ struct LinearParams : Params {
                 }
             }
             COMPILER_FENCE();
+            if (plain) {
+                const bool in_rows = !whole || at.in(e.M);
+#pragma unroll
+                for (int h = 0; h < FACTORS; ++h) {
+                    const int row = rrow + 8 * (PAIR ? h : half);
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const int second = q ^ (rrow & 1);
+                        const f32x4_t x = *(const LDS_AS f32x4_t*)(strip + row * 256 + (((c8 + 8 * second) ^ row) << 4));
+                        const int64_t col = cq + 32 * second, n = whole ? e.N - col : 4;
+                        float* to = out + h * (C::BM * BNO) + (rrow * ld + col);
+                        if (!in_rows)
+                            continue;
+                        if (!whole)
+                            *(f32x4_t*)to = x;
+                        else if (n >= 4)
+                            __builtin_nontemporal_store(x, (f32x4_any_t*)to);
+                        else
+#pragma unroll
+                            for (int i = 0; i < 3; ++i)
+                                if (i < n)
+                                    to[i] = x[i];
+                    }
+                }
+                COMPILER_FENCE();
+                at.first += 8;
+                out += 8 * ld;
+                continue;
+            }
             float v[FACTORS][kChunk];
 #pragma unroll
             for (int h = 0; h < FACTORS; ++h) {
@@ -287,19 +324,12 @@ struct LinearParams : Params {
                 }
             }
             COMPILER_FENCE();
-            if (whole) {
-                const EpilogueIn now = in;
-                const EpilogueAt here = at;
-                at.first += 8;
-                if (round + 1 < ROUNDS)
-                    in = epilogue_load<MODE>(e, at);
-                epilogue_finish<MODE>(e, now, here, v[0], v[FACTORS - 1]);
-            } else {
-#pragma unroll
-                for (int h = 0; h < FACTORS; ++h)
-                    __builtin_memcpy(part + h * (C::BM * BNO), v[h], 32);
-                part += 8 * BNO;
-            }
+            const EpilogueIn now = in;
+            const EpilogueAt here = at;
+            at.first += 8;
+            if (round + 1 < ROUNDS)
+                in = epilogue_load<MODE>(e, at);
+            epilogue_finish<MODE>(e, now, here, v[0], v[FACTORS - 1]);
         }
     }
 };
@@ -661,7 +691,7 @@ LinearPlan linear_plan(const LinearShape& q, int cus)
         pl.bm = edge;
         pl.bn = edge / q.factors;
         pl.tiles = ceil_div(q.M, pl.bm) * ceil_div(q.N, pl.bn);
-        const int64_t slots = (int64_t)cus * (edge == 256 ? 1 : 2);
+        const int64_t slots = cus;
         pl.splits = linear_splits(pl.tiles, q.K, slots, 512, pl.chunk);
         pl.grid = pl.tiles * pl.splits < slots ? pl.tiles * pl.splits : slots;
     }
