@@ -28,32 +28,19 @@ struct Activated {
     }
 };
 
-// z times the logistic function p of v(z): silu (v = z) and gelu's usual
-// approximation (v = z (a + b z^2)).
+// Gelu's usual approximation is z p(v) with p the logistic function and v = z (a +
+// b z^2); silu is z p(z).
 constexpr float kTanhA = 1.59576912f, kTanhB = 0.0713548163f;   // 2 sqrt(2 / pi), that times 0.044715
-
-// zdv: z v'(z), which the slope p + p (1 - p) z v'(z) takes.
-template <bool SLOPE>
-__device__ __forceinline__ Activated z_logistic(float z, float v, float zdv)
-{
-    if (v < (SLOPE ? kLowGateGrad : kLowGate)) {
-        // p is exp(v) to fp32.
-        const LowGate l = low_gate(v);
-        return {l.f, z == -__builtin_inff() ? __builtin_nanf("") : z, 1.0f + zdv};
-    }
-    if constexpr (SLOPE) {
-        const Sigmoid s = sigmoid(v);
-        return {1.0f, z * s.s, s.s * __builtin_fmaf(zdv, s.c, 1.0f)};
-    }
-    return {1.0f, logistic_times(v, z), 0.0f};
-}
+constexpr float kDensity = 0.398942280f;                        // 1 / sqrt(2 pi)
+constexpr float kLog2e = 1.44269504f;
 
 // The normal distribution's tail, with a >= 0:
 //
 //   Phi(-a) = h(a) exp(-a^2 / 2),   h(a) = exp(a^2 / 2) erfc(a / sqrt 2) / 2
 //
 // h as a polynomial in t = 1 / (1 + 0.325 a), fitted by weighted least squares for
-// the smallest relative error over 0 <= a <= 60.
+// the smallest relative error over 0 <= a <= 60.  The slope of z Phi(z) is Phi(z) + z
+// phi(z), phi the density exp(-z^2 / 2) / sqrt(2 pi).
 __device__ __forceinline__ float normal_tail(float a)
 {
     const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.325f, a, 1.0f));
@@ -66,41 +53,26 @@ __device__ __forceinline__ float normal_tail(float a)
     return h * t;
 }
 
-constexpr float kDensity = 0.398942280f;   // 1 / sqrt(2 pi)
-constexpr float kLog2e = 1.44269504f;
-
-// z Phi(z) for z < 0, with exp(-z^2 / 2) as f^3.  Its slope is Phi(z) + z phi(z), phi
-// the density exp(-z^2 / 2) / sqrt(2 pi).
-__device__ __forceinline__ Activated z_normal_low(float z)
-{
-    const float a = __builtin_fminf(-z, 40.0f), h = normal_tail(a);
-    const float f = __builtin_amdgcn_exp2f((-kLog2e / 6.0f) * (a * a));
-    return {f, z == -__builtin_inff() ? __builtin_nanf("") : z * h, __builtin_fmaf(-kDensity, a, h)};
-}
-
-// Any z, by the careful way.
-template <bool SLOPE>
-__device__ __forceinline__ Activated activated_low(int act, float z)
-{
-    if (act == GEMM_ACT_GELU) {
-        if (z < -5.0f)
-            return z_normal_low(z);
-        const float a = __builtin_fminf(__builtin_fabsf(z), 40.0f), h = normal_tail(a);
-        const float e = __builtin_amdgcn_exp2f((-0.5f * kLog2e) * (z * z));
-        const float tail = e * __builtin_fmaf(-kDensity, a, h);
-        return {1.0f, __builtin_fmaf(-a, h * e, __builtin_fmaxf(z, 0.0f)), z > 0.0f ? 1.0f - tail : tail};
-    }
-    if (act == GEMM_ACT_SILU)
-        return z_logistic<SLOPE>(z, z, z);
-    // Past 30 the logistic function is 0 or 1 and z^3 may overflow.
-    const float c = z > 30.0f ? 30.0f : z < -30.0f ? -30.0f : z, c2 = c * c;
-    return z_logistic<SLOPE>(z, c * __builtin_fmaf(kTanhB, c2, kTanhA), c * __builtin_fmaf(3.0f * kTanhB, c2, kTanhA));
-}
-
-// The z below which the usual way does not go: exp(-v), or exp(-z^2 / 2), within 2^120.
+// The z below which the usual way loses what exp(v), or exp(-z^2 / 2), holds.
 __device__ __forceinline__ float lowest_usual(int act)
 {
     return act == GEMM_ACT_SILU ? -80.0f : act == GEMM_ACT_GELU ? -12.5f : -9.5f;
+}
+
+// Those z.  There the logistic function is exp(v) to fp32.
+__device__ __forceinline__ Activated activated_low(int act, float z)
+{
+    // Minus infinity times zero: NaN, as the formulas have it.
+    const float zn = z == -__builtin_inff() ? __builtin_nanf("") : z;
+    if (act == GEMM_ACT_GELU) {
+        const float a = __builtin_fminf(-z, 40.0f), h = normal_tail(a);
+        return {__builtin_amdgcn_exp2f((-kLog2e / 6.0f) * (a * a)), zn * h, __builtin_fmaf(-kDensity, a, h)};
+    }
+    const bool silu = act == GEMM_ACT_SILU;
+    const float c = silu ? z : z < -30.0f ? -30.0f : z, c2 = c * c;   // exp(v) is 0 at -30, and z^3 may overflow
+    const float v = silu ? z : c * __builtin_fmaf(kTanhB, c2, kTanhA);
+    const float zdv = silu ? zn : c * __builtin_fmaf(3.0f * kTanhB, c2, kTanhA);
+    return {low_gate(v).f, zn, 1.0f + zdv};
 }
 
 template <bool SLOPE>
@@ -112,7 +84,8 @@ __device__ __forceinline__ void logistic_usual(float z, float minus_v, float zdv
         slope = __builtin_fmaf(zdv * (e * p), p, p);
 }
 
-// f(i, a) for the activation a of z[i], i = 0 .. 7; `act` is uniform.
+// f(i, a) for the activation a of z[i], i = 0 .. 7, and again with another a for the z
+// that take the other way; `act` is uniform.
 template <bool SLOPE, class F>
 __device__ __forceinline__ void activate(int act, const float (&z)[kChunk], F&& f)
 {
@@ -123,26 +96,11 @@ __device__ __forceinline__ void activate(int act, const float (&z)[kChunk], F&& 
         __device__ __forceinline__ float slope_times(float x, float y) const { return x * (y * slope); }
     };
     Usual u;
-    if (act == GEMM_ACT_NONE) {
+    if (act <= GEMM_ACT_RELU) {   // NaN stays
+        const bool relu = act == GEMM_ACT_RELU;
 #pragma unroll
         for (int i = 0; i < kChunk; ++i)
-            f(i, Usual{z[i], 1.0f});
-        return;
-    }
-    if (act == GEMM_ACT_RELU) {   // NaN stays
-#pragma unroll
-        for (int i = 0; i < kChunk; ++i)
-            f(i, Usual{z[i] < 0.0f ? 0.0f : z[i], z[i] > 0.0f ? 1.0f : z[i] <= 0.0f ? 0.0f : z[i]});
-        return;
-    }
-    float low = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kChunk; ++i)
-        low = __builtin_fminf(low, z[i]);
-    if (__builtin_expect(low < lowest_usual(act), 0)) {
-#pragma unroll
-        for (int i = 0; i < kChunk; ++i)
-            f(i, activated_low<SLOPE>(act, z[i]));
+            f(i, Usual{relu && z[i] < 0.0f ? 0.0f : z[i], relu && !(z[i] > 0.0f) ? (z[i] <= 0.0f ? 0.0f : z[i]) : 1.0f});
         return;
     }
     if (act == GEMM_ACT_SILU) {
@@ -173,6 +131,17 @@ __device__ __forceinline__ void activate(int act, const float (&z)[kChunk], F&& 
             }
             f(i, u);
         }
+    }
+    float low = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kChunk; ++i)
+        low = __builtin_fminf(low, z[i]);
+    const float bound = lowest_usual(act);
+    if (__builtin_expect(low < bound, 0)) {
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i)
+            if (z[i] < bound)
+                f(i, activated_low(act, z[i]));
     }
 }
 

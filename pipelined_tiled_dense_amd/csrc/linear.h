@@ -50,7 +50,9 @@ struct EpilogueIn {
 
 // A chunk of 8 columns from c on, the n (<= 8) of them that exist, of row first +
 // lane_row: `first` is uniform, so that a loop over rows keeps what a lane adds to a
-// matrix's address and moves the uniform part.
+// matrix's address and moves the uniform part.  INSIDE: all 8 and the row exist;
+// without a branch around them, loads and stores of a loop's rounds overlap (a branch
+// that may skip a store makes the next wait for a load wait for every store).
 struct EpilogueAt {
     int64_t first, c;
     int32_t lane_row, n;
@@ -63,36 +65,63 @@ struct EpilogueAt {
     }
 };
 
-template <int MODE>
+template <bool INSIDE>
+__device__ __forceinline__ u32x4_t load_values(const uint16_t* p, int n, int64_t c)
+{
+    if constexpr (INSIDE) {
+        u32x4_t v;
+        __builtin_memcpy(&v, p, 16);
+        return v;
+    } else {
+        return load_chunk<false>(p, n, c);
+    }
+}
+
+template <int MODE, bool INSIDE>
 __device__ __forceinline__ EpilogueIn epilogue_load(const Epilogue& e, const EpilogueAt& at)
 {
-    EpilogueIn in{};
-    const int n = at.in(e.M) ? at.n : 0;
-    const int64_t c = at.c;
+    EpilogueIn in;
+    const int n = INSIDE || at.in(e.M) ? at.n : 0;
     if constexpr (MODE == FUSE_LINEAR || MODE == FUSE_DX) {
         if (e.in0)
-            in.a = load_chunk<false>(at.of(e.in0, e.ld_in0), n, c);
+            in.a = load_values<INSIDE>(at.of(e.in0, e.ld_in0), n, at.c);
     }
     if constexpr (MODE == FUSE_DX) {
         if (e.in1)
-            in.b = load_chunk<false>(at.of(e.in1, e.ld_in1), n, c);
+            in.b = load_values<INSIDE>(at.of(e.in1, e.ld_in1), n, at.c);
     }
     if constexpr (MODE == FUSE_DGATED) {
         const uint16_t* gu = at.of(e.in0, e.ld_in0);
-        in.a = load_chunk<false>(gu, n, c);
-        in.b = load_chunk<false>(gu + e.N, n, c);
+        in.a = load_values<INSIDE>(gu, n, at.c);
+        in.b = load_values<INSIDE>(gu + e.N, n, at.c);
     }
     return in;
+}
+
+// The biases of the chunk's columns.
+template <int MODE>
+__device__ __forceinline__ EpilogueIn epilogue_bias(const Epilogue& e, int64_t c, int n)
+{
+    EpilogueIn b{};
+    if constexpr (MODE == FUSE_LINEAR || MODE == FUSE_GATED) {
+        if (e.bias) {
+            b.a = load_chunk<false>(e.bias + c, n, c);
+            if constexpr (MODE == FUSE_GATED)
+                b.b = load_chunk<false>(e.bias + e.N + c, n, c);
+        }
+    }
+    return b;
 }
 
 // Outputs go out non-temporal, as the product's C does (see Cfg::STORE_C).
 typedef u32x4_t __attribute__((aligned(2))) u32x4_any_t;
 typedef f32x4_t __attribute__((aligned(4))) f32x4_any_t;
 
+template <bool INSIDE>
 __device__ __forceinline__ void store_bf16(uint16_t* p, int n, const float (&v)[kChunk])
 {
     const u32x4_t x = chunk_bf16(v);
-    if (n >= kChunk)
+    if (INSIDE || n >= kChunk)
         __builtin_nontemporal_store(x, (u32x4_any_t*)p);
     else
         store_chunk<false>(p, n, x);
@@ -112,40 +141,51 @@ __device__ __forceinline__ void add_chunk(float (&v)[kChunk], u32x4_t x)
         v[e] += chunk_at(x, e);
 }
 
-// s: the sums (GATED: of the gate, and t those of the other factor).
-template <int MODE>
-__device__ __forceinline__ void epilogue_finish(const Epilogue& e, const EpilogueIn& in, const EpilogueAt& at,
-                                                float (&s)[kChunk], float (&t)[kChunk])
+// s: the sums (GATED: of the gate, and t those of the other factor).  `next` is called
+// once what was read is in use, to read again.
+template <int MODE, bool INSIDE, class F>
+__device__ __forceinline__ void epilogue_finish(const Epilogue& e, const EpilogueIn& in, const EpilogueIn& bias,
+                                                const EpilogueAt& at, float (&s)[kChunk], float (&t)[kChunk], F&& next)
 {
     const int n = at.n;
-    const int64_t c = at.c;
-    if (!at.in(e.M) || n <= 0)
+    if (!INSIDE && (!at.in(e.M) || n <= 0)) {
+        next();
         return;
+    }
     uint16_t* out = at.of((uint16_t*)e.out0, e.ld_out0);   // not DW's, which may be fp32
+    float a[kChunk], b[kChunk], o[kChunk], r[kChunk];
     if constexpr (MODE == FUSE_LINEAR) {
-        if (e.bias)
-            add_chunk(s, load_chunk<false>(e.bias + c, n, c));
-        if (e.out1)
-            store_bf16(at.of(e.out1, e.ld_out1), n, s);
-        activate<false>(e.act, s, [&](int i, const auto& a) { s[i] = a.times(1.0f); });
         if (e.in0)
-            add_chunk(s, in.a);
-        store_bf16(out, n, s);
+            chunk_values(a, in.a);
+        next();
+        add_chunk(s, bias.a);
+        if (e.out1)
+            store_bf16<INSIDE>(at.of(e.out1, e.ld_out1), n, s);
+        activate<false>(e.act, s, [&](int i, const auto& x) { o[i] = x.times(1.0f); });
+        if (e.in0) {
+#pragma unroll
+            for (int i = 0; i < kChunk; ++i)
+                o[i] += a[i];
+        }
+        store_bf16<INSIDE>(out, n, o);
     }
     if constexpr (MODE == FUSE_DX) {
         if (e.in1)
             add_chunk(s, in.b);
         if (e.in0) {
-            float z[kChunk];
-            chunk_values(z, in.a);
-            activate<true>(e.act, z, [&](int i, const auto& a) { s[i] = a.slope_times(s[i]); });
+            chunk_values(a, in.a);
+            next();
+            activate<true>(e.act, a, [&](int i, const auto& x) { o[i] = x.slope_times(s[i]); });
+            store_bf16<INSIDE>(out, n, o);
+        } else {
+            next();
+            store_bf16<INSIDE>(out, n, s);
         }
-        store_bf16(out, n, s);
     }
     if constexpr (MODE == FUSE_DW) {
         if (e.fp32) {
             float* p = at.of((float*)e.out0, e.ld_out0);
-            if (n >= kChunk) {
+            if (INSIDE || n >= kChunk) {
                 __builtin_nontemporal_store(f32x4_t{s[0], s[1], s[2], s[3]}, (f32x4_any_t*)p);
                 __builtin_nontemporal_store(f32x4_t{s[4], s[5], s[6], s[7]}, (f32x4_any_t*)(p + 4));
             } else {
@@ -155,34 +195,34 @@ __device__ __forceinline__ void epilogue_finish(const Epilogue& e, const Epilogu
                         p[i] = s[i];
             }
         } else {
-            store_bf16(out, n, s);
+            store_bf16<INSIDE>(out, n, s);
         }
     }
     if constexpr (MODE == FUSE_GATED) {
-        if (e.bias) {
-            add_chunk(s, load_chunk<false>(e.bias + c, n, c));
-            add_chunk(t, load_chunk<false>(e.bias + e.N + c, n, c));
-        }
+        add_chunk(s, bias.a);
+        add_chunk(t, bias.b);
         if (e.out1) {
-            store_bf16(at.of(e.out1, e.ld_out1), n, s);
-            store_bf16(at.of(e.out1, e.ld_out1) + e.N, n, t);
+            uint16_t* gu = at.of(e.out1, e.ld_out1);
+            store_bf16<INSIDE>(gu, n, s);
+            store_bf16<INSIDE>(gu + e.N, n, t);
         }
-        activate<false>(e.act, s, [&](int i, const auto& a) { s[i] = a.times(t[i]); });
-        store_bf16(out, n, s);
+        activate<false>(e.act, s, [&](int i, const auto& x) { o[i] = x.times(t[i]); });
+        store_bf16<INSIDE>(out, n, o);
     }
     if constexpr (MODE == FUSE_DGATED) {
-        float g[kChunk], dg[kChunk], du[kChunk], y[kChunk];
-        chunk_values(g, in.a);
-        activate<true>(e.act, g, [&](int i, const auto& a) {
-            const float u = chunk_at(in.b, i);
-            dg[i] = a.slope_times(s[i], u);
-            du[i] = a.times(s[i]);
-            y[i] = a.times(u);
+        chunk_values(a, in.a);
+        chunk_values(b, in.b);
+        next();
+        float y[kChunk];
+        activate<true>(e.act, a, [&](int i, const auto& x) {
+            o[i] = x.slope_times(s[i], b[i]);
+            r[i] = x.times(s[i]);
+            y[i] = x.times(b[i]);
         });
-        store_bf16(out, n, dg);
-        store_bf16(out + e.N, n, du);
         if (e.out1)
-            store_bf16(at.of(e.out1, e.ld_out1), n, y);
+            store_bf16<INSIDE>(at.of(e.out1, e.ld_out1), n, y);
+        store_bf16<INSIDE>(out, n, o);
+        store_bf16<INSIDE>(out + e.N, n, r);
     }
 }
 
@@ -229,34 +269,34 @@ struct LinearParams : Params {
     __device__ __forceinline__ void store_tile(typename C::Acc (&acc)[C::FM][C::FN], lds_char* strip, int32_t tm,
                                                int32_t tn, int32_t piece, int wm, int wn, int lane_in) const
     {
+        constexpr int FACTORS = fuse_paired(MODE) ? 2 : 1, BNO = C::BN / FACTORS;   // output columns of a tile
+        const int64_t m0 = (int64_t)tm * C::BM, n0 = (int64_t)tn * BNO;
+        if (splits > 1 || (MODE == FUSE_DW && e.fp32))
+            store_rows<C, true, false>(acc, strip, m0, n0, piece, wm, wn, lane_in);
+        else if (m0 + C::BM <= e.M && n0 + BNO <= e.N)
+            store_rows<C, false, true>(acc, strip, m0, n0, piece, wm, wn, lane_in);
+        else
+            store_rows<C, false, false>(acc, strip, m0, n0, piece, wm, wn, lane_in);
+    }
+
+    template <class C, bool SUMS, bool INSIDE>
+    __device__ __forceinline__ void store_rows(typename C::Acc (&acc)[C::FM][C::FN], lds_char* strip, int64_t m0,
+                                               int64_t n0, int32_t piece, int wm, int wn, int lane_in) const
+    {
         constexpr bool PAIR = fuse_paired(MODE);
         static_assert(C::PAIRED == PAIR && C::EPI_WAVE_BYTES == 16 * 64 * 4, "the strip");
-        constexpr int FACTORS = PAIR ? 2 : 1, JB = 4 * FACTORS, PER_I = C::FN / JB, ROUNDS = C::FM * PER_I * 2;
-        constexpr int BNO = C::BN / FACTORS;   // output columns of a tile
+        constexpr int FACTORS = PAIR ? 2 : 1, ROUNDS = C::FM * 2, BNO = C::BN / FACTORS;
+        static_assert(C::FN == 4 * FACTORS && ROUNDS <= 16, "64 columns of a factor per wave");
         const int lane = (int)opaque((uint32_t)lane_in);
         const int wrow = lane & 15, wq = lane >> 4, rrow = lane >> 3, c8 = lane & 7;
-        static_assert(PER_I == 1 && ROUNDS <= 16, "64 columns of a factor per wave");
-        const int64_t c = (int64_t)tn * BNO + wn * (C::TN / FACTORS) + c8 * 8;
-        const int32_t r0 = wm * C::TM;
-        EpilogueAt at{(int64_t)tm * C::BM + r0, c, rrow, left(e.N, c)};
-        const bool whole = splits == 1;
-        EpilogueIn in{};
-        if (whole)
-            in = epilogue_load<MODE>(e, at);
-        // fp32 sums go out as they are, 4 columns a lane, whole 128-byte lines a store:
-        // columns 4 c8 .. and, 32 further, the others, in this order in even rows (whose
-        // reads then meet the odd rows' on no bank).
-        const bool plain = !whole || (MODE == FUSE_DW && e.fp32);
-        const int64_t ld = whole ? e.ld_out0 : BNO, cq = whole ? c - 4 * c8 : c - 4 * c8 - (int64_t)tn * BNO;
-        float* out = whole ? (float*)e.out0 + at.first * ld
-                           : partial + (int64_t)piece * (C::BM * BNO * FACTORS) + (int64_t)r0 * ld;
-#pragma clang loop unroll(disable)
-        for (int round = 0; round < ROUNDS; ++round) {
-            // This round's lanes of its blocks.  A wave's LDS operations complete in
-            // order, so neither its writes nor its reads are waited for before the others.
+        const int32_t r0 = wm * C::TM, w0 = wn * (C::TN / FACTORS);
+        // The rows of `round`, written with its pass's first round, or, of two factors, by
+        // the lanes that hold them.  A wave's LDS operations complete in order, so neither
+        // writes nor reads are waited for before the others.
+        auto write = [&](int round) {
             const int half = round & 1;
             if (PAIR ? (wrow >> 3) == half : half == 0) {
-                auto write = [&]<int P>() {
+                auto pass = [&]<int P>() {
                     if constexpr (P < ROUNDS / 2) {
 #pragma unroll
                         for (int h = 0; h < FACTORS; ++h)
@@ -271,27 +311,39 @@ struct LinearParams : Params {
                     }
                 };
                 switch (round >> 1) {
-                case 0: write.template operator()<0>(); break;
-                case 1: write.template operator()<1>(); break;
-                case 2: write.template operator()<2>(); break;
-                case 3: write.template operator()<3>(); break;
-                case 4: write.template operator()<4>(); break;
-                case 5: write.template operator()<5>(); break;
-                case 6: write.template operator()<6>(); break;
-                default: write.template operator()<7>(); break;
+                case 0: pass.template operator()<0>(); break;
+                case 1: pass.template operator()<1>(); break;
+                case 2: pass.template operator()<2>(); break;
+                case 3: pass.template operator()<3>(); break;
+                case 4: pass.template operator()<4>(); break;
+                case 5: pass.template operator()<5>(); break;
+                case 6: pass.template operator()<6>(); break;
+                default: pass.template operator()<7>(); break;
                 }
             }
             COMPILER_FENCE();
-            if (plain) {
-                const bool in_rows = !whole || at.in(e.M);
+        };
+        auto strip_row = [&](int round, int h) { return rrow + 8 * (PAIR ? h : round & 1); };
+        if constexpr (SUMS) {
+            // fp32 sums as they are, 4 columns a lane, whole 128-byte lines a store: columns
+            // 4 c8 .. and, 32 further, the others, in this order in even rows (whose reads then
+            // meet the odd rows' on no bank).
+            const bool whole = splits == 1;
+            const int64_t ld = whole ? e.ld_out0 : BNO, c = (whole ? n0 : 0) + w0 + 4 * c8;
+            float* out = whole ? (float*)e.out0 + (m0 + r0) * ld
+                               : partial + (int64_t)piece * (C::BM * BNO * FACTORS) + (int64_t)r0 * ld;
+#pragma clang loop unroll(disable)
+            for (int round = 0; round < ROUNDS; ++round) {
+                write(round);
+                const bool in_rows = !whole || rrow < e.M - (m0 + r0 + 8 * round);
 #pragma unroll
                 for (int h = 0; h < FACTORS; ++h) {
-                    const int row = rrow + 8 * (PAIR ? h : half);
+                    const int row = strip_row(round, h);
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
                         const int second = q ^ (rrow & 1);
                         const f32x4_t x = *(const LDS_AS f32x4_t*)(strip + row * 256 + (((c8 + 8 * second) ^ row) << 4));
-                        const int64_t col = cq + 32 * second, n = whole ? e.N - col : 4;
+                        const int64_t col = c + 32 * second, n = whole ? e.N - col : 4;
                         float* to = out + h * (C::BM * BNO) + (rrow * ld + col);
                         if (!in_rows)
                             continue;
@@ -307,29 +359,42 @@ struct LinearParams : Params {
                     }
                 }
                 COMPILER_FENCE();
-                at.first += 8;
                 out += 8 * ld;
-                continue;
             }
-            float v[FACTORS][kChunk];
+        } else {
+            const int64_t c = n0 + w0 + c8 * 8;
+            const int n = INSIDE ? kChunk : left(e.N, c);
+            auto at = [&](int round) { return EpilogueAt{m0 + r0 + 8 * round, c, rrow, n}; };
+            const EpilogueIn bias = epilogue_bias<MODE>(e, c, n);
+            // What a round reads is on its way two rounds before.
+            EpilogueIn in[2];
 #pragma unroll
-            for (int h = 0; h < FACTORS; ++h) {
-                const int row = rrow + 8 * (PAIR ? h : half);
+            for (int i = 0; i < 2; ++i)
+                in[i] = epilogue_load<MODE, INSIDE>(e, at(i));
+            auto one = [&](EpilogueIn& now, int round) {
+                write(round);
+                float v[FACTORS][kChunk];
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const f32x4_t x = *(const LDS_AS f32x4_t*)(strip + row * 256 + (((2 * c8 + q) ^ row) << 4));
+                for (int h = 0; h < FACTORS; ++h) {
+                    const int row = strip_row(round, h);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        v[h][4 * q + i] = x[i];
+                    for (int q = 0; q < 2; ++q) {
+                        const f32x4_t x = *(const LDS_AS f32x4_t*)(strip + row * 256 + (((2 * c8 + q) ^ row) << 4));
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            v[h][4 * q + i] = x[i];
+                    }
                 }
+                COMPILER_FENCE();
+                // Past the last round the last rows are read again, and not used.
+                auto next = [&] { now = epilogue_load<MODE, INSIDE>(e, at(min(round + 2, ROUNDS - 1))); };
+                epilogue_finish<MODE, INSIDE>(e, now, bias, at(round), v[0], v[FACTORS - 1], next);
+            };
+#pragma clang loop unroll(disable)
+            for (int round = 0; round < ROUNDS; round += 2) {
+                one(in[0], round);
+                one(in[1], round + 1);
             }
-            COMPILER_FENCE();
-            const EpilogueIn now = in;
-            const EpilogueAt here = at;
-            at.first += 8;
-            if (round + 1 < ROUNDS)
-                in = epilogue_load<MODE>(e, at);
-            epilogue_finish<MODE>(e, now, here, v[0], v[FACTORS - 1]);
         }
     }
 };
@@ -351,7 +416,7 @@ __global__ void __launch_bounds__(256) k_linear_finish(LinearParams<MODE> p, int
         const EpilogueAt here{(int64_t)tm * bm, c, r, left(p.e.N, c)};
         if (!here.in(p.e.M) || here.n <= 0)
             continue;
-        const EpilogueIn in = epilogue_load<MODE>(p.e, here);
+        const EpilogueIn in = epilogue_load<MODE, false>(p.e, here);
         float v[2][kChunk] = {};
         for (int32_t sp = 0; sp < p.splits; ++sp) {
             const float* src = p.partial + (sp * (int64_t)p.span + u) * piece + (int64_t)r * bn + cc;
@@ -364,184 +429,223 @@ __global__ void __launch_bounds__(256) k_linear_finish(LinearParams<MODE> p, int
                     v[h][i] += x[i];
             }
         }
-        epilogue_finish<MODE>(p.e, in, here, v[0], v[1]);
+        epilogue_finish<MODE, false>(p.e, in, epilogue_bias<MODE>(p.e, here.c, here.n), here, v[0], v[1], [] {});
     }
 }
 
 // ---------------------------------------------------------------------------
-// Few rows: bound by the weight's bytes and by latency.  As for 8-bit operands
-// (gemm_fp8.h): a workgroup of 8 waves takes 16 MF rows by 16 NF columns (of both
-// factors), its waves share out the 128-byte blocks along k and stream fragments
-// from global memory into registers, DEPTH blocks in use and DEPTH in flight; their
-// sums meet in LDS, in wave order.  ANY: operands of any alignment and stride, K >=
-// 8, by 16-byte loads at any byte; a chunk that reaches past the row's end is read
-// from its last 16 bytes and shifted into place.
+// Small products and few rows, which latency or one operand's bytes bound: the 8
+// waves of a workgroup share out the 64-wide blocks along k (wave w takes blocks w, w
+// + 8, ...) of 16 MF rows by 16 NF columns (of each factor) and add their sums through
+// LDS in wave order.  So a workgroup has loads in flight over the whole of k, nothing
+// waits for another wave before the end, and there is little code to fetch (a launch
+// of the tiles' kernel takes 5 us longer for that alone).
+//
+// A wave loads DEPTH blocks ahead into registers, a block's 16-byte chunks in rows
+// (lanes 8 i .. 8 i + 7 a row's 128 bytes), writes them to LDS of its own and reads
+// MFMA fragments back: plain reads where k is contiguous, transposing ones where it
+// is not.  A wave's LDS operations complete in order, so there is nothing to wait
+// for but the loads.  EVEN: operands as the tiles read them (rows of whole 16-byte
+// chunks on 16-byte boundaries), by range-checked loads; otherwise any alignment and
+// stride, by 16-byte loads at any byte, and a row's last chunk from its last bytes.
+//
+// Swizzles of a 64-row block: with k along the rows of 128 bytes as the tiles' (swz_k:
+// a read's 16 lanes hold 16 rows at one chunk).  With k across, a transposing read's 32
+// lanes hold rows r, r + 8 (r = 0 .. 3) at two chunks, and rows of one parity share
+// the same banks: the chunk's pair is XORed with bits 1 and 3 of the row.
 // ---------------------------------------------------------------------------
-template <int MODE, int MF, int NF, int DEPTH, bool ANY>
-__global__ void __launch_bounds__(kSkinnyWaves * 64) k_linear_few(LinearParams<MODE> p, int32_t chunk, int32_t kblocks)
+constexpr int kWaves = 8;
+
+__device__ __forceinline__ int swz_across(int krow) { return (krow & 2) | ((krow >> 1) & 4); }
+
+// One operand's part of a wave: 16 X rows (columns, where k is across) of it.
+template <int X, bool ACROSS, bool EVEN>
+struct WaveOperand {
+    static_assert(!ACROSS || X == 4, "rows of 128 bytes");
+    const uint16_t* base;   // the first row's (column's) k = 0
+    const uint16_t* end;    // EVEN, across: past the last row's last whole chunk
+    int64_t ld, first;      // first: column of `base`, across
+    int32_t count, K;       // rows (columns) that exist from base on
+    __amdgpu_buffer_rsrc_t rsrc;
+
+    __device__ __forceinline__ WaveOperand(const char* p, int64_t ld_, int64_t at, int64_t total, int64_t k)
+    {
+        ld = ld_;
+        first = ACROSS ? at : 0;
+        count = (int32_t)min(total - at, (int64_t)X * 16);
+        K = (int32_t)k;
+        base = (const uint16_t*)p + (ACROSS ? at : at * ld);
+        if constexpr (EVEN) {
+            if constexpr (ACROSS)
+                end = (const uint16_t*)p + (k - 1) * ld + total;
+            else
+                rsrc = make_rsrc(base, ((count - 1) * ld + k) * 2);
+        }
+    }
+
+    __device__ __forceinline__ void load(u32x4_t (&v)[2 * X], int32_t kb) const
+    {
+        const int lane = threadIdx.x & 63, lr = lane >> 3, lc = lane & 7;
+        if constexpr (EVEN) {
+            const __amdgpu_buffer_rsrc_t r =
+                ACROSS ? make_rsrc(base + (int64_t)kb * 64 * ld, (end - (base + (int64_t)kb * 64 * ld)) * 2) : rsrc;
+            const bool in = ACROSS ? lc * 8 < count : kb * 64 + lc * 8 < K;
+#pragma unroll
+            for (int t = 0; t < 2 * X; ++t) {
+                const int row = 8 * t + lr;
+                const bool ok = in && (ACROSS || row < count);
+                v[t] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
+                    r, ok ? (uint32_t)row * (uint32_t)(ld * 2) + lc * 16 : kOOB, ACROSS ? 0 : kb * 128, 0));
+            }
+        } else {
+#pragma unroll
+            for (int t = 0; t < 2 * X; ++t) {
+                const int row = 8 * t + lr;
+                if constexpr (ACROSS) {
+                    const int64_t k = (int64_t)kb * 64 + row;
+                    v[t] = load_chunk<false>(base + k * ld + lc * 8, k < K ? left(count, lc * 8) : 0, first + lc * 8);
+                } else {
+                    const int32_t k = kb * 64 + lc * 8;
+                    v[t] = load_chunk<false>(base + row * ld + k, row < count ? left(K, k) : 0, k);
+                }
+            }
+        }
+    }
+
+    __device__ __forceinline__ void stage(lds_char* to, const u32x4_t (&v)[2 * X]) const
+    {
+        const int lane = threadIdx.x & 63, lr = lane >> 3, lc = lane & 7;
+#pragma unroll
+        for (int t = 0; t < 2 * X; ++t) {
+            const int row = 8 * t + lr;
+            *(LDS_AS u32x4_t*)(to + row * 128 + ((lc ^ (ACROSS ? swz_across(row) : swz_k<64>(row))) << 4)) = v[t];
+        }
+    }
+
+    // Fragments of k-step ks (32 wide).
+    __device__ __forceinline__ void fragments(bf16x8_t (&f)[X], const lds_char* from, int ks) const
+    {
+        const int lane = threadIdx.x & 63, r16 = lane & 15, h = lane >> 4;
+#pragma unroll
+        for (int i = 0; i < X; ++i) {
+            if constexpr (ACROSS) {
+                const int rr = r16 >> 2, q = r16 & 3;
+                i16x4_t half[2];
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh) {
+                    const int krow = 32 * ks + 8 * h + 4 * hh + rr;
+                    half[hh] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                        (LDS_AS i16x4_t*)(from + krow * 128 + (((2 * i + (q >> 1)) ^ swz_across(krow)) << 4) + (q & 1) * 8));
+                }
+                f[i] = __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(half[0], half[1], 0, 1, 2, 3, 4, 5, 6, 7));
+            } else {
+                const int row = 16 * i + r16;
+                f[i] = *(const LDS_AS bf16x8_t*)(from + row * 128 + (((4 * ks + h) ^ swz_k<64>(row)) << 4));
+            }
+        }
+    }
+};
+
+template <int MODE, int MF, int NF, int DEPTH, bool EVEN>
+__global__ void __launch_bounds__(kWaves * 64) k_linear_wave(LinearParams<MODE> p, int32_t chunk, int32_t kblocks)
 {
+    constexpr bool AT = MODE == FUSE_DW, BT = MODE == FUSE_LINEAR || MODE == FUSE_GATED;
     constexpr int FACTORS = fuse_paired(MODE) ? 2 : 1, NB = NF * FACTORS, FR = MF * NB;
-    __shared__ __attribute__((aligned(16))) f32x4_t sums[kSkinnyWaves][FR][64];
+    constexpr int A_BYTES = MF * 2048, B_BYTES = NF * 2048;
+    constexpr int WAVE_BYTES = std::max(A_BYTES + FACTORS * B_BYTES, FR * 1024);
+    __shared__ __attribute__((aligned(1024))) char smem[kWaves * WAVE_BYTES];
     const int lane = threadIdx.x & 63, r16 = lane & 15, g = lane >> 4;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    // The row tiles of one column tile go to one XCD, which then reads the weight once.
+    // The row tiles of one column tile go to one XCD, which then reads B once.
     const int32_t x = blockIdx.x & 7, y = blockIdx.x >> 3;
     const int32_t tm = y % p.tiles_m, tn = y / p.tiles_m * 8 + x;
     if (tn >= p.tiles_n)
         return;
     const int64_t m0 = (int64_t)tm * (MF * 16), n0 = (int64_t)tn * (NF * 16);
     const int32_t kb_first = blockIdx.y * chunk, kb_end = min(kb_first + chunk, kblocks);
-    const int64_t lda = p.lda * 2, ldb = p.ldb * 2;
-    const int32_t kbytes = (int32_t)p.K * 2;
-
-    // Rows past the end read as zeros: their offset is past the resource.
-    const int64_t a_rows = min(p.M - m0, (int64_t)MF * 16), b_rows = min(p.N - n0, (int64_t)NF * 16);
-    const char* a0 = p.A + m0 * lda;
-    const char* b0[FACTORS];
-    __amdgpu_buffer_rsrc_t rb[FACTORS];
-    const __amdgpu_buffer_rsrc_t ra = make_rsrc(a0, (a_rows - 1) * lda + kbytes);
-#pragma unroll
-    for (int h = 0; h < FACTORS; ++h) {
-        b0[h] = p.B + (n0 + h * p.N) * ldb;
-        rb[h] = make_rsrc(b0[h], (b_rows - 1) * ldb + kbytes);
-    }
-    // Lanes 4 i .. 4 i + 3 read 64 consecutive bytes of a row; an MFMA's lane (r16, g)
-    // then takes chunk g of row r16 from the lane that read it.
-    const int lr = (lane >> 2 & 3) * 4 + (lane >> 4), lc = lane & 3;
-    const int from = ((lane & 3) * 16 + (lane & 12) + g) * 4;
-    auto mfma_order = [&](u32x4_t v) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            v[i] = (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)v[i]);
-        return v;
-    };
-    uint32_t va[MF] = {}, vb[NF] = {};
-#pragma unroll
-    for (int i = 0; i < MF; ++i)
-        va[i] = i * 16 + lr < a_rows ? (uint32_t)(i * 16 + lr) * (uint32_t)lda + lc * 16 : kOOB;
-#pragma unroll
-    for (int j = 0; j < NF; ++j)
-        vb[j] = j * 16 + lr < b_rows ? (uint32_t)(j * 16 + lr) * (uint32_t)ldb + lc * 16 : kOOB;
+    const WaveOperand<MF, AT, EVEN> oa(p.A, p.lda, m0, p.M, p.K);
+    const WaveOperand<NF, !BT, EVEN> ob[2] = {{p.B, p.ldb, n0, p.N, p.K},
+                                              {p.B + (FACTORS - 1) * p.N * p.ldb * 2, p.ldb, n0, p.N, p.K}};
+    lds_char* own = (lds_char*)smem + w * WAVE_BYTES;
 
     struct Block {
-        u32x4_t a[MF][2], b[NB][2];
+        u32x4_t a[2 * MF], b[FACTORS][2 * NF];
     };
-    // ANY: where half h of block kb is read, and how many of its bytes precede it.
-    auto place = [&](int32_t kb, int h, int32_t& at) {
-        const int32_t k = kb * 128 + (h * 4 + lc) * 16;
-        at = min(k, kbytes - 16);
-        return min(k - at, 16);
+    Block ahead[DEPTH];
+    // Workgroups start at different places along k: with a power-of-two row stride,
+    // all of them reading the same columns at once fall on the same few channels.
+    const int32_t mine = (kb_end - kb_first - w + kWaves - 1) / kWaves;   // blocks of this wave
+    const int32_t rot = mine > 0 ? (int32_t)(blockIdx.x % (unsigned)mine) : 0;
+    auto load = [&](Block& v, int32_t t) {
+        if (t < mine) {
+            const int32_t kb = kb_first + w + (t + rot < mine ? t + rot : t + rot - mine) * kWaves;
+#pragma unroll
+            for (int h = 0; h < FACTORS; ++h)
+                ob[h].load(v.b[h], kb);
+            oa.load(v.a, kb);
+        }
     };
-    auto load = [&](Block& v, int32_t kb) {
-        // The halves of a line one after the other, while the line is in the L1.
-        auto halves = [&](u32x4_t (&to)[2], const char* base, int64_t row, int64_t rows, int64_t ld,
-                          const __amdgpu_buffer_rsrc_t& rsrc, uint32_t voff) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                if constexpr (ANY) {
-                    int32_t at;
-                    place(kb, h, at);
-                    // Rows past the last repeat it; no one stores their sums.
-                    __builtin_memcpy(&to[h], base + min(row, rows - 1) * ld + at, 16);
-                } else {
-                    const bool ok = kb * 128 + (h * 4 + lc) * 16 < kbytes;
-                    to[h] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
-                                                            rsrc, ok ? voff : kOOB, kb * 128 + h * 64, 0));
-                }
-            }
-        };
-#pragma unroll
-        for (int h = 0; h < FACTORS; ++h)
-#pragma unroll
-            for (int j = 0; j < NF; ++j)
-                halves(v.b[h * NF + j], b0[h], j * 16 + lr, b_rows, ldb, rb[h], vb[j]);
-#pragma unroll
-        for (int i = 0; i < MF; ++i)
-            halves(v.a[i], a0, i * 16 + lr, a_rows, lda, ra, va[i]);
-    };
-
+    for (int d = 0; d < DEPTH; ++d)
+        load(ahead[d], d);
     f32x4_t acc[MF][NB];
 #pragma unroll
     for (int i = 0; i < MF; ++i)
 #pragma unroll
         for (int j = 0; j < NB; ++j)
             acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-    auto compute = [&](const Block& v, int32_t kb) {
-        const bool tail = ANY && (kb + 1) * 128 > kbytes;
-        auto frag = [&](const u32x4_t (&raw)[2], bf16x8_t (&to)[2]) {
+    for (int32_t t0 = 0; t0 < mine; t0 += DEPTH) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                u32x4_t q = raw[h];
-                if (tail) {
-                    int32_t at;
-                    q = without_first(q, place(kb, h, at));
-                }
-                to[h] = __builtin_bit_cast(bf16x8_t, mfma_order(q));
+        for (int d = 0; d < DEPTH; ++d) {
+            if (DEPTH > 1 && t0 + d >= mine)
+                break;
+            oa.stage(own, ahead[d].a);
+#pragma unroll
+            for (int h = 0; h < FACTORS; ++h)
+                ob[h].stage(own + A_BYTES + h * B_BYTES, ahead[d].b[h]);
+            load(ahead[d], t0 + d + DEPTH);
+            COMPILER_FENCE();
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+                bf16x8_t af[MF], bf[FACTORS][NF];
+                oa.fragments(af, own, ks);
+#pragma unroll
+                for (int h = 0; h < FACTORS; ++h)
+                    ob[h].fragments(bf[h], own + A_BYTES + h * B_BYTES, ks);
+#pragma unroll
+                for (int i = 0; i < MF; ++i)
+#pragma unroll
+                    for (int j = 0; j < NB; ++j)
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf[j / NF][j % NF], af[i], acc[i][j], 0, 0, 0);
             }
-        };
-        bf16x8_t bf[NB][2];
-#pragma unroll
-        for (int j = 0; j < NB; ++j)
-            frag(v.b[j], bf[j]);
-#pragma unroll
-        for (int i = 0; i < MF; ++i) {
-            bf16x8_t af[2];
-            frag(v.a[i], af);
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int j = 0; j < NB; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf[j][h], af[h], acc[i][j], 0, 0, 0);
+            COMPILER_FENCE();
         }
-    };
-
-    Block cur[DEPTH], nxt[DEPTH];
-    constexpr int STEP = kSkinnyWaves * DEPTH;
-    auto load_all = [&](Block (&v)[DEPTH], int32_t kb0) {
-        if (kb0 < kb_end) {
-#pragma unroll
-            for (int d = 0; d < DEPTH; ++d)
-                load(v[d], kb0 + d * kSkinnyWaves);
-        }
-    };
-    auto compute_all = [&](const Block (&v)[DEPTH], int32_t kb0) {
-#pragma unroll
-        for (int d = 0; d < DEPTH; ++d)
-            if (kb0 + d * kSkinnyWaves < kb_end)
-                compute(v[d], kb0 + d * kSkinnyWaves);
-    };
-    // Workgroups start at different places along k: with a power-of-two row stride,
-    // all of them reading the same columns at once fall on the same few channels.
-    const int32_t rounds = (kb_end - kb_first + STEP - 1) / STEP, rot = (int32_t)(blockIdx.x % (unsigned)rounds);
-    auto at = [&](int32_t t) {
-        return t < rounds ? kb_first + w + (t + rot < rounds ? t + rot : t + rot - rounds) * STEP : kb_end;
-    };
-    load_all(cur, at(0));
-    for (int32_t t = 0; t < rounds; t += 2) {
-        load_all(nxt, at(t + 1));
-        compute_all(cur, at(t));
-        load_all(cur, at(t + 2));
-        compute_all(nxt, at(t + 1));
     }
 
 #pragma unroll
     for (int i = 0; i < MF; ++i)
 #pragma unroll
         for (int j = 0; j < NB; ++j)
-            sums[w][i * NB + j][lane] = acc[i][j];
+            *(LDS_AS f32x4_t*)(own + (i * NB + j) * 1024 + lane * 16) = acc[i][j];
     __syncthreads();
     // Wave w finishes fragments w, w + 8, ... of one factor with the other's beside
     // them.  Lanes of even g hold columns 8 (g / 2) .. + 3 and get + 4 .. + 7 from the
     // lane 16 further.
-    for (int f = w; f < MF * NF; f += kSkinnyWaves) {
+    for (int f = w; f < MF * NF; f += kWaves) {
         const int i = f / NF, j = f % NF;
+        const int r = i * 16 + r16, cc = j * 16 + g * 4;
+        const EpilogueAt here{m0, n0 + cc, r, (g & 1) ? 0 : left(p.e.N, n0 + cc)};
+        EpilogueIn in{};
+        if (p.splits == 1)
+            in = epilogue_load<MODE, false>(p.e, here);
         float v[2][kChunk];
 #pragma unroll
         for (int h = 0; h < FACTORS; ++h) {
-            f32x4_t s = sums[0][i * NB + h * NF + j][lane];
+            const lds_char* from = (lds_char*)smem + (i * NB + h * NF + j) * 1024 + lane * 16;
+            f32x4_t s = *(const LDS_AS f32x4_t*)from;
 #pragma unroll
-            for (int z = 1; z < kSkinnyWaves; ++z)
-                s += sums[z][i * NB + h * NF + j][lane];
+            for (int z = 1; z < kWaves; ++z)
+                s += *(const LDS_AS f32x4_t*)(from + z * WAVE_BYTES);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 v[h][q] = s[q];
@@ -550,7 +654,6 @@ __global__ void __launch_bounds__(kSkinnyWaves * 64) k_linear_few(LinearParams<M
         }
         if (g & 1)
             continue;
-        const int r = i * 16 + r16, cc = j * 16 + g * 4;
         if (p.splits > 1) {
             const int64_t piece = (int64_t)blockIdx.y * p.span + (tn * p.tiles_m + tm);
             float* to = p.partial + piece * (MF * 16 * NF * 16 * FACTORS) + r * (NF * 16) + cc;
@@ -558,8 +661,7 @@ __global__ void __launch_bounds__(kSkinnyWaves * 64) k_linear_few(LinearParams<M
             for (int h = 0; h < FACTORS; ++h)
                 __builtin_memcpy(to + h * (MF * 16 * NF * 16), v[h], 32);
         } else {
-            const EpilogueAt here{m0, n0 + cc, r, left(p.e.N, n0 + cc)};
-            epilogue_finish<MODE>(p.e, epilogue_load<MODE>(p.e, here), here, v[0], v[1]);
+            epilogue_finish<MODE, false>(p.e, in, epilogue_bias<MODE>(p.e, here.c, here.n), here, v[0], v[1], [] {});
         }
     }
 }
@@ -643,14 +745,11 @@ struct LinearShape {
     int factors;
 };
 
-enum { TILES_BIG, TILES_SMALL, TILES_FEW };
-
-// Rows of few-row workgroups and their columns of one factor.
-constexpr int kFewCols = 32;
+enum { TILES_BIG, TILES_SMALL, TILES_WAVE };
 
 struct LinearPlan {
     int kind;
-    int mf;                  // TILES_FEW: row fragments
+    int mf, nf;              // TILES_WAVE: fragments
     int bm, bn;              // outputs per workgroup
     int64_t tiles, splits, chunk, grid, workspace;   // chunk: k elements
 };
@@ -676,17 +775,27 @@ int64_t linear_splits(int64_t tiles, int64_t K, int64_t slots, int64_t least, in
 LinearPlan linear_plan(const LinearShape& q, int cus)
 {
     LinearPlan pl{};
-    if (q.bt && !q.at && q.M <= 64 && q.K >= kChunk) {
-        pl.kind = TILES_FEW;
-        pl.mf = q.M <= 16 ? 1 : q.M <= 32 ? 2 : 4;
+    const char* force = getenv("LINEAR_FORCE");
+    const int64_t waves = ceil_div(q.M, 64) * ceil_div(q.N * q.factors, 64);
+    const bool wave = force ? force[0] == 'w' : waves <= 2 * cus;
+    if (wave) {
+        pl.kind = TILES_WAVE;
+        pl.mf = q.at || q.M > 32 ? 4 : q.M > 16 ? 2 : 1;
+        pl.nf = 4 / q.factors;
+        if (pl.mf == 1 && q.bt) {
+            if (ceil_div(q.N * q.factors, 64) < cus / 2)
+                pl.nf = 2 / q.factors;
+            if (q.factors == 1 && ceil_div(q.N, 32) < cus / 2)
+                pl.nf = 1;
+        }
         pl.bm = pl.mf * 16;
-        pl.bn = kFewCols;
+        pl.bn = pl.nf * 16;
         pl.tiles = ceil_div(q.M, pl.bm) * ceil_div(q.N, pl.bn);
         pl.splits = linear_splits(pl.tiles, q.K, cus, 2048, pl.chunk);
         pl.grid = ceil_div(ceil_div(q.N, pl.bn), 8) * 8 * ceil_div(q.M, pl.bm);
     } else {
         const int64_t big = ceil_div(q.M, 256) * ceil_div(q.N * q.factors, 256);
-        const int edge = big >= cus ? 256 : 128;
+        const int edge = force ? (force[0] == 'b' ? 256 : 128) : big >= cus ? 256 : 128;
         pl.kind = edge == 256 ? TILES_BIG : TILES_SMALL;
         pl.bm = edge;
         pl.bn = edge / q.factors;
@@ -723,22 +832,36 @@ int launch_linear(const LinearParams<MODE>& p, int64_t grid, hipStream_t s)
 }
 
 template <int MODE>
-int launch_few(const LinearParams<MODE>& p, const LinearPlan& pl, bool any, hipStream_t s)
+int launch_wave(const LinearParams<MODE>& p, const LinearPlan& pl, bool even, hipStream_t s)
 {
+    constexpr int F = fuse_paired(MODE) ? 2 : 1;
+    constexpr bool BT = MODE == FUSE_LINEAR || F == 2;
     const int32_t kblocks = (int32_t)ceil_div(p.K, 64), chunk = (int32_t)ceil_div(pl.chunk, 64);
-    const dim3 g((unsigned)pl.grid, (unsigned)pl.splits), b(kSkinnyWaves * 64);
-    auto run = [&]<int MF, int DEPTH>() {
-        if (any)
-            hipLaunchKernelGGL(HIP_KERNEL_NAME(k_linear_few<MODE, MF, 2, DEPTH, true>), g, b, 0, s, p, chunk, kblocks);
+    const dim3 g((unsigned)pl.grid, (unsigned)pl.splits), b(kWaves * 64);
+    auto run = [&]<int MF, int NF, int DEPTH>() {
+        if (even)
+            hipLaunchKernelGGL(HIP_KERNEL_NAME(k_linear_wave<MODE, MF, NF, DEPTH, true>), g, b, 0, s, p, chunk, kblocks);
         else
-            hipLaunchKernelGGL(HIP_KERNEL_NAME(k_linear_few<MODE, MF, 2, DEPTH, false>), g, b, 0, s, p, chunk, kblocks);
+            hipLaunchKernelGGL(HIP_KERNEL_NAME(k_linear_wave<MODE, MF, NF, DEPTH, false>), g, b, 0, s, p, chunk, kblocks);
     };
-    if (pl.mf == 1)
-        run.template operator()<1, 2>();
-    else if (pl.mf == 2)
-        run.template operator()<2, 2>();
-    else
-        run.template operator()<4, 1>();
+    if constexpr (BT) {
+        if (pl.mf == 1 && F == 1 && pl.nf == 1) {
+            run.template operator()<1, 1, 4>();
+            return launched();
+        }
+        if (pl.mf == 1 && pl.nf * F == 2) {
+            run.template operator()<1, 2 / F, 2>();
+            return launched();
+        }
+    }
+    if constexpr (MODE != FUSE_DW) {
+        if (pl.mf == 1)
+            run.template operator()<1, 4 / F, 2>();
+        else if (pl.mf == 2)
+            run.template operator()<2, 4 / F, 1>();
+    }
+    if (pl.mf == 4)
+        run.template operator()<4, 4 / F, 1>();
     return launched();
 }
 
@@ -752,7 +875,7 @@ int linear_run(const LinearShape& q, const void* A, int64_t lda, const void* B, 
     LinearParams<MODE> p;
     memset((void*)&p, 0, sizeof p);
     p.e = e;
-    const LinearPlan pl = q.K > 0 ? linear_plan(q, cus) : LinearPlan{TILES_SMALL, 0, 128, 128 / q.factors, 0, 0, 0, 0, 0};
+    const LinearPlan pl = q.K > 0 ? linear_plan(q, cus) : LinearPlan{TILES_SMALL, 0, 0, 128, 128 / q.factors, 0, 0, 0, 0, 0};
     p.A = (const char*)A;
     p.B = (const char*)B;
     p.M = q.M;
@@ -771,7 +894,7 @@ int linear_run(const LinearShape& q, const void* A, int64_t lda, const void* B, 
     p.tiles = (int32_t)(tiles * pl.splits);
     p.ksplit = pl.chunk;
     p.k_steps = (int32_t)steps;
-    p.group_m = pl.kind == TILES_FEW ? p.tiles_m : 4;
+    p.group_m = pl.kind == TILES_WAVE ? p.tiles_m : 4;
     p.spin_limit = kSpinLimit;
     p.clock_on = g_clock_on.load(std::memory_order_relaxed) ? 1u : 0u;
     auto finish = [&]() {
@@ -790,8 +913,8 @@ int linear_run(const LinearShape& q, const void* A, int64_t lda, const void* B, 
         return ((uintptr_t)ptr & 15) == 0 && cols % kChunk == 0 && (rows <= 1 || (ld % kChunk == 0 && ld <= kMaxLd));
     };
     const bool a_ok = fits(A, a_rows, a_cols, lda), b_ok = fits(B, b_rows, b_cols, ldb);
-    const bool few = pl.kind == TILES_FEW;
-    const bool pad_a = !few && !a_ok, pad_b = !few && !b_ok;
+    const bool wave = pl.kind == TILES_WAVE;
+    const bool pad_a = !wave && !a_ok, pad_b = !wave && !b_ok;
     const int64_t a_ld = round8(a_cols), b_ld = round8(b_cols);
     const int64_t a_bytes = pad_a ? align256(a_rows * a_ld * 2) : 0, b_bytes = pad_b ? align256(b_rows * b_ld * 2) : 0;
     const int64_t bytes = a_bytes + b_bytes + pl.workspace;
@@ -827,11 +950,9 @@ int linear_run(const LinearShape& q, const void* A, int64_t lda, const void* B, 
     p.small_span = ((a_rows - 1) * p.lda + a_ld) * 2 < (int64_t)kMaxRecords &&
                    ((b_rows / q.factors - 1) * p.ldb + b_ld) * 2 < (int64_t)kMaxRecords;
     if (rc == GEMM_OK) {
-        if constexpr (BT) {
-            if (few)
-                rc = launch_few<MODE>(p, pl, !(a_ok && b_ok), s);
-        }
-        if (pl.kind == TILES_BIG)
+        if (wave)
+            rc = launch_wave<MODE>(p, pl, a_ok && b_ok, s);
+        else if (pl.kind == TILES_BIG)
             rc = launch_linear<LinearCfg<BT, AT, PAIR, true>, MODE>(p, pl.grid, s);
         else if (pl.kind == TILES_SMALL)
             rc = launch_linear<LinearCfg<BT, AT, PAIR, false>, MODE>(p, pl.grid, s);
