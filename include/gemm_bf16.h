@@ -659,6 +659,38 @@ int gemm_gated_linear_bwd_input(int64_t M, int64_t F, int64_t N, const void* dY,
                                 int act, const void* GU, int64_t ldgu, void* dGU, int64_t lddgu,
                                 void* Y, int64_t ldy, void* stream);
 
+/* How one of the products above is computed (see gemm_linear_plan_cus). */
+typedef struct gemm_linear_plan {
+    int32_t rows, cols;       /* outputs (of one factor) that a workgroup computes at a time */
+    int32_t waves_share_k;    /* 1: the waves of a workgroup share k, operands of any alignment; 0: tiles through LDS */
+    int32_t threads;          /* per workgroup */
+    int64_t tiles;            /* workgroups' worth of output */
+    int64_t k_splits;         /* chunks of the sum, added by a second launch where there are several */
+    int64_t k_chunk;          /* terms per chunk, the last one's may be fewer */
+    int64_t grid;             /* workgroups of the main launch */
+    int64_t workspace_bytes;  /* the chunks' sums (0 with one chunk) */
+    int64_t pad_bytes;        /* zero-padded copies of operands that the tiles cannot read */
+} gemm_linear_plan_t;
+
+/* The products a plan is asked for, with the sizes of their entry points (F as N for the gated ones). */
+enum {
+    GEMM_LINEAR = 0,
+    GEMM_LINEAR_BWD_INPUT = 1,
+    GEMM_LINEAR_BWD_WEIGHT = 2,
+    GEMM_GATED_LINEAR = 3,           /* (M, F, K) */
+    GEMM_GATED_LINEAR_BWD_INPUT = 4  /* (M, F, N) */
+};
+
+/*
+ * gemm_linear_plan_cus: what the product's entry point does on a device with
+ * `compute_units` compute units (256 on an MI355X), without querying one.  a_aligned,
+ * b_aligned: whether the rows of its two matrix operands (X and W, dY and W, dY and X)
+ * start on 16-byte boundaries.  A null `out`, compute_units < 1 or an unknown product is
+ * GEMM_ERR_INVALID_VALUE.  With an empty product every field is 0.
+ */
+int gemm_linear_plan_cus(int64_t M, int64_t N, int64_t K, int product, int a_aligned, int b_aligned, int compute_units,
+                         gemm_linear_plan_t* out);
+
 #ifdef __cplusplus
 }
 #endif

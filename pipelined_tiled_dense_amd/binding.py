@@ -31,6 +31,8 @@ TYPE_BF16 = 0
 TYPE_FP8 = 1
 TYPE_FP32 = 2
 FP8_EXACT = 256             # GEMM_FP8_EXACT, added to gemm_fp8_bt's c_type
+LINEAR_PRODUCTS = {"linear": 0, "linear_bwd_input": 1, "linear_bwd_weight": 2, "gated_linear": 3,
+                   "gated_linear_bwd_input": 4}   # GEMM_LINEAR, ...
 ACTIVATIONS = {None: 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}   # GEMM_ACT_*
 BLOCK = 128                 # values along k (and rows of a block) that share a scale
 NORM_MAX_WIDTH = 32768      # GEMM_NORM_MAX_WIDTH
@@ -66,6 +68,16 @@ class Fp8Plan(ctypes.Structure):
 
     def as_dict(self):
         return {name: getattr(self, name) for name, _ in self._fields_ if name != "reserved"}
+
+
+class LinearPlan(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("cols", ctypes.c_int32), ("waves_share_k", ctypes.c_int32),
+                ("threads", ctypes.c_int32), ("tiles", ctypes.c_int64), ("k_splits", ctypes.c_int64),
+                ("k_chunk", ctypes.c_int64), ("grid", ctypes.c_int64), ("workspace_bytes", ctypes.c_int64),
+                ("pad_bytes", ctypes.c_int64)]
+
+    def as_dict(self):
+        return {name: getattr(self, name) for name, _ in self._fields_}
 
 
 _lib = None
@@ -117,7 +129,8 @@ def library() -> ctypes.CDLL:
         lib.gemm_linear_bwd_weight.argtypes = [i64, i64, i64, p, i64, p, i64, p, i64, i32, p, p]
         lib.gemm_gated_linear.argtypes = [i64, i64, i64, p, i64, p, i64, p, i32, p, i64, p, i64, p]
         lib.gemm_gated_linear_bwd_input.argtypes = [i64, i64, i64, p, i64, p, i64, i32, p, i64, p, i64, p, i64, p]
-        for name in ("gemm_fp8_bt", "gemm_fp8_plan_cus", "gemm_quantize_fp8", "gemm_rms_norm", "gemm_rms_norm_bwd", "gemm_swiglu",
+        lib.gemm_linear_plan_cus.argtypes = [i64, i64, i64, i32, i32, i32, i32, ctypes.POINTER(LinearPlan)]
+        for name in ("gemm_linear_plan_cus", "gemm_fp8_bt", "gemm_fp8_plan_cus", "gemm_quantize_fp8", "gemm_rms_norm", "gemm_rms_norm_bwd", "gemm_swiglu",
                      "gemm_swiglu_bwd", "gemm_linear", "gemm_linear_bwd_input", "gemm_linear_bwd_weight",
                      "gemm_gated_linear", "gemm_gated_linear_bwd_input"):
             getattr(lib, name).restype = i32
@@ -262,6 +275,15 @@ def gemm_gated_linear(M, F, K, X, ldx, W, ldw, bias, act, GU, ldgu, Y, ldy, stre
 
 def gemm_gated_linear_bwd_input(M, F, N, dY, lddy, W, ldw, act, GU, ldgu, dGU, lddgu, Y, ldy, stream) -> int:
     return library().gemm_gated_linear_bwd_input(M, F, N, dY, lddy, W, ldw, act, GU, ldgu, dGU, lddgu, Y, ldy, stream)
+
+
+def gemm_linear_plan_cus(M, N, K, product, a_aligned, b_aligned, compute_units) -> dict:
+    out = LinearPlan()
+    rc = library().gemm_linear_plan_cus(M, N, K, LINEAR_PRODUCTS.get(product, product), int(bool(a_aligned)),
+                                        int(bool(b_aligned)), compute_units, ctypes.byref(out))
+    if rc != GEMM_OK:
+        raise GemmError(rc, "gemm_linear_plan_cus")
+    return out.as_dict()
 
 
 strerror = gemm_bf16_strerror

@@ -90,11 +90,11 @@
 #include <hip/hip_runtime.h>
 
 #include <stdint.h>
-#include <stdlib.h>
 #include <string.h>
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <mutex>
 #include <type_traits>
 #include <utility>

@@ -48,83 +48,124 @@ struct EpilogueIn {
     u32x4_t a, b;
 };
 
-// A chunk of 8 columns from c on, the n (<= 8) of them that exist, of row first +
-// lane_row: `first` is uniform, so that a loop over rows keeps what a lane adds to a
-// matrix's address and moves the uniform part.  INSIDE: all 8 and the row exist;
-// without a branch around them, loads and stores of a loop's rounds overlap (a branch
-// that may skip a store makes the next wait for a load wait for every store).
-struct EpilogueAt {
-    int64_t first, c;
-    int32_t lane_row, n;
-
-    __device__ __forceinline__ bool in(int64_t M) const { return lane_row < M - first; }
-    template <class T>
-    __device__ __forceinline__ T* of(T* base, int64_t ld) const
-    {
-        return base + first * ld + (lane_row * ld + c);
-    }
-};
-
-template <bool INSIDE>
-__device__ __forceinline__ u32x4_t load_values(const uint16_t* p, int n, int64_t c)
-{
-    if constexpr (INSIDE) {
-        u32x4_t v;
-        __builtin_memcpy(&v, p, 16);
-        return v;
-    } else {
-        return load_chunk<false>(p, n, c);
-    }
-}
-
-template <int MODE, bool INSIDE>
-__device__ __forceinline__ EpilogueIn epilogue_load(const Epilogue& e, const EpilogueAt& at)
-{
-    EpilogueIn in;
-    const int n = INSIDE || at.in(e.M) ? at.n : 0;
-    if constexpr (MODE == FUSE_LINEAR || MODE == FUSE_DX) {
-        if (e.in0)
-            in.a = load_values<INSIDE>(at.of(e.in0, e.ld_in0), n, at.c);
-    }
-    if constexpr (MODE == FUSE_DX) {
-        if (e.in1)
-            in.b = load_values<INSIDE>(at.of(e.in1, e.ld_in1), n, at.c);
-    }
-    if constexpr (MODE == FUSE_DGATED) {
-        const uint16_t* gu = at.of(e.in0, e.ld_in0);
-        in.a = load_values<INSIDE>(gu, n, at.c);
-        in.b = load_values<INSIDE>(gu + e.N, n, at.c);
-    }
-    return in;
-}
-
-// The biases of the chunk's columns.
-template <int MODE>
-__device__ __forceinline__ EpilogueIn epilogue_bias(const Epilogue& e, int64_t c, int n)
-{
-    EpilogueIn b{};
-    if constexpr (MODE == FUSE_LINEAR || MODE == FUSE_GATED) {
-        if (e.bias) {
-            b.a = load_chunk<false>(e.bias + c, n, c);
-            if constexpr (MODE == FUSE_GATED)
-                b.b = load_chunk<false>(e.bias + e.N + c, n, c);
-        }
-    }
-    return b;
-}
-
 // Outputs go out non-temporal, as the product's C does (see Cfg::STORE_C).
 typedef u32x4_t __attribute__((aligned(2))) u32x4_any_t;
 typedef f32x4_t __attribute__((aligned(4))) f32x4_any_t;
 
-template <bool INSIDE>
-__device__ __forceinline__ void store_bf16(uint16_t* p, int n, const float (&v)[kChunk])
+// Where a chunk is: 8 columns from c on, the n (<= 8) of them that exist, of row
+// `row`, in matrices of any alignment and stride.
+struct ChunkAt {
+    int64_t row, c;
+    int n;
+
+    __device__ __forceinline__ bool any() const { return n > 0; }
+    __device__ __forceinline__ u32x4_t load(const uint16_t* base, int64_t ld) const
+    {
+        return load_chunk<false>(base + row * ld + c, n, c);
+    }
+    __device__ __forceinline__ u32x4_t placed(u32x4_t v) const { return v; }
+    __device__ __forceinline__ void store(uint16_t* base, int64_t ld, u32x4_t v) const
+    {
+        uint16_t* p = base + row * ld + c;
+        if (n >= kChunk)
+            __builtin_nontemporal_store(v, (u32x4_any_t*)p);
+        else
+            store_chunk<false>(p, n, v);
+    }
+};
+
+// The same for 8 rows of a tile, from `first` (uniform) on, without branches: a branch
+// that may skip a store makes a loop's next wait for a load wait for every store
+// before it (4 us a tile).  The resource ends with the matrix's last row, and an offset
+// past it drops a lane of columns that do not exist.  `part` (uniform): the columns end
+// inside a chunk, which is loaded from the row's last 16 bytes and stored by element.
+// For leading dimensions up to kMaxTileLd and rows of 8 and more.
+constexpr int64_t kMaxTileLd = (int64_t)1 << 27;
+
+struct TileAt {
+    int64_t first, rows;     // the first row, and how many exist from there on
+    int32_t cols;            // of the matrix
+    int32_t lane_row, c;     // this lane's, c < cols + 256
+    bool part;
+
+    __device__ __forceinline__ int n() const { return min(max(cols - c, 0), kChunk); }
+    __device__ __forceinline__ bool any() const { return true; }
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const uint16_t* base, int64_t ld) const
+    {
+        return make_rsrc(base + first * ld, rows <= 0 ? 0 : ((rows - 1) * ld + cols) * 2);
+    }
+    __device__ __forceinline__ uint32_t offset(int64_t ld, int32_t col) const
+    {
+        return ((uint32_t)lane_row * (uint32_t)ld + (uint32_t)col) * 2u;
+    }
+    __device__ __forceinline__ u32x4_t load(const uint16_t* base, int64_t ld) const
+    {
+        const int m = n();
+        const uint32_t at = offset(ld, part ? min(c, cols - kChunk) : c);
+        return __builtin_bit_cast(u32x4_t,
+                                  __builtin_amdgcn_raw_buffer_load_b128(rsrc(base, ld), m > 0 ? at : kOOB, 0, 0));
+    }
+    // What was loaded, in place.  Not in load: it would wait for the load there.
+    __device__ __forceinline__ u32x4_t placed(u32x4_t v) const
+    {
+        if (part) {
+            uint64_t x[2];
+            __builtin_memcpy(x, &v, 16);
+            const int s = 16 * (kChunk - n()) & 127;   // lanes of whole chunks: 0
+            const uint64_t lo = s >= 64 ? x[1] : x[0], hi = s >= 64 ? 0u : x[1];
+            x[0] = (s & 63) ? (lo >> (s & 63)) | (hi << (64 - (s & 63))) : lo;
+            x[1] = hi >> (s & 63);
+            __builtin_memcpy(&v, x, 16);
+        }
+        return v;
+    }
+    __device__ __forceinline__ void store(uint16_t* base, int64_t ld, u32x4_t v) const
+    {
+        const __amdgpu_buffer_rsrc_t r = rsrc(base, ld);
+        const int m = n();
+        const uint32_t at = offset(ld, c);
+        __builtin_amdgcn_raw_buffer_store_b128(v, r, m >= kChunk ? at : kOOB, 0, kStoreNonTemporal);
+        if (part) {
+#pragma unroll
+            for (int i = 0; i < kChunk - 1; ++i)
+                __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(v[i >> 1] >> (16 * (i & 1))), r,
+                                                      m < kChunk && i < m ? at + 2 * i : kOOB, 0, 0);
+        }
+    }
+};
+
+template <int MODE, class At>
+__device__ __forceinline__ EpilogueIn epilogue_load(const Epilogue& e, const At& at)
 {
-    const u32x4_t x = chunk_bf16(v);
-    if (INSIDE || n >= kChunk)
-        __builtin_nontemporal_store(x, (u32x4_any_t*)p);
-    else
-        store_chunk<false>(p, n, x);
+    EpilogueIn in;
+    if constexpr (MODE == FUSE_LINEAR || MODE == FUSE_DX) {
+        if (e.in0)
+            in.a = at.load(e.in0, e.ld_in0);
+    }
+    if constexpr (MODE == FUSE_DX) {
+        if (e.in1)
+            in.b = at.load(e.in1, e.ld_in1);
+    }
+    if constexpr (MODE == FUSE_DGATED) {
+        in.a = at.load(e.in0, e.ld_in0);
+        in.b = at.load(e.in0 + e.N, e.ld_in0);
+    }
+    return in;
+}
+
+// The biases of the columns of `at`, a chunk of the first of one row.
+template <int MODE, class At>
+__device__ __forceinline__ EpilogueIn epilogue_bias(const Epilogue& e, const At& at)
+{
+    EpilogueIn b{};
+    if constexpr (MODE == FUSE_LINEAR || MODE == FUSE_GATED) {
+        if (e.bias) {
+            b.a = at.load(e.bias, 0);
+            if constexpr (MODE == FUSE_GATED)
+                b.b = at.load(e.bias + e.N, 0);
+        }
+    }
+    return b;
 }
 
 __device__ __forceinline__ void chunk_values(float (&v)[kChunk], u32x4_t x)
@@ -143,75 +184,73 @@ __device__ __forceinline__ void add_chunk(float (&v)[kChunk], u32x4_t x)
 
 // s: the sums (GATED: of the gate, and t those of the other factor).  `next` is called
 // once what was read is in use, to read again.
-template <int MODE, bool INSIDE, class F>
+template <int MODE, class At, class F>
 __device__ __forceinline__ void epilogue_finish(const Epilogue& e, const EpilogueIn& in, const EpilogueIn& bias,
-                                                const EpilogueAt& at, float (&s)[kChunk], float (&t)[kChunk], F&& next)
+                                                const At& at, float (&s)[kChunk], float (&t)[kChunk], F&& next)
 {
-    const int n = at.n;
-    if (!INSIDE && (!at.in(e.M) || n <= 0)) {
-        next();
+    if (!at.any())
         return;
-    }
-    uint16_t* out = at.of((uint16_t*)e.out0, e.ld_out0);   // not DW's, which may be fp32
+    uint16_t* out = (uint16_t*)e.out0;   // not DW's, which may be fp32
     float a[kChunk], b[kChunk], o[kChunk], r[kChunk];
     if constexpr (MODE == FUSE_LINEAR) {
         if (e.in0)
-            chunk_values(a, in.a);
+            chunk_values(a, at.placed(in.a));
         next();
-        add_chunk(s, bias.a);
+        add_chunk(s, at.placed(bias.a));
         if (e.out1)
-            store_bf16<INSIDE>(at.of(e.out1, e.ld_out1), n, s);
+            at.store(e.out1, e.ld_out1, chunk_bf16(s));
         activate<false>(e.act, s, [&](int i, const auto& x) { o[i] = x.times(1.0f); });
         if (e.in0) {
 #pragma unroll
             for (int i = 0; i < kChunk; ++i)
                 o[i] += a[i];
         }
-        store_bf16<INSIDE>(out, n, o);
+        at.store(out, e.ld_out0, chunk_bf16(o));
     }
     if constexpr (MODE == FUSE_DX) {
         if (e.in1)
-            add_chunk(s, in.b);
+            add_chunk(s, at.placed(in.b));
         if (e.in0) {
-            chunk_values(a, in.a);
+            chunk_values(a, at.placed(in.a));
             next();
             activate<true>(e.act, a, [&](int i, const auto& x) { o[i] = x.slope_times(s[i]); });
-            store_bf16<INSIDE>(out, n, o);
+            at.store(out, e.ld_out0, chunk_bf16(o));
         } else {
             next();
-            store_bf16<INSIDE>(out, n, s);
+            at.store(out, e.ld_out0, chunk_bf16(s));
         }
     }
     if constexpr (MODE == FUSE_DW) {
-        if (e.fp32) {
-            float* p = at.of((float*)e.out0, e.ld_out0);
-            if (INSIDE || n >= kChunk) {
-                __builtin_nontemporal_store(f32x4_t{s[0], s[1], s[2], s[3]}, (f32x4_any_t*)p);
-                __builtin_nontemporal_store(f32x4_t{s[4], s[5], s[6], s[7]}, (f32x4_any_t*)(p + 4));
-            } else {
+        if constexpr (std::is_same_v<At, ChunkAt>) {   // a tile's fp32 sums take a way of their own
+            if (e.fp32) {
+                float* p = (float*)e.out0 + at.row * e.ld_out0 + at.c;
+                if (at.n >= kChunk) {
+                    __builtin_nontemporal_store(f32x4_t{s[0], s[1], s[2], s[3]}, (f32x4_any_t*)p);
+                    __builtin_nontemporal_store(f32x4_t{s[4], s[5], s[6], s[7]}, (f32x4_any_t*)(p + 4));
+                } else {
 #pragma unroll
-                for (int i = 0; i < kChunk - 1; ++i)
-                    if (i < n)
-                        p[i] = s[i];
+                    for (int i = 0; i < kChunk - 1; ++i)
+                        if (i < at.n)
+                            p[i] = s[i];
+                }
+                return;
             }
-        } else {
-            store_bf16<INSIDE>(out, n, s);
         }
+        at.store(out, e.ld_out0, chunk_bf16(s));
     }
     if constexpr (MODE == FUSE_GATED) {
-        add_chunk(s, bias.a);
-        add_chunk(t, bias.b);
+        add_chunk(s, at.placed(bias.a));
+        add_chunk(t, at.placed(bias.b));
         if (e.out1) {
-            uint16_t* gu = at.of(e.out1, e.ld_out1);
-            store_bf16<INSIDE>(gu, n, s);
-            store_bf16<INSIDE>(gu + e.N, n, t);
+            at.store(e.out1, e.ld_out1, chunk_bf16(s));
+            at.store(e.out1 + e.N, e.ld_out1, chunk_bf16(t));
         }
         activate<false>(e.act, s, [&](int i, const auto& x) { o[i] = x.times(t[i]); });
-        store_bf16<INSIDE>(out, n, o);
+        at.store(out, e.ld_out0, chunk_bf16(o));
     }
     if constexpr (MODE == FUSE_DGATED) {
-        chunk_values(a, in.a);
-        chunk_values(b, in.b);
+        chunk_values(a, at.placed(in.a));
+        chunk_values(b, at.placed(in.b));
         next();
         float y[kChunk];
         activate<true>(e.act, a, [&](int i, const auto& x) {
@@ -220,9 +259,9 @@ __device__ __forceinline__ void epilogue_finish(const Epilogue& e, const Epilogu
             y[i] = x.times(b[i]);
         });
         if (e.out1)
-            store_bf16<INSIDE>(at.of(e.out1, e.ld_out1), n, y);
-        store_bf16<INSIDE>(out, n, o);
-        store_bf16<INSIDE>(out + e.N, n, r);
+            at.store(e.out1, e.ld_out1, chunk_bf16(y));
+        at.store(out, e.ld_out0, chunk_bf16(o));
+        at.store(out + e.N, e.ld_out0, chunk_bf16(r));
     }
 }
 
@@ -271,15 +310,13 @@ struct LinearParams : Params {
     {
         constexpr int FACTORS = fuse_paired(MODE) ? 2 : 1, BNO = C::BN / FACTORS;   // output columns of a tile
         const int64_t m0 = (int64_t)tm * C::BM, n0 = (int64_t)tn * BNO;
-        if (splits > 1 || (MODE == FUSE_DW && e.fp32))
-            store_rows<C, true, false>(acc, strip, m0, n0, piece, wm, wn, lane_in);
-        else if (m0 + C::BM <= e.M && n0 + BNO <= e.N)
-            store_rows<C, false, true>(acc, strip, m0, n0, piece, wm, wn, lane_in);
+        if (partial || (MODE == FUSE_DW && e.fp32))
+            store_rows<C, true>(acc, strip, m0, n0, piece, wm, wn, lane_in);
         else
-            store_rows<C, false, false>(acc, strip, m0, n0, piece, wm, wn, lane_in);
+            store_rows<C, false>(acc, strip, m0, n0, piece, wm, wn, lane_in);
     }
 
-    template <class C, bool SUMS, bool INSIDE>
+    template <class C, bool SUMS>
     __device__ __forceinline__ void store_rows(typename C::Acc (&acc)[C::FM][C::FN], lds_char* strip, int64_t m0,
                                                int64_t n0, int32_t piece, int wm, int wn, int lane_in) const
     {
@@ -328,7 +365,7 @@ struct LinearParams : Params {
             // fp32 sums as they are, 4 columns a lane, whole 128-byte lines a store: columns
             // 4 c8 .. and, 32 further, the others, in this order in even rows (whose reads then
             // meet the odd rows' on no bank).
-            const bool whole = splits == 1;
+            const bool whole = !partial;
             const int64_t ld = whole ? e.ld_out0 : BNO, c = (whole ? n0 : 0) + w0 + 4 * c8;
             float* out = whole ? (float*)e.out0 + (m0 + r0) * ld
                                : partial + (int64_t)piece * (C::BM * BNO * FACTORS) + (int64_t)r0 * ld;
@@ -362,15 +399,18 @@ struct LinearParams : Params {
                 out += 8 * ld;
             }
         } else {
-            const int64_t c = n0 + w0 + c8 * 8;
-            const int n = INSIDE ? kChunk : left(e.N, c);
-            auto at = [&](int round) { return EpilogueAt{m0 + r0 + 8 * round, c, rrow, n}; };
-            const EpilogueIn bias = epilogue_bias<MODE>(e, c, n);
+            const int32_t cols = (int32_t)e.N, c = (int32_t)n0 + w0 + c8 * kChunk;
+            const bool part = cols % kChunk != 0 && cols - (int32_t)n0 - w0 < 64;
+            auto at = [&](int round) {
+                const int64_t first = m0 + r0 + 8 * round;
+                return TileAt{first, e.M - first, cols, rrow, c, part};
+            };
+            const EpilogueIn bias = epilogue_bias<MODE>(e, TileAt{0, 1, cols, 0, c, part});
             // What a round reads is on its way two rounds before.
             EpilogueIn in[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i)
-                in[i] = epilogue_load<MODE, INSIDE>(e, at(i));
+                in[i] = epilogue_load<MODE>(e, at(i));
             auto one = [&](EpilogueIn& now, int round) {
                 write(round);
                 float v[FACTORS][kChunk];
@@ -387,8 +427,8 @@ struct LinearParams : Params {
                 }
                 COMPILER_FENCE();
                 // Past the last round the last rows are read again, and not used.
-                auto next = [&] { now = epilogue_load<MODE, INSIDE>(e, at(min(round + 2, ROUNDS - 1))); };
-                epilogue_finish<MODE, INSIDE>(e, now, bias, at(round), v[0], v[FACTORS - 1], next);
+                auto next = [&] { now = epilogue_load<MODE>(e, at(min(round + 2, ROUNDS - 1))); };
+                epilogue_finish<MODE>(e, now, bias, at(round), v[0], v[FACTORS - 1], next);
             };
 #pragma clang loop unroll(disable)
             for (int round = 0; round < ROUNDS; round += 2) {
@@ -413,11 +453,13 @@ __global__ void __launch_bounds__(256) k_linear_finish(LinearParams<MODE> p, int
         int32_t tm, tn;
         raster_tile(p, p.tile_base + u, tm, tn);
         const int64_t c = (int64_t)tn * bn + cc;
-        const EpilogueAt here{(int64_t)tm * bm, c, r, left(p.e.N, c)};
-        if (!here.in(p.e.M) || here.n <= 0)
+        const int64_t row = (int64_t)tm * bm + r;
+        const ChunkAt here{row, c, row < p.e.M ? left(p.e.N, c) : 0};
+        if (!here.any())
             continue;
-        const EpilogueIn in = epilogue_load<MODE, false>(p.e, here);
+        const EpilogueIn in = epilogue_load<MODE>(p.e, here);
         float v[2][kChunk] = {};
+#pragma unroll 4
         for (int32_t sp = 0; sp < p.splits; ++sp) {
             const float* src = p.partial + (sp * (int64_t)p.span + u) * piece + (int64_t)r * bn + cc;
 #pragma unroll
@@ -429,7 +471,7 @@ __global__ void __launch_bounds__(256) k_linear_finish(LinearParams<MODE> p, int
                     v[h][i] += x[i];
             }
         }
-        epilogue_finish<MODE, false>(p.e, in, epilogue_bias<MODE>(p.e, here.c, here.n), here, v[0], v[1], [] {});
+        epilogue_finish<MODE>(p.e, in, epilogue_bias<MODE>(p.e, ChunkAt{0, here.c, here.n}), here, v[0], v[1], [] {});
     }
 }
 
@@ -556,11 +598,12 @@ __global__ void __launch_bounds__(kWaves * 64) k_linear_wave(LinearParams<MODE> 
     __shared__ __attribute__((aligned(1024))) char smem[kWaves * WAVE_BYTES];
     const int lane = threadIdx.x & 63, r16 = lane & 15, g = lane >> 4;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    // The row tiles of one column tile go to one XCD, which then reads B once.
-    const int32_t x = blockIdx.x & 7, y = blockIdx.x >> 3;
-    const int32_t tm = y % p.tiles_m, tn = y / p.tiles_m * 8 + x;
-    if (tn >= p.tiles_n)
+    // Workgroups are dealt to the 8 XCDs in turn; each XCD takes a run of tiles, column by
+    // column, so that the row tiles of a column tile share its L2.
+    const int32_t at_tile = (blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3);
+    if (at_tile >= p.span)
         return;
+    const int32_t tn = at_tile / p.tiles_m, tm = at_tile - tn * p.tiles_m;
     const int64_t m0 = (int64_t)tm * (MF * 16), n0 = (int64_t)tn * (NF * 16);
     const int32_t kb_first = blockIdx.y * chunk, kb_end = min(kb_first + chunk, kblocks);
     const WaveOperand<MF, AT, EVEN> oa(p.A, p.lda, m0, p.M, p.K);
@@ -634,10 +677,10 @@ __global__ void __launch_bounds__(kWaves * 64) k_linear_wave(LinearParams<MODE> 
     for (int f = w; f < MF * NF; f += kWaves) {
         const int i = f / NF, j = f % NF;
         const int r = i * 16 + r16, cc = j * 16 + g * 4;
-        const EpilogueAt here{m0, n0 + cc, r, (g & 1) ? 0 : left(p.e.N, n0 + cc)};
+        const ChunkAt here{m0 + r, n0 + cc, (g & 1) || m0 + r >= p.e.M ? 0 : left(p.e.N, n0 + cc)};
         EpilogueIn in{};
-        if (p.splits == 1)
-            in = epilogue_load<MODE, false>(p.e, here);
+        if (!p.partial)
+            in = epilogue_load<MODE>(p.e, here);
         float v[2][kChunk];
 #pragma unroll
         for (int h = 0; h < FACTORS; ++h) {
@@ -654,14 +697,14 @@ __global__ void __launch_bounds__(kWaves * 64) k_linear_wave(LinearParams<MODE> 
         }
         if (g & 1)
             continue;
-        if (p.splits > 1) {
+        if (p.partial) {
             const int64_t piece = (int64_t)blockIdx.y * p.span + (tn * p.tiles_m + tm);
             float* to = p.partial + piece * (MF * 16 * NF * 16 * FACTORS) + r * (NF * 16) + cc;
 #pragma unroll
             for (int h = 0; h < FACTORS; ++h)
                 __builtin_memcpy(to + h * (MF * 16 * NF * 16), v[h], 32);
         } else {
-            epilogue_finish<MODE, false>(p.e, in, epilogue_bias<MODE>(p.e, here.c, here.n), here, v[0], v[1], [] {});
+            epilogue_finish<MODE>(p.e, in, epilogue_bias<MODE>(p.e, ChunkAt{0, here.c, here.n}), here, v[0], v[1], [] {});
         }
     }
 }
@@ -743,7 +786,15 @@ struct LinearShape {
     int64_t M, N, K;
     bool bt, at;             // B stored N x K; A stored K x M
     int factors;
+    bool a_even, b_even;     // as the tiles read them; else copied for them first
+
+    int64_t a_rows() const { return at ? K : M; }
+    int64_t a_cols() const { return at ? M : K; }
+    int64_t b_rows() const { return bt ? N * factors : K; }
+    int64_t b_cols() const { return bt ? K : N; }
 };
+
+int64_t pad_size(int64_t rows, int64_t cols) { return align256(rows * round8(cols) * 2); }
 
 enum { TILES_BIG, TILES_SMALL, TILES_WAVE };
 
@@ -754,58 +805,72 @@ struct LinearPlan {
     int64_t tiles, splits, chunk, grid, workspace;   // chunk: k elements
 };
 
-// k chunks for `tiles` work items on `slots` places: chunks of whole 64-wide k-steps,
-// each at least `least` long, all of them with work.
-int64_t linear_splits(int64_t tiles, int64_t K, int64_t slots, int64_t least, int64_t& chunk)
+// What a kind of kernel is estimated to take, in us, from the times of some 200 products
+// of 1 to 8192 rows and 64 to 8192 columns and k (within 5 to 10 percent of them at the
+// root mean square): so much for the call, for each round of tiles over the compute
+// units and each k-step of a round; k chunks cost a second launch, and the time that
+// their sums take through memory.  What every kind reads and writes alike is left out.
+double linear_time(const LinearShape& q, const LinearPlan& pl, int cus)
 {
-    chunk = K;
-    if (2 * tiles > slots)
-        return 1;
-    int64_t s = slots / tiles;
-    if (s > kMaxSplits)
-        s = kMaxSplits;
-    if (s > K / least)
-        s = K / least;
-    if (s <= 1)
-        return 1;
-    chunk = ceil_div(ceil_div(K, s), 64) * 64;
-    return ceil_div(K, chunk);
+    const double items = (double)(pl.tiles * pl.splits), fill = items / cus;
+    const int64_t steps = ceil_div(pl.chunk, 64);
+    const double sums = pl.splits > 1 ? 1e-6 * (double)pl.workspace : 0.0, copies =
+        1e-6 * (double)((q.a_even ? 0 : pad_size(q.a_rows(), q.a_cols())) + (q.b_even ? 0 : pad_size(q.b_rows(), q.b_cols())));
+    if (pl.kind == TILES_WAVE) {
+        // Narrow workgroups share a compute unit, and their loads its bandwidth.
+        const double k = (double)ceil_div(steps, kWaves) * (copies > 0 ? 1.5 : 1.0);
+        const int nb = pl.nf * q.factors;
+        double t;
+        if (pl.mf == 1)
+            t = nb == 1 ? k * (0.27 + 0.28 * fill) : nb == 2 ? k * (0.4 + 0.35 * fill) : k * (0.8 + 1.0 * fill);
+        else
+            t = std::ceil(fill) * (pl.mf == 2 ? 1.3 * k : 1.6 + 2.35 * k);
+        return (pl.mf == 4 ? 1.4 : 3.2) + t + (pl.splits > 1 ? 6.0 + 0.5 * sums : 0.0);
+    }
+    const double padding = copies > 0 ? 2.5 + copies / 2.2 : 0.0, rounds = std::ceil(fill);
+    if (pl.kind == TILES_SMALL)
+        return 3.0 + rounds * (4.3 + 0.43 * steps) + (pl.splits > 1 ? 5.3 + 0.2 * sums : 0.0) + padding;
+    return 1.5 + rounds * (9.0 + 1.1 * steps) + (pl.splits > 1 ? 5.0 + 0.17 * sums : 0.0) + padding;
 }
 
+// The kind, tile and chunks of k (whole 64-wide k-steps, all of them with work) that are
+// estimated fastest.
 LinearPlan linear_plan(const LinearShape& q, int cus)
 {
-    LinearPlan pl{};
-    const char* force = getenv("LINEAR_FORCE");
-    const int64_t waves = ceil_div(q.M, 64) * ceil_div(q.N * q.factors, 64);
-    const bool wave = force ? force[0] == 'w' : waves <= 2 * cus;
-    if (wave) {
-        pl.kind = TILES_WAVE;
-        pl.mf = q.at || q.M > 32 ? 4 : q.M > 16 ? 2 : 1;
-        pl.nf = 4 / q.factors;
-        if (pl.mf == 1 && q.bt) {
-            if (ceil_div(q.N * q.factors, 64) < cus / 2)
-                pl.nf = 2 / q.factors;
-            if (q.factors == 1 && ceil_div(q.N, 32) < cus / 2)
-                pl.nf = 1;
+    LinearPlan best{};
+    double least = 0;
+    auto consider = [&](int kind, int mf, int nf) {
+        LinearPlan pl{};
+        pl.kind = kind;
+        pl.mf = mf;
+        pl.nf = nf;
+        pl.bm = kind == TILES_WAVE ? mf * 16 : kind == TILES_BIG ? 256 : 128;
+        pl.bn = kind == TILES_WAVE ? nf * 16 : pl.bm / q.factors;
+        pl.tiles = ceil_div(q.M, pl.bm) * ceil_div(q.N, pl.bn);
+        for (int64_t s = 1; s <= kMaxSplits && (s == 1 || pl.tiles * s <= 2 * cus); ++s) {
+            pl.chunk = s == 1 ? q.K : ceil_div(ceil_div(q.K, s), 64) * 64;
+            pl.splits = ceil_div(q.K, pl.chunk);
+            if (pl.splits < s)
+                continue;   // the same as for fewer
+            pl.grid = kind == TILES_WAVE ? ceil_div(pl.tiles, 8) * 8 : std::min<int64_t>(pl.tiles * s, cus);
+            pl.workspace = s > 1 ? pl.tiles * s * pl.bm * pl.bn * q.factors * 4 : 0;
+            const double us = linear_time(q, pl, cus);
+            if (best.bm == 0 || us < least) {
+                least = us;
+                best = pl;
+            }
         }
-        pl.bm = pl.mf * 16;
-        pl.bn = pl.nf * 16;
-        pl.tiles = ceil_div(q.M, pl.bm) * ceil_div(q.N, pl.bn);
-        pl.splits = linear_splits(pl.tiles, q.K, cus, 2048, pl.chunk);
-        pl.grid = ceil_div(ceil_div(q.N, pl.bn), 8) * 8 * ceil_div(q.M, pl.bm);
-    } else {
-        const int64_t big = ceil_div(q.M, 256) * ceil_div(q.N * q.factors, 256);
-        const int edge = force ? (force[0] == 'b' ? 256 : 128) : big >= cus ? 256 : 128;
-        pl.kind = edge == 256 ? TILES_BIG : TILES_SMALL;
-        pl.bm = edge;
-        pl.bn = edge / q.factors;
-        pl.tiles = ceil_div(q.M, pl.bm) * ceil_div(q.N, pl.bn);
-        const int64_t slots = cus;
-        pl.splits = linear_splits(pl.tiles, q.K, slots, 512, pl.chunk);
-        pl.grid = pl.tiles * pl.splits < slots ? pl.tiles * pl.splits : slots;
+    };
+    const int mf = q.at || q.M > 32 ? 4 : q.M > 16 ? 2 : 1;
+    consider(TILES_WAVE, mf, 4 / q.factors);
+    if (mf == 1 && q.bt)
+        for (int nf = 2 / q.factors; nf >= 1; nf /= 2)
+            consider(TILES_WAVE, mf, nf);
+    if (q.N >= kChunk) {   // TileAt's rows
+        consider(TILES_SMALL, 0, 0);
+        consider(TILES_BIG, 0, 0);
     }
-    pl.workspace = pl.splits > 1 ? pl.tiles * pl.splits * pl.bm * pl.bn * q.factors * 4 : 0;
-    return pl;
+    return best;
 }
 
 template <class C, int MODE>
@@ -868,13 +933,21 @@ int launch_wave(const LinearParams<MODE>& p, const LinearPlan& pl, bool even, hi
 // The product of A and B into epilogue e.  The caller has checked everything but
 // the device.
 template <int MODE>
-int linear_run(const LinearShape& q, const void* A, int64_t lda, const void* B, int64_t ldb, const Epilogue& e,
+int linear_run(LinearShape q, const void* A, int64_t lda, const void* B, int64_t ldb, const Epilogue& e,
                TempMem& tm, int cus, hipStream_t s)
 {
     constexpr bool PAIR = fuse_paired(MODE), BT = MODE == FUSE_LINEAR || PAIR, AT = MODE == FUSE_DW;
     LinearParams<MODE> p;
     memset((void*)&p, 0, sizeof p);
     p.e = e;
+    // Operands as the tiles read them: rows on 16-byte boundaries, of whole 16-byte
+    // chunks, at most 2^22 elements apart.
+    const int64_t a_rows = q.a_rows(), a_cols = q.a_cols(), b_rows = q.b_rows(), b_cols = q.b_cols();
+    auto fits = [](const void* ptr, int64_t rows, int64_t cols, int64_t ld) {
+        return ((uintptr_t)ptr & 15) == 0 && cols % kChunk == 0 && (rows <= 1 || (ld % kChunk == 0 && ld <= kMaxLd));
+    };
+    q.a_even = fits(A, a_rows, a_cols, lda);
+    q.b_even = fits(B, b_rows, b_cols, ldb);
     const LinearPlan pl = q.K > 0 ? linear_plan(q, cus) : LinearPlan{TILES_SMALL, 0, 0, 128, 128 / q.factors, 0, 0, 0, 0, 0};
     p.A = (const char*)A;
     p.B = (const char*)B;
@@ -905,19 +978,15 @@ int linear_run(const LinearShape& q, const void* A, int64_t lda, const void* B, 
     if (q.K == 0)
         return finish();
 
-    // Operands as the tiles read them: rows on 16-byte boundaries, of whole 16-byte
-    // chunks, at most 2^22 elements apart.  The few-row kernel takes any.
-    const int64_t a_rows = AT ? q.K : q.M, a_cols = AT ? q.M : q.K;
-    const int64_t b_rows = BT ? q.N * q.factors : q.K, b_cols = BT ? q.K : q.N;
-    auto fits = [](const void* ptr, int64_t rows, int64_t cols, int64_t ld) {
-        return ((uintptr_t)ptr & 15) == 0 && cols % kChunk == 0 && (rows <= 1 || (ld % kChunk == 0 && ld <= kMaxLd));
-    };
-    const bool a_ok = fits(A, a_rows, a_cols, lda), b_ok = fits(B, b_rows, b_cols, ldb);
     const bool wave = pl.kind == TILES_WAVE;
-    const bool pad_a = !wave && !a_ok, pad_b = !wave && !b_ok;
+    const bool pad_a = !wave && !q.a_even, pad_b = !wave && !q.b_even;
     const int64_t a_ld = round8(a_cols), b_ld = round8(b_cols);
-    const int64_t a_bytes = pad_a ? align256(a_rows * a_ld * 2) : 0, b_bytes = pad_b ? align256(b_rows * b_ld * 2) : 0;
-    const int64_t bytes = a_bytes + b_bytes + pl.workspace;
+    const int64_t a_bytes = pad_a ? pad_size(a_rows, a_cols) : 0, b_bytes = pad_b ? pad_size(b_rows, b_cols) : 0;
+    // The tiles' epilogue addresses rows by 32-bit offsets; others' sums go through the
+    // second launch.
+    const bool far = !wave && std::max({e.ld_in0, e.ld_in1, e.ld_out0, e.ld_out1}) > kMaxTileLd;
+    const int64_t sums = pl.splits > 1 || !far ? pl.workspace : pl.tiles * pl.bm * pl.bn * q.factors * 4;
+    const int64_t bytes = a_bytes + b_bytes + sums;
     void* ws = nullptr;
     int rc = GEMM_OK;
     if (bytes > 0 && (rc = temp_take(tm, bytes, s, &ws)) != GEMM_OK)
@@ -940,7 +1009,7 @@ int linear_run(const LinearShape& q, const void* A, int64_t lda, const void* B, 
         hipLaunchKernelGGL(k_linear_pad, dim3(flat_grid(a_bytes / 16 + b_bytes / 16)), dim3(256), 0, s, c);
         rc = launched();
     }
-    if (pl.splits > 1)
+    if (sums > 0)
         p.partial = (float*)((char*)ws + a_bytes + b_bytes);
     // A single row's stride is never used, but enters sizes and offsets.
     if (a_rows <= 1)
@@ -951,13 +1020,13 @@ int linear_run(const LinearShape& q, const void* A, int64_t lda, const void* B, 
                    ((b_rows / q.factors - 1) * p.ldb + b_ld) * 2 < (int64_t)kMaxRecords;
     if (rc == GEMM_OK) {
         if (wave)
-            rc = launch_wave<MODE>(p, pl, a_ok && b_ok, s);
+            rc = launch_wave<MODE>(p, pl, q.a_even && q.b_even, s);
         else if (pl.kind == TILES_BIG)
             rc = launch_linear<LinearCfg<BT, AT, PAIR, true>, MODE>(p, pl.grid, s);
         else if (pl.kind == TILES_SMALL)
             rc = launch_linear<LinearCfg<BT, AT, PAIR, false>, MODE>(p, pl.grid, s);
     }
-    if (rc == GEMM_OK && pl.splits > 1)
+    if (rc == GEMM_OK && sums > 0)
         rc = finish();
     const int frc = temp_give(tm, ws, s);
     return rc != GEMM_OK ? rc : frc;
@@ -1041,6 +1110,42 @@ int column_sums(const void* X, int64_t rows, int64_t cols, int64_t ld, float* to
 
 extern "C" {
 
+int gemm_linear_plan_cus(int64_t M, int64_t N, int64_t K, int product, int a_aligned, int b_aligned, int compute_units,
+                         gemm_linear_plan_t* out)
+{
+    if (const int rc = linear_sizes(M, N, K))
+        return rc;
+    if (!out || compute_units < 1 || product < GEMM_LINEAR || product > GEMM_GATED_LINEAR_BWD_INPUT)
+        return GEMM_ERR_INVALID_VALUE;
+    LinearShape q{M, N, K, true, false, 1, false, false};
+    if (product == GEMM_LINEAR_BWD_INPUT)
+        q = {M, K, N, false, false, 1, false, false};
+    else if (product == GEMM_LINEAR_BWD_WEIGHT)
+        q = {N, K, M, false, true, 1, false, false};
+    else if (product == GEMM_GATED_LINEAR)
+        q.factors = 2;
+    else if (product == GEMM_GATED_LINEAR_BWD_INPUT)
+        q = {M, N, K, false, false, 1, false, false};
+    q.a_even = a_aligned && q.a_cols() % kChunk == 0;
+    q.b_even = b_aligned && q.b_cols() % kChunk == 0;
+    memset(out, 0, sizeof *out);
+    if (q.M == 0 || q.N == 0 || q.K == 0)
+        return GEMM_OK;
+    const LinearPlan pl = linear_plan(q, compute_units);
+    out->rows = pl.bm;
+    out->cols = pl.bn;
+    out->waves_share_k = pl.kind == TILES_WAVE;
+    out->threads = 512;
+    out->tiles = pl.tiles;
+    out->k_splits = pl.splits;
+    out->k_chunk = pl.chunk;
+    out->grid = pl.kind == TILES_WAVE ? pl.grid * pl.splits : pl.grid;
+    out->workspace_bytes = pl.workspace;
+    if (pl.kind != TILES_WAVE)
+        out->pad_bytes = (q.a_even ? 0 : pad_size(q.a_rows(), q.a_cols())) + (q.b_even ? 0 : pad_size(q.b_rows(), q.b_cols()));
+    return GEMM_OK;
+}
+
 int gemm_linear(int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, const void* W, int64_t ldw,
                 const void* bias, int act, const void* residual, int64_t ldr, void* Z, int64_t ldz, void* Y, int64_t ldy,
                 void* stream)
@@ -1060,7 +1165,7 @@ int gemm_linear(int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, con
         return rc;
     const Epilogue e{(const uint16_t*)bias, (const uint16_t*)residual, nullptr, Y, (uint16_t*)Z, ldr, 0, ldy, ldz,
                      M, N, act, 0};
-    return linear_enqueue<FUSE_LINEAR>({M, N, K, true, false, 1}, X, ldx, W, ldw, e, stream);
+    return linear_enqueue<FUSE_LINEAR>({M, N, K, true, false, 1, false, false}, X, ldx, W, ldw, e, stream);
 }
 
 int gemm_linear_bwd_input(int64_t M, int64_t N, int64_t K, const void* dY, int64_t lddy, const void* W, int64_t ldw,
@@ -1083,7 +1188,7 @@ int gemm_linear_bwd_input(int64_t M, int64_t N, int64_t K, const void* dY, int64
     if (const int rc = check_linear(ins, 4, outs, 1))
         return rc;
     const Epilogue e{nullptr, (const uint16_t*)Z, (const uint16_t*)dres, dX, nullptr, ldz, lddr, lddx, 0, M, K, act, 0};
-    return linear_enqueue<FUSE_DX>({M, K, N, false, false, 1}, dY, lddy, W, ldw, e, stream);
+    return linear_enqueue<FUSE_DX>({M, K, N, false, false, 1, false, false}, dY, lddy, W, ldw, e, stream);
 }
 
 int gemm_linear_bwd_weight(int64_t M, int64_t N, int64_t K, const void* dY, int64_t lddy, const void* X, int64_t ldx,
@@ -1113,7 +1218,7 @@ int gemm_linear_bwd_weight(int64_t M, int64_t N, int64_t K, const void* dY, int6
     if (!weight)
         return GEMM_OK;
     const Epilogue e{nullptr, nullptr, nullptr, dW, nullptr, 0, 0, lddw, 0, N, K, GEMM_ACT_NONE, fp32 ? 1 : 0};
-    return linear_run<FUSE_DW>({N, K, M, false, true, 1}, dY, lddy, X, ldx, e, tm, cus, (hipStream_t)stream);
+    return linear_run<FUSE_DW>({N, K, M, false, true, 1, false, false}, dY, lddy, X, ldx, e, tm, cus, (hipStream_t)stream);
 }
 
 int gemm_gated_linear(int64_t M, int64_t F, int64_t K, const void* X, int64_t ldx, const void* W, int64_t ldw,
@@ -1132,7 +1237,7 @@ int gemm_gated_linear(int64_t M, int64_t F, int64_t K, const void* X, int64_t ld
     if (const int rc = check_linear(ins, 3, outs, 2))
         return rc;
     const Epilogue e{(const uint16_t*)bias, nullptr, nullptr, Y, (uint16_t*)GU, 0, 0, ldy, ldgu, M, F, act, 0};
-    return linear_enqueue<FUSE_GATED>({M, F, K, true, false, 2}, X, ldx, W, ldw, e, stream);
+    return linear_enqueue<FUSE_GATED>({M, F, K, true, false, 2, false, false}, X, ldx, W, ldw, e, stream);
 }
 
 int gemm_gated_linear_bwd_input(int64_t M, int64_t F, int64_t N, const void* dY, int64_t lddy, const void* W, int64_t ldw,
@@ -1152,7 +1257,7 @@ int gemm_gated_linear_bwd_input(int64_t M, int64_t F, int64_t N, const void* dY,
     if (const int rc = check_linear(ins, 3, outs, 2))
         return rc;
     const Epilogue e{nullptr, (const uint16_t*)GU, nullptr, dGU, (uint16_t*)Y, ldgu, 0, lddgu, ldy, M, F, act, 0};
-    return linear_enqueue<FUSE_DGATED>({M, F, N, false, false, 1}, dY, lddy, W, ldw, e, stream);
+    return linear_enqueue<FUSE_DGATED>({M, F, N, false, false, 1, false, false}, dY, lddy, W, ldw, e, stream);
 }
 
 }  // extern "C"
