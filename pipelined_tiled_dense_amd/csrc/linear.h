@@ -439,29 +439,85 @@ struct LinearParams : Params {
     }
 };
 
-// The epilogue over the sums of k chunks, added in chunk order (with no chunk, K ==
-// 0: over zeros), for the launch's span of tiles of bm x bn outputs.
-template <int MODE>
-__global__ void __launch_bounds__(256) k_linear_finish(LinearParams<MODE> p, int32_t bm, int32_t bn)
+// Sums of columns in parts: part[r * cols + c], r = 0 .. runs - 1, added in order.
+struct ColumnSums {
+    const float* part;
+    float* to;
+    int64_t cols;
+    int32_t runs;
+    unsigned blocks;   // of 16 columns, that add them
+};
+
+__device__ __forceinline__ void join_column_sums(const ColumnSums& p, unsigned block)
 {
+    __shared__ float sums[16][16];
+    const int cl = threadIdx.x & 15, rl = threadIdx.x >> 4;
+    const int64_t c = (int64_t)block * 16 + cl;
+    float t = 0.0f;
+    if (c < p.cols) {
+#pragma unroll 4
+        for (int32_t r = rl; r < p.runs; r += 16)
+            t += p.part[r * p.cols + c];
+    }
+    sums[rl][cl] = t;
+    __syncthreads();
+    if (rl == 0 && c < p.cols) {
+        t = 0.0f;
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+            t += sums[r][cl];
+        p.to[c] = t;
+    }
+}
+
+__global__ void __launch_bounds__(256) k_join_column_sums(ColumnSums p) { join_column_sums(p, blockIdx.x); }
+
+// The epilogue over the sums of k chunks, added in chunk order (with no chunk, K ==
+// 0: over zeros), for the launch's span of tiles of bm x bn outputs.  A thread takes 8
+// columns, of fp32 results 4, so that its stores are next to its neighbours'.  The
+// first blocks add the column sums of a weight's gradient, where there are any.
+template <int MODE>
+__global__ void __launch_bounds__(256) k_linear_finish(LinearParams<MODE> p, int32_t bm, int32_t bn, ColumnSums sums)
+{
+    if (blockIdx.x < sums.blocks) {
+        join_column_sums(sums, blockIdx.x);
+        return;
+    }
     constexpr int FACTORS = fuse_paired(MODE) ? 2 : 1;
-    const int32_t per_row = bn / kChunk, units = bm * per_row;
+    const bool fp32 = MODE == FUSE_DW && p.e.fp32;
+    const int32_t width = fp32 ? 4 : kChunk, per_row = bn / width, units = bm * per_row;
     const int64_t total = (int64_t)p.span * units, piece = (int64_t)bm * bn * FACTORS;
-    for (int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x; q < total; q += (int64_t)gridDim.x * 256) {
+    for (int64_t q = (int64_t)(blockIdx.x - sums.blocks) * 256 + threadIdx.x; q < total;
+         q += (int64_t)(gridDim.x - sums.blocks) * 256) {
         const int32_t u = (int32_t)(q / units), at = (int32_t)(q - (int64_t)u * units), r = at / per_row;
-        const int32_t cc = (at - r * per_row) * kChunk;
+        const int32_t cc = (at - r * per_row) * width;
         int32_t tm, tn;
         raster_tile(p, p.tile_base + u, tm, tn);
-        const int64_t c = (int64_t)tn * bn + cc;
-        const int64_t row = (int64_t)tm * bm + r;
-        const ChunkAt here{row, c, row < p.e.M ? left(p.e.N, c) : 0};
-        if (!here.any())
+        const int64_t c = (int64_t)tn * bn + cc, row = (int64_t)tm * bm + r;
+        if (row >= p.e.M || c >= p.e.N)
             continue;
+        const float* first = p.partial + u * piece + (int64_t)r * bn + cc;
+        if (fp32) {
+            f32x4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+            for (int32_t sp = 0; sp < p.splits; ++sp)
+                v += *(const f32x4_t*)(first + sp * (int64_t)p.span * piece);
+            float* to = (float*)p.e.out0 + row * p.e.ld_out0 + c;
+            if (p.e.N - c >= 4)
+                __builtin_nontemporal_store(v, (f32x4_any_t*)to);
+            else
+#pragma unroll
+                for (int i = 0; i < 3; ++i)
+                    if (i < p.e.N - c)
+                        to[i] = v[i];
+            continue;
+        }
+        const ChunkAt here{row, c, left(p.e.N, c)};
         const EpilogueIn in = epilogue_load<MODE>(p.e, here);
         float v[2][kChunk] = {};
 #pragma unroll 4
         for (int32_t sp = 0; sp < p.splits; ++sp) {
-            const float* src = p.partial + (sp * (int64_t)p.span + u) * piece + (int64_t)r * bn + cc;
+            const float* src = first + sp * (int64_t)p.span * piece;
 #pragma unroll
             for (int h = 0; h < FACTORS; ++h) {
                 float x[kChunk];
@@ -710,53 +766,37 @@ __global__ void __launch_bounds__(kWaves * 64) k_linear_wave(LinearParams<MODE> 
 }
 
 // ---------------------------------------------------------------------------
-// Column sums of bf16 X (rows x cols) in fp32: dbias.  A workgroup sums 256 columns
-// of a run of rows, 8 rows at a time; a second launch adds the runs in order.
+// Column sums of bf16 X (rows x cols) in fp32: dbias.  A workgroup sums 64 columns of a
+// run of rows, `threads` / 8 rows at a time; runs are added in order (ColumnSums).
+// Up to kOneRun rows a workgroup of 1024 takes them all: the second launch would take
+// longer.
 // ---------------------------------------------------------------------------
-__global__ void __launch_bounds__(256) k_column_sums(const uint16_t* x, int64_t rows, int64_t cols, int64_t ld,
-                                                     int64_t run, float* to)
+constexpr int64_t kOneRun = 512;
+
+__global__ void __launch_bounds__(1024) k_column_sums(const uint16_t* x, int64_t rows, int64_t cols, int64_t ld,
+                                                      int64_t run, float* to)
 {
-    __shared__ float sums[8][32][kChunk];
-    const int cl = threadIdx.x & 31, rl = threadIdx.x >> 5;
-    const int64_t c = ((int64_t)blockIdx.x * 32 + cl) * kChunk;
+    __shared__ float sums[128][65];
+    const int cl = threadIdx.x & 7, rl = threadIdx.x >> 3, step = blockDim.x >> 3;
+    const int64_t c = ((int64_t)blockIdx.x * 8 + cl) * kChunk;
     const int n = left(cols, c);
     const int64_t first = (int64_t)blockIdx.y * run, end = min(first + run, rows);
     float s[kChunk] = {};
-    for (int64_t r = first + rl; r < end; r += 8)
+#pragma unroll 4
+    for (int64_t r = first + rl; r < end; r += step)
         add_chunk(s, load_chunk<false>(x + r * ld + c, n, c));
 #pragma unroll
     for (int i = 0; i < kChunk; ++i)
-        sums[rl][cl][i] = s[i];
+        sums[rl][cl * kChunk + i] = s[i];
     __syncthreads();
-    const int col = threadIdx.x;
-    float t = 0.0f;
-#pragma unroll
-    for (int r = 0; r < 8; ++r)
-        t += sums[r][col / kChunk][col % kChunk];
-    if ((int64_t)blockIdx.x * 256 + col < cols)
-        to[blockIdx.y * cols + (int64_t)blockIdx.x * 256 + col] = t;
-}
-
-__global__ void __launch_bounds__(256) k_column_sums_join(const float* part, int64_t cols, int32_t runs, float* to)
-{
-    __shared__ float sums[16][16];
-    const int cl = threadIdx.x & 15, rl = threadIdx.x >> 4;
-    const int64_t c = (int64_t)blockIdx.x * 16 + cl;
-    float t = 0.0f;
-    if (c < cols) {
-#pragma unroll 4
-        for (int32_t r = rl; r < runs; r += 16)
-            t += part[r * cols + c];
+    // Halves of the rows' sums, added until one is left.
+    for (int half = step / 2; half >= 1; half /= 2) {
+        for (int at = threadIdx.x; at < half * 64; at += blockDim.x)
+            sums[at >> 6][at & 63] += sums[(at >> 6) + half][at & 63];
+        __syncthreads();
     }
-    sums[rl][cl] = t;
-    __syncthreads();
-    if (rl == 0 && c < cols) {
-        t = 0.0f;
-#pragma unroll
-        for (int r = 0; r < 16; ++r)
-            t += sums[r][cl];
-        to[c] = t;
-    }
+    if (threadIdx.x < 64 && (int64_t)blockIdx.x * 64 + threadIdx.x < cols)
+        to[blockIdx.y * cols + (int64_t)blockIdx.x * 64 + threadIdx.x] = sums[0][threadIdx.x];
 }
 
 // Zero-padded copies of the operands whose rows do not start on 16-byte boundaries
@@ -828,9 +868,10 @@ double linear_time(const LinearShape& q, const LinearPlan& pl, int cus)
         return (pl.mf == 4 ? 1.4 : 3.2) + t + (pl.splits > 1 ? 6.0 + 0.5 * sums : 0.0);
     }
     const double padding = copies > 0 ? 2.5 + copies / 2.2 : 0.0, rounds = std::ceil(fill);
+    // The weight's gradient reads both operands transposed.
     if (pl.kind == TILES_SMALL)
-        return 3.0 + rounds * (4.3 + 0.43 * steps) + (pl.splits > 1 ? 5.3 + 0.2 * sums : 0.0) + padding;
-    return 1.5 + rounds * (9.0 + 1.1 * steps) + (pl.splits > 1 ? 5.0 + 0.17 * sums : 0.0) + padding;
+        return 3.0 + rounds * (4.3 + (q.at ? 0.47 : 0.43) * steps) + (pl.splits > 1 ? 5.3 + 0.2 * sums : 0.0) + padding;
+    return 1.5 + rounds * (9.0 + (q.at ? 1.35 : 1.1) * steps) + (pl.splits > 1 ? 5.0 + 0.17 * sums : 0.0) + padding;
 }
 
 // The kind, tile and chunks of k (whole 64-wide k-steps, all of them with work) that are
@@ -934,7 +975,7 @@ int launch_wave(const LinearParams<MODE>& p, const LinearPlan& pl, bool even, hi
 // the device.
 template <int MODE>
 int linear_run(LinearShape q, const void* A, int64_t lda, const void* B, int64_t ldb, const Epilogue& e,
-               TempMem& tm, int cus, hipStream_t s)
+               TempMem& tm, int cus, hipStream_t s, float* dbias = nullptr)
 {
     constexpr bool PAIR = fuse_paired(MODE), BT = MODE == FUSE_LINEAR || PAIR, AT = MODE == FUSE_DW;
     LinearParams<MODE> p;
@@ -948,7 +989,7 @@ int linear_run(LinearShape q, const void* A, int64_t lda, const void* B, int64_t
     };
     q.a_even = fits(A, a_rows, a_cols, lda);
     q.b_even = fits(B, b_rows, b_cols, ldb);
-    const LinearPlan pl = q.K > 0 ? linear_plan(q, cus) : LinearPlan{TILES_SMALL, 0, 0, 128, 128 / q.factors, 0, 0, 0, 0, 0};
+    const LinearPlan pl = q.K > 0 && q.N > 0 ? linear_plan(q, cus) : LinearPlan{TILES_SMALL, 0, 0, 128, 128 / q.factors, 0, 0, 0, 0, 0};
     p.A = (const char*)A;
     p.B = (const char*)B;
     p.M = q.M;
@@ -970,13 +1011,47 @@ int linear_run(LinearShape q, const void* A, int64_t lda, const void* B, int64_t
     p.group_m = pl.kind == TILES_WAVE ? p.tiles_m : 4;
     p.spin_limit = kSpinLimit;
     p.clock_on = g_clock_on.load(std::memory_order_relaxed) ? 1u : 0u;
+    // dbias: sums of A's columns, in runs of rows where there are many.
+    ColumnSums sums{};
+    int64_t run = a_rows;
+    if (dbias) {
+        const int64_t groups = ceil_div(a_cols, 64);
+        if (a_rows > kOneRun)
+            run = ceil_div(a_rows, std::max<int64_t>(1, std::min(4 * (int64_t)cus / groups, a_rows / 128)));
+        sums = {nullptr, dbias, a_cols, (int32_t)ceil_div(std::max<int64_t>(a_rows, 1), std::max<int64_t>(run, 1)), 0};
+    }
+    const int64_t runs_bytes = sums.runs > 1 ? align256(sums.runs * a_cols * 4) : 0;
     auto finish = [&]() {
-        const int64_t units = (int64_t)p.span * pl.bm * pl.bn / kChunk;
-        hipLaunchKernelGGL(k_linear_finish<MODE>, dim3(flat_grid(units)), dim3(256), 0, s, p, pl.bm, pl.bn);
+        const int64_t units = (int64_t)p.span * pl.bm * pl.bn / (MODE == FUSE_DW && e.fp32 ? 4 : kChunk);
+        hipLaunchKernelGGL(k_linear_finish<MODE>, dim3(flat_grid(units) + sums.blocks), dim3(256), 0, s, p, pl.bm, pl.bn,
+                           sums);
         return launched();
     };
-    if (q.K == 0)
-        return finish();
+    auto start_sums = [&](float* part) {
+        const bool one = sums.runs <= 1;
+        const unsigned threads = one ? 1024 : 256;
+        hipLaunchKernelGGL(k_column_sums, dim3((unsigned)ceil_div(a_cols, 64), (unsigned)sums.runs), dim3(threads), 0, s,
+                           (const uint16_t*)A, a_rows, a_cols, lda, run, one ? dbias : part);
+        sums.part = part;
+        sums.blocks = one ? 0u : (unsigned)ceil_div(a_cols, 16);
+        return launched();
+    };
+    auto join_sums = [&]() {
+        if (sums.blocks == 0)
+            return (int)GEMM_OK;
+        hipLaunchKernelGGL(k_join_column_sums, dim3(sums.blocks), dim3(256), 0, s, sums);
+        return launched();
+    };
+    if (q.K == 0 || q.N == 0) {   // nothing to multiply
+        void* ws = nullptr;
+        int rc = runs_bytes > 0 ? temp_take(tm, runs_bytes, s, &ws) : (int)GEMM_OK;
+        if (rc == GEMM_OK && dbias && (rc = start_sums((float*)ws)) == GEMM_OK)
+            rc = join_sums();
+        if (rc == GEMM_OK && q.N > 0)
+            rc = finish();
+        const int frc = temp_give(tm, ws, s);
+        return rc != GEMM_OK ? rc : frc;
+    }
 
     const bool wave = pl.kind == TILES_WAVE;
     const bool pad_a = !wave && !q.a_even, pad_b = !wave && !q.b_even;
@@ -985,13 +1060,15 @@ int linear_run(LinearShape q, const void* A, int64_t lda, const void* B, int64_t
     // The tiles' epilogue addresses rows by 32-bit offsets; others' sums go through the
     // second launch.
     const bool far = !wave && std::max({e.ld_in0, e.ld_in1, e.ld_out0, e.ld_out1}) > kMaxTileLd;
-    const int64_t sums = pl.splits > 1 || !far ? pl.workspace : pl.tiles * pl.bm * pl.bn * q.factors * 4;
-    const int64_t bytes = a_bytes + b_bytes + sums;
+    const int64_t sums_bytes = pl.splits > 1 || !far ? pl.workspace : pl.tiles * pl.bm * pl.bn * q.factors * 4;
+    const int64_t bytes = a_bytes + b_bytes + runs_bytes + sums_bytes;
     void* ws = nullptr;
     int rc = GEMM_OK;
     if (bytes > 0 && (rc = temp_take(tm, bytes, s, &ws)) != GEMM_OK)
         return rc;
-    if (pad_a || pad_b) {
+    if (dbias)
+        rc = start_sums((float*)((char*)ws + a_bytes + b_bytes));
+    if (rc == GEMM_OK && (pad_a || pad_b)) {
         LinearPad c{{(const uint16_t*)A, (const uint16_t*)B},
                     {(uint16_t*)ws, (uint16_t*)((char*)ws + a_bytes)},
                     {pad_a ? a_rows : 0, pad_b ? b_rows : 0},
@@ -1009,8 +1086,8 @@ int linear_run(LinearShape q, const void* A, int64_t lda, const void* B, int64_t
         hipLaunchKernelGGL(k_linear_pad, dim3(flat_grid(a_bytes / 16 + b_bytes / 16)), dim3(256), 0, s, c);
         rc = launched();
     }
-    if (sums > 0)
-        p.partial = (float*)((char*)ws + a_bytes + b_bytes);
+    if (sums_bytes > 0)
+        p.partial = (float*)((char*)ws + a_bytes + b_bytes + runs_bytes);
     // A single row's stride is never used, but enters sizes and offsets.
     if (a_rows <= 1)
         p.lda = a_ld;
@@ -1026,8 +1103,8 @@ int linear_run(LinearShape q, const void* A, int64_t lda, const void* B, int64_t
         else if (pl.kind == TILES_SMALL)
             rc = launch_linear<LinearCfg<BT, AT, PAIR, false>, MODE>(p, pl.grid, s);
     }
-    if (rc == GEMM_OK && sums > 0)
-        rc = finish();
+    if (rc == GEMM_OK)
+        rc = sums_bytes > 0 ? finish() : join_sums();
     const int frc = temp_give(tm, ws, s);
     return rc != GEMM_OK ? rc : frc;
 }
@@ -1074,36 +1151,13 @@ int check_linear(const LinearOperand* ins, int n_ins, const LinearOperand* outs,
 // The device, then the product.
 template <int MODE>
 int linear_enqueue(const LinearShape& q, const void* A, int64_t lda, const void* B, int64_t ldb, const Epilogue& e,
-                   void* stream)
+                   void* stream, float* dbias = nullptr)
 {
     int cus = 0;
     TempMem tm;
     if (const int rc = device_info(&cus, &tm.pool, nullptr, &tm.info))
         return rc;
-    return linear_run<MODE>(q, A, lda, B, ldb, e, tm, cus, (hipStream_t)stream);
-}
-
-// dbias: the column sums of dY.
-int column_sums(const void* X, int64_t rows, int64_t cols, int64_t ld, float* to, TempMem& tm, int cus, hipStream_t s)
-{
-    const int64_t groups = ceil_div(cols, 256);
-    int64_t runs = std::max<int64_t>(1, std::min(4 * (int64_t)cus / groups, rows / 64));
-    const int64_t run = ceil_div(rows, runs);
-    runs = rows > 0 ? ceil_div(rows, run) : 1;
-    void* ws = nullptr;
-    int rc = GEMM_OK;
-    if (runs > 1 && (rc = temp_take(tm, runs * cols * 4, s, &ws)) != GEMM_OK)
-        return rc;
-    hipLaunchKernelGGL(k_column_sums, dim3((unsigned)groups, (unsigned)runs), dim3(256), 0, s, (const uint16_t*)X, rows,
-                       cols, ld, run, runs > 1 ? (float*)ws : to);
-    rc = launched();
-    if (rc == GEMM_OK && runs > 1) {
-        hipLaunchKernelGGL(k_column_sums_join, dim3((unsigned)ceil_div(cols, 16)), dim3(256), 0, s, (const float*)ws, cols,
-                           (int32_t)runs, to);
-        rc = launched();
-    }
-    const int frc = temp_give(tm, ws, s);
-    return rc != GEMM_OK ? rc : frc;
+    return linear_run<MODE>(q, A, lda, B, ldb, e, tm, cus, (hipStream_t)stream, dbias);
 }
 
 }  // namespace
@@ -1208,17 +1262,9 @@ int gemm_linear_bwd_weight(int64_t M, int64_t N, int64_t K, const void* dY, int6
                                   {{dbias, 1, N, N, 4}, false, nullptr}};
     if (const int rc = check_linear(ins, 2, outs, 2))
         return rc;
-    int cus = 0;
-    TempMem tm;
-    if (const int rc = device_info(&cus, &tm.pool, nullptr, &tm.info))
-        return rc;
-    if (bias)
-        if (const int rc = column_sums(dY, M, N, lddy, dbias, tm, cus, (hipStream_t)stream))
-            return rc;
-    if (!weight)
-        return GEMM_OK;
     const Epilogue e{nullptr, nullptr, nullptr, dW, nullptr, 0, 0, lddw, 0, N, K, GEMM_ACT_NONE, fp32 ? 1 : 0};
-    return linear_run<FUSE_DW>({N, K, M, false, true, 1, false, false}, dY, lddy, X, ldx, e, tm, cus, (hipStream_t)stream);
+    return linear_enqueue<FUSE_DW>({N, K, M, false, true, 1, false, false}, dY, lddy, X, ldx, e, stream,
+                                   bias ? dbias : nullptr);
 }
 
 int gemm_gated_linear(int64_t M, int64_t F, int64_t K, const void* X, int64_t ldx, const void* W, int64_t ldw,
