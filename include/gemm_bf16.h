@@ -127,8 +127,9 @@ enum {
     GEMM_ERR_DEVICE = -6,            /* no HIP device, or the current device is not gfx950 */
     GEMM_ERR_LAUNCH = -7,            /* the kernel launch was rejected by the runtime */
     GEMM_ERR_ALIAS = -8,             /* C overlaps A or B */
-    GEMM_ERR_SCRATCH = -9            /* gemm_bf16_noalloc only: the call needs more temporary
-                                        memory than its scratch region holds */
+    GEMM_ERR_SCRATCH = -9            /* gemm_bf16_noalloc: the call needs more temporary memory than
+                                        its scratch region holds; linear layers: more than the
+                                        caller's workspace, or some under capture without one */
 };
 
 /* Size of gemm_bf16_noalloc's per-device scratch region, in bytes. */
@@ -576,9 +577,14 @@ int gemm_swiglu_bwd(int64_t M, int64_t F, const void* dY, int64_t lddy,
  * boundaries and are at most 2^22 elements apart; they copy any other, zero-padded,
  * into temporary memory first (but not where M <= 64 and both operands are read
  * along their rows).  Few output tiles and a long sum are split into chunks along
- * it, whose fp32 sums a second launch adds in a fixed order.  Temporary memory is
- * gemm_bf16's (kept blocks, see there).  Results are deterministic for given sizes,
- * strides and alignment.
+ * it, whose fp32 sums a second launch adds in a fixed order.  Results are
+ * deterministic for given sizes, strides and alignment.
+ *
+ * Temporary memory: `workspace` (device memory, 256-byte aligned, apart from the
+ * operands) of workspace_bytes, at least gemm_linear_plan_cus's scratch_bytes, which the
+ * call's work uses until it is done; or NULL for gemm_bf16's (kept blocks, see there).
+ * Under graph capture a call that needs any has to be given it.  A workspace that is too
+ * small, and none under capture, is GEMM_ERR_SCRATCH, and nothing is enqueued.
  *
  * Activations and their slopes follow these formulas for every z, up to the rounding
  * of fp32; an infinity or a NaN gives what the formula gives.
@@ -603,7 +609,7 @@ enum {
  */
 int gemm_linear(int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, const void* W, int64_t ldw,
                 const void* bias, int act, const void* residual, int64_t ldr, void* Z, int64_t ldz,
-                void* Y, int64_t ldy, void* stream);
+                void* Y, int64_t ldy, void* workspace, int64_t workspace_bytes, void* stream);
 
 /*
  * gemm_linear_bwd_input: the gradient of a layer's input X (M x K) from that of its
@@ -617,7 +623,7 @@ int gemm_linear(int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, con
  */
 int gemm_linear_bwd_input(int64_t M, int64_t N, int64_t K, const void* dY, int64_t lddy, const void* W, int64_t ldw,
                           int act, const void* Z, int64_t ldz, const void* dres, int64_t lddr,
-                          void* dX, int64_t lddx, void* stream);
+                          void* dX, int64_t lddx, void* workspace, int64_t workspace_bytes, void* stream);
 
 /*
  * gemm_linear_bwd_weight: the gradients of a layer's weight and bias:
@@ -628,7 +634,8 @@ int gemm_linear_bwd_input(int64_t M, int64_t N, int64_t K, const void* dY, int64
  * values) may be NULL.  Both are overwritten; M == 0 gives zeros.
  */
 int gemm_linear_bwd_weight(int64_t M, int64_t N, int64_t K, const void* dY, int64_t lddy, const void* X, int64_t ldx,
-                           void* dW, int64_t lddw, int dw_type, float* dbias, void* stream);
+                           void* dW, int64_t lddw, int dw_type, float* dbias,
+                           void* workspace, int64_t workspace_bytes, void* stream);
 
 /*
  * gemm_gated_linear: both projections of a gated unit, the activation and their
@@ -642,7 +649,8 @@ int gemm_linear_bwd_weight(int64_t M, int64_t N, int64_t K, const void* dY, int6
  * M == 0 or F == 0 is a no-op.
  */
 int gemm_gated_linear(int64_t M, int64_t F, int64_t K, const void* X, int64_t ldx, const void* W, int64_t ldw,
-                      const void* bias, int act, void* GU, int64_t ldgu, void* Y, int64_t ldy, void* stream);
+                      const void* bias, int act, void* GU, int64_t ldgu, void* Y, int64_t ldy,
+                      void* workspace, int64_t workspace_bytes, void* stream);
 
 /*
  * gemm_gated_linear_bwd_input: the gradients of g and u, side by side in dGU (M x
@@ -657,7 +665,7 @@ int gemm_gated_linear(int64_t M, int64_t F, int64_t K, const void* X, int64_t ld
  */
 int gemm_gated_linear_bwd_input(int64_t M, int64_t F, int64_t N, const void* dY, int64_t lddy, const void* W, int64_t ldw,
                                 int act, const void* GU, int64_t ldgu, void* dGU, int64_t lddgu,
-                                void* Y, int64_t ldy, void* stream);
+                                void* Y, int64_t ldy, void* workspace, int64_t workspace_bytes, void* stream);
 
 /* How one of the products above is computed (see gemm_linear_plan_cus). */
 typedef struct gemm_linear_plan {
@@ -670,6 +678,8 @@ typedef struct gemm_linear_plan {
     int64_t grid;             /* workgroups of the main launch */
     int64_t workspace_bytes;  /* the chunks' sums (0 with one chunk) */
     int64_t pad_bytes;        /* zero-padded copies of operands that the tiles cannot read */
+    int64_t scratch_bytes;    /* temporary memory in all: the two, and dbias's sums of a weight's gradient.  Outputs
+                                 or what an epilogue reads more than 2^27 elements apart may take more. */
 } gemm_linear_plan_t;
 
 /* The products a plan is asked for, with the sizes of their entry points (F as N for the gated ones). */
@@ -686,7 +696,7 @@ enum {
  * `compute_units` compute units (256 on an MI355X), without querying one.  a_aligned,
  * b_aligned: whether the rows of its two matrix operands (X and W, dY and W, dY and X)
  * start on 16-byte boundaries.  A null `out`, compute_units < 1 or an unknown product is
- * GEMM_ERR_INVALID_VALUE.  With an empty product every field is 0.
+ * GEMM_ERR_INVALID_VALUE.  With an empty product every field but scratch_bytes is 0.
  */
 int gemm_linear_plan_cus(int64_t M, int64_t N, int64_t K, int product, int a_aligned, int b_aligned, int compute_units,
                          gemm_linear_plan_t* out);

@@ -11,20 +11,27 @@
 
 namespace {
 
-// a(z) and a'(z) as value * f^3 and slope * f^3.  f is 1, except where the two are
-// too small for fp32: then it is the third root of what they hold of an
-// exponential, a normal number, and each factor beside the activation takes an f
-// first, so that a large one meets a small one before anything overflows or is lost.
+// x times y times a slope of at most 1.13: the slope goes with the larger of the two
+// first, so that neither a product overflows nor a small one is lost before the third
+// factor brings it back.
+__device__ __forceinline__ float times_slope(float x, float y, float slope)
+{
+    const bool x_larger = __builtin_fabsf(x) > __builtin_fabsf(y);
+    return (x_larger ? x : y) * slope * (x_larger ? y : x);
+}
+
+// a(z) and a'(z) as value * f^3 and slope * f^3, where the two are too small for fp32: f is
+// the third root of what they hold of an exponential, a normal number, and each factor
+// beside the activation takes an f first.
 struct Activated {
     float f, value, slope;
 
     __device__ __forceinline__ float times(float x) const { return (x * f) * (value * f) * f; }
     __device__ __forceinline__ float slope_times(float x) const { return (x * f) * (slope * f) * f; }
-    // x y alone may overflow beside a small slope, y times a slope be lost beside a large x.
     __device__ __forceinline__ float slope_times(float x, float y) const
     {
-        const float xf = x * f, yf = y * f, sf = slope * f;
-        return f > 0.01f ? xf * (yf * sf) : xf * yf * sf;
+        const bool x_larger = __builtin_fabsf(x) > __builtin_fabsf(y);
+        return ((x_larger ? x : y) * f) * (slope * f) * (x_larger ? y : x) * f;
     }
 };
 
@@ -93,7 +100,7 @@ __device__ __forceinline__ void activate(int act, const float (&z)[kChunk], F&& 
         float value, slope;
         __device__ __forceinline__ float times(float x) const { return x * value; }
         __device__ __forceinline__ float slope_times(float x) const { return x * slope; }
-        __device__ __forceinline__ float slope_times(float x, float y) const { return x * (y * slope); }
+        __device__ __forceinline__ float slope_times(float x, float y) const { return times_slope(x, y, slope); }
     };
     Usual u;
     if (act <= GEMM_ACT_RELU) {   // NaN stays

@@ -834,6 +834,14 @@ struct LinearShape {
     int64_t b_cols() const { return bt ? K : N; }
 };
 
+// Rows that a workgroup sums the columns of (see k_column_sums).
+int64_t column_run(int64_t rows, int64_t cols, int cus)
+{
+    if (rows <= kOneRun)
+        return rows;
+    return ceil_div(rows, std::max<int64_t>(1, std::min(4 * (int64_t)cus / ceil_div(cols, 64), rows / 128)));
+}
+
 int64_t pad_size(int64_t rows, int64_t cols) { return align256(rows * round8(cols) * 2); }
 
 enum { TILES_BIG, TILES_SMALL, TILES_WAVE };
@@ -971,6 +979,23 @@ int launch_wave(const LinearParams<MODE>& p, const LinearPlan& pl, bool even, hi
     return launched();
 }
 
+// Temporary memory of `bytes` for one call.  Not from the library's pool under graph
+// capture: a graph with memory of its own ended in an illegal access on replay, and its
+// cause is not known, so such a call is refused.
+int linear_take(TempMem& tm, int64_t bytes, hipStream_t s, void** p)
+{
+    if (!tm.fixed) {
+        hipStreamCaptureStatus cs = hipStreamCaptureStatusNone;
+        if (hipStreamIsCapturing(s, &cs) != hipSuccess) {
+            (void)hipGetLastError();
+            return GEMM_ERR_DEVICE;
+        }
+        if (cs != hipStreamCaptureStatusNone)
+            return GEMM_ERR_SCRATCH;
+    }
+    return temp_take(tm, bytes, s, p);
+}
+
 // The product of A and B into epilogue e.  The caller has checked everything but
 // the device.
 template <int MODE>
@@ -1015,9 +1040,7 @@ int linear_run(LinearShape q, const void* A, int64_t lda, const void* B, int64_t
     ColumnSums sums{};
     int64_t run = a_rows;
     if (dbias) {
-        const int64_t groups = ceil_div(a_cols, 64);
-        if (a_rows > kOneRun)
-            run = ceil_div(a_rows, std::max<int64_t>(1, std::min(4 * (int64_t)cus / groups, a_rows / 128)));
+        run = column_run(a_rows, a_cols, cus);
         sums = {nullptr, dbias, a_cols, (int32_t)ceil_div(std::max<int64_t>(a_rows, 1), std::max<int64_t>(run, 1)), 0};
     }
     const int64_t runs_bytes = sums.runs > 1 ? align256(sums.runs * a_cols * 4) : 0;
@@ -1044,7 +1067,7 @@ int linear_run(LinearShape q, const void* A, int64_t lda, const void* B, int64_t
     };
     if (q.K == 0 || q.N == 0) {   // nothing to multiply
         void* ws = nullptr;
-        int rc = runs_bytes > 0 ? temp_take(tm, runs_bytes, s, &ws) : (int)GEMM_OK;
+        int rc = runs_bytes > 0 ? linear_take(tm, runs_bytes, s, &ws) : (int)GEMM_OK;
         if (rc == GEMM_OK && dbias && (rc = start_sums((float*)ws)) == GEMM_OK)
             rc = join_sums();
         if (rc == GEMM_OK && q.N > 0)
@@ -1064,7 +1087,7 @@ int linear_run(LinearShape q, const void* A, int64_t lda, const void* B, int64_t
     const int64_t bytes = a_bytes + b_bytes + runs_bytes + sums_bytes;
     void* ws = nullptr;
     int rc = GEMM_OK;
-    if (bytes > 0 && (rc = temp_take(tm, bytes, s, &ws)) != GEMM_OK)
+    if (bytes > 0 && (rc = linear_take(tm, bytes, s, &ws)) != GEMM_OK)
         return rc;
     if (dbias)
         rc = start_sums((float*)((char*)ws + a_bytes + b_bytes));
@@ -1148,16 +1171,37 @@ int check_linear(const LinearOperand* ins, int n_ins, const LinearOperand* outs,
     return GEMM_OK;
 }
 
-// The device, then the product.
+// The device, then the product, with the caller's workspace or, without one, memory that
+// the library keeps.
 template <int MODE>
 int linear_enqueue(const LinearShape& q, const void* A, int64_t lda, const void* B, int64_t ldb, const Epilogue& e,
-                   void* stream, float* dbias = nullptr)
+                   void* workspace, int64_t workspace_bytes, void* stream, float* dbias = nullptr)
 {
     int cus = 0;
     TempMem tm;
     if (const int rc = device_info(&cus, &tm.pool, nullptr, &tm.info))
         return rc;
+    if (workspace) {
+        tm.fixed = (char*)workspace;
+        tm.fixed_left = workspace_bytes;
+    }
     return linear_run<MODE>(q, A, lda, B, ldb, e, tm, cus, (hipStream_t)stream, dbias);
+}
+
+int check_workspace(const void* workspace, int64_t bytes, const LinearOperand* ins, int n_ins, const LinearOperand* outs,
+                    int n_outs)
+{
+    if (!workspace)
+        return GEMM_OK;
+    if (bytes < 0)
+        return GEMM_ERR_INVALID_VALUE;
+    if ((uintptr_t)workspace & 255)
+        return GEMM_ERR_MISALIGNED;
+    const Operand w{workspace, 1, bytes, bytes, 1};
+    for (int i = 0; i < n_ins + n_outs; ++i)
+        if (meet(w, (i < n_ins ? ins[i] : outs[i - n_ins]).o))
+            return GEMM_ERR_ALIAS;
+    return GEMM_OK;
 }
 
 }  // namespace
@@ -1183,6 +1227,8 @@ int gemm_linear_plan_cus(int64_t M, int64_t N, int64_t K, int product, int a_ali
     q.a_even = a_aligned && q.a_cols() % kChunk == 0;
     q.b_even = b_aligned && q.b_cols() % kChunk == 0;
     memset(out, 0, sizeof *out);
+    if (product == GEMM_LINEAR_BWD_WEIGHT && N > 0 && M > kOneRun)
+        out->scratch_bytes = align256(ceil_div(M, column_run(M, N, compute_units)) * N * 4);
     if (q.M == 0 || q.N == 0 || q.K == 0)
         return GEMM_OK;
     const LinearPlan pl = linear_plan(q, compute_units);
@@ -1197,12 +1243,13 @@ int gemm_linear_plan_cus(int64_t M, int64_t N, int64_t K, int product, int a_ali
     out->workspace_bytes = pl.workspace;
     if (pl.kind != TILES_WAVE)
         out->pad_bytes = (q.a_even ? 0 : pad_size(q.a_rows(), q.a_cols())) + (q.b_even ? 0 : pad_size(q.b_rows(), q.b_cols()));
+    out->scratch_bytes += align256(pl.workspace) + out->pad_bytes;
     return GEMM_OK;
 }
 
 int gemm_linear(int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, const void* W, int64_t ldw,
                 const void* bias, int act, const void* residual, int64_t ldr, void* Z, int64_t ldz, void* Y, int64_t ldy,
-                void* stream)
+                void* workspace, int64_t workspace_bytes, void* stream)
 {
     if (const int rc = linear_sizes(M, N, K))
         return rc;
@@ -1217,14 +1264,16 @@ int gemm_linear(int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, con
     const LinearOperand outs[] = {{{Y, M, N, ldy, 2}, true, residual}, {{Z, M, N, ldz, 2}, false, nullptr}};
     if (const int rc = check_linear(ins, 4, outs, 2))
         return rc;
+    if (const int rc = check_workspace(workspace, workspace_bytes, ins, 4, outs, 2))
+        return rc;
     const Epilogue e{(const uint16_t*)bias, (const uint16_t*)residual, nullptr, Y, (uint16_t*)Z, ldr, 0, ldy, ldz,
                      M, N, act, 0};
-    return linear_enqueue<FUSE_LINEAR>({M, N, K, true, false, 1, false, false}, X, ldx, W, ldw, e, stream);
+    return linear_enqueue<FUSE_LINEAR>({M, N, K, true, false, 1, false, false}, X, ldx, W, ldw, e, workspace, workspace_bytes, stream);
 }
 
 int gemm_linear_bwd_input(int64_t M, int64_t N, int64_t K, const void* dY, int64_t lddy, const void* W, int64_t ldw,
                           int act, const void* Z, int64_t ldz, const void* dres, int64_t lddr, void* dX, int64_t lddx,
-                          void* stream)
+                          void* workspace, int64_t workspace_bytes, void* stream)
 {
     if (const int rc = linear_sizes(M, N, K))
         return rc;
@@ -1241,12 +1290,15 @@ int gemm_linear_bwd_input(int64_t M, int64_t N, int64_t K, const void* dY, int64
     const LinearOperand outs[] = {{{dX, M, K, lddx, 2}, true, dX == Z ? Z : dres}};
     if (const int rc = check_linear(ins, 4, outs, 1))
         return rc;
+    if (const int rc = check_workspace(workspace, workspace_bytes, ins, 4, outs, 1))
+        return rc;
     const Epilogue e{nullptr, (const uint16_t*)Z, (const uint16_t*)dres, dX, nullptr, ldz, lddr, lddx, 0, M, K, act, 0};
-    return linear_enqueue<FUSE_DX>({M, K, N, false, false, 1, false, false}, dY, lddy, W, ldw, e, stream);
+    return linear_enqueue<FUSE_DX>({M, K, N, false, false, 1, false, false}, dY, lddy, W, ldw, e, workspace, workspace_bytes, stream);
 }
 
 int gemm_linear_bwd_weight(int64_t M, int64_t N, int64_t K, const void* dY, int64_t lddy, const void* X, int64_t ldx,
-                           void* dW, int64_t lddw, int dw_type, float* dbias, void* stream)
+                           void* dW, int64_t lddw, int dw_type, float* dbias, void* workspace, int64_t workspace_bytes,
+                           void* stream)
 {
     if (const int rc = linear_sizes(M, N, K))
         return rc;
@@ -1262,13 +1314,16 @@ int gemm_linear_bwd_weight(int64_t M, int64_t N, int64_t K, const void* dY, int6
                                   {{dbias, 1, N, N, 4}, false, nullptr}};
     if (const int rc = check_linear(ins, 2, outs, 2))
         return rc;
+    if (const int rc = check_workspace(workspace, workspace_bytes, ins, 2, outs, 2))
+        return rc;
     const Epilogue e{nullptr, nullptr, nullptr, dW, nullptr, 0, 0, lddw, 0, N, K, GEMM_ACT_NONE, fp32 ? 1 : 0};
-    return linear_enqueue<FUSE_DW>({N, K, M, false, true, 1, false, false}, dY, lddy, X, ldx, e, stream,
-                                   bias ? dbias : nullptr);
+    return linear_enqueue<FUSE_DW>({N, K, M, false, true, 1, false, false}, dY, lddy, X, ldx, e, workspace, workspace_bytes,
+                                   stream, bias ? dbias : nullptr);
 }
 
 int gemm_gated_linear(int64_t M, int64_t F, int64_t K, const void* X, int64_t ldx, const void* W, int64_t ldw,
-                      const void* bias, int act, void* GU, int64_t ldgu, void* Y, int64_t ldy, void* stream)
+                      const void* bias, int act, void* GU, int64_t ldgu, void* Y, int64_t ldy, void* workspace,
+                      int64_t workspace_bytes, void* stream)
 {
     if (const int rc = linear_sizes(M, F, K))
         return rc;
@@ -1282,13 +1337,15 @@ int gemm_gated_linear(int64_t M, int64_t F, int64_t K, const void* X, int64_t ld
     const LinearOperand outs[] = {{{Y, M, F, ldy, 2}, true, nullptr}, {{GU, M, 2 * F, ldgu, 2}, false, nullptr}};
     if (const int rc = check_linear(ins, 3, outs, 2))
         return rc;
+    if (const int rc = check_workspace(workspace, workspace_bytes, ins, 3, outs, 2))
+        return rc;
     const Epilogue e{(const uint16_t*)bias, nullptr, nullptr, Y, (uint16_t*)GU, 0, 0, ldy, ldgu, M, F, act, 0};
-    return linear_enqueue<FUSE_GATED>({M, F, K, true, false, 2, false, false}, X, ldx, W, ldw, e, stream);
+    return linear_enqueue<FUSE_GATED>({M, F, K, true, false, 2, false, false}, X, ldx, W, ldw, e, workspace, workspace_bytes, stream);
 }
 
 int gemm_gated_linear_bwd_input(int64_t M, int64_t F, int64_t N, const void* dY, int64_t lddy, const void* W, int64_t ldw,
                                 int act, const void* GU, int64_t ldgu, void* dGU, int64_t lddgu, void* Y, int64_t ldy,
-                                void* stream)
+                                void* workspace, int64_t workspace_bytes, void* stream)
 {
     if (const int rc = linear_sizes(M, F, N))
         return rc;
@@ -1302,8 +1359,10 @@ int gemm_gated_linear_bwd_input(int64_t M, int64_t F, int64_t N, const void* dY,
     const LinearOperand outs[] = {{{dGU, M, 2 * F, lddgu, 2}, true, GU}, {{Y, M, F, ldy, 2}, false, nullptr}};
     if (const int rc = check_linear(ins, 3, outs, 2))
         return rc;
+    if (const int rc = check_workspace(workspace, workspace_bytes, ins, 3, outs, 2))
+        return rc;
     const Epilogue e{nullptr, (const uint16_t*)GU, nullptr, dGU, (uint16_t*)Y, ldgu, 0, lddgu, ldy, M, F, act, 0};
-    return linear_enqueue<FUSE_DGATED>({M, F, N, false, false, 1, false, false}, dY, lddy, W, ldw, e, stream);
+    return linear_enqueue<FUSE_DGATED>({M, F, N, false, false, 1, false, false}, dY, lddy, W, ldw, e, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"
