@@ -11,12 +11,13 @@ import importlib
 _FROM_BINDING = ("gemm", "gemm_fp8", "quantize_fp8", "rms_norm", "rms_norm_backward", "swiglu", "swiglu_backward",
                  "linear", "linear_backward_input", "linear_backward_weight", "gated_linear",
                  "gated_linear_backward_input", "RmsNorm", "GemmError", "SYNC_MODES")
-__all__ = ["binding", "inputs", "mlp", *_FROM_BINDING, "FeedForward"]
+_FROM_MLP = ("FeedForward", "FeedForwardBF16")
+__all__ = ["binding", "inputs", "mlp", *_FROM_BINDING, *_FROM_MLP]
 
 
 def __getattr__(name):
     if name in _FROM_BINDING:
         return getattr(importlib.import_module(__name__ + ".binding"), name)
-    if name == "FeedForward":
-        return importlib.import_module(__name__ + ".mlp").FeedForward
+    if name in _FROM_MLP:
+        return getattr(importlib.import_module(__name__ + ".mlp"), name)
     raise AttributeError(name)
