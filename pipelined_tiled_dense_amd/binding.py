@@ -130,9 +130,9 @@ def library() -> ctypes.CDLL:
         lib.gemm_gated_linear.argtypes = [i64, i64, i64, p, i64, p, i64, p, i32, p, i64, p, i64, p, i64, p]
         lib.gemm_gated_linear_bwd_input.argtypes = [i64, i64, i64, p, i64, p, i64, i32, p, i64, p, i64, p, i64, p, i64, p]
         lib.gemm_linear_plan_cus.argtypes = [i64, i64, i64, i32, i32, i32, i32, ctypes.POINTER(LinearPlan)]
-        for name in ("gemm_linear_plan_cus", "gemm_fp8_bt", "gemm_fp8_plan_cus", "gemm_quantize_fp8", "gemm_rms_norm", "gemm_rms_norm_bwd", "gemm_swiglu",
-                     "gemm_swiglu_bwd", "gemm_linear", "gemm_linear_bwd_input", "gemm_linear_bwd_weight",
-                     "gemm_gated_linear", "gemm_gated_linear_bwd_input"):
+        for name in ("gemm_fp8_bt", "gemm_fp8_plan_cus", "gemm_quantize_fp8", "gemm_rms_norm", "gemm_rms_norm_bwd",
+                     "gemm_swiglu", "gemm_swiglu_bwd", "gemm_linear", "gemm_linear_bwd_input", "gemm_linear_bwd_weight",
+                     "gemm_gated_linear", "gemm_gated_linear_bwd_input", "gemm_linear_plan_cus"):
             getattr(lib, name).restype = i32
         _lib = lib
     return _lib
@@ -257,27 +257,32 @@ def gemm_swiglu_bwd(M, F, dY, lddy, GU, ldgu, dGU, lddgu, stream) -> int:
     return library().gemm_swiglu_bwd(M, F, dY, lddy, GU, ldgu, dGU, lddgu, stream)
 
 
-def gemm_linear(M, N, K, X, ldx, W, ldw, bias, act, residual, ldr, Z, ldz, Y, ldy, stream, workspace=None, workspace_bytes=0) -> int:
+def gemm_linear(M, N, K, X, ldx, W, ldw, bias, act, residual, ldr, Z, ldz, Y, ldy, stream, workspace=None,
+                workspace_bytes=0) -> int:
     return library().gemm_linear(M, N, K, X, ldx, W, ldw, bias, act, residual, ldr, Z, ldz, Y, ldy, workspace,
                                  workspace_bytes, stream)
 
 
-def gemm_linear_bwd_input(M, N, K, dY, lddy, W, ldw, act, Z, ldz, dres, lddr, dX, lddx, stream, workspace=None, workspace_bytes=0) -> int:
+def gemm_linear_bwd_input(M, N, K, dY, lddy, W, ldw, act, Z, ldz, dres, lddr, dX, lddx, stream, workspace=None,
+                          workspace_bytes=0) -> int:
     return library().gemm_linear_bwd_input(M, N, K, dY, lddy, W, ldw, act, Z, ldz, dres, lddr, dX, lddx, workspace,
                                            workspace_bytes, stream)
 
 
-def gemm_linear_bwd_weight(M, N, K, dY, lddy, X, ldx, dW, lddw, dw_type, dbias, stream, workspace=None, workspace_bytes=0) -> int:
+def gemm_linear_bwd_weight(M, N, K, dY, lddy, X, ldx, dW, lddw, dw_type, dbias, stream, workspace=None,
+                           workspace_bytes=0) -> int:
     return library().gemm_linear_bwd_weight(M, N, K, dY, lddy, X, ldx, dW, lddw, dw_type, dbias, workspace,
                                             workspace_bytes, stream)
 
 
-def gemm_gated_linear(M, F, K, X, ldx, W, ldw, bias, act, GU, ldgu, Y, ldy, stream, workspace=None, workspace_bytes=0) -> int:
+def gemm_gated_linear(M, F, K, X, ldx, W, ldw, bias, act, GU, ldgu, Y, ldy, stream, workspace=None,
+                      workspace_bytes=0) -> int:
     return library().gemm_gated_linear(M, F, K, X, ldx, W, ldw, bias, act, GU, ldgu, Y, ldy, workspace,
                                        workspace_bytes, stream)
 
 
-def gemm_gated_linear_bwd_input(M, F, N, dY, lddy, W, ldw, act, GU, ldgu, dGU, lddgu, Y, ldy, stream, workspace=None, workspace_bytes=0) -> int:
+def gemm_gated_linear_bwd_input(M, F, N, dY, lddy, W, ldw, act, GU, ldgu, dGU, lddgu, Y, ldy, stream, workspace=None,
+                                workspace_bytes=0) -> int:
     return library().gemm_gated_linear_bwd_input(M, F, N, dY, lddy, W, ldw, act, GU, ldgu, dGU, lddgu, Y, ldy, workspace,
                                                  workspace_bytes, stream)
 
@@ -608,21 +613,20 @@ def _optional(name, x, dtype, rows, cols):
 _units = {}
 
 
-def _scratch(torch, product, M, N, K, a, lda, b, ldb):
-    """Temporary memory for a captured call, from torch, whose graphs keep theirs apart;
-    None where the stream is not capturing: the library keeps its own."""
-    if not torch.cuda.is_current_stream_capturing():
-        return None
-    d = a.get_device()
-    if d not in _units:
-        _units[d] = torch.cuda.get_device_properties(d).multi_processor_count
-    even = lambda x, ld: x.data_ptr() % 16 == 0 and (x.shape[0] <= 1 or (ld % 8 == 0 and ld <= 1 << 22))  # noqa: E731
-    n = gemm_linear_plan_cus(M, N, K, product, even(a, lda), even(b, ldb), _units[d])["scratch_bytes"]
-    return torch.empty(n, dtype=torch.uint8, device=a.device) if n else None
-
-
-def _memory(scratch):
-    return (None, 0) if scratch is None else (scratch.data_ptr(), scratch.numel())
+def _linear_call(torch, f, args, s, product, M, N, K, a, lda, b, ldb):
+    """One entry point's call.  Where it needs temporary memory and the stream is
+    capturing, again with some from torch, whose graphs keep theirs apart."""
+    rc = f(*args, None, 0, s)
+    if rc == GEMM_ERR_SCRATCH:
+        d = a.get_device()
+        if d not in _units:
+            _units[d] = torch.cuda.get_device_properties(d).multi_processor_count
+        even = lambda x, ld: x.data_ptr() % 16 == 0 and (x.shape[0] <= 1 or (ld % 8 == 0 and ld <= 1 << 22))  # noqa: E731
+        n = gemm_linear_plan_cus(M, N, K, product, even(a, lda), even(b, ldb), _units[d])["scratch_bytes"]
+        w = torch.empty(n, dtype=torch.uint8, device=a.device)
+        rc = f(*args, w.data_ptr(), n, s)
+    if rc != GEMM_OK:
+        raise GemmError(rc, "gemm_" + product)
 
 
 def linear(x, weight, *, bias=None, activation=None, residual=None, return_preactivation=False, stream=None):
@@ -646,10 +650,10 @@ def linear(x, weight, *, bias=None, activation=None, residual=None, return_preac
     s, dev = _current(torch, x, weight, bias, residual), x.device
     y = torch.empty(M, N, dtype=bf16, device=dev)
     z = torch.empty(M, N, dtype=bf16, device=dev) if return_preactivation else None
-    w = _scratch(torch, "linear", M, N, K, x, ldx, weight, ldw)
-    _done(library().gemm_linear(M, N, K, x.data_ptr(), ldx, weight.data_ptr(), ldw,
-                                None if bias is None else bias.data_ptr(), act, r, ldr,
-                                None if z is None else z.data_ptr(), N, y.data_ptr(), N, *_memory(w), s), "gemm_linear")
+    _linear_call(torch, library().gemm_linear,
+                 (M, N, K, x.data_ptr(), ldx, weight.data_ptr(), ldw, None if bias is None else bias.data_ptr(), act,
+                  r, ldr, None if z is None else z.data_ptr(), N, y.data_ptr(), N), s, "linear", M, N, K, x, ldx,
+                  weight, ldw)
     return (y, z) if return_preactivation else y
 
 
@@ -677,9 +681,9 @@ def linear_backward_input(dy, weight, *, preactivation=None, activation=None, dr
     r, ldr = _optional("dresidual", dresidual, bf16, M, K)
     s = _current(torch, dy, weight, preactivation, dresidual)
     dx = torch.empty(M, K, dtype=bf16, device=dy.device)
-    w = _scratch(torch, "linear_bwd_input", M, N, K, dy, lddy, weight, ldw)
-    _done(library().gemm_linear_bwd_input(M, N, K, dy.data_ptr(), lddy, weight.data_ptr(), ldw, act, z, ldz, r, ldr,
-                                          dx.data_ptr(), K, *_memory(w), s), "gemm_linear_bwd_input")
+    _linear_call(torch, library().gemm_linear_bwd_input,
+                 (M, N, K, dy.data_ptr(), lddy, weight.data_ptr(), ldw, act, z, ldz, r, ldr, dx.data_ptr(), K), s,
+                  "linear_bwd_input", M, N, K, dy, lddy, weight, ldw)
     return dx
 
 
@@ -703,11 +707,10 @@ def linear_backward_weight(dy, x, *, bias=False, out_dtype=None, stream=None):
     s, dev = _current(torch, dy, x), dy.device
     dw = torch.empty(N, K, dtype=out_dtype, device=dev)
     db = torch.empty(N, dtype=f32, device=dev) if bias else None
-    w = _scratch(torch, "linear_bwd_weight", M, N, K, dy, lddy, x, ldx)
-    _done(library().gemm_linear_bwd_weight(M, N, K, dy.data_ptr(), lddy, x.data_ptr(), ldx, dw.data_ptr(), K,
-                                           TYPE_FP32 if out_dtype is f32 else TYPE_BF16,
-                                           None if db is None else db.data_ptr(), *_memory(w), s),
-          "gemm_linear_bwd_weight")
+    _linear_call(torch, library().gemm_linear_bwd_weight,
+                 (M, N, K, dy.data_ptr(), lddy, x.data_ptr(), ldx, dw.data_ptr(), K,
+                  TYPE_FP32 if out_dtype is f32 else TYPE_BF16, None if db is None else db.data_ptr()), s, "linear_bwd_weight", M, N, K, dy, lddy, x,
+                  ldx)
     return (dw, db) if bias else dw
 
 
@@ -733,11 +736,10 @@ def gated_linear(x, weight, *, bias=None, activation="silu", return_gu=False, st
     s, dev, F = _current(torch, x, weight, bias), x.device, F2 // 2
     y = torch.empty(M, F, dtype=bf16, device=dev)
     gu = torch.empty(M, F2, dtype=bf16, device=dev) if return_gu else None
-    w = _scratch(torch, "gated_linear", M, F, K, x, ldx, weight, ldw)
-    _done(library().gemm_gated_linear(M, F, K, x.data_ptr(), ldx, weight.data_ptr(), ldw,
-                                      None if bias is None else bias.data_ptr(), act,
-                                      None if gu is None else gu.data_ptr(), F2, y.data_ptr(), F, *_memory(w), s),
-          "gemm_gated_linear")
+    _linear_call(torch, library().gemm_gated_linear,
+                 (M, F, K, x.data_ptr(), ldx, weight.data_ptr(), ldw, None if bias is None else bias.data_ptr(), act,
+                  None if gu is None else gu.data_ptr(), F2, y.data_ptr(), F), s, "gated_linear", M, F, K, x, ldx,
+                  weight, ldw)
     return (y, gu) if return_gu else y
 
 
@@ -760,9 +762,8 @@ def gated_linear_backward_input(dy, weight, gu, *, activation="silu", return_y=F
     s, dev = _current(torch, dy, weight, gu), dy.device
     dgu = torch.empty(M, 2 * F, dtype=bf16, device=dev)
     y = torch.empty(M, F, dtype=bf16, device=dev) if return_y else None
-    w = _scratch(torch, "gated_linear_bwd_input", M, F, N, dy, lddy, weight, ldw)
-    _done(library().gemm_gated_linear_bwd_input(M, F, N, dy.data_ptr(), lddy, weight.data_ptr(), ldw, act,
-                                                gu.data_ptr(), ldgu, dgu.data_ptr(), 2 * F,
-                                                None if y is None else y.data_ptr(), F, *_memory(w), s),
-          "gemm_gated_linear_bwd_input")
+    _linear_call(torch, library().gemm_gated_linear_bwd_input,
+                 (M, F, N, dy.data_ptr(), lddy, weight.data_ptr(), ldw, act, gu.data_ptr(), ldgu, dgu.data_ptr(),
+                  2 * F, None if y is None else y.data_ptr(), F), s, "gated_linear_bwd_input", M, F, N, dy, lddy, weight,
+                  ldw)
     return (dgu, y) if return_y else dgu
