@@ -2789,7 +2789,9 @@ int temp_take(TempMem& t, int64_t bytes, hipStream_t s, void** p, hipEvent_t* do
         while (size < bytes)
             size <<= 1;
         WsBlock b;
-        if (hipEventCreateWithFlags(&b.done, hipEventDisableTiming) != hipSuccess) {
+        // Nothing but the device's kernels reads a block: without the release to the
+        // host's memory the next kernel on the stream starts 2 us sooner.
+        if (hipEventCreateWithFlags(&b.done, hipEventDisableTiming | hipEventDisableSystemFence) != hipSuccess) {
             (void)hipGetLastError();
             return GEMM_ERR_DEVICE;
         }

@@ -52,6 +52,19 @@ struct EpilogueIn {
 typedef u32x4_t __attribute__((aligned(2))) u32x4_any_t;
 typedef f32x4_t __attribute__((aligned(4))) f32x4_any_t;
 
+// A chunk without its first n (< 8) elements, zeros behind the others.
+__device__ __forceinline__ u32x4_t shifted_chunk(u32x4_t v, int n)
+{
+    uint64_t x[2];
+    __builtin_memcpy(x, &v, 16);
+    const int s = 16 * n;
+    const uint64_t lo = s >= 64 ? x[1] : x[0], hi = s >= 64 ? 0u : x[1];
+    x[0] = (s & 63) ? (lo >> (s & 63)) | (hi << (64 - (s & 63))) : lo;
+    x[1] = hi >> (s & 63);
+    __builtin_memcpy(&v, x, 16);
+    return v;
+}
+
 // Where a chunk is: 8 columns from c on, the n (<= 8) of them that exist, of row
 // `row`, in matrices of any alignment and stride.
 struct ChunkAt {
@@ -108,16 +121,7 @@ struct TileAt {
     // What was loaded, in place.  Not in load: it would wait for the load there.
     __device__ __forceinline__ u32x4_t placed(u32x4_t v) const
     {
-        if (part) {
-            uint64_t x[2];
-            __builtin_memcpy(x, &v, 16);
-            const int s = 16 * (kChunk - n()) & 127;   // lanes of whole chunks: 0
-            const uint64_t lo = s >= 64 ? x[1] : x[0], hi = s >= 64 ? 0u : x[1];
-            x[0] = (s & 63) ? (lo >> (s & 63)) | (hi << (64 - (s & 63))) : lo;
-            x[1] = hi >> (s & 63);
-            __builtin_memcpy(&v, x, 16);
-        }
-        return v;
+        return part ? shifted_chunk(v, (kChunk - n()) & 7) : v;   // lanes of whole chunks: 0
     }
     __device__ __forceinline__ void store(uint16_t* base, int64_t ld, u32x4_t v) const
     {
@@ -269,9 +273,8 @@ __device__ __forceinline__ void epilogue_finish(const Epilogue& e, const Epilogu
 // Tiles.
 // ---------------------------------------------------------------------------
 // 256 x 256 tiles on the split-window ring, 8 waves: the bf16 product's default.
-// 128 x 128 tiles on a two-stage ring, 4 waves: two workgroups share a compute
-// unit, so that one's epilogue runs beside the other's main loop and small outputs
-// give more workgroups.  A paired B needs both factors' 64 columns in a wave.
+// 128 x 128 tiles on a four-stage ring, 8 waves, where those give the compute units
+// too little to share.  A paired B needs both factors' 64 columns in a wave.
 template <bool BT_, bool AT_, bool PAIRED_, bool BIG_>
 struct LinearCfg;
 
@@ -279,14 +282,12 @@ template <bool BT_, bool AT_, bool PAIRED_>
 struct LinearCfg<BT_, AT_, PAIRED_, true>
     : Cfg<256, 256, 64, 2, PAIRED_ ? 4 : 2, PAIRED_ ? 2 : 4, SYNC_BARRIER, BT_, 0, true, 16> {
     static constexpr bool AT = AT_, PAIRED = PAIRED_, ANY_SIZE = true;
-    static constexpr int PER_CU = 1;
 };
 
 template <bool BT_, bool AT_, bool PAIRED_>
 struct LinearCfg<BT_, AT_, PAIRED_, false>
     : Cfg<128, 128, 64, 4, 4, PAIRED_ ? 1 : 2, SYNC_BARRIER, BT_, 0, false, 16> {
     static constexpr bool AT = AT_, PAIRED = PAIRED_, ANY_SIZE = true;
-    static constexpr int PER_CU = 1;
 };
 
 // Sums of the k chunks: chunk sp's of the launch's u-th tile are piece sp * span +
@@ -800,21 +801,41 @@ __global__ void __launch_bounds__(1024) k_column_sums(const uint16_t* x, int64_t
 }
 
 // Zero-padded copies of the operands whose rows do not start on 16-byte boundaries
-// or end inside a 16-byte chunk, one launch for both.
+// or end inside a 16-byte chunk, one launch for both.  `lanes` of a workgroup take a
+// row together, four chunks each at a time, and a row's last chunk is loaded from its
+// last 16 bytes, so that no load waits for another.
 struct LinearPad {
     const uint16_t* src[2];
     uint16_t* dst[2];
     int64_t rows[2], cols[2], ld[2], dst_ld[2];
+    uint32_t blocks[2];
+    int32_t lanes[2];        // a power of two, at most 64
 };
 
 __global__ void __launch_bounds__(256) k_linear_pad(LinearPad p)
 {
-    const int64_t first = p.rows[0] * (p.dst_ld[0] / kChunk), total = first + p.rows[1] * (p.dst_ld[1] / kChunk);
-    for (int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x; id < total; id += (int64_t)gridDim.x * 256) {
-        const int o = id >= first;
-        const int64_t per_row = p.dst_ld[o] / kChunk, at = o ? id - first : id, r = at / per_row;
-        const int64_t c = (at - r * per_row) * kChunk;
-        *(u32x4_t*)(p.dst[o] + r * p.dst_ld[o] + c) = load_chunk<false>(p.src[o] + r * p.ld[o] + c, left(p.cols[o], c), c);
+    const int o = blockIdx.x >= p.blocks[0];
+    const uint32_t block = blockIdx.x - (o ? p.blocks[0] : 0u);
+    const int lanes = p.lanes[o], rows = 256 / lanes, lane = threadIdx.x & (lanes - 1), first = threadIdx.x / lanes;
+    const int32_t cols = (int32_t)p.cols[o], chunks = (int32_t)(p.dst_ld[o] / kChunk);
+    for (int64_t r = (int64_t)block * rows + first; r < p.rows[o]; r += (int64_t)p.blocks[o] * rows) {
+        const uint16_t* from = p.src[o] + r * p.ld[o];
+        u32x4_t* to = (u32x4_t*)(p.dst[o] + r * p.dst_ld[o]);
+        if (cols < kChunk) {
+            if (lane == 0)
+                *to = load_chunk<false>(from, cols, 0);
+            continue;
+        }
+        for (int32_t c = lane; c < chunks; c += 4 * lanes) {
+            u32x4_t v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                __builtin_memcpy(&v[i], from + min((c + i * lanes) * kChunk, cols - kChunk), 16);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (const int32_t at = c + i * lanes; at < chunks)
+                    to[at] = shifted_chunk(v[i], max(at * kChunk - (cols - kChunk), 0));
+        }
     }
 }
 
@@ -922,8 +943,20 @@ LinearPlan linear_plan(const LinearShape& q, int cus)
     return best;
 }
 
+// One launch.  `done`, where there is one, becomes this kernel's completion: recorded as a
+// marker behind it, it holds up the stream's next kernel 1.3 us longer.
+template <class K, class... Args>
+int enqueue(K kernel, dim3 grid, dim3 block, hipStream_t s, hipEvent_t done, Args... args)
+{
+    if (done)
+        hipExtLaunchKernelGGL(kernel, grid, block, 0, s, nullptr, done, 0, args...);
+    else
+        hipLaunchKernelGGL(kernel, grid, block, 0, s, args...);
+    return launched();
+}
+
 template <class C, int MODE>
-int launch_linear(const LinearParams<MODE>& p, int64_t grid, hipStream_t s)
+int launch_linear(const LinearParams<MODE>& p, int64_t grid, hipStream_t s, hipEvent_t done)
 {
     // Masks per lane only where a position may be partial: the k tail inside rows,
     // and columns past N of a K x N B.
@@ -932,57 +965,47 @@ int launch_linear(const LinearParams<MODE>& p, int64_t grid, hipStream_t s)
     const dim3 g((unsigned)grid), b(C::THREADS);
     auto run = [&]<bool LONGK, bool EDGE>() {
         if constexpr (C::WIN)
-            hipLaunchKernelGGL(HIP_KERNEL_NAME(k_gemm_win<C, LONGK, EDGE, LinearParams<MODE>>), g, b, 0, s, p);
+            return enqueue(k_gemm_win<C, LONGK, EDGE, LinearParams<MODE>>, g, b, s, done, p);
         else
-            hipLaunchKernelGGL(HIP_KERNEL_NAME(k_gemm<C, LONGK, EDGE, LinearParams<MODE>>), g, b, 0, s, p);
+            return enqueue(k_gemm<C, LONGK, EDGE, LinearParams<MODE>>, g, b, s, done, p);
     };
     if (longk && !edge)
-        run.template operator()<true, false>();
-    else if (longk)
-        run.template operator()<true, true>();
-    else
-        run.template operator()<false, true>();
-    return launched();
+        return run.template operator()<true, false>();
+    if (longk)
+        return run.template operator()<true, true>();
+    return run.template operator()<false, true>();
 }
 
 template <int MODE>
-int launch_wave(const LinearParams<MODE>& p, const LinearPlan& pl, bool even, hipStream_t s)
+int launch_wave(const LinearParams<MODE>& p, const LinearPlan& pl, bool even, hipStream_t s, hipEvent_t done)
 {
     constexpr int F = fuse_paired(MODE) ? 2 : 1;
     constexpr bool BT = MODE == FUSE_LINEAR || F == 2;
     const int32_t kblocks = (int32_t)ceil_div(p.K, 64), chunk = (int32_t)ceil_div(pl.chunk, 64);
     const dim3 g((unsigned)pl.grid, (unsigned)pl.splits), b(kWaves * 64);
     auto run = [&]<int MF, int NF, int DEPTH>() {
-        if (even)
-            hipLaunchKernelGGL(HIP_KERNEL_NAME(k_linear_wave<MODE, MF, NF, DEPTH, true>), g, b, 0, s, p, chunk, kblocks);
-        else
-            hipLaunchKernelGGL(HIP_KERNEL_NAME(k_linear_wave<MODE, MF, NF, DEPTH, false>), g, b, 0, s, p, chunk, kblocks);
+        return even ? enqueue(k_linear_wave<MODE, MF, NF, DEPTH, true>, g, b, s, done, p, chunk, kblocks)
+                    : enqueue(k_linear_wave<MODE, MF, NF, DEPTH, false>, g, b, s, done, p, chunk, kblocks);
     };
     if constexpr (BT) {
-        if (pl.mf == 1 && F == 1 && pl.nf == 1) {
-            run.template operator()<1, 1, 4>();
-            return launched();
-        }
-        if (pl.mf == 1 && pl.nf * F == 2) {
-            run.template operator()<1, 2 / F, 2>();
-            return launched();
-        }
+        if (pl.mf == 1 && F == 1 && pl.nf == 1)
+            return run.template operator()<1, 1, 4>();
+        if (pl.mf == 1 && pl.nf * F == 2)
+            return run.template operator()<1, 2 / F, 2>();
     }
     if constexpr (MODE != FUSE_DW) {
         if (pl.mf == 1)
-            run.template operator()<1, 4 / F, 2>();
-        else if (pl.mf == 2)
-            run.template operator()<2, 4 / F, 1>();
+            return run.template operator()<1, 4 / F, 2>();
+        if (pl.mf == 2)
+            return run.template operator()<2, 4 / F, 1>();
     }
-    if (pl.mf == 4)
-        run.template operator()<4, 4 / F, 1>();
-    return launched();
+    return run.template operator()<4, 4 / F, 1>();
 }
 
 // Temporary memory of `bytes` for one call.  Not from the library's pool under graph
 // capture: a graph with memory of its own ended in an illegal access on replay, and its
 // cause is not known, so such a call is refused.
-int linear_take(TempMem& tm, int64_t bytes, hipStream_t s, void** p)
+int linear_take(TempMem& tm, int64_t bytes, hipStream_t s, void** p, hipEvent_t* done)
 {
     if (!tm.fixed) {
         hipStreamCaptureStatus cs = hipStreamCaptureStatusNone;
@@ -993,7 +1016,7 @@ int linear_take(TempMem& tm, int64_t bytes, hipStream_t s, void** p)
         if (cs != hipStreamCaptureStatusNone)
             return GEMM_ERR_SCRATCH;
     }
-    return temp_take(tm, bytes, s, p);
+    return temp_take(tm, bytes, s, p, done);
 }
 
 // The product of A and B into epilogue e.  The caller has checked everything but
@@ -1044,11 +1067,13 @@ int linear_run(LinearShape q, const void* A, int64_t lda, const void* B, int64_t
         sums = {nullptr, dbias, a_cols, (int32_t)ceil_div(std::max<int64_t>(a_rows, 1), std::max<int64_t>(run, 1)), 0};
     }
     const int64_t runs_bytes = sums.runs > 1 ? align256(sums.runs * a_cols * 4) : 0;
+    // The call's temporary memory is free once its last kernel is done.
+    void* ws = nullptr;
+    hipEvent_t done = nullptr;
     auto finish = [&]() {
         const int64_t units = (int64_t)p.span * pl.bm * pl.bn / (MODE == FUSE_DW && e.fp32 ? 4 : kChunk);
-        hipLaunchKernelGGL(k_linear_finish<MODE>, dim3(flat_grid(units) + sums.blocks), dim3(256), 0, s, p, pl.bm, pl.bn,
-                           sums);
-        return launched();
+        return enqueue(k_linear_finish<MODE>, dim3(flat_grid(units) + sums.blocks), dim3(256), s, done, p,
+                       (int32_t)pl.bm, (int32_t)pl.bn, sums);
     };
     auto start_sums = [&](float* part) {
         const bool one = sums.runs <= 1;
@@ -1060,19 +1085,17 @@ int linear_run(LinearShape q, const void* A, int64_t lda, const void* B, int64_t
         return launched();
     };
     auto join_sums = [&]() {
-        if (sums.blocks == 0)
-            return (int)GEMM_OK;
-        hipLaunchKernelGGL(k_join_column_sums, dim3(sums.blocks), dim3(256), 0, s, sums);
-        return launched();
+        return enqueue(k_join_column_sums, dim3(sums.blocks), dim3(256), s, done, sums);
     };
     if (q.K == 0 || q.N == 0) {   // nothing to multiply
-        void* ws = nullptr;
-        int rc = runs_bytes > 0 ? linear_take(tm, runs_bytes, s, &ws) : (int)GEMM_OK;
-        if (rc == GEMM_OK && dbias && (rc = start_sums((float*)ws)) == GEMM_OK)
-            rc = join_sums();
+        int rc = runs_bytes > 0 ? linear_take(tm, runs_bytes, s, &ws, &done) : (int)GEMM_OK;
+        if (rc == GEMM_OK && dbias)
+            rc = start_sums((float*)ws);
         if (rc == GEMM_OK && q.N > 0)
             rc = finish();
-        const int frc = temp_give(tm, ws, s);
+        else if (rc == GEMM_OK && sums.blocks > 0)
+            rc = join_sums();
+        const int frc = temp_give(tm, ws, s, rc == GEMM_OK && done != nullptr);
         return rc != GEMM_OK ? rc : frc;
     }
 
@@ -1085,9 +1108,8 @@ int linear_run(LinearShape q, const void* A, int64_t lda, const void* B, int64_t
     const bool far = !wave && std::max({e.ld_in0, e.ld_in1, e.ld_out0, e.ld_out1}) > kMaxTileLd;
     const int64_t sums_bytes = pl.splits > 1 || !far ? pl.workspace : pl.tiles * pl.bm * pl.bn * q.factors * 4;
     const int64_t bytes = a_bytes + b_bytes + runs_bytes + sums_bytes;
-    void* ws = nullptr;
     int rc = GEMM_OK;
-    if (bytes > 0 && (rc = linear_take(tm, bytes, s, &ws)) != GEMM_OK)
+    if (bytes > 0 && (rc = linear_take(tm, bytes, s, &ws, &done)) != GEMM_OK)
         return rc;
     if (dbias)
         rc = start_sums((float*)((char*)ws + a_bytes + b_bytes));
@@ -1097,7 +1119,14 @@ int linear_run(LinearShape q, const void* A, int64_t lda, const void* B, int64_t
                     {pad_a ? a_rows : 0, pad_b ? b_rows : 0},
                     {a_cols, b_cols},
                     {lda, ldb},
-                    {a_ld, b_ld}};
+                    {a_ld, b_ld},
+                    {0, 0},
+                    {1, 1}};
+        for (int o = 0; o < 2; ++o) {
+            while (c.lanes[o] < 64 && c.lanes[o] * kChunk < c.cols[o])
+                c.lanes[o] *= 2;
+            c.blocks[o] = (uint32_t)std::min<int64_t>(ceil_div(c.rows[o] * c.lanes[o], 256), 1 << 20);
+        }
         if (pad_a) {
             p.A = (const char*)c.dst[0];
             p.lda = a_ld;
@@ -1106,7 +1135,7 @@ int linear_run(LinearShape q, const void* A, int64_t lda, const void* B, int64_t
             p.B = (const char*)c.dst[1];
             p.ldb = b_ld;
         }
-        hipLaunchKernelGGL(k_linear_pad, dim3(flat_grid(a_bytes / 16 + b_bytes / 16)), dim3(256), 0, s, c);
+        hipLaunchKernelGGL(k_linear_pad, dim3(c.blocks[0] + c.blocks[1]), dim3(256), 0, s, c);
         rc = launched();
     }
     if (sums_bytes > 0)
@@ -1118,17 +1147,19 @@ int linear_run(LinearShape q, const void* A, int64_t lda, const void* B, int64_t
         p.ldb = b_ld;
     p.small_span = ((a_rows - 1) * p.lda + a_ld) * 2 < (int64_t)kMaxRecords &&
                    ((b_rows / q.factors - 1) * p.ldb + b_ld) * 2 < (int64_t)kMaxRecords;
+    const bool second = sums_bytes > 0 || sums.blocks > 0;
     if (rc == GEMM_OK) {
+        const hipEvent_t d = second ? nullptr : done;
         if (wave)
-            rc = launch_wave<MODE>(p, pl, q.a_even && q.b_even, s);
+            rc = launch_wave<MODE>(p, pl, q.a_even && q.b_even, s, d);
         else if (pl.kind == TILES_BIG)
-            rc = launch_linear<LinearCfg<BT, AT, PAIR, true>, MODE>(p, pl.grid, s);
-        else if (pl.kind == TILES_SMALL)
-            rc = launch_linear<LinearCfg<BT, AT, PAIR, false>, MODE>(p, pl.grid, s);
+            rc = launch_linear<LinearCfg<BT, AT, PAIR, true>, MODE>(p, pl.grid, s, d);
+        else
+            rc = launch_linear<LinearCfg<BT, AT, PAIR, false>, MODE>(p, pl.grid, s, d);
     }
-    if (rc == GEMM_OK)
+    if (rc == GEMM_OK && second)
         rc = sums_bytes > 0 ? finish() : join_sums();
-    const int frc = temp_give(tm, ws, s);
+    const int frc = temp_give(tm, ws, s, rc == GEMM_OK && done != nullptr);
     return rc != GEMM_OK ? rc : frc;
 }
 
