@@ -253,7 +253,8 @@ struct Cfg {
     static constexpr int CPR_K = BK / 8;                             // 16-byte chunks per K-contiguous row
     static constexpr int CPR_N = BN / 8;                             // chunks per row of a K x N B tile
     static constexpr int CPR_M = BM / 8;                             // chunks per row of a K x M A tile
-    static constexpr int RING_BYTES = WIN ? NWIN * A_BYTES : PIPES * S * STAGE_BYTES;
+    static constexpr int WIN_BYTES = A_BYTES > B_BYTES ? A_BYTES : B_BYTES;
+    static constexpr int RING_BYTES = WIN ? NWIN * WIN_BYTES : PIPES * S * STAGE_BYTES;
     // Ring counters (2 x S 32-bit words, or S 64-bit signal words) and the
     // workgroup's poison word (SyncState), padded to 8 bytes.
     static constexpr int FLAG_BYTES = (SYNC != SYNC_BARRIER) ? PIPES * 2 * S * 4 + 8 : 0;
@@ -265,7 +266,7 @@ struct Cfg {
     // slowed the epilogue where all workgroups store at once); with 32 x 32
     // blocks, 32 rows x 32 columns.
     static constexpr bool EPI_FULL =
-        WIN ? NCW * 32 * 64 * 2 <= A_BYTES : RING_BYTES + NCW * 32 * 64 * 2 + FLAG_BYTES <= 160 * 1024;
+        WIN ? NCW * 32 * 64 * 2 <= WIN_BYTES : RING_BYTES + NCW * 32 * 64 * 2 + FLAG_BYTES <= 160 * 1024;
     static constexpr int EPI_W = (EPI_FULL || MF_ == 16) ? 64 : 32;
     static constexpr int EPI_H = (EPI_FULL || MF_ != 16) ? 32 : 16;
     static constexpr int EPI_WAVE_BYTES = EPI_H * EPI_W * 2;
@@ -299,9 +300,8 @@ struct Cfg {
     static_assert(S >= 2 && S <= 4, "stages");
     static_assert(SPREAD_ >= 0 && SPREAD_ <= 8 && (SPREAD_ == 0 || PRODUCERS), "loader spread");
     static_assert(!DUAL || (SYNC == SYNC_PINGPONG && NP % GROUPS == 0), "one pipeline per ping-pong group");
-    static_assert(!WIN || (SYNC == SYNC_BARRIER && S == 2 && KK == 4 && A_BYTES == B_BYTES &&
-                           NCW * EPI_WAVE_BYTES <= A_BYTES),
-                  "the window ring runs the barrier kernel on equal A and B tiles");
+    static_assert(!WIN || (SYNC == SYNC_BARRIER && S == 2 && KK == 4 && NCW * EPI_WAVE_BYTES <= WIN_BYTES),
+                  "the window ring runs the barrier kernel, and the epilogue stages in a window");
 };
 
 // A work item is one output tile and one chunk of the k range.  Without a
@@ -1883,7 +1883,7 @@ __global__ void __launch_bounds__(C::THREADS) k_gemm_win(P p)
     clock_begin(p);
 
     constexpr int AH = C::A_LOADS / 2, BH = C::B_LOADS / 2;   // DMA instructions per half tile
-    auto win = [&](int i) { return smem + i * C::A_BYTES; };
+    auto win = [&](int i) { return smem + i * C::WIN_BYTES; };
     auto step5 = [](int i, int d) { return i + d >= 5 ? i + d - 5 : i + d; };
     using Prep = typename Loader<C, LONGK, EDGE>::Prep;
 
@@ -1903,7 +1903,13 @@ __global__ void __launch_bounds__(C::THREADS) k_gemm_win(P p)
     block_barrier();
 
     Frags<C> fr[2];
-    read_frags<C>(fr[0], win(0), wm, wn, lane, 0);   // A at window 0, B at window 1
+    auto first_frags = [&](int a) {   // of the position whose A is in window a
+        const FragReader<C> rd(wm, wn, lane, 0);
+#pragma unroll
+        for (int d = 0; d < frag_reads<C>(); ++d)
+            rd.read(fr[0], win(a), win(step5(a, 1)), wn, d);
+    };
+    first_frags(0);
     int wa = 0;                                      // A window of the position being computed
     Prep prep_a = prep_b;
 
@@ -1974,10 +1980,7 @@ __global__ void __launch_bounds__(C::THREADS) k_gemm_win(P p)
             block_barrier();
             // The next tile's first fragments again: held through a longer epilogue, their
             // registers would push it into spills.
-            const FragReader<C> rd(wm, wn, lane, 0);
-#pragma unroll
-            for (int d = 0; d < frag_reads<C>(); ++d)
-                rd.read(fr[0], win(wa), win(step5(wa, 1)), wn, d);
+            first_frags(wa);
         } else if (p.splits > 1) {
             store_partial<C>(p, acc, sp * p.span + u, wm, wn, lane);
         } else {

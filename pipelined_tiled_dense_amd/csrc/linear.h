@@ -273,19 +273,23 @@ __device__ __forceinline__ void epilogue_finish(const Epilogue& e, const Epilogu
 // Tiles.
 // ---------------------------------------------------------------------------
 // 256 x 256 tiles on the split-window ring, 8 waves: the bf16 product's default.
+// 192 x 256 tiles on the same ring, where A is K-contiguous and B one matrix: a round
+// of them takes 0.84 of the time, for sizes that leave fewer compute units idle so
+// (6952 x 1344 x 5952: 222 tiles 103 us, 168 of 256 rows 123; 4088 x 7608 x 1728: 3
+// rounds 116, 2 of 256 rows 102).
 // 128 x 128 tiles on a four-stage ring, 8 waves, where those give the compute units
 // too little to share.  A paired B needs both factors' 64 columns in a wave.
-template <bool BT_, bool AT_, bool PAIRED_, bool BIG_>
-struct LinearCfg;
+enum { TILES_BIG, TILES_192, TILES_SMALL, TILES_WAVE };
 
-template <bool BT_, bool AT_, bool PAIRED_>
-struct LinearCfg<BT_, AT_, PAIRED_, true>
-    : Cfg<256, 256, 64, 2, PAIRED_ ? 4 : 2, PAIRED_ ? 2 : 4, SYNC_BARRIER, BT_, 0, true, 16> {
+template <bool BT_, bool AT_, bool PAIRED_, int KIND_>
+struct LinearCfg : Cfg<KIND_ == TILES_192 ? 192 : 256, 256, 64, 2, PAIRED_ ? 4 : 2, PAIRED_ ? 2 : 4, SYNC_BARRIER, BT_, 0,
+                       true, 16> {
+    static_assert(KIND_ == TILES_BIG || (!AT_ && !PAIRED_), "192 rows: 96 a wave, of a K-contiguous A");
     static constexpr bool AT = AT_, PAIRED = PAIRED_, ANY_SIZE = true;
 };
 
 template <bool BT_, bool AT_, bool PAIRED_>
-struct LinearCfg<BT_, AT_, PAIRED_, false>
+struct LinearCfg<BT_, AT_, PAIRED_, TILES_SMALL>
     : Cfg<128, 128, 64, 4, 4, PAIRED_ ? 1 : 2, SYNC_BARRIER, BT_, 0, false, 16> {
     static constexpr bool AT = AT_, PAIRED = PAIRED_, ANY_SIZE = true;
 };
@@ -865,8 +869,6 @@ int64_t column_run(int64_t rows, int64_t cols, int cus)
 
 int64_t pad_size(int64_t rows, int64_t cols) { return align256(rows * round8(cols) * 2); }
 
-enum { TILES_BIG, TILES_SMALL, TILES_WAVE };
-
 struct LinearPlan {
     int kind;
     int mf, nf;              // TILES_WAVE: fragments
@@ -900,7 +902,8 @@ double linear_time(const LinearShape& q, const LinearPlan& pl, int cus)
     // The weight's gradient reads both operands transposed.
     if (pl.kind == TILES_SMALL)
         return 3.0 + rounds * (4.3 + (q.at ? 0.47 : 0.43) * steps) + (pl.splits > 1 ? 5.3 + 0.2 * sums : 0.0) + padding;
-    return 1.5 + rounds * (9.0 + (q.at ? 1.35 : 1.1) * steps) + (pl.splits > 1 ? 5.0 + 0.17 * sums : 0.0) + padding;
+    const double round = pl.kind == TILES_192 ? 7.6 + 0.93 * steps : 9.0 + (q.at ? 1.35 : 1.1) * steps;
+    return 1.5 + rounds * round + (pl.splits > 1 ? 5.0 + 0.17 * sums : 0.0) + padding;
 }
 
 // The kind, tile and chunks of k (whole 64-wide k-steps, all of them with work) that are
@@ -914,8 +917,8 @@ LinearPlan linear_plan(const LinearShape& q, int cus)
         pl.kind = kind;
         pl.mf = mf;
         pl.nf = nf;
-        pl.bm = kind == TILES_WAVE ? mf * 16 : kind == TILES_BIG ? 256 : 128;
-        pl.bn = kind == TILES_WAVE ? nf * 16 : pl.bm / q.factors;
+        pl.bm = kind == TILES_WAVE ? mf * 16 : kind == TILES_BIG ? 256 : kind == TILES_192 ? 192 : 128;
+        pl.bn = kind == TILES_WAVE ? nf * 16 : (kind == TILES_SMALL ? 128 : 256) / q.factors;
         pl.tiles = ceil_div(q.M, pl.bm) * ceil_div(q.N, pl.bn);
         for (int64_t s = 1; s <= kMaxSplits && (s == 1 || pl.tiles * s <= 2 * cus); ++s) {
             pl.chunk = s == 1 ? q.K : ceil_div(ceil_div(q.K, s), 64) * 64;
@@ -939,6 +942,8 @@ LinearPlan linear_plan(const LinearShape& q, int cus)
     if (q.N >= kChunk) {   // TileAt's rows
         consider(TILES_SMALL, 0, 0);
         consider(TILES_BIG, 0, 0);
+        if (!q.at && q.factors == 1)
+            consider(TILES_192, 0, 0);
     }
     return best;
 }
@@ -1152,10 +1157,12 @@ int linear_run(LinearShape q, const void* A, int64_t lda, const void* B, int64_t
         const hipEvent_t d = second ? nullptr : done;
         if (wave)
             rc = launch_wave<MODE>(p, pl, q.a_even && q.b_even, s, d);
+        else if (pl.kind == TILES_SMALL)
+            rc = launch_linear<LinearCfg<BT, AT, PAIR, TILES_SMALL>, MODE>(p, pl.grid, s, d);
         else if (pl.kind == TILES_BIG)
-            rc = launch_linear<LinearCfg<BT, AT, PAIR, true>, MODE>(p, pl.grid, s, d);
-        else
-            rc = launch_linear<LinearCfg<BT, AT, PAIR, false>, MODE>(p, pl.grid, s, d);
+            rc = launch_linear<LinearCfg<BT, AT, PAIR, TILES_BIG>, MODE>(p, pl.grid, s, d);
+        else if constexpr (!AT && !PAIR)
+            rc = launch_linear<LinearCfg<BT, AT, PAIR, TILES_192>, MODE>(p, pl.grid, s, d);
     }
     if (rc == GEMM_OK && second)
         rc = sums_bytes > 0 ? finish() : join_sums();

@@ -41,13 +41,14 @@ def stream():
     return torch.cuda.current_stream().cuda_stream
 
 
-# (M, N, K) of each kernel: waves, small tiles, large tiles; and with k chunks.
-KINDS = [(5, 40, 64), (40, 200, 520), (300, 600, 1096), (600, 2100, 200), (4200, 4096, 136), (20, 32, 9000), (400, 320, 6000)]
+# (M, N, K) of each kernel: waves, small tiles, tiles of 192 and of 256 rows; and with k chunks.
+KINDS = [(5, 40, 64), (40, 200, 520), (300, 600, 1096), (600, 2100, 200), (4200, 4096, 136), (4090, 4096, 136), (20, 32, 9000),
+         (400, 320, 6000)]
 
 
 def test_kinds_are_of_every_kind():
     p = [bd.gemm_linear_plan_cus(m, n, k, "linear", 1, 1, 256) for m, n, k in KINDS]
-    assert {x["rows"] for x in p} >= {16, 64, 128, 256} and {x["k_splits"] > 1 for x in p} == {False, True}
+    assert {x["rows"] for x in p} >= {16, 64, 128, 192, 256} and {x["k_splits"] > 1 for x in p} == {False, True}
 
 
 # -- gates of any size ------------------------------------------------------------------
