@@ -570,13 +570,14 @@ int gemm_swiglu_bwd(int64_t M, int64_t F, const void* dY, int64_t lddy,
  * output.  Entry points are asynchronous on `stream`, validate as gemm_bf16 does and
  * return the same status codes; leading dimensions, alignment and overlaps are as
  * for the 8-bit operators above.  Optional operands are NULL where absent (their
- * leading dimension is then ignored).  M is 0 .. 2^31 - 1, the other sizes 0 .. 2^22
- * (GEMM_ERR_UNSUPPORTED_SHAPE above).
+ * leading dimension is then ignored).  M is 0 .. 2^31 - 1, 0 .. 2^28 where an output has
+ * fewer than 8 columns (of a factor, and not a weight's gradient), the other sizes 0 ..
+ * 2^22 (GEMM_ERR_UNSUPPORTED_SHAPE above).
  *
- * The products run on operands whose rows are multiples of 8 long, start on 16-byte
- * boundaries and are at most 2^22 elements apart; they copy any other, zero-padded,
- * into temporary memory first (but not where M <= 64 and both operands are read
- * along their rows).  Few output tiles and a long sum are split into chunks along
+ * Products in tiles run on operands whose rows are multiples of 8 long, start on
+ * 16-byte boundaries and are at most 2^22 elements apart; they copy any other,
+ * zero-padded, into temporary memory first.  Few rows and small products are read as
+ * they lie (gemm_linear_plan_cus says which is which).  Few output tiles and a long sum are split into chunks along
  * it, whose fp32 sums a second launch adds in a fixed order.  Results are
  * deterministic for given sizes, strides and alignment.
  *

@@ -881,6 +881,11 @@ int64_t column_run(int64_t rows, int64_t cols, int cus)
 
 int64_t pad_size(int64_t rows, int64_t cols) { return align256(rows * round8(cols) * 2); }
 
+// A launch holds fewer than 2^32 threads, so many tiles of the waves' kernel, which outputs
+// of fewer than 8 columns have to take: 64 rows a tile where there are more than 32.
+constexpr int64_t kMaxWaveTiles = (int64_t)1 << 22, kMaxNarrowRows = kMaxWaveTiles * 64;
+static_assert((kMaxWaveTiles + 7) * kWaves * 64 < (int64_t)1 << 32, "threads of a launch");
+
 struct LinearPlan {
     int kind;
     int mf, nf;              // TILES_WAVE: fragments
@@ -932,6 +937,8 @@ LinearPlan linear_plan(const LinearShape& q, int cus)
         pl.bm = kind == TILES_WAVE ? mf * 16 : kind == TILES_BIG ? 256 : kind == TILES_192 ? 192 : 128;
         pl.bn = kind == TILES_WAVE ? nf * 16 : (kind == TILES_SMALL ? 128 : 256) / q.factors;
         pl.tiles = ceil_div(q.M, pl.bm) * ceil_div(q.N, pl.bn);
+        if (kind == TILES_WAVE && pl.tiles > kMaxWaveTiles)
+            return;
         for (int64_t s = 1; s <= kMaxSplits && (s == 1 || pl.tiles * s <= 2 * cus); ++s) {
             pl.chunk = s == 1 ? q.K : ceil_div(ceil_div(q.K, s), 64) * 64;
             pl.splits = ceil_div(q.K, pl.chunk);
@@ -1182,11 +1189,13 @@ int linear_run(LinearShape q, const void* A, int64_t lda, const void* B, int64_t
     return rc != GEMM_OK ? rc : frc;
 }
 
-int linear_sizes(int64_t M, int64_t N, int64_t K)
+// M rows, the other sizes, and which of them is the output's columns.
+int linear_sizes(int64_t M, int64_t N, int64_t K, int64_t cols)
 {
     if (M < 0 || N < 0 || K < 0)
         return GEMM_ERR_INVALID_VALUE;
-    return M > kMaxRows || N > kMaxLd || K > kMaxLd ? GEMM_ERR_UNSUPPORTED_SHAPE : GEMM_OK;
+    return M > kMaxRows || N > kMaxLd || K > kMaxLd || (cols < kChunk && M > kMaxNarrowRows) ? GEMM_ERR_UNSUPPORTED_SHAPE
+                                                                                             : GEMM_OK;
 }
 
 bool known_act(int act) { return act >= GEMM_ACT_NONE && act <= GEMM_ACT_SILU; }
@@ -1261,7 +1270,7 @@ extern "C" {
 int gemm_linear_plan_cus(int64_t M, int64_t N, int64_t K, int product, int a_aligned, int b_aligned, int compute_units,
                          gemm_linear_plan_t* out)
 {
-    if (const int rc = linear_sizes(M, N, K))
+    if (const int rc = linear_sizes(M, N, K, product == GEMM_LINEAR_BWD_INPUT ? K : product == GEMM_LINEAR_BWD_WEIGHT ? kChunk : N))
         return rc;
     if (!out || compute_units < 1 || product < GEMM_LINEAR || product > GEMM_GATED_LINEAR_BWD_INPUT)
         return GEMM_ERR_INVALID_VALUE;
@@ -1301,7 +1310,7 @@ int gemm_linear(int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, con
                 const void* bias, int act, const void* residual, int64_t ldr, void* Z, int64_t ldz, void* Y, int64_t ldy,
                 void* workspace, int64_t workspace_bytes, void* stream)
 {
-    if (const int rc = linear_sizes(M, N, K))
+    if (const int rc = linear_sizes(M, N, K, N))
         return rc;
     if (!known_act(act))
         return GEMM_ERR_INVALID_VALUE;
@@ -1325,7 +1334,7 @@ int gemm_linear_bwd_input(int64_t M, int64_t N, int64_t K, const void* dY, int64
                           int act, const void* Z, int64_t ldz, const void* dres, int64_t lddr, void* dX, int64_t lddx,
                           void* workspace, int64_t workspace_bytes, void* stream)
 {
-    if (const int rc = linear_sizes(M, N, K))
+    if (const int rc = linear_sizes(M, N, K, K))
         return rc;
     if (!known_act(act))
         return GEMM_ERR_INVALID_VALUE;
@@ -1350,7 +1359,7 @@ int gemm_linear_bwd_weight(int64_t M, int64_t N, int64_t K, const void* dY, int6
                            void* dW, int64_t lddw, int dw_type, float* dbias, void* workspace, int64_t workspace_bytes,
                            void* stream)
 {
-    if (const int rc = linear_sizes(M, N, K))
+    if (const int rc = linear_sizes(M, N, K, kChunk))
         return rc;
     const bool fp32 = dw_type == GEMM_TYPE_FP32;
     if (!fp32 && dw_type != GEMM_TYPE_BF16)
@@ -1375,7 +1384,7 @@ int gemm_gated_linear(int64_t M, int64_t F, int64_t K, const void* X, int64_t ld
                       const void* bias, int act, void* GU, int64_t ldgu, void* Y, int64_t ldy, void* workspace,
                       int64_t workspace_bytes, void* stream)
 {
-    if (const int rc = linear_sizes(M, F, K))
+    if (const int rc = linear_sizes(M, F, K, F))
         return rc;
     if (!known_act(act))
         return GEMM_ERR_INVALID_VALUE;
@@ -1397,7 +1406,7 @@ int gemm_gated_linear_bwd_input(int64_t M, int64_t F, int64_t N, const void* dY,
                                 int act, const void* GU, int64_t ldgu, void* dGU, int64_t lddgu, void* Y, int64_t ldy,
                                 void* workspace, int64_t workspace_bytes, void* stream)
 {
-    if (const int rc = linear_sizes(M, F, N))
+    if (const int rc = linear_sizes(M, F, N, F))
         return rc;
     if (!known_act(act))
         return GEMM_ERR_INVALID_VALUE;

@@ -509,3 +509,26 @@ def test_two_layers_against_autograd(M, D, F, act):
     want.backward(dout.double())
     for got, ref64 in ((out, want.detach()), (dw2, w2d.grad), (db2, b2d.grad), (dw1, w1d.grad), (db1, b1d.grad), (dx, xd.grad)):
         assert float((got.double() - ref64).norm() / ref64.norm()) < 12 * ref.U16
+
+
+@pytest.mark.parametrize("M,N,K", [(400, 320, 6000), (300, 601, 1000), (64, 2056, 8200)])
+def test_results_on_the_host(M, N, K):
+    """Copied to the host right behind the call, pageable and pinned, by calls whose last
+    launch frees the kept memory: every copy is that call's result."""
+    g = gen(M + N + K)
+    xs = [rand(g, M, K) for _ in range(3)]
+    w = rand(g, N, K, size=K ** -0.5)
+    want = []
+    for x in xs:
+        y = bd.linear(x, w)
+        torch.cuda.synchronize()
+        want.append(y.clone().cpu())
+    assert not torch.equal(want[0], want[1])
+    pinned = torch.empty(M, N, dtype=BF16, pin_memory=True)
+    done = torch.cuda.Event()
+    for i in range(12):
+        assert torch.equal(bd.linear(xs[i % 3], w).cpu(), want[i % 3])
+        pinned.copy_(bd.linear(xs[(i + 1) % 3], w), non_blocking=True)
+        done.record()
+        done.synchronize()
+        assert torch.equal(pinned, want[(i + 1) % 3])

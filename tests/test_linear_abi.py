@@ -35,12 +35,15 @@ def dgated(M=64, F=256, N=512, dy=X, lddy=512, w=W, ldw=256, act=SILU, gu=Z, ldg
 
 
 BIG = (1 << 22) + 1
+NARROW = (1 << 28) + 1
 REFUSED = [
     # sizes, activations, types
     *((f, {k: -1}, BAD) for f in (linear, dinput, dweight) for k in "MNK"), (gated, {"F": -1}, BAD), (dgated, {"F": -1}, BAD),
     *((f, {"M": 1 << 31}, SHAPE) for f in (linear, dinput, dweight, gated, dgated)),
     *((f, {k: BIG}, SHAPE) for f in (linear, dinput, dweight) for k in "NK"), (gated, {"F": BIG}, SHAPE),
     (gated, {"K": BIG}, SHAPE), (dgated, {"F": BIG}, SHAPE), (dgated, {"N": BIG}, SHAPE),
+    (linear, {"M": NARROW, "N": 7}, SHAPE), (dinput, {"M": NARROW, "K": 7}, SHAPE), (gated, {"M": NARROW, "F": 7}, SHAPE),
+    (dgated, {"M": NARROW, "F": 1}, SHAPE),
     *((f, {"act": a}, BAD) for f in (linear, dinput, gated, dgated) for a in (-1, 5)),
     (dweight, {"t": bd.TYPE_FP8}, BAD), (dweight, {"t": 3}, BAD),
     # null pointers
@@ -243,3 +246,19 @@ def test_check_rejects_a_step():
     bad[3, 3] = float("nan")
     with pytest.raises(AssertionError):
         ref.check(bad, y, b)
+
+
+@pytest.mark.parametrize("product", list(bd.LINEAR_PRODUCTS))
+@pytest.mark.parametrize("cols", [1, 7, 8, 100])
+@pytest.mark.parametrize("even", [0, 1])
+def test_launches_stay_below_their_limit(product, cols, even):
+    """A launch holds fewer than 2^32 threads, at the most rows that are taken."""
+    rows = 1 << 22 if product == "linear_bwd_weight" else 1 << 28 if cols < 8 else (1 << 31) - 1
+    for inner in (1, 64, 1000):
+        sizes = {"linear_bwd_input": (rows, inner, cols), "linear_bwd_weight": (inner, rows, cols)}.get(product, (rows, cols, inner))
+        p = plan(*sizes, product, even, even)
+        assert p["grid"] * p["threads"] < 1 << 32, p
+    if product != "linear_bwd_weight" and cols < 8:
+        more = {"linear_bwd_input": (NARROW, 64, cols)}.get(product, (NARROW, cols, 64))
+        with pytest.raises(bd.GemmError):
+            plan(*more, product, even, even)
