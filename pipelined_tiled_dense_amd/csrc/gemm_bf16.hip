@@ -94,7 +94,6 @@
 
 #include <algorithm>
 #include <atomic>
-#include <cmath>
 #include <mutex>
 #include <type_traits>
 #include <utility>

@@ -900,7 +900,8 @@ struct LinearPlan {
 // their sums take through memory.  What every kind reads and writes alike is left out.
 double linear_time(const LinearShape& q, const LinearPlan& pl, int cus)
 {
-    const double items = (double)(pl.tiles * pl.splits), fill = items / cus;
+    const int64_t items = pl.tiles * pl.splits;
+    const double fill = (double)items / cus, rounds = (double)ceil_div(items, cus);
     const int64_t steps = ceil_div(pl.chunk, 64);
     const double sums = pl.splits > 1 ? 1e-6 * (double)pl.workspace : 0.0, copies =
         1e-6 * (double)((q.a_even ? 0 : pad_size(q.a_rows(), q.a_cols())) + (q.b_even ? 0 : pad_size(q.b_rows(), q.b_cols())));
@@ -912,10 +913,10 @@ double linear_time(const LinearShape& q, const LinearPlan& pl, int cus)
         if (pl.mf == 1)
             t = nb == 1 ? k * (0.27 + 0.28 * fill) : nb == 2 ? k * (0.4 + 0.35 * fill) : k * (0.8 + 1.0 * fill);
         else
-            t = std::ceil(fill) * (pl.mf == 2 ? 1.3 * k : 1.6 + 2.35 * k);
+            t = rounds * (pl.mf == 2 ? 1.3 * k : 1.6 + 2.35 * k);
         return (pl.mf == 4 ? 1.4 : 3.2) + t + (pl.splits > 1 ? 6.0 + 0.5 * sums : 0.0);
     }
-    const double padding = copies > 0 ? 2.5 + copies / 2.2 : 0.0, rounds = std::ceil(fill);
+    const double padding = copies > 0 ? 2.5 + copies / 2.2 : 0.0;
     // The weight's gradient reads both operands transposed.
     if (pl.kind == TILES_SMALL)
         return 3.0 + rounds * (4.3 + (q.at ? 0.47 : 0.43) * steps) + (pl.splits > 1 ? 5.3 + 0.2 * sums : 0.0) + padding;
@@ -929,6 +930,7 @@ LinearPlan linear_plan(const LinearShape& q, int cus)
 {
     LinearPlan best{};
     double least = 0;
+    const uint32_t steps = (uint32_t)ceil_div(q.K, 64);
     auto consider = [&](int kind, int mf, int nf) {
         LinearPlan pl{};
         pl.kind = kind;
@@ -939,9 +941,10 @@ LinearPlan linear_plan(const LinearShape& q, int cus)
         pl.tiles = ceil_div(q.M, pl.bm) * ceil_div(q.N, pl.bn);
         if (kind == TILES_WAVE && pl.tiles > kMaxWaveTiles)
             return;
-        for (int64_t s = 1; s <= kMaxSplits && (s == 1 || pl.tiles * s <= 2 * cus); ++s) {
-            pl.chunk = s == 1 ? q.K : ceil_div(ceil_div(q.K, s), 64) * 64;
-            pl.splits = ceil_div(q.K, pl.chunk);
+        for (uint32_t s = 1; s <= std::min<uint32_t>(kMaxSplits, steps) && (s == 1 || pl.tiles * s <= 2 * cus); ++s) {
+            const uint32_t per = (steps + s - 1) / s;
+            pl.chunk = s == 1 ? q.K : (int64_t)per * 64;
+            pl.splits = (steps + per - 1) / per;
             if (pl.splits < s)
                 continue;   // the same as for fewer
             pl.grid = kind == TILES_WAVE ? ceil_div(pl.tiles, 8) * 8 : std::min<int64_t>(pl.tiles * s, cus);
