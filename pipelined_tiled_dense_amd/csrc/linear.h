@@ -302,10 +302,11 @@ template <int MODE>
 struct LinearParams : Params {
     Epilogue e;
 
-    // What an epilogue reads and writes beside the accumulators bounds it, not its
-    // arithmetic: 8192 x 8192 over 4096 takes 387 us as a plain gradient, 420 through any of
-    // the activations (134 MB more), 458 with both factors' (268 MB more each way), since all
-    // workgroups reach theirs at about the same time, and then wait for memory.
+    // What an epilogue reads and writes beside the accumulators bounds it first: 8192 x 8192
+    // over 4096 takes 407 us as a plain gradient, 435 through relu and 437 through silu (134 MB
+    // more), 470 with both factors' (268 MB more each way), since all workgroups reach theirs
+    // at about the same time, and then wait for memory.  Activations with more steps add to that
+    // (gelu 450, and activations.h).
     //
     // The accumulators, 8 rows by 64 columns of each factor at a time, through the
     // wave's strip of LDS into rows, 8 consecutive columns a lane.  A rolled loop,
