@@ -17,13 +17,13 @@
 
 namespace {
 
-// x times y times a slope of at most 1.13: the slope goes with the larger of the two
-// first, so that neither a product overflows nor a small one is lost before the third
-// factor brings it back.
+// x times y times a slope of at most 1.13: half the slope goes with the larger of the two
+// first, so that neither a product overflows where the result does not, nor a small
+// one is lost before the third factor brings it back.
 __device__ __forceinline__ float times_slope(float x, float y, float slope)
 {
     const bool x_larger = __builtin_fabsf(x) > __builtin_fabsf(y);
-    return (x_larger ? x : y) * slope * (x_larger ? y : x);
+    return 2.0f * ((x_larger ? x : y) * (0.5f * slope) * (x_larger ? y : x));
 }
 
 // a(z) and a'(z) as value * f^3 and slope * f^3, where the two are too small for fp32: f is

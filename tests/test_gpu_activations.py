@@ -147,3 +147,27 @@ def test_values_at_every_value(gpu, act, M):
     yg = bd.gated_linear(x, both, activation=act)
     within(yg[:1].cpu()[0], value, err, "gated value of %s" % act)
     assert torch.equal(yg, yg[:1].expand(M, -1))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M", [3, 4096])
+@pytest.mark.parametrize("act", ["gelu", "gelu_tanh", "silu"])
+def test_largest_factors_beside_slopes_above_one(gpu, act, M):
+    """dg = t u act'(g) with t or u at the type's largest and a slope of up to 1.13: the
+    result is finite where the other factor is small, in whichever order."""
+    big = float(torch.finfo(BF16).max)
+    gates = torch.linspace(0.0, 6.0, 64).to(BF16).repeat(8)
+    for t, u in ((0.1, big), (big, 0.1), (1e-30, -big), (-big, 1e-30), (0.85, 3.2e38), (3.2e38, 0.85), (2e-38, big), (1.0, -2.9e38)):
+        F = gates.numel()
+        gu = torch.cat([gates, torch.full((F,), u).to(BF16)]).cuda().expand(M, -1).contiguous()
+        dy, w = torch.zeros(M, 64, dtype=BF16, device="cuda"), torch.zeros(64, F, dtype=BF16, device="cuda")
+        dy[:, 3], w[3] = t, 1.0
+        td, ud = dy[0, 3].double().cpu(), gu[0, F].double().cpu()
+        _, slope, _, err = formula(gates, act)
+        want = td * ud * slope
+        keep = want.abs() < 3.38e38                    # above, a bf16 result may be infinite
+        assert (keep | (slope > 1)).all() and keep.any()
+        dgu = bd.gated_linear_backward_input(dy, w, gu, activation=act)
+        got = dgu[0, :F].cpu()
+        within(got[keep], want[keep], ((td * ud).abs() * err + 8 * U32 * want.abs())[keep], "%g %g" % (t, u))
+        assert torch.equal(dgu, dgu[:1].expand(M, -1))
