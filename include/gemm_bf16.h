@@ -588,7 +588,9 @@ int gemm_swiglu_bwd(int64_t M, int64_t F, const void* dY, int64_t lddy,
  * small, and none under capture, is GEMM_ERR_SCRATCH, and nothing is enqueued.
  *
  * Activations and their slopes follow these formulas for every z, up to the rounding
- * of fp32; an infinity or a NaN gives what the formula gives.
+ * of fp32.  NaN gives NaN, and an infinity what the formula gives: a product of zero and
+ * infinity in it is NaN.  So gelu, gelu_tanh and silu are infinity at plus infinity and NaN at
+ * minus infinity, and their slopes NaN at both; relu is infinity and 0, its slope 1 and 0.
  * ------------------------------------------------------------------------- */
 enum {
     GEMM_ACT_NONE = 0,       /* z */

@@ -83,22 +83,22 @@ __device__ __forceinline__ Activated activated_low(int act, float z)
     const float zn = z == -__builtin_inff() ? __builtin_nanf("") : z;
     if (act == GEMM_ACT_GELU) {
         const float a = __builtin_fminf(-z, 40.0f), h = normal_tail(a);
-        return {__builtin_amdgcn_exp2f((-kLog2e / 6.0f) * (a * a)), zn * h, __builtin_fmaf(-kDensity, a, h)};
+        return {__builtin_amdgcn_exp2f((-kLog2e / 6.0f) * (a * a)), zn * h, __builtin_fmaf(kDensity, zn, h)};
     }
     const bool silu = act == GEMM_ACT_SILU;
     const float c = silu ? z : z < -30.0f ? -30.0f : z, c2 = c * c;   // exp(v) is 0 at -30, and z^3 may overflow
     const float v = silu ? z : c * __builtin_fmaf(kTanhB, c2, kTanhA);
-    const float zdv = silu ? zn : c * __builtin_fmaf(3.0f * kTanhB, c2, kTanhA);
+    const float zdv = silu ? zn : __builtin_fmaf(0.0f, zn, c * __builtin_fmaf(3.0f * kTanhB, c2, kTanhA));
     return {low_gate(v).f, zn, 1.0f + zdv};
 }
 
 template <bool SLOPE>
-__device__ __forceinline__ void logistic_usual(float z, float minus_v, float zdv, float& value, float& slope)
+__device__ __forceinline__ void logistic_usual(float z, float minus_v, float dv, float& value, float& slope)
 {
     const float e = __builtin_amdgcn_exp2f(minus_v * kLog2e), p = __builtin_amdgcn_rcpf(1.0f + e);
     value = z * p;
     if constexpr (SLOPE)
-        slope = __builtin_fmaf(zdv * (e * p), p, p);
+        slope = __builtin_fmaf(z * (e * p) * dv, p, p);
 }
 
 // f(i, a) for the activation a of z[i], i = 0 .. 7, and again with another a for the z
@@ -123,27 +123,28 @@ __device__ __forceinline__ void activate(int act, const float (&z)[kChunk], F&& 
     if (act == GEMM_ACT_SILU) {
 #pragma unroll
         for (int i = 0; i < kChunk; ++i) {
-            logistic_usual<SLOPE>(z[i], -z[i], z[i], u.value, u.slope);
+            logistic_usual<SLOPE>(z[i], -z[i], 1.0f, u.value, u.slope);
             f(i, u);
         }
     } else if (act == GEMM_ACT_GELU_TANH) {
 #pragma unroll
         for (int i = 0; i < kChunk; ++i) {
             const float z2 = z[i] * z[i];
-            const float c = __builtin_amdgcn_fmed3f(z[i], -10.0f, 30.0f);   // the slope is 1 there, and z^3 may overflow
+            const float c = __builtin_amdgcn_fmed3f(z[i], -10.0f, 30.0f);   // the slope is 1 there, and z^2 may overflow
             logistic_usual<SLOPE>(z[i], z[i] * __builtin_fmaf(-kTanhB, z2, -kTanhA),
-                                  c * __builtin_fmaf(3.0f * kTanhB * c, c, kTanhA), u.value, u.slope);
+                                  __builtin_fmaf(3.0f * kTanhB * c, c, kTanhA), u.value, u.slope);
             f(i, u);
         }
     } else {
 #pragma unroll
         for (int i = 0; i < kChunk; ++i) {
-            // The bounds keep infinity out of a product with zero; NaN comes through e.
+            // The bounds keep infinity out of the value's product with zero, which the slope's
+            // formula has; NaN comes through e.
             const float a = __builtin_amdgcn_fmed3f(__builtin_fabsf(z[i]), 0.0f, 30.0f), h = normal_tail(a);
             const float e = __builtin_amdgcn_exp2f((-0.5f * kLog2e) * (z[i] * z[i]));
             u.value = __builtin_fmaf(-a, h * e, __builtin_amdgcn_fmed3f(z[i], 0.0f, __builtin_inff()));
             if constexpr (SLOPE) {
-                const float tail = e * __builtin_fmaf(-kDensity, a, h);
+                const float tail = e * __builtin_fmaf(-kDensity, __builtin_fabsf(z[i]), h);
                 u.slope = z[i] > 0.0f ? 1.0f - tail : tail;
             }
             f(i, u);

@@ -171,3 +171,31 @@ def test_largest_factors_beside_slopes_above_one(gpu, act, M):
         got = dgu[0, :F].cpu()
         within(got[keep], want[keep], ((td * ud).abs() * err + 8 * U32 * want.abs())[keep], "%g %g" % (t, u))
         assert torch.equal(dgu, dgu[:1].expand(M, -1))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,F", [(3, 64), (4096, 4096)])
+@pytest.mark.parametrize("act", ACTS)
+def test_infinities_and_nan(gpu, act, M, F):
+    """What the formulas give: z Phi(z) at minus infinity and z phi(z) at both have a product of
+    zero and infinity, and so have the logistic ones.  Finite values next to them stay."""
+    inf, nan, big = float("inf"), float("nan"), float(torch.finfo(BF16).max)
+    at = torch.tensor([inf, -inf, nan, big, -big, 1e20, -1e20, 0.0])
+    values = {None: [inf, -inf, nan], "relu": [inf, 0.0, nan]}.get(act, [inf, nan, nan])
+    slopes = {None: [1.0] * 3, "relu": [1.0, 0.0, nan]}.get(act, [nan] * 3)
+    half = 0.0 if act == "relu" else 0.5
+    values += [big, -big, 1e20, -1e20, 0.0] if act is None else [big, 0.0, 1e20, 0.0, 0.0]
+    slopes += [1.0] * 5 if act is None else [1.0, 0.0, 1.0, 0.0, half]
+    same = lambda got, want, what: torch.testing.assert_close(  # noqa: E731
+        got, torch.tensor(want).to(BF16).repeat(F // 8).cuda().expand(M, F), rtol=0, atol=0, equal_nan=True, msg=what)
+    z = at.to(BF16).repeat(F // 8).cuda()
+    dy, wd = torch.zeros(M, 64, dtype=BF16, device="cuda"), torch.zeros(64, F, dtype=BF16, device="cuda")
+    dy[:, 3], wd[3] = 1.0, 1.0
+    gu = torch.cat([z, torch.ones_like(z)]).expand(M, -1).contiguous()
+    same(bd.linear_backward_input(dy, wd, preactivation=gu[:, :F] if act else None, activation=act), slopes, "slope")
+    dgu, y = bd.gated_linear_backward_input(dy, wd, gu, activation=act, return_y=True)
+    same(dgu[:, :F], slopes, "dg"), same(dgu[:, F:], values, "du"), same(y, values, "y again")
+    # Forward: the sums themselves are infinite, through a bias.
+    x, w = torch.zeros(M, 64, dtype=BF16, device="cuda"), torch.zeros(2 * F, 64, dtype=BF16, device="cuda")
+    same(bd.linear(x, w[:F], bias=z, activation=act), values, "value")
+    same(bd.gated_linear(x, w, bias=torch.cat([z, torch.ones_like(z)]), activation=act), values, "gated value")
