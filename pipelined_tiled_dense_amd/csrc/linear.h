@@ -1057,6 +1057,17 @@ int linear_run(LinearShape q, const void* A, int64_t lda, const void* B, int64_t
     LinearParams<MODE> p;
     memset((void*)&p, 0, sizeof p);
     p.e = e;
+    // Leading dimensions that do not count, a single row's and an absent operand's, may be
+    // anything: TileAt's offsets take that of 8 rows, and `far` below all of them.
+    auto counted = [&](int64_t& ld, const void* ptr, int64_t width) {
+        if (q.M <= 1 || !ptr)
+            ld = width;
+    };
+    const int64_t both = 2 * e.N;
+    counted(p.e.ld_in0, e.in0, MODE == FUSE_DGATED ? both : e.N);
+    counted(p.e.ld_in1, e.in1, e.N);
+    counted(p.e.ld_out0, e.out0, MODE == FUSE_DGATED ? both : e.N);
+    counted(p.e.ld_out1, e.out1, MODE == FUSE_GATED ? both : e.N);
     // Operands as the tiles read them: rows on 16-byte boundaries, of whole 16-byte
     // chunks, at most 2^22 elements apart.
     const int64_t a_rows = q.a_rows(), a_cols = q.a_cols(), b_rows = q.b_rows(), b_cols = q.b_cols();
@@ -1133,7 +1144,7 @@ int linear_run(LinearShape q, const void* A, int64_t lda, const void* B, int64_t
     const int64_t a_bytes = pad_a ? pad_size(a_rows, a_cols) : 0, b_bytes = pad_b ? pad_size(b_rows, b_cols) : 0;
     // The tiles' epilogue addresses rows by 32-bit offsets; others' sums go through the
     // second launch.
-    const bool far = !wave && std::max({e.ld_in0, e.ld_in1, e.ld_out0, e.ld_out1}) > kMaxTileLd;
+    const bool far = !wave && std::max({p.e.ld_in0, p.e.ld_in1, p.e.ld_out0, p.e.ld_out1}) > kMaxTileLd;
     const int64_t sums_bytes = pl.splits > 1 || !far ? pl.workspace : pl.tiles * pl.bm * pl.bn * q.factors * 4;
     const int64_t bytes = a_bytes + b_bytes + runs_bytes + sums_bytes;
     int rc = GEMM_OK;
