@@ -681,8 +681,9 @@ typedef struct gemm_linear_plan {
     int64_t grid;             /* workgroups of the main launch */
     int64_t workspace_bytes;  /* the chunks' sums (0 with one chunk) */
     int64_t pad_bytes;        /* zero-padded copies of operands that the tiles cannot read */
-    int64_t scratch_bytes;    /* temporary memory in all: the two, and dbias's sums of a weight's gradient.  Outputs
-                                 or what an epilogue reads more than 2^27 elements apart may take more. */
+    int64_t scratch_bytes;    /* temporary memory in all: the two, and dbias's sums of a weight's gradient.  Where rows of
+                                 outputs or of what an epilogue reads are more than 2^27 elements apart, tiles in one
+                                 chunk take tiles * rows * cols * 4 bytes more, twice that for the gated product. */
 } gemm_linear_plan_t;
 
 /* The products a plan is asked for, with the sizes of their entry points (F as N for the gated ones). */

@@ -118,3 +118,118 @@ def test_absent_operands_need_no_memory(M, N, K):
             assert call(ld, ws.data_ptr(), n) == bd.GEMM_OK, (name, ld)
             assert torch.equal(out, plain()), (name, ld)
     assert tiles >= 3
+
+
+# -- rows further apart than a tile's offsets reach -----------------------------------------
+FAR = (1 << 27) + 8
+
+
+def far(x, ld=FAR):
+    """A view of x's values in rows that far apart; what lies between is not written."""
+    view = torch.empty((x.shape[0] - 1) * ld + x.shape[1], dtype=x.dtype, device="cuda").as_strided(x.shape, (ld, 1))
+    view.copy_(x)
+    return view
+
+
+def planned(product, M, N, K):
+    """The plan, and the temporary memory of a call whose epilogue is out of the tiles' reach: of
+    one chunk, the sums of every tile beside what the plan says."""
+    p = bd.gemm_linear_plan_cus(*((M, K, N) if product == "linear_bwd_input" else (M, N, K)), product, 1, 1, units())
+    assert not p["waves_share_k"]
+    sums = p["tiles"] * p["rows"] * p["cols"] * 4 * (2 if product == "gated_linear" else 1)
+    return p, p["scratch_bytes"] + (sums if p["k_splits"] == 1 else 0)
+
+
+def run(call, need):
+    """The call in a workspace of exactly `need` bytes, which less is refused for."""
+    ws = torch.full((need + 512,), 0xA5, dtype=torch.uint8, device="cuda")
+    assert call(ws.data_ptr(), need - 256) == bd.GEMM_ERR_SCRATCH
+    assert call(ws.data_ptr(), need) == bd.GEMM_OK
+    torch.cuda.synchronize()
+    assert (ws[need:] == 0xA5).all()
+
+
+# 33 rows (a far one takes 9 GB) of 128- and 192-row tiles (256 where paired), one chunk; and k chunks.
+WIDE = [(33, 32768, 64), (33, 65536, 64), (33, 8192, 8192)]
+
+
+@pytest.mark.parametrize("which", ["residual", "z", "y", "y over residual"])
+@pytest.mark.parametrize("M,N,K", WIDE)
+def test_far_linear(M, N, K, which):
+    plan, need = planned("linear", M, N, K)
+    g = gen(N)
+    x, w, r = rand(g, M, K), rand(g, N, K, size=K ** -0.5), rand(g, M, N)
+    want = ref.linear(x.double(), w.double(), None, "silu", r.double())
+    at = lambda name, t: far(t) if name in which else t  # noqa: E731
+    res, z, y = at("residual", r), at("z", torch.zeros_like(r)), None
+    y = res if "over" in which else at("y", torch.zeros_like(r))
+    run(lambda m, n: bd.gemm_linear(M, N, K, x.data_ptr(), K, w.data_ptr(), K, None, 4, res.data_ptr(), res.stride(0), z.data_ptr(),
+                                    z.stride(0), y.data_ptr(), y.stride(0), stream(), m, n), need)
+    ref.check(y, *want["y"], "y")
+    ref.check(z, *want["z"], "z")
+
+
+@pytest.mark.parametrize("which", ["z", "dres", "dx", "dx over z"])
+@pytest.mark.parametrize("M,N,K", WIDE)
+def test_far_linear_backward_input(M, N, K, which):
+    plan, need = planned("linear_bwd_input", M, N, K)
+    g = gen(N + 1)
+    dy, w, z, r = rand(g, M, K), rand(g, K, N, size=K ** -0.5), rand(g, M, N), rand(g, M, N)
+    want = ref.linear_backward_input(dy.double(), w.double(), z.double(), "gelu", r.double())
+    zs = far(z) if which in ("z", "dx over z") else z
+    rs = far(r) if which == "dres" else r
+    dx = zs if "over" in which else far(torch.zeros_like(z)) if which == "dx" else torch.zeros_like(z)
+    run(lambda m, n: bd.gemm_linear_bwd_input(M, K, N, dy.data_ptr(), K, w.data_ptr(), N, bd.ACTIVATIONS["gelu"], zs.data_ptr(),
+                                              zs.stride(0), rs.data_ptr(), rs.stride(0), dx.data_ptr(), dx.stride(0), stream(), m, n), need)
+    ref.check(dx, *want, "dx")
+
+
+@pytest.mark.parametrize("which", ["gu", "y"])
+@pytest.mark.parametrize("M,F,K", [(33, 14336, 64), (33, 32768, 64), (33, 4096, 8192)])
+def test_far_gated_linear(M, F, K, which):
+    plan, need = planned("gated_linear", M, F, K)
+    g = gen(F + 2)
+    x, w = rand(g, M, K), rand(g, 2 * F, K, size=K ** -0.5)
+    want = ref.gated(x.double(), w.double(), None, "silu")
+    y, gu = torch.zeros(M, F, dtype=BF16, device="cuda"), torch.zeros(M, 2 * F, dtype=BF16, device="cuda")
+    y, gu = (far(y), gu) if which == "y" else (y, far(gu))
+    run(lambda m, n: bd.gemm_gated_linear(M, F, K, x.data_ptr(), K, w.data_ptr(), K, None, 4, gu.data_ptr(), gu.stride(0), y.data_ptr(),
+                                          y.stride(0), stream(), m, n), need)
+    ref.check(y, *want["y"], "y")
+    ref.check(gu, *want["gu"], "gu")
+
+
+@pytest.mark.parametrize("which", ["gu", "dgu", "dgu over gu", "y"])
+@pytest.mark.parametrize("M,F,N", WIDE)
+def test_far_gated_linear_backward_input(M, F, N, which):
+    plan, need = planned("gated_linear_bwd_input", M, F, N)
+    g = gen(F + 3)
+    dy, w, gu = rand(g, M, N), rand(g, N, F, size=N ** -0.5), rand(g, M, 2 * F)
+    want = ref.gated_backward_input(dy.double(), w.double(), gu.double(), "silu")
+    gs = far(gu) if which in ("gu", "dgu over gu") else gu
+    d = gs if "over" in which else far(torch.zeros_like(gu)) if which == "dgu" else torch.zeros_like(gu)
+    y = torch.zeros(M, F, dtype=BF16, device="cuda")
+    y = far(y) if which == "y" else y
+    run(lambda m, n: bd.gemm_gated_linear_bwd_input(M, F, N, dy.data_ptr(), N, w.data_ptr(), F, 4, gs.data_ptr(), gs.stride(0),
+                                                    d.data_ptr(), d.stride(0), y.data_ptr(), y.stride(0), stream(), m, n), need)
+    ref.check(d, *want["dgu"], "dgu")
+    ref.check(y, *want["y"], "y")
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("M,N,K", [(64, 3, 32768), (64, 2, 65536), (8192, 4, 8192)])
+def test_far_weight(M, N, K, dtype):
+    p = bd.gemm_linear_plan_cus(M, N, K, "linear_bwd_weight", 0, 1, units())
+    assert not p["waves_share_k"]
+    sums = p["tiles"] * p["rows"] * p["cols"] * 4
+    need = p["scratch_bytes"] + (sums if p["k_splits"] == 1 else 0)
+    g = gen(K + 4)
+    dy, x = rand(g, M, N), rand(g, M, K)
+    want, err = ref.product(dy.double().t(), x.double())
+    dw = far(torch.zeros(N, K, dtype=dtype, device="cuda"))
+    code = bd.TYPE_FP32 if dtype is F32 else bd.TYPE_BF16
+    db = torch.empty(N, device="cuda")
+    run(lambda m, n: bd.gemm_linear_bwd_weight(M, N, K, dy.data_ptr(), N, x.data_ptr(), K, dw.data_ptr(), FAR, code, db.data_ptr(),
+                                               stream(), m, n), need)
+    ref.check(dw, want, err if dtype is F32 else ref.rounded(want, err), "dw")
+    ref.check(db, dy.double().sum(0), (M + 4) * ref.U32 * dy.double().abs().sum(0), "dbias")
