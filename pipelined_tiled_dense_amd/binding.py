@@ -622,9 +622,14 @@ def _linear_call(torch, f, args, s, product, M, N, K, a, lda, b, ldb):
         if d not in _units:
             _units[d] = torch.cuda.get_device_properties(d).multi_processor_count
         even = lambda x, ld: x.data_ptr() % 16 == 0 and (x.shape[0] <= 1 or (ld % 8 == 0 and ld <= 1 << 22))  # noqa: E731
-        n = gemm_linear_plan_cus(M, N, K, product, even(a, lda), even(b, ldb), _units[d])["scratch_bytes"]
+        plan = gemm_linear_plan_cus(M, N, K, product, even(a, lda), even(b, ldb), _units[d])
+        n = plan["scratch_bytes"]
         w = torch.empty(n, dtype=torch.uint8, device=a.device)
         rc = f(*args, w.data_ptr(), n, s)
+        if rc == GEMM_ERR_SCRATCH:   # rows out of the tiles' reach
+            n += plan["tiles"] * plan["rows"] * plan["cols"] * (8 if product == "gated_linear" else 4)
+            w = torch.empty(n, dtype=torch.uint8, device=a.device)
+            rc = f(*args, w.data_ptr(), n, s)
     if rc != GEMM_OK:
         raise GemmError(rc, "gemm_" + product)
 

@@ -233,3 +233,31 @@ def test_far_weight(M, N, K, dtype):
                                                stream(), m, n), need)
     ref.check(dw, want, err if dtype is F32 else ref.rounded(want, err), "dw")
     ref.check(db, dy.double().sum(0), (M + 4) * ref.U32 * dy.double().abs().sum(0), "dbias")
+
+
+@pytest.mark.parametrize("M,N,K", WIDE)
+def test_far_rows_under_capture(M, N, K):
+    """A captured call whose residual, preactivation or [g, u] is that far apart: torch's memory is
+    as much as it takes, and every replay gives the eager result."""
+    g = gen(N + 5)
+    x, w, wt = rand(g, M, K), rand(g, N, K, size=K ** -0.5), rand(g, K, N, size=K ** -0.5)
+    r, gu = far(rand(g, M, N)), far(rand(g, M, 2 * N))
+    calls = lambda: [bd.linear(x, w, activation="silu", residual=r), bd.linear_backward_input(x, wt, preactivation=r, activation="gelu"),  # noqa: E731
+                     bd.gated_linear_backward_input(x, wt, gu)]
+    want = [t.clone() for t in calls()]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side):
+        with torch.cuda.graph(graph, stream=side):
+            out = calls()
+    for _ in range(3):
+        for t in out:
+            t.fill_(0.0)
+        for a, b in zip(calls(), want):
+            assert torch.equal(a, b)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(out, want):
+            assert torch.equal(a, b)
