@@ -277,10 +277,10 @@ __device__ __forceinline__ void epilogue_finish(const Epilogue& e, const Epilogu
 // of them takes 0.84 of the time, for sizes that leave fewer compute units idle so
 // (6952 x 1344 x 5952: 222 tiles 103 us, 168 of 256 rows 123; 4088 x 7608 x 1728: 3
 // rounds 116, 2 of 256 rows 102).
-// 128 x 128 tiles on a four-stage ring, 8 waves, where those give the compute units
-// too little to share (1936 x 1024 x 1216: 15 us, 29 in tiles of 192 rows and k chunks;
-// 1400 x 2272 x 3200: 29 and 39; but 8200 x 1856 x 960 46 and 47, 6952 x 1344 x 5952 139
-// and 103).  A paired B needs both factors' 64 columns in a wave.
+// 128 x 128 tiles on a four-stage ring, 8 waves (4 where B is paired: a wave needs both
+// factors' 64 columns), where those give the compute units too little to share (1936 x
+// 1024 x 1216: 15 us, 29 in tiles of 192 rows and k chunks; 1400 x 2272 x 3200: 29 and
+// 39; but 8200 x 1856 x 960 46 and 47, 6952 x 1344 x 5952 139 and 103).
 enum { TILES_BIG, TILES_192, TILES_SMALL, TILES_WAVE };
 
 template <bool BT_, bool AT_, bool PAIRED_, int KIND_>
@@ -295,6 +295,9 @@ struct LinearCfg<BT_, AT_, PAIRED_, TILES_SMALL>
     : Cfg<128, 128, 64, 4, 4, PAIRED_ ? 1 : 2, SYNC_BARRIER, BT_, 0, false, 16> {
     static constexpr bool AT = AT_, PAIRED = PAIRED_, ANY_SIZE = true;
 };
+static_assert(LinearCfg<true, false, false, TILES_BIG>::THREADS == 512 && LinearCfg<true, false, true, TILES_BIG>::THREADS == 512 &&
+                  LinearCfg<true, false, false, TILES_192>::THREADS == 512,
+              "8 waves, as k_linear_wave (gemm_linear_plan_cus)");
 
 // Sums of the k chunks: chunk sp's of the launch's u-th tile are piece sp * span +
 // u of the workspace, a tile's rows (of both factors, one after the other) in fp32.
@@ -1309,7 +1312,9 @@ int gemm_linear_plan_cus(int64_t M, int64_t N, int64_t K, int product, int a_ali
     out->rows = pl.bm;
     out->cols = pl.bn;
     out->waves_share_k = pl.kind == TILES_WAVE;
-    out->threads = 512;
+    out->threads = pl.kind != TILES_SMALL ? kWaves * 64
+                   : q.factors == 2       ? LinearCfg<true, false, true, TILES_SMALL>::THREADS
+                                          : LinearCfg<true, false, false, TILES_SMALL>::THREADS;
     out->tiles = pl.tiles;
     out->k_splits = pl.splits;
     out->k_chunk = pl.chunk;
