@@ -2636,7 +2636,8 @@ struct WsBlock {
     char* ptr = nullptr;
     int64_t bytes = 0;
     hipStream_t stream = nullptr;  // stream of the block's last use
-    hipEvent_t done = nullptr;     // recorded on `stream` right after that use
+    hipEvent_t events[2] = {};     // [0], and [1] without a release to the host's memory (see TempMem)
+    hipEvent_t done = nullptr;     // the one recorded on `stream` right after that use
     bool busy = false;             // taken by a call that has not handed it back
 };
 
@@ -2719,7 +2720,17 @@ int device_info(int* cus, hipMemPool_t* pool = nullptr, char** scratch_ptr = nul
 // copies) comes from.  Kept (fixed == nullptr): the device's reusable blocks
 // (temp_take).  Fixed: consecutive pieces of this device's scratch region,
 // taken in order and never released; nothing is allocated or freed.
+//
+// device_done: a block's completion event is one that releases to the device
+// only.  It is the completion of the call's last kernel, so what that kernel
+// wrote is then released to the host's memory by whatever the host waits with
+// (a stream, the device, a later event, a copy).  Nobody but this library
+// waits with the block's own event, and only before kernels use the block
+// again.  The next kernel on the stream starts 2 us sooner.  For calls whose
+// results are device memory by contract and tested in each of these ways: the
+// linear layers; the others keep the full release.
 struct TempMem {
+    bool device_done = false;
     DeviceInfo* info = nullptr;
     hipMemPool_t pool = nullptr;
     char* fixed = nullptr;
@@ -2729,6 +2740,13 @@ struct TempMem {
 int64_t align256(int64_t b)
 {
     return (b + 255) & ~(int64_t)255;
+}
+
+void release_events(const WsBlock& b)
+{
+    for (hipEvent_t e : b.events)
+        if (e)
+            (void)hipEventDestroy(e);
 }
 
 hipError_t pool_alloc(const TempMem& t, void** p, int64_t bytes, hipStream_t s)
@@ -2791,15 +2809,14 @@ int temp_take(TempMem& t, int64_t bytes, hipStream_t s, void** p, hipEvent_t* do
         while (size < bytes)
             size <<= 1;
         WsBlock b;
-        // Nothing but the device's kernels reads a block: without the release to the
-        // host's memory the next kernel on the stream starts 2 us sooner.
-        if (hipEventCreateWithFlags(&b.done, hipEventDisableTiming | hipEventDisableSystemFence) != hipSuccess) {
+        if (hipEventCreateWithFlags(&b.events[0], hipEventDisableTiming) != hipSuccess) {
             (void)hipGetLastError();
             return GEMM_ERR_DEVICE;
         }
         void* q = nullptr;
-        if (pool_alloc(t, &q, size, s) != hipSuccess || !q) {
-            (void)hipEventDestroy(b.done);
+        if (hipEventCreateWithFlags(&b.events[1], hipEventDisableTiming | hipEventDisableSystemFence) != hipSuccess ||
+            pool_alloc(t, &q, size, s) != hipSuccess || !q) {
+            release_events(b);
             (void)hipGetLastError();
             return GEMM_ERR_DEVICE;
         }
@@ -2810,6 +2827,7 @@ int temp_take(TempMem& t, int64_t bytes, hipStream_t s, void** p, hipEvent_t* do
     }
     v[best].busy = true;
     v[best].stream = s;
+    v[best].done = v[best].events[t.device_done];
     *p = v[best].ptr;
     if (done)
         *done = v[best].done;
@@ -3344,7 +3362,7 @@ int gemm_bf16_release_workspaces(void)
         // A block is busy only while a call on another thread enqueues its
         // work; that call still owns it.
         if (!b.busy && hipFreeAsync(b.ptr, nullptr) == hipSuccess) {
-            (void)hipEventDestroy(b.done);
+            release_events(b);
             continue;
         }
         if (!b.busy) {

@@ -1256,6 +1256,7 @@ int linear_enqueue(const LinearShape& q, const void* A, int64_t lda, const void*
 {
     int cus = 0;
     TempMem tm;
+    tm.device_done = true;
     if (const int rc = device_info(&cus, &tm.pool, nullptr, &tm.info))
         return rc;
     if (workspace) {
