@@ -1629,7 +1629,7 @@ __device__ __forceinline__ void poison_tile(typename C::Acc (&acc)[C::FM][C::FN]
 // P: Params, whose tiles are rounded and stored as they are, or a type derived
 // from it with a store_tile of its own (the linear layers' epilogues).
 template <class C, bool LONGK, bool EDGE, class P = Params>
-__global__ void __launch_bounds__(C::THREADS, 2) k_gemm(P p)
+__global__ void __launch_bounds__(C::THREADS) k_gemm(P p)
 {
     static_assert(!C::PRODUCERS, "configs with loader waves use k_gemm_ws / k_gemm_pp");
     __shared__ __attribute__((aligned(1024))) char smem_raw[C::LDS_BYTES];
