@@ -41,18 +41,18 @@ __device__ __forceinline__ Sigmoid sigmoid(float x)
     return x < 0.0f ? Sigmoid{tr, r} : Sigmoid{r, tr};
 }
 
-// w / (1 + exp(-x)) alone, in fewer steps (the 8-bit forward kernel, which takes
-// silu(x) * u from it, is bound by its vector instructions as much as by memory),
-// for x from kLowGate on, where exp(-x) stays below 2^127.7.  The denominator is
-// taken times 1/4, so that its reciprocal stays a normal number, which v_rcp_f32
-// needs, and w with it, so that no product passes |w|; a Newton step corrects the reciprocal
+// silu(x) * u alone, in fewer steps (the 8-bit forward kernel is bound by its
+// vector instructions as much as by memory): x u / (1 + exp(-x)) for x from
+// kLowGate on, where exp(-x) stays below 2^127.7.  The denominator is taken times
+// 1/4, so that its reciprocal stays a normal number, which v_rcp_f32 needs, and x
+// with it, so that no product passes |x|; a Newton step corrects the reciprocal
 // (its ulp alone turned twice as many 8-bit roundings as the other steps; 3 us at
 // 8192 x 8192).
 constexpr float kLowGate = -88.5f;
 // The gradients': higher, so that u s stays a normal number for every u that matters.
 constexpr float kLowGateGrad = -40.0f;
 
-__device__ __forceinline__ float logistic_times(float x, float w)
+__device__ __forceinline__ float silu_times(float x, float u)
 {
     constexpr float kLog2e = 0x1.715476p+0f, kLog2eRest = 0x1.4ae0cp-26f, kLn2 = 0x1.62e430p-1f;
     const float nx = x > 150.0f ? -150.0f : -x;
@@ -62,10 +62,8 @@ __device__ __forceinline__ float logistic_times(float x, float w)
     const float e = __builtin_fmaf(e0, rest * kLn2, e0);
     const float d = __builtin_fmaf(e, 0.25f, 0.25f), r0 = __builtin_amdgcn_rcpf(d);
     const float r = __builtin_fmaf(__builtin_fmaf(-d, r0, 1.0f), r0, r0);
-    return (0.25f * w) * r;
+    return (0.25f * x) * r * u;
 }
-
-__device__ __forceinline__ float silu_times(float x, float u) { return logistic_times(x, x) * u; }
 
 // Below these gates 1 + exp(-x) is exp(-x) to fp32, and exp(x) the third power of f =
 // exp(x / 3), a normal number: each of the factors beside exp(x) takes an f first,
