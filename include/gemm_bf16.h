@@ -203,7 +203,10 @@ typedef struct gemm_bf16_plan {
  * GPU: a stream-ordered free (hipFreeAsync) returns only after the stream's
  * queued work has finished, which is why they keep their blocks.  Under
  * graph capture the memory is allocated and freed inside the captured graph
- * instead.  A failed allocation returns GEMM_ERR_DEVICE.
+ * instead; so it is for gemm_bf16_bt, gemm_fp8_bt and gemm_rms_norm_bwd.  A graph
+ * of several such nodes (of calls that no longer make any: the linear layers)
+ * has ended in an illegal access on replay once, for a cause that is not known:
+ * gemm_bf16_noalloc, and entry points with a workspace, make none.  A failed allocation returns GEMM_ERR_DEVICE.
  * gemm_bf16_workspace_info reports what is kept.
  *
  * Returns GEMM_OK once the work is enqueued, else a negative status.
@@ -539,6 +542,21 @@ int gemm_rms_norm_bwd(int64_t M, int64_t D, const void* dY, int64_t lddy,
                       const void* H, int64_t ldh, const void* weight, const float* rstd,
                       const void* dres, int64_t lddr, void* dX, int64_t lddx,
                       float* dweight, void* stream);
+
+/*
+ * gemm_rms_norm_bwd_given: the same, with the caller's temporary memory as the linear
+ * layers below take it: `workspace` of at least gemm_rms_norm_bwd_scratch_cus bytes on a device of
+ * that many compute units, or NULL for memory that the library keeps.  Under graph
+ * capture it has to be given where any is needed (GEMM_ERR_SCRATCH else, and nothing
+ * is enqueued): the graph then holds no memory of its own.
+ */
+int gemm_rms_norm_bwd_given(int64_t M, int64_t D, const void* dY, int64_t lddy,
+                            const void* H, int64_t ldh, const void* weight, const float* rstd,
+                            const void* dres, int64_t lddr, void* dX, int64_t lddx,
+                            float* dweight, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Bytes (0 for a few rows), or a negative status. */
+int64_t gemm_rms_norm_bwd_scratch_cus(int64_t M, int64_t D, int compute_units);
 
 /*
  * gemm_swiglu: y = g / (1 + exp(-g)) * u for bf16 GU (M x 2F, ldgu >= 2F; row

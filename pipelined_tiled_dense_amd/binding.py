@@ -121,6 +121,9 @@ def library() -> ctypes.CDLL:
         lib.gemm_quantize_fp8.argtypes = [i64, i64, p, i64, p, i64, p, i64, i32, i32, p]
         lib.gemm_rms_norm.argtypes = [i64, i64, p, i64, p, i64, p, ctypes.c_float, p, i64, p, i64, i32, p, i64, p, p]
         lib.gemm_rms_norm_bwd.argtypes = [i64, i64, p, i64, p, i64, p, p, p, i64, p, i64, p, p]
+        lib.gemm_rms_norm_bwd_given.argtypes = [i64, i64, p, i64, p, i64, p, p, p, i64, p, i64, p, p, i64, p]
+        lib.gemm_rms_norm_bwd_scratch_cus.argtypes = [i64, i64, i32]
+        lib.gemm_rms_norm_bwd_scratch_cus.restype = i64
         lib.gemm_swiglu.argtypes = [i64, i64, p, i64, p, i64, i32, p, i64, p]
         lib.gemm_swiglu_bwd.argtypes = [i64, i64, p, i64, p, i64, p, i64, p]
         lib.gemm_fp8_plan_cus.argtypes = [i64, i64, i64, i32, i32, i32, i32, i32, ctypes.POINTER(Fp8Plan)]
@@ -131,6 +134,7 @@ def library() -> ctypes.CDLL:
         lib.gemm_gated_linear_bwd_input.argtypes = [i64, i64, i64, p, i64, p, i64, i32, p, i64, p, i64, p, i64, p, i64, p]
         lib.gemm_linear_plan_cus.argtypes = [i64, i64, i64, i32, i32, i32, i32, ctypes.POINTER(LinearPlan)]
         for name in ("gemm_fp8_bt", "gemm_fp8_plan_cus", "gemm_quantize_fp8", "gemm_rms_norm", "gemm_rms_norm_bwd",
+                     "gemm_rms_norm_bwd_given",
                      "gemm_swiglu", "gemm_swiglu_bwd", "gemm_linear", "gemm_linear_bwd_input", "gemm_linear_bwd_weight",
                      "gemm_gated_linear", "gemm_gated_linear_bwd_input", "gemm_linear_plan_cus"):
             getattr(lib, name).restype = i32
@@ -247,6 +251,19 @@ def gemm_rms_norm(M, D, X, ldx, residual, ldr, weight, eps, H, ldh, Y, ldy, y_ty
 
 def gemm_rms_norm_bwd(M, D, dY, lddy, H, ldh, weight, rstd, dres, lddr, dX, lddx, dweight, stream) -> int:
     return library().gemm_rms_norm_bwd(M, D, dY, lddy, H, ldh, weight, rstd, dres, lddr, dX, lddx, dweight, stream)
+
+
+def gemm_rms_norm_bwd_given(M, D, dY, lddy, H, ldh, weight, rstd, dres, lddr, dX, lddx, dweight, stream, workspace=None,
+                            workspace_bytes=0) -> int:
+    return library().gemm_rms_norm_bwd_given(M, D, dY, lddy, H, ldh, weight, rstd, dres, lddr, dX, lddx, dweight, workspace,
+                                             workspace_bytes, stream)
+
+
+def gemm_rms_norm_bwd_scratch_cus(M, D, compute_units) -> int:
+    n = library().gemm_rms_norm_bwd_scratch_cus(M, D, compute_units)
+    if n < 0:
+        raise GemmError(n, "gemm_rms_norm_bwd_scratch_cus")
+    return n
 
 
 def gemm_swiglu(M, F, GU, ldgu, Y, ldy, y_type, scale, lds, stream) -> int:
@@ -397,6 +414,15 @@ def _current(torch, x, *others):
     return torch._C._cuda_getCurrentRawStream(d)
 
 
+_units = {}
+
+
+def _compute_units(torch, d):
+    if d not in _units:
+        _units[d] = torch.cuda.get_device_properties(d).multi_processor_count
+    return _units[d]
+
+
 def _on_stream(stream, tensors, call):
     """``call`` with ``stream`` as the current stream, for which it then
     allocates; the tensors it reads are marked as used there."""
@@ -542,9 +568,14 @@ def rms_norm_backward(dy, h, weight, rstd, *, dresidual=None, stream=None):
         _shaped("dresidual", dresidual, M, D)
     s = _current(torch, dy, h, weight, rstd, dresidual)
     dx, dweight = torch.empty(M, D, dtype=bf16, device=dev), torch.empty(D, dtype=torch.float32, device=dev)
-    _done(library().gemm_rms_norm_bwd(M, D, dy.data_ptr(), lddy, h.data_ptr(), ldh, weight.data_ptr(), rstd.data_ptr(),
-                                      None if dresidual is None else dresidual.data_ptr(), lddr, dx.data_ptr(), D,
-                                      dweight.data_ptr(), s), "gemm_rms_norm_bwd")
+    args = (M, D, dy.data_ptr(), lddy, h.data_ptr(), ldh, weight.data_ptr(), rstd.data_ptr(),
+            None if dresidual is None else dresidual.data_ptr(), lddr, dx.data_ptr(), D, dweight.data_ptr())
+    rc = library().gemm_rms_norm_bwd_given(*args, None, 0, s)
+    if rc == GEMM_ERR_SCRATCH:   # a capturing stream: see _linear_call
+        n = gemm_rms_norm_bwd_scratch_cus(M, D, _compute_units(torch, dy.get_device()))
+        w = torch.empty(n, dtype=torch.uint8, device=dev)
+        rc = library().gemm_rms_norm_bwd_given(*args, w.data_ptr(), n, s)
+    _done(rc, "gemm_rms_norm_bwd_given")
     return dx, dweight
 
 
@@ -610,19 +641,14 @@ def _optional(name, x, dtype, rows, cols):
     return x.data_ptr(), ld
 
 
-_units = {}
-
-
 def _linear_call(torch, f, args, s, product, M, N, K, a, lda, b, ldb):
     """One entry point's call.  Where it needs temporary memory and the stream is
     capturing, again with some from torch, whose graphs keep theirs apart."""
     rc = f(*args, None, 0, s)
     if rc == GEMM_ERR_SCRATCH:
-        d = a.get_device()
-        if d not in _units:
-            _units[d] = torch.cuda.get_device_properties(d).multi_processor_count
         even = lambda x, ld: x.data_ptr() % 16 == 0 and (x.shape[0] <= 1 or (ld % 8 == 0 and ld <= 1 << 22))  # noqa: E731
-        plan = gemm_linear_plan_cus(M, N, K, product, even(a, lda), even(b, ldb), _units[d])
+        plan = gemm_linear_plan_cus(M, N, K, product, even(a, lda), even(b, ldb),
+                                    _compute_units(torch, a.get_device()))
         n = plan["scratch_bytes"]
         w = torch.empty(n, dtype=torch.uint8, device=a.device)
         rc = f(*args, w.data_ptr(), n, s)

@@ -2735,6 +2735,15 @@ struct TempMem {
     hipMemPool_t pool = nullptr;
     char* fixed = nullptr;
     int64_t fixed_left = 0;
+
+    // A caller's workspace, where there is one.
+    void given(void* workspace, int64_t bytes)
+    {
+        if (workspace) {
+            fixed = (char*)workspace;
+            fixed_left = bytes;
+        }
+    }
 };
 
 int64_t align256(int64_t b)
@@ -2832,6 +2841,24 @@ int temp_take(TempMem& t, int64_t bytes, hipStream_t s, void** p, hipEvent_t* do
     if (done)
         *done = v[best].done;
     return GEMM_OK;
+}
+
+// The same for entry points that take a caller's workspace: under graph capture
+// they have to be given it.  A captured step whose graph held memory of its own
+// (several allocations and frees, two of 53 MB) ended in an illegal access on
+// replay, and the cause is not known.
+int temp_take_outside_graphs(TempMem& t, int64_t bytes, hipStream_t s, void** p, hipEvent_t* done)
+{
+    if (!t.fixed) {
+        hipStreamCaptureStatus cs = hipStreamCaptureStatusNone;
+        if (hipStreamIsCapturing(s, &cs) != hipSuccess) {
+            (void)hipGetLastError();
+            return GEMM_ERR_DEVICE;
+        }
+        if (cs != hipStreamCaptureStatusNone)
+            return GEMM_ERR_SCRATCH;
+    }
+    return temp_take(t, bytes, s, p, done);
 }
 
 // Hands back what temp_take gave: a kept block becomes free once its

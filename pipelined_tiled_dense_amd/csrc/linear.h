@@ -1033,23 +1033,6 @@ int launch_wave(const LinearParams<MODE>& p, const LinearPlan& pl, bool even, hi
     return run.template operator()<4, 4 / F, 1>();
 }
 
-// Temporary memory of `bytes` for one call.  Not from the library's pool under graph
-// capture: a graph with memory of its own ended in an illegal access on replay, and its
-// cause is not known, so such a call is refused.
-int linear_take(TempMem& tm, int64_t bytes, hipStream_t s, void** p, hipEvent_t* done)
-{
-    if (!tm.fixed) {
-        hipStreamCaptureStatus cs = hipStreamCaptureStatusNone;
-        if (hipStreamIsCapturing(s, &cs) != hipSuccess) {
-            (void)hipGetLastError();
-            return GEMM_ERR_DEVICE;
-        }
-        if (cs != hipStreamCaptureStatusNone)
-            return GEMM_ERR_SCRATCH;
-    }
-    return temp_take(tm, bytes, s, p, done);
-}
-
 // The product of A and B into epilogue e.  The caller has checked everything but
 // the device.
 template <int MODE>
@@ -1130,7 +1113,7 @@ int linear_run(LinearShape q, const void* A, int64_t lda, const void* B, int64_t
         return enqueue(k_join_column_sums, dim3(sums.blocks), dim3(256), s, done, sums);
     };
     if (q.K == 0 || q.N == 0) {   // nothing to multiply
-        int rc = runs_bytes > 0 ? linear_take(tm, runs_bytes, s, &ws, &done) : (int)GEMM_OK;
+        int rc = runs_bytes > 0 ? temp_take_outside_graphs(tm, runs_bytes, s, &ws, &done) : (int)GEMM_OK;
         if (rc == GEMM_OK && dbias)
             rc = start_sums((float*)ws);
         if (rc == GEMM_OK && q.N > 0)
@@ -1151,7 +1134,7 @@ int linear_run(LinearShape q, const void* A, int64_t lda, const void* B, int64_t
     const int64_t sums_bytes = pl.splits > 1 || !far ? pl.workspace : pl.tiles * pl.bm * pl.bn * q.factors * 4;
     const int64_t bytes = a_bytes + b_bytes + runs_bytes + sums_bytes;
     int rc = GEMM_OK;
-    if (bytes > 0 && (rc = linear_take(tm, bytes, s, &ws, &done)) != GEMM_OK)
+    if (bytes > 0 && (rc = temp_take_outside_graphs(tm, bytes, s, &ws, &done)) != GEMM_OK)
         return rc;
     if (dbias)
         rc = start_sums((float*)((char*)ws + a_bytes + b_bytes));
@@ -1259,10 +1242,7 @@ int linear_enqueue(const LinearShape& q, const void* A, int64_t lda, const void*
     tm.device_done = true;
     if (const int rc = device_info(&cus, &tm.pool, nullptr, &tm.info))
         return rc;
-    if (workspace) {
-        tm.fixed = (char*)workspace;
-        tm.fixed_left = workspace_bytes;
-    }
+    tm.given(workspace, workspace_bytes);
     return linear_run<MODE>(q, A, lda, B, ldb, e, tm, cus, (hipStream_t)stream, dbias);
 }
 

@@ -303,11 +303,99 @@ void with_row_shape(const RowShape& rs, int64_t D, F&& f)
         even ? f.template operator()<4, true>() : f.template operator()<4, false>();
 }
 
+// Workgroups of the gradients' kernel.  Each writes D partial sums, so there are only as
+// many as give a compute unit 8 waves (8191 x 4096, 8 waves a row, both launches: one
+// workgroup each 54.1 us, two 59.5), and none with fewer than 2 rows.  A few rows: one
+// workgroup, whose sums are the weight's gradient, in one launch (3 x 4096 5.5 us, in
+// two launches 9.2; 8 rows are level at 4096 wide, 20.1 against 17.5 at 16384).
+int64_t norm_bwd_grid(int64_t M, int64_t D, int cus)
+{
+    const int nw = row_shape(D, 1).nw;
+    if (M <= 4)
+        return M > 0 ? 1 : 0;
+    return std::min<int64_t>((int64_t)cus * ((8 + nw - 1) / nw), (M + 1) / 2);
+}
+
 int norm_shape(int64_t M, int64_t D)
 {
     if (M < 0 || D < 1)
         return GEMM_ERR_INVALID_VALUE;
     return M > kMaxRows || D > GEMM_NORM_MAX_WIDTH ? GEMM_ERR_UNSUPPORTED_SHAPE : GEMM_OK;
+}
+
+// `take`: where the workgroups' shares of the weight's gradient come from.
+int rms_norm_bwd(int64_t M, int64_t D, const void* dY, int64_t lddy, const void* H, int64_t ldh, const void* weight,
+                 const float* rstd, const void* dres, int64_t lddr, void* dX, int64_t lddx, float* dweight,
+                 int (*take)(TempMem&, int64_t, hipStream_t, void**, hipEvent_t*), void* workspace,
+                 int64_t workspace_bytes, void* stream)
+{
+    if (int rc = norm_shape(M, D))
+        return rc;
+    const Operand dw{dweight, 1, D, D, 4};
+    int rc = check_operand(dw);
+    if (rc != GEMM_OK)
+        return rc;
+    const Operand dy{dY, M, D, lddy, 2}, h{H, M, D, ldh, 2}, w{weight, 1, D, D, 2}, v{rstd, 1, M, M, 4};
+    const Operand s{dres, M, D, lddr, 2}, dx{dX, M, D, lddx, 2};
+    if (M > 0) {
+        const Operand in[] = {dy, h, w, v, s};
+        rc = check_operands(in, dres ? 5 : 4);
+        if (rc == GEMM_OK)
+            rc = check_operand(dx);
+        if (rc != GEMM_OK)
+            return rc;
+        // As in the forward pass, a lane has read its values of the row before it writes them.
+        for (const Operand& i : in) {
+            if (meet(dw, i) || (meet(dx, i) && !((i.p == dy.p || i.p == s.p) && same_memory(dx, i))))
+                return GEMM_ERR_ALIAS;
+        }
+        if (meet(dx, dw))
+            return GEMM_ERR_ALIAS;
+    }
+    if (workspace) {
+        if (workspace_bytes < 0)
+            return GEMM_ERR_INVALID_VALUE;
+        if ((uintptr_t)workspace & 255)
+            return GEMM_ERR_MISALIGNED;
+        const Operand t{workspace, 1, workspace_bytes, workspace_bytes, 1};
+        for (const Operand& o : {dy, h, w, v, s, dx, dw})
+            if (meet(t, o))
+                return GEMM_ERR_ALIAS;
+    }
+    int cus = 0;
+    TempMem tm;
+    rc = device_info(&cus, &tm.pool, nullptr, &tm.info);
+    if (rc != GEMM_OK)
+        return rc;
+    tm.given(workspace, workspace_bytes);
+    hipStream_t st = (hipStream_t)stream;
+    const RowShape rs = row_shape(D, 1);
+    const int64_t grid = norm_bwd_grid(M, D, cus);
+    void* ws = nullptr;
+    hipEvent_t done = nullptr;
+    if (grid > 1) {
+        rc = take(tm, grid * D * 4, st, &ws, &done);
+        if (rc != GEMM_OK)
+            return rc;
+    }
+    if (grid > 0) {
+        NormBwdParams p{(const uint16_t*)dY, (const uint16_t*)H, (const uint16_t*)weight, rstd, (const uint16_t*)dres,
+                        (uint16_t*)dX, grid > 1 ? (float*)ws : dweight, M, lddy, ldh, lddr, lddx, (int32_t)D,
+                        1.0f / (float)D};
+        const dim3 g((unsigned)grid), b((unsigned)(rs.nw * 64));
+        with_row_shape(rs, D, [&]<int NCH, bool EVEN>() {
+            hipLaunchKernelGGL(HIP_KERNEL_NAME(k_rms_norm_bwd<NCH, EVEN>), g, b, 0, st, p, rs.nw);
+        });
+        rc = launched();
+    }
+    if (rc == GEMM_OK && grid != 1) {
+        // The shares' last use: its completion records the block's event.
+        hipExtLaunchKernelGGL(k_norm_weight_grad, dim3((unsigned)((D + 15) / 16)), dim3(1024), 0, st, nullptr, done, 0,
+                              (const float*)ws, (int32_t)grid, (int32_t)D, dweight);
+        rc = launched();
+    }
+    const int frc = temp_give(tm, ws, st, rc == GEMM_OK && done != nullptr);
+    return rc != GEMM_OK ? rc : frc;
 }
 
 }  // namespace
@@ -381,72 +469,25 @@ int gemm_rms_norm_bwd(int64_t M, int64_t D, const void* dY, int64_t lddy, const 
                       const void* weight, const float* rstd, const void* dres, int64_t lddr, void* dX, int64_t lddx,
                       float* dweight, void* stream)
 {
-    if (int rc = norm_shape(M, D))
+    return rms_norm_bwd(M, D, dY, lddy, H, ldh, weight, rstd, dres, lddr, dX, lddx, dweight, temp_take, nullptr, 0, stream);
+}
+
+int gemm_rms_norm_bwd_given(int64_t M, int64_t D, const void* dY, int64_t lddy, const void* H, int64_t ldh,
+                            const void* weight, const float* rstd, const void* dres, int64_t lddr, void* dX,
+                            int64_t lddx, float* dweight, void* workspace, int64_t workspace_bytes, void* stream)
+{
+    return rms_norm_bwd(M, D, dY, lddy, H, ldh, weight, rstd, dres, lddr, dX, lddx, dweight, temp_take_outside_graphs,
+                        workspace, workspace_bytes, stream);
+}
+
+int64_t gemm_rms_norm_bwd_scratch_cus(int64_t M, int64_t D, int compute_units)
+{
+    if (const int rc = norm_shape(M, D))
         return rc;
-    const Operand dw{dweight, 1, D, D, 4};
-    int rc = check_operand(dw);
-    if (rc != GEMM_OK)
-        return rc;
-    const Operand dy{dY, M, D, lddy, 2}, h{H, M, D, ldh, 2}, w{weight, 1, D, D, 2}, v{rstd, 1, M, M, 4};
-    const Operand s{dres, M, D, lddr, 2}, dx{dX, M, D, lddx, 2};
-    if (M > 0) {
-        const Operand in[] = {dy, h, w, v, s};
-        rc = check_operands(in, dres ? 5 : 4);
-        if (rc == GEMM_OK)
-            rc = check_operand(dx);
-        if (rc != GEMM_OK)
-            return rc;
-        // As in the forward pass, a lane has read its values of the row before it writes them.
-        for (const Operand& i : in) {
-            if (meet(dw, i) || (meet(dx, i) && !((i.p == dy.p || i.p == s.p) && same_memory(dx, i))))
-                return GEMM_ERR_ALIAS;
-        }
-        if (meet(dx, dw))
-            return GEMM_ERR_ALIAS;
-    }
-    int cus = 0;
-    TempMem tm;
-    rc = device_info(&cus, &tm.pool, nullptr, &tm.info);
-    if (rc != GEMM_OK)
-        return rc;
-    hipStream_t st = (hipStream_t)stream;
-    const RowShape rs = row_shape(D, 1);
-    // Each workgroup writes D partial sums, so there are only as many as give a
-    // compute unit 8 waves (8191 x 4096, 8 waves a row, both launches: one
-    // workgroup each 54.1 us, two 59.5), and none with fewer than 2 rows.
-    int64_t grid = (int64_t)cus * ((8 + rs.nw - 1) / rs.nw);
-    if (grid > (M + 1) / 2)
-        grid = (M + 1) / 2;
-    // A few rows: one workgroup, whose sums are the weight's gradient, in one launch
-    // (3 x 4096 5.5 us, in two launches 9.2; 8 rows are level at 4096 wide, 20.1 against
-    // 17.5 at 16384).
-    if (M <= 4)
-        grid = M > 0 ? 1 : 0;
-    void* ws = nullptr;
-    hipEvent_t done = nullptr;
-    if (grid > 1) {
-        rc = temp_take(tm, grid * D * 4, st, &ws, &done);
-        if (rc != GEMM_OK)
-            return rc;
-    }
-    if (grid > 0) {
-        NormBwdParams p{(const uint16_t*)dY, (const uint16_t*)H, (const uint16_t*)weight, rstd, (const uint16_t*)dres,
-                        (uint16_t*)dX, grid > 1 ? (float*)ws : dweight, M, lddy, ldh, lddr, lddx, (int32_t)D,
-                        1.0f / (float)D};
-        const dim3 g((unsigned)grid), b((unsigned)(rs.nw * 64));
-        with_row_shape(rs, D, [&]<int NCH, bool EVEN>() {
-            hipLaunchKernelGGL(HIP_KERNEL_NAME(k_rms_norm_bwd<NCH, EVEN>), g, b, 0, st, p, rs.nw);
-        });
-        rc = launched();
-    }
-    if (rc == GEMM_OK && grid != 1) {
-        // The shares' last use: its completion records the block's event.
-        hipExtLaunchKernelGGL(k_norm_weight_grad, dim3((unsigned)((D + 15) / 16)), dim3(1024), 0, st, nullptr, done, 0,
-                              (const float*)ws, (int32_t)grid, (int32_t)D, dweight);
-        rc = launched();
-    }
-    const int frc = temp_give(tm, ws, st, rc == GEMM_OK && done != nullptr);
-    return rc != GEMM_OK ? rc : frc;
+    if (compute_units < 1)
+        return GEMM_ERR_INVALID_VALUE;
+    const int64_t grid = norm_bwd_grid(M, D, compute_units);
+    return grid > 1 ? align256(grid * D * 4) : 0;
 }
 
 }  // extern "C"
