@@ -575,7 +575,7 @@ def rms_norm_backward(dy, h, weight, rstd, *, dresidual=None, stream=None):
         n = gemm_rms_norm_bwd_scratch_cus(M, D, _compute_units(torch, dy.get_device()))
         w = torch.empty(n, dtype=torch.uint8, device=dev)
         rc = library().gemm_rms_norm_bwd_given(*args, w.data_ptr(), n, s)
-    _done(rc, "gemm_rms_norm_bwd_given")
+    _done(rc, "gemm_rms_norm_bwd")
     return dx, dweight
 
 

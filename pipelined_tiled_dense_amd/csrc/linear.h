@@ -557,8 +557,9 @@ __global__ void __launch_bounds__(256) k_linear_finish(LinearParams<MODE> p, int
 // waits for another wave before the end, and there is little code to fetch (a launch
 // of the tiles' kernel takes 5 us longer for that alone).  512 x 512 x 512: 9 us, 11 in
 // tiles; the gated gradient of 25 x 72 over 1344 9.5 and 19.  One row reads the weight at
-// 5 TB/s (8192 x 4096 in 13 us); 300 x 1000 x 4112 takes 13.9 in 240 workgroups, whose
-// loads the L2 serves (27 MB from memory, 138 MB through it).
+// 5 TB/s (8192 x 4096 in 13 us); 300 x 1000 x 4112 takes 13.9 in 240 workgroups that load
+// 138 MB, 27 of them from memory: each wave has two or three blocks in series, and which
+// of the start, the loads and the join is the time was not separated.
 //
 // A wave loads DEPTH blocks ahead into registers, a block's 16-byte chunks in rows
 // (lanes 8 i .. 8 i + 7 a row's 128 bytes), writes them to LDS of its own and reads
